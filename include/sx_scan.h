@@ -20,6 +20,14 @@
  *   linear-scan   the same section: matrix-scan over one-by-one matrices,
  *                 a and b broadcast to one shape (cumsum: a = 1).
  *
+ * and the operators of a linear-attention layer, whose state is a matrix-scan
+ * with a scalar step and a rank-one input, read out by a query:
+ *
+ *   decay-attention  linear attention with a decay for each head, over prompts,
+ *                 with its gradient, and for single tokens.
+ *   head-norm-rotate  the norm of each head of queries and keys and the
+ *                 rotation by position, with its gradient.
+ *
  * Conventions shared by every entry point:
  *
  *  - Pointers to tensor data are DEVICE pointers on the device that is
@@ -402,6 +410,171 @@ int sx_linear_scan_out_shape(int a_rank, const int64_t* a_shape, int b_rank, con
 sx_status sx_table_scan(int states, int nsym, const int32_t* table, int rank, const int64_t* shape,
                         const int64_t* strides, const int32_t* symbols, int axis, int32_t start, int32_t* out,
                         void* stream);
+
+/*
+ * sx_decay_attention: linear attention with a decay for each head. With S a
+ * dk-by-dv state for every batch row and head, from `initial` (or zero),
+ *   S[t] = exp(g[t]) S[t-1] + k[t] v[t]^T,   out[t] = scale * S[t]^T q[t].
+ * States, running sums and products are f32 (and finer) for f32 and bf16
+ * operands alike; out is rounded to bf16 to nearest even once, on store. With
+ * bf16 operands the state enters its products as three bf16 parts that carry
+ * all of it, and the scores q[t] . k[s] as two that carry 16 bits.
+ *
+ *  dtype         SX_F32 or SX_BF16, shared by q, k, v and out.
+ *  q, k, v       [B, T, heads, width]: shape (4 entries), strides (NULL for
+ *                contiguous; any value) and data. q and k share their width dk,
+ *                v has dv, each 1..256. The number of heads of each divides H;
+ *                head h of the call uses head h / (H / heads) of it.
+ *  g_*, log_decay  g, the natural log of the decay, f32: [H] (g_rank 1, one
+ *                value a head) or [B, T, H] (g_rank 3), with strides. H is the
+ *                number of heads of out. -INFINITY cuts: nothing of what came
+ *                before is left. Values are taken into [-200, 200], where exp is
+ *                0 and infinite in f32.
+ *  initial       f32, contiguous [B, H, dk, dv], or NULL for zero.
+ *  lengths       int32 [B], or NULL. Tokens of row b from lengths[b] on do not
+ *                exist: they are not read, their rows of out are zero and the
+ *                state ends before them. Taken into [0, T].
+ *  out           contiguous [B, T, H, dv].
+ *  final_state   f32, contiguous [B, H, dk, dv]: the state after the last token,
+ *                or NULL.
+ *  workspace     at least sx_decay_attention_workspace_bytes() bytes, 256-byte
+ *                aligned; may hold anything; may be NULL when that is 0.
+ *
+ * An infinity or NaN of one token reaches that token's own row and later ones of
+ * its head, never earlier ones (an infinity may come out as NaN). out and
+ * final_state are 16-byte aligned (else SX_E_UNSUPPORTED) and overlap no input
+ * and not each other (SX_E_ALIAS). Errors otherwise as the scans: E-DIM-001 shapes,
+ * E-DIM-002 dtypes, E-DIM-003 a NULL tensor that has elements, SX_E_UNSUPPORTED
+ * heads wider than 256.
+ */
+sx_status sx_decay_attention(sx_dtype dtype, const int64_t* q_shape, const int64_t* q_strides, const void* q,
+                             const int64_t* k_shape, const int64_t* k_strides, const void* k, const int64_t* v_shape,
+                             const int64_t* v_strides, const void* v, int g_rank, const int64_t* g_shape,
+                             const int64_t* g_strides, const float* log_decay, const float* initial,
+                             const int32_t* lengths, float scale, void* out, float* final_state, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Workspace bytes sx_decay_attention needs for H = heads (0 when none, or for shapes it would reject). */
+size_t sx_decay_attention_workspace_bytes(sx_dtype dtype, const int64_t* q_shape, const int64_t* v_shape,
+                                          int64_t heads);
+
+/*
+ * sx_decay_attention_backward: gradients of sx_decay_attention. With A[t] the
+ * adjoint of S[t],
+ *   A[t] = exp(g[t+1]) A[t+1] + scale q[t] grad_out[t]^T   (grad_state after the last token)
+ *   grad_q[t] = scale S[t] grad_out[t],  grad_k[t] = A[t] v[t],  grad_v[t] = A[t]^T k[t],
+ *   grad_log_decay[t] = exp(g[t]) <A[t], S[t-1]>,  grad_initial = exp(g[0]) A[0].
+ *
+ *  dtype .. log_decay, initial, lengths, scale   as for the forward call.
+ *  grad_out      [B, T, H, dv], dtype `dtype`, with strides (NULL for contiguous).
+ *  grad_state    f32, contiguous [B, H, dk, dv]: the gradient of final_state, or
+ *                NULL for none.
+ *  grad_q/k/v    contiguous, the shapes of q, k and v, dtype `dtype`. A head that
+ *                several heads of the call share gets the sum of their
+ *                gradients, summed in f32 and rounded once.
+ *  grad_log_decay  f32, contiguous, the shape of log_decay ([H]: summed over rows
+ *                and tokens). Zero where the decay is.
+ *  grad_initial  f32, contiguous [B, H, dk, dv]; may be NULL when initial is.
+ *  workspace     at least sx_decay_attention_backward_workspace_bytes() bytes,
+ *                256-byte aligned; may hold anything.
+ *
+ * Gradients of tokens that do not exist are zero. The outputs are 16-byte
+ * aligned and overlap nothing. Results do not change from call to call (no
+ * atomics). Errors as sx_decay_attention.
+ */
+sx_status sx_decay_attention_backward(sx_dtype dtype, const int64_t* q_shape, const int64_t* q_strides, const void* q,
+                                      const int64_t* k_shape, const int64_t* k_strides, const void* k,
+                                      const int64_t* v_shape, const int64_t* v_strides, const void* v, int g_rank,
+                                      const int64_t* g_shape, const int64_t* g_strides, const float* log_decay,
+                                      const int64_t* grad_out_strides, const void* grad_out, const float* grad_state,
+                                      const float* initial, const int32_t* lengths, float scale, void* grad_q,
+                                      void* grad_k, void* grad_v, float* grad_log_decay, float* grad_initial,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes sx_decay_attention_backward needs for H = heads (0 for shapes it would reject). */
+size_t sx_decay_attention_backward_workspace_bytes(sx_dtype dtype, const int64_t* q_shape, const int64_t* k_shape,
+                                                   const int64_t* v_shape, int64_t heads);
+
+/*
+ * sx_decay_attention_step: one token of every request of a batch, the states
+ * updated in place: S = exp(g) S + k v^T, out = scale * S^T q.
+ *
+ *  q, k, v       [B, heads, width] (3 entries of shape and strides), heads and
+ *                widths as for sx_decay_attention.
+ *  g_*, log_decay  [H] (g_rank 1) or [B, H] (g_rank 2), f32.
+ *  pool, state_strides, state
+ *                f32 states [pool, H, dk, dv]; each head's dk-by-dv block
+ *                row-major contiguous (else SX_E_UNSUPPORTED), no two blocks
+ *                overlapping.
+ *  slots         int32 [B]: the state of each row, or NULL (row b uses state b;
+ *                pool >= B then). A row whose slot lies outside [0, pool) is
+ *                idle: its row of out is zero and no state changes. Two rows with
+ *                the same slot race: that state and those rows of out are then
+ *                undefined.
+ *  out           contiguous [B, H, dv], 16-byte aligned.
+ *
+ * No workspace. Errors as sx_decay_attention.
+ */
+sx_status sx_decay_attention_step(sx_dtype dtype, const int64_t* q_shape, const int64_t* q_strides, const void* q,
+                                  const int64_t* k_shape, const int64_t* k_strides, const void* k,
+                                  const int64_t* v_shape, const int64_t* v_strides, const void* v, int g_rank,
+                                  const int64_t* g_shape, const int64_t* g_strides, const float* log_decay,
+                                  int64_t pool, const int64_t* state_strides, float* state, const int32_t* slots,
+                                  float scale, void* out, void* stream);
+
+/*
+ * sx_head_norm_rotate: the root-mean-square norm of each head of the queries and
+ * keys, and the rotation by position, in one pass. For each row x of width d,
+ *   u = x / sqrt(mean(x^2) + eps) * weight,
+ *   y = u with the pairs of its first `rotated` components turned by
+ *       2 pi position turns[i]:  (a, b) -> (a cos - b sin, a sin + b cos).
+ * Pair i is (i, i + rotated/2), or (2i, 2i+1) when `neighbours` is nonzero; the
+ * components behind `rotated` are not turned. Angles are reduced in 64 bits, so
+ * far positions lose nothing; the rest is f32, rounded to `dtype` once.
+ *
+ *  dtype         SX_F32 or SX_BF16: q, k and the results.
+ *  q, k          [B, T, heads, d] with strides (NULL for contiguous; any value),
+ *                the same B, T and d (1..256); the numbers of heads are free.
+ *  positions     [B, T], int64 (positions_i64 nonzero) or int32, with strides
+ *                (NULL for contiguous; 0 for one row or one value for all).
+ *  rotated, turns  an even number up to d, and f64 [rotated/2]: turns (of 2 pi)
+ *                of pair i for each position.
+ *  q_weight, k_weight  f32 [d], or NULL for ones.
+ *  out_q, out_k  contiguous, the shapes of q and k, 16-byte aligned; overlap
+ *                nothing.
+ */
+sx_status sx_head_norm_rotate(sx_dtype dtype, const int64_t* q_shape, const int64_t* q_strides, const void* q,
+                              const int64_t* k_shape, const int64_t* k_strides, const void* k, int positions_i64,
+                              const int64_t* position_strides, const void* positions, int64_t rotated,
+                              const double* turns, const float* q_weight, const float* k_weight, float eps,
+                              int neighbours, void* out_q, void* out_k, void* stream);
+
+/*
+ * sx_head_norm_rotate_backward: gradients of sx_head_norm_rotate. With r = 1 /
+ * sqrt(mean(x^2) + eps) and gu the gradient of a row turned back,
+ *   grad_weight = sum over rows of gu x r,
+ *   grad_x = r (gu weight - x r^2 mean(gu weight x)).
+ *
+ *  dtype .. neighbours  as for the forward call; grad_out_q and grad_out_k have
+ *                the shapes of q and k, with strides (NULL for contiguous).
+ *  grad_q, grad_k  contiguous, the shapes of q and k, dtype `dtype`.
+ *  grad_q_weight, grad_k_weight  f32 [d], or NULL where not wanted. Summed in a
+ *                fixed order (no atomics).
+ *  workspace     at least sx_head_norm_rotate_backward_workspace_bytes() bytes,
+ *                256-byte aligned, when a weight's gradient is wanted; may hold
+ *                anything.
+ */
+sx_status sx_head_norm_rotate_backward(sx_dtype dtype, const int64_t* q_shape, const int64_t* q_strides,
+                                       const void* q, const int64_t* k_shape, const int64_t* k_strides, const void* k,
+                                       int positions_i64, const int64_t* position_strides, const void* positions,
+                                       int64_t rotated, const double* turns, const int64_t* gq_strides,
+                                       const void* grad_out_q, const int64_t* gk_strides, const void* grad_out_k,
+                                       const float* q_weight, const float* k_weight, float eps, int neighbours,
+                                       void* grad_q, void* grad_k, float* grad_q_weight, float* grad_k_weight,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes sx_head_norm_rotate_backward needs for the weights' gradients. */
+size_t sx_head_norm_rotate_backward_workspace_bytes(const int64_t* q_shape);
 
 /* "E-DIM-001" etc. for a status; "OK" for SX_OK. Static storage. */
 const char* sx_status_name(sx_status status);

@@ -9,6 +9,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -94,6 +95,29 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                    c_int, c_int, c_int, vp, vp]
     lib.sx_linear_scan_out_shape.restype = c_int
     lib.sx_linear_scan_out_shape.argtypes = [c_int, _i64p, c_int, _i64p, _i64p]
+    c_i64, c_f = ctypes.c_int64, ctypes.c_float
+    tensor = [_i64p, _i64p, vp]  # shape, strides, data
+    lib.sx_decay_attention.restype = c_int
+    lib.sx_decay_attention.argtypes = [c_int, *tensor, *tensor, *tensor, c_int, *tensor, vp, vp, c_f, vp, vp, vp,
+                                       c_size, vp]
+    lib.sx_decay_attention_workspace_bytes.restype = c_size
+    lib.sx_decay_attention_workspace_bytes.argtypes = [c_int, _i64p, _i64p, c_i64]
+    lib.sx_decay_attention_backward.restype = c_int
+    lib.sx_decay_attention_backward.argtypes = [c_int, *tensor, *tensor, *tensor, c_int, *tensor, _i64p, vp, vp, vp,
+                                                vp, c_f, vp, vp, vp, vp, vp, vp, c_size, vp]
+    lib.sx_decay_attention_backward_workspace_bytes.restype = c_size
+    lib.sx_decay_attention_backward_workspace_bytes.argtypes = [c_int, _i64p, _i64p, _i64p, c_i64]
+    lib.sx_decay_attention_step.restype = c_int
+    lib.sx_decay_attention_step.argtypes = [c_int, *tensor, *tensor, *tensor, c_int, *tensor, c_i64, _i64p, vp, vp,
+                                            c_f, vp, vp]
+    lib.sx_head_norm_rotate.restype = c_int
+    lib.sx_head_norm_rotate.argtypes = [c_int, *tensor, *tensor, c_int, _i64p, vp, c_i64, vp, vp, vp, c_f, c_int, vp,
+                                        vp, vp]
+    lib.sx_head_norm_rotate_backward.restype = c_int
+    lib.sx_head_norm_rotate_backward.argtypes = [c_int, *tensor, *tensor, c_int, _i64p, vp, c_i64, vp, _i64p, vp,
+                                                 _i64p, vp, vp, vp, c_f, c_int, vp, vp, vp, vp, vp, c_size, vp]
+    lib.sx_head_norm_rotate_backward_workspace_bytes.restype = c_size
+    lib.sx_head_norm_rotate_backward_workspace_bytes.argtypes = [_i64p]
     lib.sx_matrix_scan_workspace_status.restype = c_int
     lib.sx_matrix_scan_workspace_status.argtypes = [vp, c_size, vp]
     lib.sx_set_lookback_spin_limit.restype = None
@@ -540,3 +564,290 @@ def _matrix_dims_contiguous(t: torch.Tensor) -> bool:
     rows, cols = t.shape[-2], t.shape[-1]
     st = t.stride()
     return (cols <= 1 or st[-1] == 1) and (rows <= 1 or cols == 0 or st[-2] == cols)
+
+
+# ---------------------------------------------------------------- linear attention
+
+def _require_same_device(op: str, tensors) -> torch.device:
+    given = [(name, t) for name, t in tensors if t is not None]
+    for name, t in given:
+        _require_device_tensor(f"{op}: {name}", t)
+    if any(t.device != given[0][1].device for _, t in given):
+        raise SxError(SX_E_UNSUPPORTED, f"{op}: operands on different devices")
+    return given[0][1].device
+
+
+def _require_dtype(op: str, tensors) -> int:
+    """One float dtype (f32 or bf16) for all; its code."""
+    first = tensors[0][1].dtype
+    if first not in _DTYPES or any(t.dtype != first for _, t in tensors):
+        said = ", ".join(f"{name} is {t.dtype}" for name, t in tensors)
+        raise SxError(SX_E_DIM_002, f"{op}: {said}; one float dtype (f32 or bf16) is required")
+    return _DTYPES[first]
+
+
+def _require(op: str, name: str, t, dtype, shape) -> None:
+    """An optional operand of a fixed dtype and shape."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise SxError(SX_E_DIM_002, f"{op}: {name} is {t.dtype}, {dtype} is required")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise SxError(SX_E_DIM_001, f"{op}: {name} is {tuple(t.shape)}, {tuple(shape)} is required")
+
+
+def _args(t: torch.Tensor):
+    return i64_array(t.shape), i64_array(t.stride()), t.data_ptr()
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _contiguous(t):
+    return None if t is None else t.contiguous()
+
+
+def _decay_operands(op, q, k, v, log_decay, initial, lengths, token_dims):
+    """Checks what the C library cannot see (types, devices, optional operands); the dtype code and H."""
+    dev = _require_same_device(op, [("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("initial", initial),
+                                    ("lengths", lengths)])
+    code = _require_dtype(op, [("q", q), ("k", k), ("v", v)])
+    rank = 2 + token_dims
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dim() != rank:
+            raise SxError(SX_E_DIM_001, f"{op}: {name} {tuple(t.shape)} must have {rank} dims")
+    if log_decay.dtype != torch.float32:
+        raise SxError(SX_E_DIM_002, f"{op}: log_decay is {log_decay.dtype}, torch.float32 is required")
+    if log_decay.dim() not in (1, 1 + token_dims):
+        raise SxError(SX_E_DIM_001, f"{op}: log_decay {tuple(log_decay.shape)} must be [heads] or have a value a token")
+    heads = int(log_decay.shape[-1])
+    _require(op, "initial", initial, torch.float32, (q.shape[0], heads, q.shape[-1], v.shape[-1]))
+    _require(op, "lengths", lengths, torch.int32, (q.shape[0],))
+    return code, heads, dev
+
+
+def decay_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, initial=None,
+                    lengths=None, scale: float = 1.0, return_state: bool = False):
+    """Linear attention with a decay for each head, on the GPU:
+    ``S[t] = exp(log_decay[t]) S[t-1] + k[t] v[t]^T`` and ``out[t] = scale * S[t]^T q[t]``.
+
+    ``q`` and ``k`` are ``[B, T, heads, dk]`` and ``v`` ``[B, T, heads, dv]``, of one
+    dtype (f32 or bf16) and any strides; ``log_decay`` is f32, ``[H]`` or
+    ``[B, T, H]`` (``-inf`` cuts off what came before). The heads of q, k and v
+    each divide H, and are shared by H / heads heads. ``initial`` is the state
+    before the first token (f32 ``[B, H, dk, dv]``, zero when None); tokens of
+    row b from ``lengths[b]`` (int32 ``[B]``) on do not exist. Returns out
+    ``[B, T, H, dv]``, and the last state too when ``return_state``. When autograd
+    records, the gradient runs through ``decay_attention_backward``.
+    """
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad
+                                       for t in (q, k, v, log_decay, initial)):
+        out, state = _DecayAttentionFunction.apply(q, k, v, log_decay, initial, lengths, scale, return_state)
+    else:
+        out, state = _decay_attention_forward(q, k, v, log_decay, initial, lengths, scale, return_state)
+    return (out, state) if return_state else out
+
+
+def _decay_attention_forward(q, k, v, log_decay, initial, lengths, scale, return_state):
+    op = "decay-attention"
+    code, heads, dev = _decay_operands(op, q, k, v, log_decay, initial, lengths, 2)
+    initial, lengths = _contiguous(initial), _contiguous(lengths)
+    lib = load_library()
+    out = torch.empty((q.shape[0], q.shape[1], heads, v.shape[-1]), dtype=q.dtype, device=dev)
+    state = None
+    if return_state:
+        state = torch.empty((q.shape[0], heads, q.shape[-1], v.shape[-1]), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        qa, va = _args(q), _args(v)
+        nbytes = lib.sx_decay_attention_workspace_bytes(code, qa[0], va[0], heads)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        _check(lib.sx_decay_attention(code, *qa, *_args(k), *va, log_decay.dim(), *_args(log_decay), _ptr(initial),
+                                      _ptr(lengths), float(scale), out.data_ptr(), _ptr(state), _ptr(ws), nbytes,
+                                      _stream_handle(dev)))
+    return out, state
+
+
+def decay_attention_backward(q, k, v, log_decay, grad_out, initial=None, lengths=None, scale: float = 1.0,
+                             grad_state=None):
+    """Gradients ``(grad_q, grad_k, grad_v, grad_log_decay, grad_initial)`` of a loss through
+    ``decay_attention(q, k, v, log_decay, initial, lengths, scale)``.
+
+    ``grad_out`` is the loss's gradient with respect to out (its shape, q's
+    dtype), ``grad_state`` the one with respect to the last state (f32, or None).
+    Each gradient has its operand's shape and dtype; ``grad_initial`` is the
+    gradient of the state before the first token, also when that was zero.
+    """
+    op = "decay-attention gradient"
+    code, heads, dev = _decay_operands(op, q, k, v, log_decay, initial, lengths, 2)
+    _require_same_device(op, [("q", q), ("grad_out", grad_out), ("grad_state", grad_state)])
+    _require(op, "grad_out", grad_out, q.dtype, (q.shape[0], q.shape[1], heads, v.shape[-1]))
+    state_shape = (q.shape[0], heads, q.shape[-1], v.shape[-1])
+    _require(op, "grad_state", grad_state, torch.float32, state_shape)
+    initial, lengths, grad_state = _contiguous(initial), _contiguous(lengths), _contiguous(grad_state)
+    lib = load_library()
+    gq, gk, gv = (torch.empty(tuple(t.shape), dtype=t.dtype, device=dev) for t in (q, k, v))
+    gg = torch.empty(tuple(log_decay.shape), dtype=torch.float32, device=dev)
+    gi = torch.empty(state_shape, dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        qa, ka, va = _args(q), _args(k), _args(v)
+        nbytes = lib.sx_decay_attention_backward_workspace_bytes(code, qa[0], ka[0], va[0], heads)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        _check(lib.sx_decay_attention_backward(
+            code, *qa, *ka, *va, log_decay.dim(), *_args(log_decay), i64_array(grad_out.stride()),
+            grad_out.data_ptr(), _ptr(grad_state), _ptr(initial), _ptr(lengths), float(scale), gq.data_ptr(),
+            gk.data_ptr(), gv.data_ptr(), gg.data_ptr(), gi.data_ptr(), _ptr(ws), nbytes, _stream_handle(dev)))
+    return gq, gk, gv, gg, gi
+
+
+class _DecayAttentionFunction(torch.autograd.Function):
+    """decay_attention with its gradient from the library: saves the inputs."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, initial, lengths, scale, return_state):
+        out, state = _decay_attention_forward(q, k, v, log_decay, initial, lengths, scale, return_state)
+        ctx.save_for_backward(q, k, v, log_decay, initial, lengths)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return out, state
+
+    @staticmethod
+    def backward(ctx, grad_out, grad_state):
+        q, k, v, log_decay, initial, lengths = ctx.saved_tensors
+        if grad_out is None:
+            grad_out = torch.zeros((1, 1, 1, 1), dtype=q.dtype, device=q.device).expand(
+                q.shape[0], q.shape[1], log_decay.shape[-1], v.shape[-1])
+        gq, gk, gv, gg, gi = decay_attention_backward(q, k, v, log_decay, grad_out, initial=initial, lengths=lengths,
+                                                      scale=ctx.scale, grad_state=grad_state)
+        return gq, gk, gv, gg, gi if initial is not None else None, None, None, None
+
+
+def decay_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                         state: torch.Tensor, slots=None, scale: float = 1.0) -> torch.Tensor:
+    """One token of every request of a batch: ``S = exp(log_decay) S + k v^T``, ``out = scale * S^T q``.
+
+    ``q`` and ``k`` are ``[B, heads, dk]``, ``v`` ``[B, heads, dv]``, ``log_decay``
+    ``[H]`` or ``[B, H]``. ``state`` (f32 ``[pool, H, dk, dv]``) is updated in
+    place; row b uses state ``slots[b]`` (int32 ``[B]``; state b when None). A row
+    whose slot lies outside the pool is idle: zero out, no state changed; two
+    rows of one slot race. Returns out ``[B, H, dv]``. No gradient is recorded.
+    """
+    op = "decay-attention step"
+    code, heads, dev = _decay_operands(op, q, k, v, log_decay, None, None, 1)
+    _require_same_device(op, [("q", q), ("state", state), ("slots", slots)])
+    if state.dim() != 4 or tuple(state.shape[1:]) != (heads, q.shape[-1], v.shape[-1]):
+        raise SxError(SX_E_DIM_001, f"{op}: state is {tuple(state.shape)}, "
+                                    f"[states, {heads}, {q.shape[-1]}, {v.shape[-1]}] is required")
+    _require(op, "state", state, torch.float32, None)
+    _require(op, "slots", slots, torch.int32, (q.shape[0],))
+    slots = _contiguous(slots)
+    lib = load_library()
+    out = torch.empty((q.shape[0], heads, v.shape[-1]), dtype=q.dtype, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib.sx_decay_attention_step(code, *_args(q), *_args(k), *_args(v), log_decay.dim(), *_args(log_decay),
+                                           int(state.shape[0]), i64_array(state.stride()), state.data_ptr(),
+                                           _ptr(slots), float(scale), out.data_ptr(), _stream_handle(dev)))
+    return out
+
+
+def rotation_turns(rotated: int, base: float = 10000.0, device=None) -> torch.Tensor:
+    """Turns (of 2 pi) a position of each pair of ``rotated`` components: ``base^(-2 i / rotated) / (2 pi)``,
+    f64 ``[rotated / 2]``, for ``head_norm_rotate``."""
+    if rotated < 0 or rotated % 2 != 0:
+        raise SxError(SX_E_DIM_001, f"rotation_turns: {rotated} components do not make pairs")
+    i = torch.arange(rotated // 2, dtype=torch.float64, device=device)
+    return float(base) ** (-2.0 * i / max(rotated, 1)) / (2.0 * math.pi)
+
+
+def _rotate_operands(op, q, k, positions, turns, q_weight, k_weight):
+    dev = _require_same_device(op, [("q", q), ("k", k), ("positions", positions), ("turns", turns),
+                                    ("q_weight", q_weight), ("k_weight", k_weight)])
+    code = _require_dtype(op, [("q", q), ("k", k)])
+    for name, t in (("q", q), ("k", k)):
+        if t.dim() != 4:
+            raise SxError(SX_E_DIM_001, f"{op}: {name} {tuple(t.shape)} must be [batch, tokens, heads, width]")
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise SxError(SX_E_DIM_002, f"{op}: positions are {positions.dtype}, int32 or int64 is required")
+    if tuple(positions.shape) == (q.shape[1],):
+        positions = positions[None].expand(q.shape[0], q.shape[1])
+    _require(op, "positions", positions, positions.dtype, tuple(q.shape[:2]))
+    if turns.dim() != 1:
+        raise SxError(SX_E_DIM_001, f"{op}: turns {tuple(turns.shape)} must have one dim")
+    _require(op, "turns", turns, torch.float64, None)
+    _require(op, "q_weight", q_weight, torch.float32, (q.shape[-1],))
+    _require(op, "k_weight", k_weight, torch.float32, (q.shape[-1],))
+    return code, dev, positions, turns.contiguous(), _contiguous(q_weight), _contiguous(k_weight)
+
+
+def head_norm_rotate(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, turns: torch.Tensor, q_weight=None,
+                     k_weight=None, eps: float = 1e-6, neighbours: bool = False):
+    """The root-mean-square norm of each head of ``q`` and ``k`` and their rotation by position, in one pass.
+
+    ``q`` and ``k`` are ``[B, T, heads, d]`` (f32 or bf16, any strides),
+    ``positions`` int32 or int64 ``[B, T]`` or ``[T]``, ``turns`` f64 (see
+    ``rotation_turns``): the first ``2 * len(turns)`` components turn in pairs
+    ``(i, i + len(turns))``, or ``(2 i, 2 i + 1)`` when ``neighbours``. The weights
+    are f32 ``[d]`` (ones when None). Returns the two results, contiguous, in q's
+    dtype. When autograd records, the gradient runs through
+    ``head_norm_rotate_backward``.
+    """
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad
+                                       for t in (q, k, q_weight, k_weight)):
+        return _HeadNormRotateFunction.apply(q, k, positions, turns, q_weight, k_weight, eps, neighbours)
+    return _head_norm_rotate_forward(q, k, positions, turns, q_weight, k_weight, eps, neighbours)
+
+
+def _head_norm_rotate_forward(q, k, positions, turns, q_weight, k_weight, eps, neighbours):
+    op = "head-norm-rotate"
+    code, dev, positions, turns, q_weight, k_weight = _rotate_operands(op, q, k, positions, turns, q_weight, k_weight)
+    lib = load_library()
+    oq, ok = (torch.empty(tuple(t.shape), dtype=t.dtype, device=dev) for t in (q, k))
+    with torch.cuda.device(dev):
+        _check(lib.sx_head_norm_rotate(code, *_args(q), *_args(k), int(positions.dtype == torch.int64),
+                                       i64_array(positions.stride()), positions.data_ptr(), 2 * turns.shape[0],
+                                       turns.data_ptr(), _ptr(q_weight), _ptr(k_weight), float(eps),
+                                       int(bool(neighbours)), oq.data_ptr(), ok.data_ptr(), _stream_handle(dev)))
+    return oq, ok
+
+
+def head_norm_rotate_backward(q, k, positions, turns, grad_out_q, grad_out_k, q_weight=None, k_weight=None,
+                              eps: float = 1e-6, neighbours: bool = False):
+    """Gradients ``(grad_q, grad_k, grad_q_weight, grad_k_weight)`` of a loss through
+    ``head_norm_rotate(q, k, positions, turns, q_weight, k_weight, eps, neighbours)``, given its gradients with
+    respect to the two results (their shapes, q's dtype). A weight that is None has None for its gradient."""
+    op = "head-norm-rotate gradient"
+    code, dev, positions, turns, q_weight, k_weight = _rotate_operands(op, q, k, positions, turns, q_weight, k_weight)
+    _require_same_device(op, [("q", q), ("grad_out_q", grad_out_q), ("grad_out_k", grad_out_k)])
+    _require(op, "grad_out_q", grad_out_q, q.dtype, tuple(q.shape))
+    _require(op, "grad_out_k", grad_out_k, k.dtype, tuple(k.shape))
+    lib = load_library()
+    gq, gk = (torch.empty(tuple(t.shape), dtype=t.dtype, device=dev) for t in (q, k))
+    gqw, gkw = (None if w is None else torch.empty_like(w) for w in (q_weight, k_weight))
+    with torch.cuda.device(dev):
+        qa = _args(q)
+        nbytes = lib.sx_head_norm_rotate_backward_workspace_bytes(qa[0]) if gqw is not None or gkw is not None else 0
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        _check(lib.sx_head_norm_rotate_backward(
+            code, *qa, *_args(k), int(positions.dtype == torch.int64), i64_array(positions.stride()),
+            positions.data_ptr(), 2 * turns.shape[0], turns.data_ptr(), i64_array(grad_out_q.stride()),
+            grad_out_q.data_ptr(), i64_array(grad_out_k.stride()), grad_out_k.data_ptr(), _ptr(q_weight),
+            _ptr(k_weight), float(eps), int(bool(neighbours)), gq.data_ptr(), gk.data_ptr(), _ptr(gqw), _ptr(gkw),
+            _ptr(ws), nbytes, _stream_handle(dev)))
+    return gq, gk, gqw, gkw
+
+
+class _HeadNormRotateFunction(torch.autograd.Function):
+    """head_norm_rotate with its gradient from the library: saves the inputs."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, turns, q_weight, k_weight, eps, neighbours):
+        ctx.save_for_backward(q, k, positions, turns, q_weight, k_weight)
+        ctx.eps, ctx.neighbours = eps, neighbours
+        return _head_norm_rotate_forward(q, k, positions, turns, q_weight, k_weight, eps, neighbours)
+
+    @staticmethod
+    def backward(ctx, grad_out_q, grad_out_k):
+        q, k, positions, turns, q_weight, k_weight = ctx.saved_tensors
+        gq, gk, gqw, gkw = head_norm_rotate_backward(q, k, positions, turns, grad_out_q, grad_out_k, q_weight=q_weight,
+                                                     k_weight=k_weight, eps=ctx.eps, neighbours=ctx.neighbours)
+        return gq, gk, None, None, gqw, gkw, None, None

@@ -13,6 +13,7 @@
 #include <cstdio>
 #include <string>
 
+#include "sx_attention.hpp"
 #include "sx_common.hpp"
 
 namespace sx {
@@ -1092,6 +1093,676 @@ sx_status sx_linear_scan(sx_dtype dtype, int a_rank, const int64_t* a_shape, con
   return device_status(sx::launch_linear_scan(p, dtype == SX_BF16, out_dtype == SX_BF16,
                                               static_cast<hipStream_t>(stream)),
                        "linear-scan launch");
+}
+
+// ------------------------------------------------------------------ decay attention, head norm and rotation
+
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kMostHeadWidth = 256;
+constexpr int64_t kMostTokens = int64_t(1) << 30;
+constexpr int64_t kMostGrid = (int64_t(1) << 31) - 1;
+
+// A [B, T, heads, d] operand (a single token: T = 1).
+struct HeadArg {
+  const char* name;
+  const int64_t* shape;    // [B, T, heads, d]
+  const int64_t* strides;  // nullptr: contiguous
+  const void* data;
+};
+
+sx_status missing(const char* op, const char* name) {
+  return fail(SX_E_DIM_003, "%s: %s is NULL; a tensor was expected", op, name);
+}
+
+void head_strides(const HeadArg& a, int64_t* st) {
+  if (a.strides) std::copy(a.strides, a.strides + 4, st); else contiguous_strides(4, a.shape, st);
+}
+
+// `piece`: elements that have to divide d for rows to be read 16 bytes at a time.
+sx::HeadView head_view(const HeadArg& a, size_t elem, int64_t heads, int64_t piece) {
+  int64_t st[4];
+  head_strides(a, st);
+  sx::HeadView v{};
+  v.p = a.data;
+  v.sb = st[0];
+  v.st = st[1];
+  v.sh = st[2];
+  v.sd = st[3];
+  v.rep = int(heads / std::max<int64_t>(a.shape[2], 1));
+  auto whole = [&](int64_t n, int64_t s) { return n <= 1 || (s * int64_t(elem)) % 16 == 0; };
+  v.vec = st[3] == 1 && a.shape[3] % piece == 0 && (reinterpret_cast<uintptr_t>(a.data) & 15u) == 0 &&
+          whole(a.shape[0], st[0]) && whole(a.shape[1], st[1]) && whole(a.shape[2], st[2]);
+  return v;
+}
+
+int64_t numel4(const int64_t* s) { return s[0] * s[1] * s[2] * s[3]; }
+
+struct Span {
+  const char* name;
+  uintptr_t lo, hi;
+};
+
+Span head_span(const HeadArg& a, size_t elem) {
+  Span s{a.name, 0, 0};
+  if (!a.data || numel4(a.shape) == 0) return s;
+  int64_t st[4];
+  head_strides(a, st);
+  span_bytes(a.data, 4, a.shape, st, elem, &s.lo, &s.hi);
+  return s;
+}
+
+Span flat_span(const char* name, const void* p, int64_t bytes) {
+  const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+  return p && bytes > 0 ? Span{name, b, b + uintptr_t(bytes)} : Span{name, 0, 0};
+}
+
+// Every output against every input and every other output.
+sx_status no_overlap(const char* op, const Span* in, int nin, const Span* out, int nout) {
+  for (int i = 0; i < nout; ++i) {
+    for (int j = 0; j < nin; ++j)
+      if (overlaps(out[i].lo, out[i].hi, in[j].lo, in[j].hi))
+        return fail(SX_E_ALIAS, "%s: %s overlaps %s", op, out[i].name, in[j].name);
+    for (int j = i + 1; j < nout; ++j)
+      if (overlaps(out[i].lo, out[i].hi, out[j].lo, out[j].hi))
+        return fail(SX_E_ALIAS, "%s: %s overlaps %s", op, out[i].name, out[j].name);
+    if ((out[i].lo & 15u) != 0)
+      return fail(SX_E_UNSUPPORTED, "%s: %s must be 16-byte aligned", op, out[i].name);
+  }
+  return ok();
+}
+
+struct DecayShapes {
+  int64_t B, T, H, hq, hk, hv, dk, dv;
+  int64_t gb, gt, gh;
+};
+
+// Shapes of q, k [B, T, *, dk], v [B, T, *, dv] and log_decay ([H] or [B, T, H]).
+sx_status decay_shapes(const char* op, const HeadArg& q, const HeadArg& k, const HeadArg& v, int g_rank,
+                       const int64_t* g_shape, const int64_t* g_strides, DecayShapes* s) {
+  for (const HeadArg* a : {&q, &k, &v}) {
+    int64_t n;
+    if (!a->shape) return fail(SX_E_DIM_001, "%s: %s has no shape", op, a->name);
+    if (!checked_numel(4, a->shape, &n))
+      return fail(SX_E_DIM_001, "%s: bad shape %s of %s", op, shape_str(4, a->shape).c_str(), a->name);
+  }
+  if (!g_shape || (g_rank != 1 && g_rank != 3))
+    return fail(SX_E_DIM_001, "%s: log_decay must be [heads] or [batch, tokens, heads]", op);
+  s->B = q.shape[0];
+  s->T = q.shape[1];
+  s->H = g_shape[g_rank - 1];
+  s->hq = q.shape[2];
+  s->hk = k.shape[2];
+  s->hv = v.shape[2];
+  s->dk = q.shape[3];
+  s->dv = v.shape[3];
+  if (k.shape[0] != s->B || k.shape[1] != s->T || k.shape[3] != s->dk)
+    return fail(SX_E_DIM_001, "%s: k %s does not fit q %s", op, shape_str(4, k.shape).c_str(),
+                shape_str(4, q.shape).c_str());
+  if (v.shape[0] != s->B || v.shape[1] != s->T)
+    return fail(SX_E_DIM_001, "%s: v %s does not fit q %s", op, shape_str(4, v.shape).c_str(),
+                shape_str(4, q.shape).c_str());
+  if (g_rank == 3 && (g_shape[0] != s->B || g_shape[1] != s->T))
+    return fail(SX_E_DIM_001, "%s: log_decay %s does not fit q %s", op, shape_str(3, g_shape).c_str(),
+                shape_str(4, q.shape).c_str());
+  if (s->H < 1) return fail(SX_E_DIM_001, "%s: log_decay %s has no heads", op, shape_str(g_rank, g_shape).c_str());
+  for (const HeadArg* a : {&q, &k, &v})
+    if (a->shape[2] < 1 || s->H % a->shape[2] != 0)
+      return fail(SX_E_DIM_001, "%s: the %lld heads of %s do not divide the %lld of log_decay", op,
+                  (long long)a->shape[2], a->name, (long long)s->H);
+  if (s->dk < 1 || s->dv < 1) return fail(SX_E_DIM_001, "%s: heads of width 0 (q %s, v %s)", op,
+                                          shape_str(4, q.shape).c_str(), shape_str(4, v.shape).c_str());
+  if (s->dk > kMostHeadWidth || s->dv > kMostHeadWidth)
+    return fail(SX_E_UNSUPPORTED, "%s: heads wider than %lld (q %s, v %s)", op, (long long)kMostHeadWidth,
+                shape_str(4, q.shape).c_str(), shape_str(4, v.shape).c_str());
+  if (s->T > kMostTokens || s->B > kMostTokens || s->H > kMostTokens || s->B * s->H > kMostGrid / 1024)
+    return fail(SX_E_UNSUPPORTED, "%s: too many tokens, rows or heads (q %s)", op, shape_str(4, q.shape).c_str());
+  int64_t st[3];
+  if (g_strides) std::copy(g_strides, g_strides + g_rank, st); else contiguous_strides(g_rank, g_shape, st);
+  s->gb = g_rank == 3 ? st[0] : 0;
+  s->gt = g_rank == 3 ? st[1] : 0;
+  s->gh = st[g_rank - 1];
+  return ok();
+}
+
+Span decay_span(const DecayShapes& s, const float* g) {
+  const int64_t shape[3] = {s.B, s.T, s.H}, st[3] = {s.gb, s.gt, s.gh};
+  Span r{"log_decay", 0, 0};
+  if (g && s.B * s.T * s.H > 0) span_bytes(g, 3, shape, st, sizeof(float), &r.lo, &r.hi);
+  return r;
+}
+
+sx::DaParams decay_params(const DecayShapes& s, bool bf16, const float* g, const int32_t* lengths) {
+  sx::DaParams p{};
+  p.B = int(s.B);
+  p.T = int(s.T);
+  p.H = int(s.H);
+  p.dk = int(s.dk);
+  p.dv = int(s.dv);
+  p.g = g;
+  p.gb = s.gb;
+  p.gt = s.gt;
+  p.gh = s.gh;
+  p.lengths = lengths;
+  p.bf16 = bf16;
+  sx::decay_attention_split(p);
+  return p;
+}
+
+// Hands out 256-byte aligned pieces of a workspace; with base 0 it only adds them up.
+struct Carve {
+  uintptr_t base;
+  size_t used = 0;
+  template <typename T>
+  T* take(int64_t n) {
+    const size_t at = used;
+    used += (size_t(n) * sizeof(T) + 255) & ~size_t(255);
+    return n > 0 && base ? reinterpret_cast<T*>(base + at) : nullptr;
+  }
+};
+
+void carve_segments(Carve& c, sx::DaParams& p, sx::DaMarch& m) {
+  const int64_t n = int64_t(p.segments - 1) * p.B * p.H;
+  m.seg = c.take<float>(n * p.dk * p.dv);
+  m.seg_decay = c.take<float>(n);
+}
+
+struct GradPieces {
+  float *rows, *sources, *rows_chunk, *sources_chunk, *chunk_decay;
+  double* partial;
+  float *share_q, *share_k, *share_v;
+  int chunks, blocks;
+};
+
+GradPieces carve_gradient(Carve& c, const DecayShapes& s, sx::DaParams& p) {
+  GradPieces g{};
+  carve_segments(c, p, p.m[0]);
+  carve_segments(c, p, p.m[1]);
+  p.m[2].seg = p.m[1].seg;
+  p.m[2].seg_decay = p.m[1].seg_decay;
+  const int chunk = sx::decay_attention_chunk(p.bf16 != 0);
+  const int64_t BH = s.B * s.H;
+  g.chunks = int((s.T + chunk - 1) / chunk);
+  g.blocks = sx::decay_attention_column_blocks(p.dv, p.dk);
+  g.rows = c.take<float>(g.blocks * BH * s.T);
+  g.sources = c.take<float>(g.blocks * BH * s.T);
+  g.rows_chunk = c.take<float>(g.blocks * BH * g.chunks);
+  g.sources_chunk = c.take<float>(g.blocks * BH * g.chunks);
+  g.chunk_decay = c.take<float>(BH * g.chunks);
+  g.partial = c.take<double>(BH);
+  // gradients of shared heads are summed over the heads that share them, from f32
+  const int64_t n = s.B * s.T * s.H;
+  g.share_q = c.take<float>(s.hq == s.H ? 0 : n * s.dk);
+  g.share_k = c.take<float>(s.hk == s.H ? 0 : n * s.dk);
+  g.share_v = c.take<float>(s.hv == s.H ? 0 : n * s.dv);
+  return g;
+}
+
+sx_status check_workspace(const char* op, const void* workspace, size_t bytes, size_t need) {
+  if (need > 0 && (workspace == nullptr || bytes < need))
+    return fail(SX_E_WORKSPACE, "%s: workspace of %zu bytes given, %zu needed", op, bytes, need);
+  if (need > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(SX_E_WORKSPACE, "%s: workspace must be 256-byte aligned", op);
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sx_decay_attention_workspace_bytes(sx_dtype dtype, const int64_t* q_shape, const int64_t* v_shape,
+                                          int64_t heads) {
+  if (!dtype_ok(dtype)) return 0;
+  const HeadArg q{"q", q_shape, nullptr, nullptr}, v{"v", v_shape, nullptr, nullptr};
+  DecayShapes s;
+  if (decay_shapes("decay-attention", q, q, v, 1, &heads, nullptr, &s) != SX_OK) return 0;
+  sx::DaParams p = decay_params(s, dtype == SX_BF16, nullptr, nullptr);
+  Carve c{0};
+  carve_segments(c, p, p.m[0]);
+  return c.used;
+}
+
+sx_status sx_decay_attention(sx_dtype dtype, const int64_t* q_shape, const int64_t* q_strides, const void* q,
+                             const int64_t* k_shape, const int64_t* k_strides, const void* k, const int64_t* v_shape,
+                             const int64_t* v_strides, const void* v, int g_rank, const int64_t* g_shape,
+                             const int64_t* g_strides, const float* log_decay, const float* initial,
+                             const int32_t* lengths, float scale, void* out, float* final_state, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  const char* op = "decay-attention";
+  if (!dtype_ok(dtype))
+    return fail(SX_E_DIM_002, "%s: q, k and v must be f32 or bf16 (dtype code %d)", op, enum_code(dtype));
+  const HeadArg qa{"q", q_shape, q_strides, q}, ka{"k", k_shape, k_strides, k}, va{"v", v_shape, v_strides, v};
+  DecayShapes s;
+  sx_status st = decay_shapes(op, qa, ka, va, g_rank, g_shape, g_strides, &s);
+  if (st != SX_OK) return st;
+  const int64_t state = s.B * s.H * s.dk * s.dv, rows = s.B * s.T * s.H;
+  if (s.B == 0 || (s.T == 0 && !final_state)) return ok();
+  if (rows > 0) {
+    for (const HeadArg* a : {&qa, &ka, &va})
+      if (!a->data) return missing(op, a->name);
+    if (!log_decay) return missing(op, "log_decay");
+    if (!out) return missing(op, "out");
+  }
+  const size_t e = dtype == SX_BF16 ? 2 : 4;
+  const Span in[] = {head_span(qa, e), head_span(ka, e), head_span(va, e), decay_span(s, log_decay),
+                     flat_span("initial", initial, state * 4), flat_span("lengths", lengths, s.B * 4)};
+  const Span to[] = {flat_span("out", out, rows * s.dv * int64_t(e)), flat_span("the final state", final_state, state * 4)};
+  if ((st = no_overlap(op, in, 6, to, 2)) != SX_OK) return st;
+  sx::DaParams p = decay_params(s, dtype == SX_BF16, log_decay, lengths);
+  Carve c{reinterpret_cast<uintptr_t>(workspace)};
+  sx::DaMarch& m = p.m[0];
+  carve_segments(c, p, m);
+  if ((st = check_workspace(op, workspace, workspace_bytes, c.used)) != SX_OK) return st;
+  const int64_t piece = 16 / int64_t(e);
+  p.marches = 1;
+  m.x = head_view(qa, e, s.H, piece);
+  m.y = head_view(ka, e, s.H, piece);
+  m.z = head_view(va, e, s.H, piece);
+  m.dx = p.dk;
+  m.dz = p.dv;
+  m.scale_out = scale;
+  m.scale_src = 1.0f;
+  m.out = out;
+  m.sr = s.dv;
+  m.sc = 1;
+  m.first = initial;
+  m.last = final_state;
+  return device_status(sx::launch_decay_attention(p, static_cast<hipStream_t>(stream)), "decay-attention launch");
+}
+
+size_t sx_decay_attention_backward_workspace_bytes(sx_dtype dtype, const int64_t* q_shape, const int64_t* k_shape,
+                                                   const int64_t* v_shape, int64_t heads) {
+  if (!dtype_ok(dtype)) return 0;
+  const HeadArg q{"q", q_shape, nullptr, nullptr}, k{"k", k_shape, nullptr, nullptr}, v{"v", v_shape, nullptr, nullptr};
+  DecayShapes s;
+  if (decay_shapes("decay-attention gradient", q, k, v, 1, &heads, nullptr, &s) != SX_OK) return 0;
+  sx::DaParams p = decay_params(s, dtype == SX_BF16, nullptr, nullptr);
+  Carve c{0};
+  carve_gradient(c, s, p);
+  return c.used;
+}
+
+sx_status sx_decay_attention_backward(sx_dtype dtype, const int64_t* q_shape, const int64_t* q_strides, const void* q,
+                                      const int64_t* k_shape, const int64_t* k_strides, const void* k,
+                                      const int64_t* v_shape, const int64_t* v_strides, const void* v, int g_rank,
+                                      const int64_t* g_shape, const int64_t* g_strides, const float* log_decay,
+                                      const int64_t* grad_out_strides, const void* grad_out, const float* grad_state,
+                                      const float* initial, const int32_t* lengths, float scale, void* grad_q,
+                                      void* grad_k, void* grad_v, float* grad_log_decay, float* grad_initial,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  const char* op = "decay-attention gradient";
+  if (!dtype_ok(dtype))
+    return fail(SX_E_DIM_002, "%s: q, k, v and grad_out must be f32 or bf16 (dtype code %d)", op, enum_code(dtype));
+  const HeadArg qa{"q", q_shape, q_strides, q}, ka{"k", k_shape, k_strides, k}, va{"v", v_shape, v_strides, v};
+  DecayShapes s;
+  sx_status st = decay_shapes(op, qa, ka, va, g_rank, g_shape, g_strides, &s);
+  if (st != SX_OK) return st;
+  const int64_t out_shape[4] = {s.B, s.T, s.H, s.dv};
+  const HeadArg oa{"grad_out", out_shape, grad_out_strides, grad_out};
+  const int64_t state = s.B * s.H * s.dk * s.dv, rows = s.B * s.T * s.H;
+  if (rows > 0) {
+    for (const HeadArg* a : {&qa, &ka, &va, &oa})
+      if (!a->data) return missing(op, a->name);
+    if (!log_decay) return missing(op, "log_decay");
+    if (!grad_q) return missing(op, "grad_q");
+    if (!grad_k) return missing(op, "grad_k");
+    if (!grad_v) return missing(op, "grad_v");
+  }
+  if (!grad_log_decay && (rows > 0 || g_rank == 1)) return missing(op, "grad_log_decay");
+  if (initial && !grad_initial && state > 0) return missing(op, "grad_initial");
+  const size_t e = dtype == SX_BF16 ? 2 : 4;
+  const Span in[] = {head_span(qa, e), head_span(ka, e), head_span(va, e), head_span(oa, e), decay_span(s, log_decay),
+                     flat_span("initial", initial, state * 4), flat_span("grad_state", grad_state, state * 4),
+                     flat_span("lengths", lengths, s.B * 4)};
+  const Span to[] = {flat_span("grad_q", grad_q, numel4(q_shape) * int64_t(e)),
+                     flat_span("grad_k", grad_k, numel4(k_shape) * int64_t(e)),
+                     flat_span("grad_v", grad_v, numel4(v_shape) * int64_t(e)),
+                     flat_span("grad_log_decay", grad_log_decay, (g_rank == 1 ? s.H : rows) * 4),
+                     flat_span("grad_initial", grad_initial, state * 4)};
+  if ((st = no_overlap(op, in, 8, to, 5)) != SX_OK) return st;
+  sx::DaParams p = decay_params(s, dtype == SX_BF16, log_decay, lengths);
+  Carve c{reinterpret_cast<uintptr_t>(workspace)};
+  const GradPieces w = carve_gradient(c, s, p);
+  if ((st = check_workspace(op, workspace, workspace_bytes, c.used)) != SX_OK) return st;
+
+  const int64_t piece = 16 / int64_t(e);
+  const sx::HeadView qv = head_view(qa, e, s.H, piece), kv = head_view(ka, e, s.H, piece),
+                     vv = head_view(va, e, s.H, piece), ov = head_view(oa, e, s.H, piece);
+  p.marches = 3;
+  sx::DaMarch &dq = p.m[0], &dk = p.m[1], &dv = p.m[2];
+  dq.x = ov; dq.y = vv; dq.z = kv; dq.w = qv;
+  dk.x = vv; dk.y = ov; dk.z = qv; dk.w = kv;
+  dv.x = kv; dv.y = qv; dv.z = ov;
+  dq.dx = dk.dx = p.dv;
+  dq.dz = dk.dz = p.dk;
+  dv.dx = p.dk;
+  dv.dz = p.dv;
+  dk.reverse = dv.reverse = 1;
+  dq.scale_out = scale;
+  dq.scale_src = 1.0f;
+  dk.scale_out = dv.scale_out = 1.0f;
+  dk.scale_src = dv.scale_src = scale;
+  dq.sr = dk.sr = 1;   // states are [dk, dv] in memory; these two hold them transposed
+  dq.sc = dk.sc = s.dv;
+  dv.sr = s.dv;
+  dv.sc = 1;
+  dq.first = initial;
+  dk.first = dv.first = grad_state;
+  dk.last = grad_initial;
+  dq.out = w.share_q ? w.share_q : grad_q;
+  dq.out_f32 = w.share_q != nullptr;
+  dk.out = w.share_k ? w.share_k : grad_k;
+  dk.out_f32 = w.share_k != nullptr;
+  dv.out = w.share_v ? w.share_v : grad_v;
+  dv.out_f32 = w.share_v != nullptr;
+  dq.mass = w.rows;
+  dq.mass_chunk = w.rows_chunk;
+  dq.chunk_decay = w.chunk_decay;
+  dk.mass = w.sources;
+  dk.mass_chunk = w.sources_chunk;
+  const hipStream_t str = static_cast<hipStream_t>(stream);
+  hipError_t err = hipSuccess;
+  if (s.B > 0) {
+    err = sx::launch_decay_attention(p, str);
+    if (err != hipSuccess) return device_status(err, "decay-attention gradient launch");
+    const struct { const float* src; void* to; int64_t heads, d; } shared[3] = {
+        {w.share_q, grad_q, s.hq, s.dk}, {w.share_k, grad_k, s.hk, s.dk}, {w.share_v, grad_v, s.hv, s.dv}};
+    for (const auto& x : shared) {
+      if (!x.src) continue;
+      sx::DaShare sh{};
+      sh.src = x.src;
+      sh.out = x.to;
+      sh.rows = s.B * s.T * x.heads;
+      sh.rep = int(s.H / x.heads);
+      sh.d = int(x.d);
+      sh.bf16 = p.bf16;
+      err = sx::launch_share_sum(sh, str);
+      if (err != hipSuccess) return device_status(err, "decay-attention gradient launch");
+    }
+  }
+  sx::DaDecayGrad d{};
+  d.B = p.B;
+  d.T = p.T;
+  d.H = p.H;
+  d.dk = p.dk;
+  d.dv = p.dv;
+  d.chunk = sx::decay_attention_chunk(p.bf16 != 0);
+  d.chunks = w.chunks;
+  d.blocks = w.blocks;
+  d.g = log_decay;
+  d.gb = s.gb;
+  d.gt = s.gt;
+  d.gh = s.gh;
+  d.lengths = lengths;
+  d.rows = w.rows;
+  d.sources = w.sources;
+  d.rows_chunk = w.rows_chunk;
+  d.sources_chunk = w.sources_chunk;
+  d.chunk_decay = w.chunk_decay;
+  d.initial = initial;
+  d.grad_initial = grad_initial;
+  d.partial = w.partial;
+  d.grad_g = grad_log_decay;
+  d.per_head = g_rank == 1;
+  return device_status(sx::launch_decay_grad(d, str), "decay-attention gradient launch");
+}
+
+sx_status sx_decay_attention_step(sx_dtype dtype, const int64_t* q_shape, const int64_t* q_strides, const void* q,
+                                  const int64_t* k_shape, const int64_t* k_strides, const void* k,
+                                  const int64_t* v_shape, const int64_t* v_strides, const void* v, int g_rank,
+                                  const int64_t* g_shape, const int64_t* g_strides, const float* log_decay,
+                                  int64_t pool, const int64_t* state_strides, float* state, const int32_t* slots,
+                                  float scale, void* out, void* stream) {
+  const char* op = "decay-attention step";
+  if (!dtype_ok(dtype))
+    return fail(SX_E_DIM_002, "%s: q, k and v must be f32 or bf16 (dtype code %d)", op, enum_code(dtype));
+  if (!q_shape || !k_shape || !v_shape) return fail(SX_E_DIM_001, "%s: q, k and v need shapes", op);
+  // [B, heads, d] as [B, 1, heads, d]
+  int64_t sh[3][4], ss[3][4];
+  const int64_t* shapes[3] = {q_shape, k_shape, v_shape};
+  const int64_t* strides[3] = {q_strides, k_strides, v_strides};
+  for (int i = 0; i < 3; ++i) {
+    int64_t st[3];
+    if (strides[i]) std::copy(strides[i], strides[i] + 3, st); else contiguous_strides(3, shapes[i], st);
+    sh[i][0] = shapes[i][0];
+    sh[i][1] = 1;
+    sh[i][2] = shapes[i][1];
+    sh[i][3] = shapes[i][2];
+    ss[i][0] = st[0];
+    ss[i][1] = 0;
+    ss[i][2] = st[1];
+    ss[i][3] = st[2];
+  }
+  const HeadArg qa{"q", sh[0], ss[0], q}, ka{"k", sh[1], ss[1], k}, va{"v", sh[2], ss[2], v};
+  if (!g_shape || (g_rank != 1 && g_rank != 2))
+    return fail(SX_E_DIM_001, "%s: log_decay must be [heads] or [batch, heads]", op);
+  int64_t gs[3], gst[3], gn[2];
+  if (g_strides) std::copy(g_strides, g_strides + g_rank, gn); else contiguous_strides(g_rank, g_shape, gn);
+  gs[0] = g_rank == 2 ? g_shape[0] : sh[0][0];
+  gs[1] = 1;
+  gs[2] = g_shape[g_rank - 1];
+  gst[0] = g_rank == 2 ? gn[0] : 0;
+  gst[1] = 0;
+  gst[2] = gn[g_rank - 1];
+  DecayShapes s;
+  sx_status st = decay_shapes(op, qa, ka, va, 3, gs, gst, &s);
+  if (st != SX_OK) return st;
+  if (pool < 0) return fail(SX_E_DIM_001, "%s: a pool of %lld states", op, (long long)pool);
+  if (!slots && pool < s.B)
+    return fail(SX_E_DIM_001, "%s: %lld states for %lld rows and no slots", op, (long long)pool, (long long)s.B);
+  const int64_t pool_shape[4] = {pool, s.H, s.dk, s.dv};
+  int64_t ps[4], numel = 0;
+  if (!checked_numel(4, pool_shape, &numel))
+    return fail(SX_E_DIM_001, "%s: bad state shape %s", op, shape_str(4, pool_shape).c_str());
+  if (state_strides) std::copy(state_strides, state_strides + 4, ps); else contiguous_strides(4, pool_shape, ps);
+  if ((s.dk > 1 && ps[2] != s.dv) || (s.dv > 1 && ps[3] != 1))
+    return fail(SX_E_UNSUPPORTED, "%s: a head's state must be row-major contiguous", op);
+  const int64_t one = s.dk * s.dv;
+  auto wide = [&](int i, int64_t below) { return pool_shape[i] <= 1 || ps[i] >= below || -ps[i] >= below; };
+  if (numel > 0 && (!wide(1, one) || !wide(0, one) ||
+                    (pool > 1 && s.H > 1 && !wide(0, (s.H - 1) * std::abs(ps[1]) + one) &&
+                     !wide(1, (pool - 1) * std::abs(ps[0]) + one))))
+    return fail(SX_E_UNSUPPORTED, "%s: states overlap each other", op);
+  if (s.B == 0) return ok();
+  for (const HeadArg* a : {&qa, &ka, &va})
+    if (!a->data) return missing(op, a->name);
+  if (!log_decay) return missing(op, "log_decay");
+  if (!state && numel > 0) return missing(op, "state");
+  if (!out) return missing(op, "out");
+  const size_t e = dtype == SX_BF16 ? 2 : 4;
+  const Span in[] = {head_span(qa, e), head_span(ka, e), head_span(va, e), decay_span(s, log_decay),
+                     flat_span("slots", slots, s.B * 4)};
+  Span to[] = {flat_span("out", out, s.B * s.H * s.dv * int64_t(e)), {"state", 0, 0}};
+  if (state && numel > 0) span_bytes(state, 4, pool_shape, ps, sizeof(float), &to[1].lo, &to[1].hi);
+  if ((st = no_overlap(op, in, 5, to, 2)) != SX_OK) return st;
+  sx::DaStep p{};
+  p.B = int(s.B);
+  p.H = int(s.H);
+  p.dk = int(s.dk);
+  p.dv = int(s.dv);
+  p.q = head_view(qa, e, s.H, 4);
+  p.k = head_view(ka, e, s.H, 4);
+  p.v = head_view(va, e, s.H, 4);
+  p.g = log_decay;
+  p.gb = s.gb;
+  p.gh = s.gh;
+  p.state = state;
+  p.ss = ps[0];
+  p.sh = ps[1];
+  p.slots_in_pool = pool;
+  p.slots = slots;
+  p.scale = scale;
+  p.bf16 = dtype == SX_BF16;
+  p.out = out;
+  return device_status(sx::launch_decay_step(p, static_cast<hipStream_t>(stream)), "decay-attention step launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+struct RotateArgs {
+  HeadArg q, k, gq, gk;
+  const void* positions;
+  int positions_i64;
+  const int64_t* position_strides;
+  int64_t rotated;
+  const double* turns;
+  const float *qw, *kw;
+  float eps;
+  int neighbours;
+};
+
+sx_status plan_rotate(const char* op, sx_dtype dtype, const RotateArgs& a, bool gradient, sx::HrParams* p) {
+  if (!dtype_ok(dtype))
+    return fail(SX_E_DIM_002, "%s: q and k must be f32 or bf16 (dtype code %d)", op, enum_code(dtype));
+  for (const HeadArg* x : {&a.q, &a.k}) {
+    int64_t n;
+    if (!x->shape) return fail(SX_E_DIM_001, "%s: %s has no shape", op, x->name);
+    if (!checked_numel(4, x->shape, &n))
+      return fail(SX_E_DIM_001, "%s: bad shape %s of %s", op, shape_str(4, x->shape).c_str(), x->name);
+  }
+  const int64_t* qs = a.q.shape;
+  const int64_t* ks = a.k.shape;
+  if (qs[0] != ks[0] || qs[1] != ks[1] || qs[3] != ks[3])
+    return fail(SX_E_DIM_001, "%s: k %s does not fit q %s", op, shape_str(4, ks).c_str(), shape_str(4, qs).c_str());
+  const int64_t d = qs[3];
+  if (d < 1) return fail(SX_E_DIM_001, "%s: heads of width 0 (q %s)", op, shape_str(4, qs).c_str());
+  if (d > kMostHeadWidth)
+    return fail(SX_E_UNSUPPORTED, "%s: heads wider than %lld (q %s)", op, (long long)kMostHeadWidth,
+                shape_str(4, qs).c_str());
+  if (a.rotated < 0 || a.rotated % 2 != 0 || a.rotated > d)
+    return fail(SX_E_DIM_001, "%s: %lld rotated components of heads of width %lld; an even number up to the width",
+                op, (long long)a.rotated, (long long)d);
+  if (!(a.eps >= 0.0f)) return fail(SX_E_DIM_001, "%s: eps %g is negative", op, double(a.eps));
+  if (qs[0] > kMostTokens || qs[1] > kMostTokens || qs[0] * qs[1] > kMostTokens || qs[2] + ks[2] > (1 << 20))
+    return fail(SX_E_UNSUPPORTED, "%s: too many tokens or heads (q %s)", op, shape_str(4, qs).c_str());
+  *p = sx::HrParams{};
+  p->B = int(qs[0]);
+  p->T = int(qs[1]);
+  p->hq = int(qs[2]);
+  p->hk = int(ks[2]);
+  p->d = int(d);
+  p->rot = int(a.rotated);
+  const size_t e = dtype == SX_BF16 ? 2 : 4;
+  p->q = head_view(a.q, e, qs[2], 8);
+  p->k = head_view(a.k, e, ks[2], 8);
+  if (gradient) {
+    p->gq = head_view(a.gq, e, qs[2], 8);
+    p->gk = head_view(a.gk, e, ks[2], 8);
+  }
+  p->positions = a.positions;
+  p->pos64 = a.positions_i64 ? 1 : 0;
+  p->pb = a.position_strides ? a.position_strides[0] : qs[1];
+  p->pt = a.position_strides ? a.position_strides[1] : 1;
+  p->turns = a.turns;
+  p->qw = a.qw;
+  p->kw = a.kw;
+  p->eps = a.eps;
+  p->neighbours = a.neighbours ? 1 : 0;
+  p->bf16 = dtype == SX_BF16;
+  return ok();
+}
+
+sx_status rotate_pointers(const char* op, const RotateArgs& a, bool gradient, int64_t rows) {
+  if (rows == 0) return ok();
+  for (const HeadArg* x : {&a.q, &a.k, &a.gq, &a.gk})
+    if (x->shape && numel4(x->shape) > 0 && !x->data && (gradient || x == &a.q || x == &a.k))
+      return missing(op, x->name);
+  if (a.rotated > 0 && !a.positions) return missing(op, "positions");
+  if (a.rotated > 0 && !a.turns) return missing(op, "turns");
+  return ok();
+}
+
+sx_status rotate_overlap(const char* op, const RotateArgs& a, const sx::HrParams& p, const Span* out, int nout) {
+  const size_t e = p.bf16 ? 2 : 4;
+  const int64_t ps[2] = {p.B, p.T}, st[2] = {p.pb, p.pt};
+  Span pos{"positions", 0, 0};
+  if (a.positions && int64_t(p.B) * p.T > 0) span_bytes(a.positions, 2, ps, st, p.pos64 ? 8 : 4, &pos.lo, &pos.hi);
+  const Span in[] = {head_span(a.q, e), head_span(a.k, e), a.gq.shape ? head_span(a.gq, e) : Span{"", 0, 0},
+                     a.gk.shape ? head_span(a.gk, e) : Span{"", 0, 0}, pos,
+                     flat_span("turns", a.turns, a.rotated / 2 * 8), flat_span("q_weight", a.qw, int64_t(p.d) * 4),
+                     flat_span("k_weight", a.kw, int64_t(p.d) * 4)};
+  return no_overlap(op, in, 8, out, nout);
+}
+
+}  // namespace
+
+extern "C" {
+
+sx_status sx_head_norm_rotate(sx_dtype dtype, const int64_t* q_shape, const int64_t* q_strides, const void* q,
+                              const int64_t* k_shape, const int64_t* k_strides, const void* k, int positions_i64,
+                              const int64_t* position_strides, const void* positions, int64_t rotated,
+                              const double* turns, const float* q_weight, const float* k_weight, float eps,
+                              int neighbours, void* out_q, void* out_k, void* stream) {
+  const char* op = "head-norm-rotate";
+  const RotateArgs a{{"q", q_shape, q_strides, q}, {"k", k_shape, k_strides, k}, {}, {}, positions, positions_i64,
+                     position_strides, rotated, turns, q_weight, k_weight, eps, neighbours};
+  sx::HrParams p;
+  sx_status st = plan_rotate(op, dtype, a, false, &p);
+  if (st != SX_OK) return st;
+  const int64_t nq = numel4(q_shape), nk = numel4(k_shape);
+  if (nq + nk == 0) return ok();
+  if ((st = rotate_pointers(op, a, false, nq + nk)) != SX_OK) return st;
+  if (nq > 0 && !out_q) return missing(op, "out_q");
+  if (nk > 0 && !out_k) return missing(op, "out_k");
+  const int64_t e = p.bf16 ? 2 : 4;
+  const Span to[] = {flat_span("out_q", out_q, nq * e), flat_span("out_k", out_k, nk * e)};
+  if ((st = rotate_overlap(op, a, p, to, 2)) != SX_OK) return st;
+  p.out_q = out_q;
+  p.out_k = out_k;
+  return device_status(sx::launch_head_rotate(p, static_cast<hipStream_t>(stream)), "head-norm-rotate launch");
+}
+
+size_t sx_head_norm_rotate_backward_workspace_bytes(const int64_t* q_shape) {
+  int64_t n;
+  if (!q_shape || !checked_numel(4, q_shape, &n) || q_shape[0] > kMostTokens || q_shape[1] > kMostTokens ||
+      q_shape[0] * q_shape[1] > kMostTokens || q_shape[3] > kMostHeadWidth)
+    return 0;
+  sx::HrParams p{};
+  p.B = int(q_shape[0]);
+  p.T = int(q_shape[1]);
+  return size_t(sx::head_rotate_backward_groups(p)) * 2 * size_t(q_shape[3]) * sizeof(float);
+}
+
+sx_status sx_head_norm_rotate_backward(sx_dtype dtype, const int64_t* q_shape, const int64_t* q_strides,
+                                       const void* q, const int64_t* k_shape, const int64_t* k_strides, const void* k,
+                                       int positions_i64, const int64_t* position_strides, const void* positions,
+                                       int64_t rotated, const double* turns, const int64_t* gq_strides,
+                                       const void* grad_out_q, const int64_t* gk_strides, const void* grad_out_k,
+                                       const float* q_weight, const float* k_weight, float eps, int neighbours,
+                                       void* grad_q, void* grad_k, float* grad_q_weight, float* grad_k_weight,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  const char* op = "head-norm-rotate gradient";
+  const RotateArgs a{{"q", q_shape, q_strides, q}, {"k", k_shape, k_strides, k},
+                     {"grad_out_q", q_shape, gq_strides, grad_out_q}, {"grad_out_k", k_shape, gk_strides, grad_out_k},
+                     positions, positions_i64, position_strides, rotated, turns, q_weight, k_weight, eps, neighbours};
+  sx::HrParams p;
+  sx_status st = plan_rotate(op, dtype, a, true, &p);
+  if (st != SX_OK) return st;
+  const int64_t nq = numel4(q_shape), nk = numel4(k_shape);
+  if ((st = rotate_pointers(op, a, true, nq + nk)) != SX_OK) return st;
+  if (nq > 0 && !grad_q) return missing(op, "grad_q");
+  if (nk > 0 && !grad_k) return missing(op, "grad_k");
+  const int64_t e = p.bf16 ? 2 : 4;
+  const Span to[] = {flat_span("grad_q", grad_q, nq * e), flat_span("grad_k", grad_k, nk * e),
+                     flat_span("grad_q_weight", grad_q_weight, int64_t(p.d) * 4),
+                     flat_span("grad_k_weight", grad_k_weight, int64_t(p.d) * 4)};
+  if ((st = rotate_overlap(op, a, p, to, 4)) != SX_OK) return st;
+  if (grad_q_weight || grad_k_weight) {
+    const size_t need = sx_head_norm_rotate_backward_workspace_bytes(q_shape);
+    if ((st = check_workspace(op, workspace, workspace_bytes, need)) != SX_OK) return st;
+  }
+  if (nq + nk == 0 && !grad_q_weight && !grad_k_weight) return ok();
+  p.out_q = grad_q;
+  p.out_k = grad_k;
+  p.partial = static_cast<float*>(workspace);
+  p.gqw = grad_q_weight;
+  p.gkw = grad_k_weight;
+  return device_status(sx::launch_head_rotate_backward(p, static_cast<hipStream_t>(stream)),
+                       "head-norm-rotate gradient launch");
 }
 
 }  // extern "C"
