@@ -574,7 +574,7 @@ sx_status sx_head_norm_rotate_backward(sx_dtype dtype, const int64_t* q_shape, c
                                        void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace bytes sx_head_norm_rotate_backward needs for the weights' gradients. */
-size_t sx_head_norm_rotate_backward_workspace_bytes(const int64_t* q_shape);
+size_t sx_head_norm_rotate_backward_workspace_bytes(const int64_t* q_shape, const int64_t* k_shape);
 
 /* "E-DIM-001" etc. for a status; "OK" for SX_OK. Static storage. */
 const char* sx_status_name(sx_status status);

@@ -9,6 +9,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -117,7 +118,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sx_head_norm_rotate_backward.argtypes = [c_int, *tensor, *tensor, c_int, _i64p, vp, c_i64, vp, _i64p, vp,
                                                  _i64p, vp, vp, vp, c_f, c_int, vp, vp, vp, vp, vp, c_size, vp]
     lib.sx_head_norm_rotate_backward_workspace_bytes.restype = c_size
-    lib.sx_head_norm_rotate_backward_workspace_bytes.argtypes = [_i64p]
+    lib.sx_head_norm_rotate_backward_workspace_bytes.argtypes = [_i64p, _i64p]
     lib.sx_matrix_scan_workspace_status.restype = c_int
     lib.sx_matrix_scan_workspace_status.argtypes = [vp, c_size, vp]
     lib.sx_set_lookback_spin_limit.restype = None
@@ -567,37 +568,63 @@ def _matrix_dims_contiguous(t: torch.Tensor) -> bool:
 
 
 # ---------------------------------------------------------------- linear attention
+#
+# A single token's call takes the GPU a few microseconds, so what the binding
+# does in Python counts: shape and stride arrays are kept by value, and the
+# device is switched only when another one is current.
 
-def _require_same_device(op: str, tensors) -> torch.device:
-    given = [(name, t) for name, t in tensors if t is not None]
-    for name, t in given:
-        _require_device_tensor(f"{op}: {name}", t)
-    if any(t.device != given[0][1].device for _, t in given):
-        raise SxError(SX_E_UNSUPPORTED, f"{op}: operands on different devices")
-    return given[0][1].device
+@functools.lru_cache(maxsize=4096)
+def _i64(values: tuple) -> ctypes.Array:
+    """The values as an array the library reads (never one it writes)."""
+    return i64_array(values)
 
 
-def _require_dtype(op: str, tensors) -> int:
+def _device_index(op: str, names, tensors, optional=()) -> int:
+    """The index of the one device all tensors are on. `optional` (name, tensor) pairs may be None."""
+    index = -1
+    for name, t in zip(names, tensors):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            _require_device_tensor(f"{op}: {name}", t)
+        at = t.get_device()
+        if index >= 0 and at != index:
+            raise SxError(SX_E_UNSUPPORTED, f"{op}: operands on different devices")
+        index = at
+    for name, t in optional:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            _require_device_tensor(f"{op}: {name}", t)
+        if t.get_device() != index:
+            raise SxError(SX_E_UNSUPPORTED, f"{op}: operands on different devices")
+    return index
+
+
+def _require_dtype(op: str, names, tensors) -> int:
     """One float dtype (f32 or bf16) for all; its code."""
-    first = tensors[0][1].dtype
-    if first not in _DTYPES or any(t.dtype != first for _, t in tensors):
-        said = ", ".join(f"{name} is {t.dtype}" for name, t in tensors)
+    first = tensors[0].dtype
+    code = _DTYPES.get(first)
+    if code is not None:
+        for t in tensors:
+            if t.dtype is not first:
+                code = None
+    if code is None:
+        said = ", ".join(f"{name} is {t.dtype}" for name, t in zip(names, tensors))
         raise SxError(SX_E_DIM_002, f"{op}: {said}; one float dtype (f32 or bf16) is required")
-    return _DTYPES[first]
+    return code
 
 
 def _require(op: str, name: str, t, dtype, shape) -> None:
     """An optional operand of a fixed dtype and shape."""
     if t is None:
         return
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise SxError(SX_E_DIM_002, f"{op}: {name} is {t.dtype}, {dtype} is required")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise SxError(SX_E_DIM_001, f"{op}: {name} is {tuple(t.shape)}, {tuple(shape)} is required")
 
 
 def _args(t: torch.Tensor):
-    return i64_array(t.shape), i64_array(t.stride()), t.data_ptr()
+    return _i64(t.shape), _i64(t.stride()), t.data_ptr()
 
 
 def _ptr(t):
@@ -608,23 +635,57 @@ def _contiguous(t):
     return None if t is None else t.contiguous()
 
 
-def _decay_operands(op, q, k, v, log_decay, initial, lengths, token_dims):
-    """Checks what the C library cannot see (types, devices, optional operands); the dtype code and H."""
-    dev = _require_same_device(op, [("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("initial", initial),
-                                    ("lengths", lengths)])
-    code = _require_dtype(op, [("q", q), ("k", k), ("v", v)])
+def _records(*tensors) -> bool:
+    """Whether autograd has to see the call."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                return True
+    return False
+
+
+def _enqueue(index: int, entry, *args) -> None:
+    """Call a library entry with the current stream of device `index` as its last argument."""
+    if torch.cuda.current_device() == index:
+        _check(entry(*args, _raw_stream(index)))
+    else:
+        with torch.cuda.device(index):
+            _check(entry(*args, _raw_stream(index)))
+
+
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _workspace(nbytes: int, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _decay_operands(op, q, k, v, log_decay, token_dims, more, optional):
+    """Checks what the C library cannot see (types, devices, optional operands); the dtype code, H and the device."""
+    index = _device_index(op, ("q", "k", "v", "log_decay", *(n for n, _ in more)),
+                          (q, k, v, log_decay, *(t for _, t in more)), optional)
+    code = _require_dtype(op, ("q", "k", "v"), (q, k, v))
     rank = 2 + token_dims
     for name, t in (("q", q), ("k", k), ("v", v)):
         if t.dim() != rank:
             raise SxError(SX_E_DIM_001, f"{op}: {name} {tuple(t.shape)} must have {rank} dims")
-    if log_decay.dtype != torch.float32:
+    if log_decay.dtype is not torch.float32:
         raise SxError(SX_E_DIM_002, f"{op}: log_decay is {log_decay.dtype}, torch.float32 is required")
     if log_decay.dim() not in (1, 1 + token_dims):
         raise SxError(SX_E_DIM_001, f"{op}: log_decay {tuple(log_decay.shape)} must be [heads] or have a value a token")
-    heads = int(log_decay.shape[-1])
-    _require(op, "initial", initial, torch.float32, (q.shape[0], heads, q.shape[-1], v.shape[-1]))
-    _require(op, "lengths", lengths, torch.int32, (q.shape[0],))
-    return code, heads, dev
+    return code, log_decay.shape[-1], index
+
+
+@functools.lru_cache(maxsize=1024)
+def _decay_workspace_bytes(code, q_shape, v_shape, heads):
+    return load_library().sx_decay_attention_workspace_bytes(code, _i64(q_shape), _i64(v_shape), heads)
+
+
+@functools.lru_cache(maxsize=1024)
+def _decay_backward_workspace_bytes(code, q_shape, k_shape, v_shape, heads):
+    return load_library().sx_decay_attention_backward_workspace_bytes(code, _i64(q_shape), _i64(k_shape),
+                                                                      _i64(v_shape), heads)
 
 
 def decay_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, initial=None,
@@ -641,8 +702,7 @@ def decay_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay
     ``[B, T, H, dv]``, and the last state too when ``return_state``. When autograd
     records, the gradient runs through ``decay_attention_backward``.
     """
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad
-                                       for t in (q, k, v, log_decay, initial)):
+    if _records(q, k, v, log_decay, initial):
         out, state = _DecayAttentionFunction.apply(q, k, v, log_decay, initial, lengths, scale, return_state)
     else:
         out, state = _decay_attention_forward(q, k, v, log_decay, initial, lengths, scale, return_state)
@@ -651,20 +711,20 @@ def decay_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay
 
 def _decay_attention_forward(q, k, v, log_decay, initial, lengths, scale, return_state):
     op = "decay-attention"
-    code, heads, dev = _decay_operands(op, q, k, v, log_decay, initial, lengths, 2)
+    code, heads, index = _decay_operands(op, q, k, v, log_decay, 2, (), (("initial", initial), ("lengths", lengths)))
+    b, t, _, dk = q.shape
+    dv = v.shape[-1]
+    _require(op, "initial", initial, torch.float32, (b, heads, dk, dv))
+    _require(op, "lengths", lengths, torch.int32, (b,))
     initial, lengths = _contiguous(initial), _contiguous(lengths)
-    lib = load_library()
-    out = torch.empty((q.shape[0], q.shape[1], heads, v.shape[-1]), dtype=q.dtype, device=dev)
-    state = None
-    if return_state:
-        state = torch.empty((q.shape[0], heads, q.shape[-1], v.shape[-1]), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        qa, va = _args(q), _args(v)
-        nbytes = lib.sx_decay_attention_workspace_bytes(code, qa[0], va[0], heads)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        _check(lib.sx_decay_attention(code, *qa, *_args(k), *va, log_decay.dim(), *_args(log_decay), _ptr(initial),
-                                      _ptr(lengths), float(scale), out.data_ptr(), _ptr(state), _ptr(ws), nbytes,
-                                      _stream_handle(dev)))
+    dev = q.device
+    out = torch.empty((b, t, heads, dv), dtype=q.dtype, device=dev)
+    state = torch.empty((b, heads, dk, dv), dtype=torch.float32, device=dev) if return_state else None
+    nbytes = _decay_workspace_bytes(code, q.shape, v.shape, heads)
+    ws = _workspace(nbytes, dev)
+    _enqueue(index, load_library().sx_decay_attention, code, *_args(q), *_args(k), *_args(v), log_decay.dim(),
+             *_args(log_decay), _ptr(initial), _ptr(lengths), float(scale), out.data_ptr(), _ptr(state), _ptr(ws),
+             nbytes)
     return out, state
 
 
@@ -679,24 +739,26 @@ def decay_attention_backward(q, k, v, log_decay, grad_out, initial=None, lengths
     gradient of the state before the first token, also when that was zero.
     """
     op = "decay-attention gradient"
-    code, heads, dev = _decay_operands(op, q, k, v, log_decay, initial, lengths, 2)
-    _require_same_device(op, [("q", q), ("grad_out", grad_out), ("grad_state", grad_state)])
-    _require(op, "grad_out", grad_out, q.dtype, (q.shape[0], q.shape[1], heads, v.shape[-1]))
-    state_shape = (q.shape[0], heads, q.shape[-1], v.shape[-1])
+    code, heads, index = _decay_operands(op, q, k, v, log_decay, 2, (("grad_out", grad_out),),
+                                         (("initial", initial), ("lengths", lengths), ("grad_state", grad_state)))
+    b, t, _, dk = q.shape
+    dv = v.shape[-1]
+    state_shape = (b, heads, dk, dv)
+    _require(op, "initial", initial, torch.float32, state_shape)
+    _require(op, "lengths", lengths, torch.int32, (b,))
+    _require(op, "grad_out", grad_out, q.dtype, (b, t, heads, dv))
     _require(op, "grad_state", grad_state, torch.float32, state_shape)
     initial, lengths, grad_state = _contiguous(initial), _contiguous(lengths), _contiguous(grad_state)
-    lib = load_library()
-    gq, gk, gv = (torch.empty(tuple(t.shape), dtype=t.dtype, device=dev) for t in (q, k, v))
-    gg = torch.empty(tuple(log_decay.shape), dtype=torch.float32, device=dev)
+    dev = q.device
+    gq, gk, gv = (torch.empty(x.shape, dtype=x.dtype, device=dev) for x in (q, k, v))
+    gg = torch.empty(log_decay.shape, dtype=torch.float32, device=dev)
     gi = torch.empty(state_shape, dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        qa, ka, va = _args(q), _args(k), _args(v)
-        nbytes = lib.sx_decay_attention_backward_workspace_bytes(code, qa[0], ka[0], va[0], heads)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        _check(lib.sx_decay_attention_backward(
-            code, *qa, *ka, *va, log_decay.dim(), *_args(log_decay), i64_array(grad_out.stride()),
-            grad_out.data_ptr(), _ptr(grad_state), _ptr(initial), _ptr(lengths), float(scale), gq.data_ptr(),
-            gk.data_ptr(), gv.data_ptr(), gg.data_ptr(), gi.data_ptr(), _ptr(ws), nbytes, _stream_handle(dev)))
+    nbytes = _decay_backward_workspace_bytes(code, q.shape, k.shape, v.shape, heads)
+    ws = _workspace(nbytes, dev)
+    _enqueue(index, load_library().sx_decay_attention_backward, code, *_args(q), *_args(k), *_args(v),
+             log_decay.dim(), *_args(log_decay), _i64(grad_out.stride()), grad_out.data_ptr(), _ptr(grad_state),
+             _ptr(initial), _ptr(lengths), float(scale), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), gg.data_ptr(),
+             gi.data_ptr(), _ptr(ws), nbytes)
     return gq, gk, gv, gg, gi
 
 
@@ -712,6 +774,7 @@ class _DecayAttentionFunction(torch.autograd.Function):
         return out, state
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, grad_out, grad_state):
         q, k, v, log_decay, initial, lengths = ctx.saved_tensors
         if grad_out is None:
@@ -733,20 +796,18 @@ def decay_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_
     rows of one slot race. Returns out ``[B, H, dv]``. No gradient is recorded.
     """
     op = "decay-attention step"
-    code, heads, dev = _decay_operands(op, q, k, v, log_decay, None, None, 1)
-    _require_same_device(op, [("q", q), ("state", state), ("slots", slots)])
-    if state.dim() != 4 or tuple(state.shape[1:]) != (heads, q.shape[-1], v.shape[-1]):
-        raise SxError(SX_E_DIM_001, f"{op}: state is {tuple(state.shape)}, "
-                                    f"[states, {heads}, {q.shape[-1]}, {v.shape[-1]}] is required")
+    code, heads, index = _decay_operands(op, q, k, v, log_decay, 1, (("state", state),), (("slots", slots),))
+    b, _, dk = q.shape
+    dv = v.shape[-1]
+    if state.dim() != 4 or state.shape[1:] != (heads, dk, dv):
+        raise SxError(SX_E_DIM_001, f"{op}: state is {tuple(state.shape)}, [states, {heads}, {dk}, {dv}] is required")
     _require(op, "state", state, torch.float32, None)
-    _require(op, "slots", slots, torch.int32, (q.shape[0],))
+    _require(op, "slots", slots, torch.int32, (b,))
     slots = _contiguous(slots)
-    lib = load_library()
-    out = torch.empty((q.shape[0], heads, v.shape[-1]), dtype=q.dtype, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib.sx_decay_attention_step(code, *_args(q), *_args(k), *_args(v), log_decay.dim(), *_args(log_decay),
-                                           int(state.shape[0]), i64_array(state.stride()), state.data_ptr(),
-                                           _ptr(slots), float(scale), out.data_ptr(), _stream_handle(dev)))
+    out = torch.empty((b, heads, dv), dtype=q.dtype, device=q.device)
+    _enqueue(index, load_library().sx_decay_attention_step, code, *_args(q), *_args(k), *_args(v), log_decay.dim(),
+             *_args(log_decay), state.shape[0], _i64(state.stride()), state.data_ptr(), _ptr(slots), float(scale),
+             out.data_ptr())
     return out
 
 
@@ -759,24 +820,31 @@ def rotation_turns(rotated: int, base: float = 10000.0, device=None) -> torch.Te
     return float(base) ** (-2.0 * i / max(rotated, 1)) / (2.0 * math.pi)
 
 
-def _rotate_operands(op, q, k, positions, turns, q_weight, k_weight):
-    dev = _require_same_device(op, [("q", q), ("k", k), ("positions", positions), ("turns", turns),
-                                    ("q_weight", q_weight), ("k_weight", k_weight)])
-    code = _require_dtype(op, [("q", q), ("k", k)])
+def _rotate_operands(op, q, k, positions, turns, q_weight, k_weight, more=()):
+    index = _device_index(op, ("q", "k", "positions", "turns", *(n for n, _ in more)),
+                          (q, k, positions, turns, *(t for _, t in more)),
+                          (("q_weight", q_weight), ("k_weight", k_weight)))
+    code = _require_dtype(op, ("q", "k"), (q, k))
     for name, t in (("q", q), ("k", k)):
         if t.dim() != 4:
             raise SxError(SX_E_DIM_001, f"{op}: {name} {tuple(t.shape)} must be [batch, tokens, heads, width]")
-    if positions.dtype not in (torch.int32, torch.int64):
+    b, t, _, d = q.shape
+    if positions.dtype is not torch.int64 and positions.dtype is not torch.int32:
         raise SxError(SX_E_DIM_002, f"{op}: positions are {positions.dtype}, int32 or int64 is required")
-    if tuple(positions.shape) == (q.shape[1],):
-        positions = positions[None].expand(q.shape[0], q.shape[1])
-    _require(op, "positions", positions, positions.dtype, tuple(q.shape[:2]))
+    if positions.shape == (t,):
+        positions = positions[None].expand(b, t)
+    _require(op, "positions", positions, positions.dtype, (b, t))
     if turns.dim() != 1:
         raise SxError(SX_E_DIM_001, f"{op}: turns {tuple(turns.shape)} must have one dim")
     _require(op, "turns", turns, torch.float64, None)
-    _require(op, "q_weight", q_weight, torch.float32, (q.shape[-1],))
-    _require(op, "k_weight", k_weight, torch.float32, (q.shape[-1],))
-    return code, dev, positions, turns.contiguous(), _contiguous(q_weight), _contiguous(k_weight)
+    _require(op, "q_weight", q_weight, torch.float32, (d,))
+    _require(op, "k_weight", k_weight, torch.float32, (d,))
+    return code, index, positions, turns.contiguous(), _contiguous(q_weight), _contiguous(k_weight)
+
+
+@functools.lru_cache(maxsize=1024)
+def _rotate_workspace_bytes(q_shape, k_shape):
+    return load_library().sx_head_norm_rotate_backward_workspace_bytes(_i64(q_shape), _i64(k_shape))
 
 
 def head_norm_rotate(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, turns: torch.Tensor, q_weight=None,
@@ -791,22 +859,20 @@ def head_norm_rotate(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, 
     dtype. When autograd records, the gradient runs through
     ``head_norm_rotate_backward``.
     """
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad
-                                       for t in (q, k, q_weight, k_weight)):
+    if _records(q, k, q_weight, k_weight):
         return _HeadNormRotateFunction.apply(q, k, positions, turns, q_weight, k_weight, eps, neighbours)
     return _head_norm_rotate_forward(q, k, positions, turns, q_weight, k_weight, eps, neighbours)
 
 
 def _head_norm_rotate_forward(q, k, positions, turns, q_weight, k_weight, eps, neighbours):
     op = "head-norm-rotate"
-    code, dev, positions, turns, q_weight, k_weight = _rotate_operands(op, q, k, positions, turns, q_weight, k_weight)
-    lib = load_library()
-    oq, ok = (torch.empty(tuple(t.shape), dtype=t.dtype, device=dev) for t in (q, k))
-    with torch.cuda.device(dev):
-        _check(lib.sx_head_norm_rotate(code, *_args(q), *_args(k), int(positions.dtype == torch.int64),
-                                       i64_array(positions.stride()), positions.data_ptr(), 2 * turns.shape[0],
-                                       turns.data_ptr(), _ptr(q_weight), _ptr(k_weight), float(eps),
-                                       int(bool(neighbours)), oq.data_ptr(), ok.data_ptr(), _stream_handle(dev)))
+    code, index, positions, turns, q_weight, k_weight = _rotate_operands(op, q, k, positions, turns, q_weight, k_weight)
+    dev = q.device
+    oq, ok = torch.empty(q.shape, dtype=q.dtype, device=dev), torch.empty(k.shape, dtype=k.dtype, device=dev)
+    _enqueue(index, load_library().sx_head_norm_rotate, code, *_args(q), *_args(k),
+             1 if positions.dtype is torch.int64 else 0, _i64(positions.stride()), positions.data_ptr(),
+             2 * turns.shape[0], turns.data_ptr(), _ptr(q_weight), _ptr(k_weight), float(eps), 1 if neighbours else 0,
+             oq.data_ptr(), ok.data_ptr())
     return oq, ok
 
 
@@ -816,23 +882,20 @@ def head_norm_rotate_backward(q, k, positions, turns, grad_out_q, grad_out_k, q_
     ``head_norm_rotate(q, k, positions, turns, q_weight, k_weight, eps, neighbours)``, given its gradients with
     respect to the two results (their shapes, q's dtype). A weight that is None has None for its gradient."""
     op = "head-norm-rotate gradient"
-    code, dev, positions, turns, q_weight, k_weight = _rotate_operands(op, q, k, positions, turns, q_weight, k_weight)
-    _require_same_device(op, [("q", q), ("grad_out_q", grad_out_q), ("grad_out_k", grad_out_k)])
-    _require(op, "grad_out_q", grad_out_q, q.dtype, tuple(q.shape))
-    _require(op, "grad_out_k", grad_out_k, k.dtype, tuple(k.shape))
-    lib = load_library()
-    gq, gk = (torch.empty(tuple(t.shape), dtype=t.dtype, device=dev) for t in (q, k))
-    gqw, gkw = (None if w is None else torch.empty_like(w) for w in (q_weight, k_weight))
-    with torch.cuda.device(dev):
-        qa = _args(q)
-        nbytes = lib.sx_head_norm_rotate_backward_workspace_bytes(qa[0]) if gqw is not None or gkw is not None else 0
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        _check(lib.sx_head_norm_rotate_backward(
-            code, *qa, *_args(k), int(positions.dtype == torch.int64), i64_array(positions.stride()),
-            positions.data_ptr(), 2 * turns.shape[0], turns.data_ptr(), i64_array(grad_out_q.stride()),
-            grad_out_q.data_ptr(), i64_array(grad_out_k.stride()), grad_out_k.data_ptr(), _ptr(q_weight),
-            _ptr(k_weight), float(eps), int(bool(neighbours)), gq.data_ptr(), gk.data_ptr(), _ptr(gqw), _ptr(gkw),
-            _ptr(ws), nbytes, _stream_handle(dev)))
+    code, index, positions, turns, q_weight, k_weight = _rotate_operands(
+        op, q, k, positions, turns, q_weight, k_weight, (("grad_out_q", grad_out_q), ("grad_out_k", grad_out_k)))
+    _require(op, "grad_out_q", grad_out_q, q.dtype, q.shape)
+    _require(op, "grad_out_k", grad_out_k, k.dtype, k.shape)
+    dev = q.device
+    gq, gk = torch.empty(q.shape, dtype=q.dtype, device=dev), torch.empty(k.shape, dtype=k.dtype, device=dev)
+    gqw, gkw = (None if w is None else torch.empty(w.shape, dtype=w.dtype, device=dev) for w in (q_weight, k_weight))
+    nbytes = 0 if gqw is None and gkw is None else _rotate_workspace_bytes(q.shape, k.shape)
+    ws = _workspace(nbytes, dev)
+    _enqueue(index, load_library().sx_head_norm_rotate_backward, code, *_args(q), *_args(k),
+             1 if positions.dtype is torch.int64 else 0, _i64(positions.stride()), positions.data_ptr(),
+             2 * turns.shape[0], turns.data_ptr(), _i64(grad_out_q.stride()), grad_out_q.data_ptr(),
+             _i64(grad_out_k.stride()), grad_out_k.data_ptr(), _ptr(q_weight), _ptr(k_weight), float(eps),
+             1 if neighbours else 0, gq.data_ptr(), gk.data_ptr(), _ptr(gqw), _ptr(gkw), _ptr(ws), nbytes)
     return gq, gk, gqw, gkw
 
 
@@ -846,6 +909,7 @@ class _HeadNormRotateFunction(torch.autograd.Function):
         return _head_norm_rotate_forward(q, k, positions, turns, q_weight, k_weight, eps, neighbours)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, grad_out_q, grad_out_k):
         q, k, positions, turns, q_weight, k_weight = ctx.saved_tensors
         gq, gk, gqw, gkw = head_norm_rotate_backward(q, k, positions, turns, grad_out_q, grad_out_k, q_weight=q_weight,

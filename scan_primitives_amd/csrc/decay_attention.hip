@@ -108,6 +108,15 @@ struct Op<true> {
     auto bad = [](uint32_t u) { return (u & 0x7f800000u) == 0x7f800000u || (u & 0x7f80u) == 0x7f80u; };
     return !(bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w));
   }
+  // infinities and NaN taken out
+  static __device__ __forceinline__ Pair finite_part(Pair v) {
+    auto f = [](uint32_t u) {
+      if ((u & 0x7f800000u) == 0x7f800000u) u &= 0xffffu;
+      if ((u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
+      return u;
+    };
+    return make_uint4(f(v.x), f(v.y), f(v.z), f(v.w));
+  }
   static __device__ __forceinline__ void put4(E* p, f32x4 v) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
   }
@@ -152,6 +161,14 @@ struct Op<false> {
   static __device__ __forceinline__ bool finite(uint4 v) {
     auto bad = [](uint32_t u) { return (u & 0x7f800000u) == 0x7f800000u; };
     return !(bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w));
+  }
+  static __device__ __forceinline__ Pair finite_part(Pair v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if ((__float_as_uint(v.a[i]) & 0x7f800000u) == 0x7f800000u) v.a[i] = 0.0f;
+      if ((__float_as_uint(v.b[i]) & 0x7f800000u) == 0x7f800000u) v.b[i] = 0.0f;
+    }
+    return v;
   }
   static __device__ __forceinline__ void put4(E* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
   static __device__ __forceinline__ E round(float v) { return v; }
@@ -453,25 +470,27 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
         O::template split<O::kState>(O::low(z[n]) * f0, O::high(z[n]) * f1, zs[n]);
       }
       if constexpr (OUT) {
-        if (!odd) {
+        // An infinity or NaN in z times a score of zero would reach rows that do not see its token: such
+        // values are left out here and added below to the rows that do.
+        if (odd)
+          for (int n = 0; n < NV; ++n) z[n] = O::finite_part(z[n]);
 #pragma unroll
-          for (int it = 0; it < CT; ++it) {
-            if (REV ? it <= 2 * j2 + 1 : it >= 2 * j2) {
-              // the one tile of a pair beyond the diagonal was not written
-              const bool half = REV ? it == 2 * j2 + 1 : it == 2 * j2;
+        for (int it = 0; it < CT; ++it) {
+          if (REV ? it <= 2 * j2 + 1 : it >= 2 * j2) {
+            // the one tile of a pair beyond the diagonal was not written
+            const bool half = REV ? it == 2 * j2 + 1 : it == 2 * j2;
 #pragma unroll
-              for (int q = O::kScore - 1; q >= 0; --q) {
-                Pair s = O::row_pair(l.score[q] + (16 * it + c) * S::SP + 32 * j2, g);
-                if (half) {
-                  if constexpr (BF) {
-                    if (REV) s.x = s.y = 0; else s.z = s.w = 0;
-                  } else {
-                    if (REV) s.a = zero4(); else s.b = zero4();
-                  }
+            for (int q = O::kScore - 1; q >= 0; --q) {
+              Pair s = O::row_pair(l.score[q] + (16 * it + c) * S::SP + 32 * j2, g);
+              if (half) {
+                if constexpr (BF) {
+                  if (REV) s.x = s.y = 0; else s.z = s.w = 0;
+                } else {
+                  if (REV) s.a = zero4(); else s.b = zero4();
                 }
-#pragma unroll
-                for (int n = 0; n < NV; ++n) acc[n][it] = O::mma(z[n], s, acc[n][it]);
               }
+#pragma unroll
+              for (int n = 0; n < NV; ++n) acc[n][it] = O::mma(z[n], s, acc[n][it]);
             }
           }
         }
@@ -490,22 +509,19 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
 
     if constexpr (OUT) {
       if (odd) {
-        // An infinity or NaN in z: a product over the whole chunk would carry it (times a score of
-        // zero) into rows that do not see its token, so the sources are added one by one.
         for (int j = 0; j < C; ++j)
 #pragma unroll
-          for (int it = 0; it < CT; ++it) {
-            const int row = 16 * it + c;
-            if (REV ? j >= row : j <= row) {
-              float s = 0.0f;
-              for (int q = O::kScore - 1; q >= 0; --q) s += O::one(l.score[q][row * S::SP + j]);
+          for (int n = 0; n < NV; ++n)
 #pragma unroll
-              for (int n = 0; n < NV; ++n)
+            for (int r = 0; r < 4; ++r) {
+              const float v = O::one(l.z[j * S::SZ + wc0 + 16 * n + 4 * g + r]);
+              if ((__float_as_uint(v) & 0x7f800000u) != 0x7f800000u) continue;
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  acc[n][it][r] = fmaf(s, O::one(l.z[j * S::SZ + wc0 + 16 * n + 4 * g + r]), acc[n][it][r]);
+              for (int it = 0; it < CT; ++it) {
+                const int row = 16 * it + c;
+                if (REV ? j >= row : j <= row) acc[n][it][r] += O::one(l.score[0][row * S::SP + j]) * v;
+              }
             }
-          }
       }
       const bool whole = (m.dz & 3) == 0;
 #pragma unroll

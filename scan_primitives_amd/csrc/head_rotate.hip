@@ -8,9 +8,12 @@
 //
 // A row (one head of one token) is cut into units of two components that turn
 // together: (i, i + rot/2) or (2i, 2i+1), and neighbours behind `rot` that do not
-// turn. A lane holds four consecutive units of a row, so a pair never leaves its
-// lane. A token's cosines and sines are formed once for all its heads, through
-// LDS. The angle is reduced in 64 bits: position times turns, its nearest whole
+// turn. A lane holds U units of a row, so a pair never leaves its lane: where
+// alignment allows it U consecutive ones (two 16-byte loads a row), else every
+// G-th one, so that a load's lanes touch neighbouring elements. A workgroup takes
+// some tokens of the queries or of the keys; their cosines and sines are formed
+// once for all its heads, through LDS, while its first rows are on their way.
+// The angle is reduced in 64 bits: position times turns, its nearest whole
 // number taken off; 32 bits would lose the angle of far positions.
 #include <hip/hip_runtime.h>
 
@@ -24,103 +27,137 @@ namespace sx {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 4;       // tokens a workgroup takes at a time where there are many
+constexpr int kMostTokens = 16;  // tokens of a workgroup at a time
 constexpr int kMaxUnits = 128;   // d <= 256
+constexpr int kSumRows = 64;     // partial sums of a weight's gradient that are read at once
 
 template <bool BF>
-struct El {
+struct El;
+template <>
+struct El<true> {
   using E = uint16_t;
+  static constexpr int U = 8;  // units a lane
   static __device__ __forceinline__ float get(E v) { return bf16_to_f32(v); }
   static __device__ __forceinline__ E put(float v) { return f32_to_bf16_rne(v); }
-  static __device__ __forceinline__ f32x4 get4(const E* p) {
-    const uint2 a = *reinterpret_cast<const uint2*>(p);
-    return f32x4{__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u), __uint_as_float(a.y << 16),
-                 __uint_as_float(a.y & 0xffff0000u)};
+  static __device__ __forceinline__ void open(uint4 a, float* v) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
   }
-  static __device__ __forceinline__ void put4(E* p, f32x4 v) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  static __device__ __forceinline__ uint4 close(const float* v) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
   }
 };
 template <>
 struct El<false> {
   using E = float;
+  static constexpr int U = 4;
   static __device__ __forceinline__ float get(E v) { return v; }
   static __device__ __forceinline__ E put(float v) { return v; }
-  static __device__ __forceinline__ f32x4 get4(const E* p) { return *reinterpret_cast<const f32x4*>(p); }
-  static __device__ __forceinline__ void put4(E* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+  static __device__ __forceinline__ void open(uint4 a, float* v) {
+    v[0] = __uint_as_float(a.x);
+    v[1] = __uint_as_float(a.y);
+    v[2] = __uint_as_float(a.z);
+    v[3] = __uint_as_float(a.w);
+  }
+  static __device__ __forceinline__ uint4 close(const float* v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
 };
 
-// The components of a lane's four units.
-struct Units {
-  int first[4], second[4];
-  bool four;   // first[] and second[] are each four consecutive components, or eight in a row
-  bool joint;  // units are neighbours: first, second alternate
+// Which components a lane holds. WIDE: U consecutive units (16-byte pieces), else every G-th.
+template <bool BF, int G, bool WIDE>
+struct Lane {
+  using T = El<BF>;
+  using E = typename T::E;
+  static constexpr int U = T::U;
+  int lr, half, d;
+  bool split;  // pairs are halves apart, not neighbours
+
+  __device__ __forceinline__ Lane(const HrParams& p, int lane_in_row)
+      : lr(lane_in_row), half(p.rot / 2), d(p.d), split(!p.neighbours) {}
+  __device__ __forceinline__ int unit(int i) const { return WIDE ? U * lr + i : lr + G * i; }
+  __device__ __forceinline__ int first(int i) const {
+    const int k = unit(i);
+    return split && k < half ? k : 2 * k;
+  }
+  __device__ __forceinline__ int second(int i) const {
+    const int k = unit(i);
+    return split && k < half ? k + half : 2 * k + 1;
+  }
+  // WIDE: the first components of the lane's two pieces; all U units lie on one side of `half`
+  __device__ __forceinline__ bool apart() const { return split && U * lr < half; }
+  __device__ __forceinline__ int piece(int i) const {
+    return apart() ? U * lr + i * half : 2 * U * lr + i * U;
+  }
+
+  struct Raw {
+    uint4 a, b;          // WIDE
+    E x[U], y[U];        // not
+  };
+  __device__ __forceinline__ void load(const E* row, int64_t sd, Raw& r) const {
+    if constexpr (WIDE) {
+      r.a = r.b = make_uint4(0, 0, 0, 0);
+      if (piece(0) < d) r.a = *reinterpret_cast<const uint4*>(row + piece(0));
+      if (piece(1) < d) r.b = *reinterpret_cast<const uint4*>(row + piece(1));
+    } else {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        r.x[i] = first(i) < d ? row[first(i) * sd] : E(0);
+        r.y[i] = second(i) < d ? row[second(i) * sd] : E(0);
+      }
+    }
+  }
+  __device__ __forceinline__ void open(const Raw& r, float (&x)[U], float (&y)[U]) const {
+    if constexpr (WIDE) {
+      float v[2 * U];
+      T::open(r.a, v);
+      T::open(r.b, v + U);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        x[i] = apart() ? v[i] : v[2 * i];
+        y[i] = apart() ? v[U + i] : v[2 * i + 1];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        x[i] = T::get(r.x[i]);
+        y[i] = T::get(r.y[i]);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(E* row, const float (&x)[U], const float (&y)[U]) const {
+    if constexpr (WIDE) {
+      float v[2 * U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        v[i] = apart() ? x[i] : (i & 1 ? y[i / 2] : x[i / 2]);
+        v[U + i] = apart() ? y[i] : (i & 1 ? y[(U + i) / 2] : x[(U + i) / 2]);
+      }
+      if (piece(0) < d) *reinterpret_cast<uint4*>(row + piece(0)) = T::close(v);
+      if (piece(1) < d) *reinterpret_cast<uint4*>(row + piece(1)) = T::close(v + U);
+    } else {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (first(i) < d) row[first(i)] = T::put(x[i]);
+        if (second(i) < d) row[second(i)] = T::put(y[i]);
+      }
+    }
+  }
+  __device__ __forceinline__ void weights(const float* w, float (&x)[U], float (&y)[U]) const {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      x[i] = first(i) < d ? (w ? w[first(i)] : 1.0f) : 0.0f;
+      y[i] = second(i) < d ? (w ? w[second(i)] : 1.0f) : 0.0f;
+    }
+  }
 };
 
-__device__ __forceinline__ Units units_of(const HrParams& p, int lane_in_row) {
-  Units u;
-  const int half = p.rot / 2, i0 = 4 * lane_in_row;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int k = i0 + i;
-    const bool split = k < half && !p.neighbours;
-    u.first[i] = split ? k : 2 * k;
-    u.second[i] = split ? k + half : 2 * k + 1;
-  }
-  u.joint = !(i0 < half && !p.neighbours);
-  u.four = (half & 3) == 0 || p.neighbours;
-  return u;
-}
-
-// A lane's components of a row (zero where there are none): x[i] the firsts, y[i] the seconds.
-template <bool BF>
-__device__ __forceinline__ void load_units(const typename El<BF>::E* row, int64_t sd, bool vec, int d, const Units& u,
-                                           f32x4& x, f32x4& y) {
-  using T = El<BF>;
-  x = y = zero4();
-  if (vec && u.four) {
-    if (u.joint) {
-      if (u.first[0] < d) {
-        const f32x4 a = T::get4(row + u.first[0]), b = T::get4(row + u.first[0] + 4);
-        x = f32x4{a[0], a[2], b[0], b[2]};
-        y = f32x4{a[1], a[3], b[1], b[3]};
-      }
-    } else {
-      x = T::get4(row + u.first[0]);
-      y = T::get4(row + u.second[0]);
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (u.first[i] < d) x[i] = T::get(row[u.first[i] * sd]);
-    if (u.second[i] < d) y[i] = T::get(row[u.second[i] * sd]);
-  }
-}
-
-template <bool BF>
-__device__ __forceinline__ void store_units(typename El<BF>::E* row, bool vec, int d, const Units& u, f32x4 x,
-                                            f32x4 y) {
-  using T = El<BF>;
-  if (vec && u.four) {
-    if (u.joint) {
-      if (u.first[0] < d) {
-        T::put4(row + u.first[0], f32x4{x[0], y[0], x[1], y[1]});
-        T::put4(row + u.first[0] + 4, f32x4{x[2], y[2], x[3], y[3]});
-      }
-    } else {
-      T::put4(row + u.first[0], x);
-      T::put4(row + u.second[0], y);
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (u.first[i] < d) row[u.first[i]] = T::put(x[i]);
-    if (u.second[i] < d) row[u.second[i]] = T::put(y[i]);
-  }
-}
-
+// Sum over the G lanes of a row, the same in each.
 template <int G>
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
@@ -128,20 +165,18 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ double position_of(const HrParams& p, int64_t tok) {
-  const int64_t at = tok / p.T * p.pb + tok % p.T * p.pt;
-  return p.pos64 ? double(static_cast<const int64_t*>(p.positions)[at])
-                 : double(static_cast<const int32_t*>(p.positions)[at]);
-}
-
-// Cosine and sine of `count` tokens' units into cs[token][unit].
-__device__ __forceinline__ void angles(const HrParams& p, int64_t tok0, int count, float2 (*cs)[kMaxUnits]) {
+// Cosine and sine of `count` tokens' units from token tok0 on, into cs[token][unit].
+__device__ __forceinline__ void angles(const HrParams& p, uint32_t tok0, int count, float2 (*cs)[kMaxUnits]) {
   const int half = p.rot / 2, units = (p.d + 1) / 2;
   for (int q = int(threadIdx.x); q < count * units; q += kThreads) {
     const int t = q / units, i = q % units;
     float2 v = make_float2(1.0f, 0.0f);
     if (i < half) {
-      const double turn = position_of(p, tok0 + t) * p.turns[i];
+      const uint32_t tok = tok0 + uint32_t(t), b = tok / uint32_t(p.T);
+      const int64_t at = int64_t(b) * p.pb + int64_t(tok - b * uint32_t(p.T)) * p.pt;
+      const double pos = p.pos64 ? double(static_cast<const int64_t*>(p.positions)[at])
+                                 : double(static_cast<const int32_t*>(p.positions)[at]);
+      const double turn = pos * p.turns[i];
       const float f = float(turn - rint(turn));
       v = make_float2(cospif(2.0f * f), sinpif(2.0f * f));
     }
@@ -149,205 +184,236 @@ __device__ __forceinline__ void angles(const HrParams& p, int64_t tok0, int coun
   }
 }
 
-__device__ __forceinline__ void load_weights(const float* w, int d, const Units& u, f32x4& x, f32x4& y) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[i] = u.first[i] < d ? (w ? w[u.first[i]] : 1.0f) : 0.0f;
-    y[i] = u.second[i] < d ? (w ? w[u.second[i]] : 1.0f) : 0.0f;
-  }
+// Row q of a group: head q % heads of token tok0 + q / heads.
+template <typename E>
+__device__ __forceinline__ const E* row_of(const HrParams& p, const HeadView& v, uint32_t tok0, int heads, int q) {
+  const uint32_t t = uint32_t(q) / uint32_t(heads), h = uint32_t(q) - t * uint32_t(heads);
+  const uint32_t tok = tok0 + t, b = tok / uint32_t(p.T);
+  return static_cast<const E*>(v.p) + int64_t(b) * v.sb + int64_t(tok - b * uint32_t(p.T)) * v.st + int64_t(h) * v.sh;
 }
 
-// G lanes a row.
-template <bool BF, int G>
-__global__ __launch_bounds__(kThreads) void rotate_forward(HrParams p, int tokens) {
-  using E = typename El<BF>::E;
-  __shared__ float2 cs[kTokens][kMaxUnits];
-  const int lr = int(threadIdx.x) % G, slot = int(threadIdx.x) / G, heads = p.hq + p.hk;
-  const int64_t all = int64_t(p.B) * p.T, tok0 = int64_t(blockIdx.x) * tokens;
-  const int count = int(min(int64_t(tokens), all - tok0));
+// blockIdx.y: queries or keys. G lanes a row.
+template <bool BF, int G, bool WIDE>
+__global__ __launch_bounds__(kThreads) void rotate_forward(HrParams p) {
+  using L = Lane<BF, G, WIDE>;
+  using E = typename L::E;
+  constexpr int U = L::U, kSlots = kThreads / G;
+  __shared__ float2 cs[kMostTokens][kMaxUnits];
+  const bool isq = blockIdx.y == 0;
+  const HeadView& v = isq ? p.q : p.k;
+  const int heads = isq ? p.hq : p.hk, tokens = isq ? p.tokens_q : p.tokens_k;
+  const uint32_t all = uint32_t(p.B) * uint32_t(p.T);
+  const int64_t first = int64_t(blockIdx.x) * tokens;
+  if (first >= all || heads == 0) return;
+  const uint32_t tok0 = uint32_t(first);
+  const int count = int(min(uint32_t(tokens), all - tok0)), rows = count * heads;
+  const int slot = int(threadIdx.x) / G;
+  const L l(p, int(threadIdx.x) % G);
   const int units = (p.d + 1) / 2;
-  const Units u = units_of(p, lr);
-  f32x4 wq0, wq1, wk0, wk1;
-  load_weights(p.qw, p.d, u, wq0, wq1);
-  load_weights(p.kw, p.d, u, wk0, wk1);
+  typename L::Raw raw;
+  if (slot < rows) l.load(row_of<E>(p, v, tok0, heads, slot), v.sd, raw);
+  float w0[U], w1[U];
+  l.weights(isq ? p.qw : p.kw, w0, w1);
   angles(p, tok0, count, cs);
   __syncthreads();
   const float inv = 1.0f / float(p.d);
-  for (int q = slot; q < count * heads; q += kThreads / G) {
-    const int t = q / heads, hh = q % heads;
-    const bool isq = hh < p.hq;
-    const int h = isq ? hh : hh - p.hq, nh = isq ? p.hq : p.hk;
-    const HeadView& v = isq ? p.q : p.k;
-    const int64_t tok = tok0 + t, b = tok / p.T, tt = tok % p.T;
-    f32x4 x, y;
-    load_units<BF>(static_cast<const E*>(v.p) + b * v.sb + tt * v.st + h * v.sh, v.sd, v.vec, p.d, u, x, y);
+  E* out = static_cast<E*>(isq ? p.out_q : p.out_k) + int64_t(tok0) * heads * p.d;
+  for (int q = slot; q < rows; q += kSlots) {
+    float x[U], y[U];
+    l.open(raw, x, y);
+    if (q + kSlots < rows) l.load(row_of<E>(p, v, tok0, heads, q + kSlots), v.sd, raw);
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s = fmaf(x[i], x[i], fmaf(y[i], y[i], s));
+    for (int i = 0; i < U; ++i) s = fmaf(x[i], x[i], fmaf(y[i], y[i], s));
     const float r = rsqrtf(row_sum<G>(s) * inv + p.eps);
-    const f32x4 a = x * r * (isq ? wq0 : wk0), c = y * r * (isq ? wq1 : wk1);
-    f32x4 o0, o1;
+    const float2* turn = cs[q / heads];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 z = 4 * lr + i < units ? cs[t][4 * lr + i] : make_float2(1.0f, 0.0f);
-      o0[i] = a[i] * z.x - c[i] * z.y;
-      o1[i] = a[i] * z.y + c[i] * z.x;
+    for (int i = 0; i < U; ++i) {
+      const float2 z = l.unit(i) < units ? turn[l.unit(i)] : make_float2(1.0f, 0.0f);
+      const float a = x[i] * r * w0[i], c = y[i] * r * w1[i];
+      x[i] = a * z.x - c * z.y;
+      y[i] = a * z.y + c * z.x;
     }
-    E* to = static_cast<E*>(isq ? p.out_q : p.out_k) + (tok * nh + h) * p.d;
-    store_units<BF>(to, (p.d & 7) == 0, p.d, u, o0, o1);
+    l.store(out + int64_t(q) * p.d, x, y);
   }
 }
 
-template <bool BF, int G>
-__global__ __launch_bounds__(kThreads) void rotate_backward(HrParams p, int tokens, int64_t groups) {
-  using E = typename El<BF>::E;
-  __shared__ float2 cs[kTokens][kMaxUnits];
-  __shared__ float sums[kThreads / G][2][2 * 4 * G];
-  const int lr = int(threadIdx.x) % G, slot = int(threadIdx.x) / G, heads = p.hq + p.hk;
-  const int64_t all = int64_t(p.B) * p.T;
+// A workgroup takes every gridDim.x-th group of tokens and leaves one partial sum of the weight's gradient.
+template <bool BF, int G, bool WIDE>
+__global__ __launch_bounds__(kThreads) void rotate_backward(HrParams p) {
+  using L = Lane<BF, G, WIDE>;
+  using E = typename L::E;
+  constexpr int U = L::U, kSlots = kThreads / G;
+  __shared__ union {
+    float2 cs[kMostTokens][kMaxUnits];
+    float sums[kSlots][2 * U * G];
+  } lds;
+  const bool isq = blockIdx.y == 0;
+  const HeadView& v = isq ? p.q : p.k;
+  const HeadView& gv = isq ? p.gq : p.gk;
+  const int heads = isq ? p.hq : p.hk, tokens = isq ? p.tokens_q : p.tokens_k;
+  const uint32_t all = uint32_t(p.B) * uint32_t(p.T);
+  const int slot = int(threadIdx.x) / G;
+  const L l(p, int(threadIdx.x) % G);
   const int units = (p.d + 1) / 2;
-  const Units u = units_of(p, lr);
-  f32x4 wq0, wq1, wk0, wk1;
-  load_weights(p.qw, p.d, u, wq0, wq1);
-  load_weights(p.kw, p.d, u, wk0, wk1);
-  f32x4 gq0 = zero4(), gq1 = zero4(), gk0 = zero4(), gk1 = zero4();
-  const float inv = 1.0f / float(p.d);
-  for (int64_t grp = blockIdx.x; grp < groups; grp += gridDim.x) {
-    const int64_t tok0 = grp * tokens;
-    const int count = int(min(int64_t(tokens), all - tok0));
-    __syncthreads();
-    angles(p, tok0, count, cs);
-    __syncthreads();
-    for (int q = slot; q < count * heads; q += kThreads / G) {
-      const int t = q / heads, hh = q % heads;
-      const bool isq = hh < p.hq;
-      const int h = isq ? hh : hh - p.hq, nh = isq ? p.hq : p.hk;
-      const HeadView& v = isq ? p.q : p.k;
-      const HeadView& gv = isq ? p.gq : p.gk;
-      const int64_t tok = tok0 + t, b = tok / p.T, tt = tok % p.T;
-      f32x4 x, y, e, f;
-      load_units<BF>(static_cast<const E*>(v.p) + b * v.sb + tt * v.st + h * v.sh, v.sd, v.vec, p.d, u, x, y);
-      load_units<BF>(static_cast<const E*>(gv.p) + b * gv.sb + tt * gv.st + h * gv.sh, gv.sd, gv.vec, p.d, u, e, f);
-      f32x4 a, c;  // the gradient of u
+  float w0[U], w1[U], g0[U], g1[U];
+  l.weights(isq ? p.qw : p.kw, w0, w1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 z = 4 * lr + i < units ? cs[t][4 * lr + i] : make_float2(1.0f, 0.0f);
-        a[i] = e[i] * z.x + f[i] * z.y;
-        c[i] = f[i] * z.x - e[i] * z.y;
+  for (int i = 0; i < U; ++i) g0[i] = g1[i] = 0.0f;
+  const float inv = 1.0f / float(p.d);
+  for (int64_t first = int64_t(blockIdx.x) * tokens; first < all && heads > 0; first += int64_t(gridDim.x) * tokens) {
+    const uint32_t tok0 = uint32_t(first);
+    const int count = int(min(uint32_t(tokens), all - tok0)), rows = count * heads;
+    typename L::Raw raw, graw;
+    if (slot < rows) {
+      l.load(row_of<E>(p, v, tok0, heads, slot), v.sd, raw);
+      l.load(row_of<E>(p, gv, tok0, heads, slot), gv.sd, graw);
+    }
+    __syncthreads();
+    angles(p, tok0, count, lds.cs);
+    __syncthreads();
+    E* out = static_cast<E*>(isq ? p.out_q : p.out_k) + int64_t(tok0) * heads * p.d;
+    for (int q = slot; q < rows; q += kSlots) {
+      float x[U], y[U], a[U], c[U];
+      l.open(raw, x, y);
+      l.open(graw, a, c);
+      if (q + kSlots < rows) {
+        l.load(row_of<E>(p, v, tok0, heads, q + kSlots), v.sd, raw);
+        l.load(row_of<E>(p, gv, tok0, heads, q + kSlots), gv.sd, graw);
       }
-      const f32x4 n0 = a * (isq ? wq0 : wk0), n1 = c * (isq ? wq1 : wk1);
+      const float2* turn = lds.cs[q / heads];
       float s = 0.0f, dot = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < U; ++i) {
+        const float2 z = l.unit(i) < units ? turn[l.unit(i)] : make_float2(1.0f, 0.0f);
+        const float e = a[i], f = c[i];
+        a[i] = e * z.x + f * z.y;  // the gradient of u
+        c[i] = f * z.x - e * z.y;
         s = fmaf(x[i], x[i], fmaf(y[i], y[i], s));
-        dot = fmaf(n0[i], x[i], fmaf(n1[i], y[i], dot));
+        dot = fmaf(a[i] * w0[i], x[i], fmaf(c[i] * w1[i], y[i], dot));
       }
       const float r = rsqrtf(row_sum<G>(s) * inv + p.eps);
       const float along = row_sum<G>(dot) * inv * r * r;
-      if (isq) {
-        gq0 += a * x * r;
-        gq1 += c * y * r;
-      } else {
-        gk0 += a * x * r;
-        gk1 += c * y * r;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        g0[i] = fmaf(a[i], x[i] * r, g0[i]);
+        g1[i] = fmaf(c[i], y[i] * r, g1[i]);
+        x[i] = (a[i] * w0[i] - x[i] * along) * r;
+        y[i] = (c[i] * w1[i] - y[i] * along) * r;
       }
-      E* to = static_cast<E*>(isq ? p.out_q : p.out_k) + (tok * nh + h) * p.d;
-      store_units<BF>(to, (p.d & 7) == 0, p.d, u, (n0 - x * along) * r, (n1 - y * along) * r);
+      l.store(out + int64_t(q) * p.d, x, y);
     }
   }
-  if (!p.gqw && !p.gkw) return;
+  if (!(isq ? p.gqw : p.gkw)) return;
+  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    sums[slot][0][8 * lr + i] = gq0[i];
-    sums[slot][0][8 * lr + 4 + i] = gq1[i];
-    sums[slot][1][8 * lr + i] = gk0[i];
-    sums[slot][1][8 * lr + 4 + i] = gk1[i];
+  for (int i = 0; i < U; ++i) {
+    lds.sums[slot][2 * U * l.lr + i] = g0[i];
+    lds.sums[slot][2 * U * l.lr + U + i] = g1[i];
   }
   __syncthreads();
-  for (int q = int(threadIdx.x); q < 2 * 8 * G; q += kThreads) {
-    const int which = q / (8 * G), at = q % (8 * G);
+  float* partial = p.partial + (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * p.d;
+  for (int q = int(threadIdx.x); q < 2 * U * G; q += kThreads) {
     float s = 0.0f;
-    for (int i = 0; i < kThreads / G; ++i) s += sums[i][which][at];
-    const Units w = units_of(p, at / 8);
-    int col = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (at % 8 == i) col = w.first[i];
-      if (at % 8 == 4 + i) col = w.second[i];
-    }
-    if (col < p.d) p.partial[(int64_t(blockIdx.x) * 2 + which) * p.d + col] = s;
+    for (int i = 0; i < kSlots; ++i) s += lds.sums[i][q];
+    const L w(p, q / (2 * U));
+    const int i = q % U, col = q % (2 * U) < U ? w.first(i) : w.second(i);
+    if (col < p.d) partial[col] = s;
   }
 }
 
-// The workgroups' partial weight gradients, in their order: one workgroup a 64 columns.
+// The workgroups' partial sums, in a fixed order: a workgroup takes 4 columns, kSumRows partial sums at once.
 __global__ __launch_bounds__(kThreads) void weight_sum(HrParams p, int groups) {
-  __shared__ float l[kThreads / 64][64];
-  const int which = blockIdx.y, lane = int(threadIdx.x) & 63, part = int(threadIdx.x) >> 6;
-  const int col = int(blockIdx.x) * 64 + lane;
+  __shared__ float l[kSumRows][4];
+  const int which = blockIdx.y, c = int(threadIdx.x) & 3, part = int(threadIdx.x) >> 2;
+  const int col = int(blockIdx.x) * 4 + c;
   float* to = which ? p.gkw : p.gqw;
   if (!to) return;
+  const float* from = p.partial + int64_t(which) * groups * p.d;
   float s = 0.0f;
-  if (col < p.d)
-    for (int i = part; i < groups; i += kThreads / 64) s += p.partial[(int64_t(i) * 2 + which) * p.d + col];
-  l[part][lane] = s;
+  if (col < p.d) {
+#pragma unroll 4
+    for (int i = part; i < groups; i += kSumRows) s += from[int64_t(i) * p.d + col];
+  }
+  l[part][c] = s;
   __syncthreads();
-  if (part == 0 && col < p.d) {
-    for (int i = 1; i < kThreads / 64; ++i) s += l[i][lane];
-    to[col] = s;
+  for (int d = kSumRows / 2; d > 0; d /= 2) {
+    if (part < d) l[part][c] += l[part + d][c];
+    __syncthreads();
   }
+  if (part == 0 && col < p.d) to[col] = l[0][c];
 }
 
-int lanes_of(int d) {
-  const int need = ((d + 1) / 2 + 3) / 4;
-  int g = 4;
-  while (g < need) g *= 2;
-  return g;
+// Tokens of a workgroup at a time: about 256 rows, but four workgroups a compute unit where there are so many.
+int tokens_of(int64_t all, int heads) {
+  const int64_t rows = std::max<int64_t>(1, 256 / std::max(heads, 1));
+  const int64_t spread = std::max<int64_t>(1, all / (4 * device_cu_count()));
+  return int(std::min<int64_t>({rows, spread, kMostTokens}));
 }
 
-int tokens_of(const HrParams& p) { return int64_t(p.B) * p.T >= 2048 ? kTokens : 1; }
+int64_t groups_of(const HrParams& p) {
+  const int64_t all = int64_t(p.B) * p.T;
+  return std::max((all + p.tokens_q - 1) / p.tokens_q, (all + p.tokens_k - 1) / p.tokens_k);
+}
+
+HrParams with_tokens(const HrParams& given) {
+  HrParams p = given;
+  const int64_t all = int64_t(p.B) * p.T;
+  p.tokens_q = tokens_of(all, p.hq);
+  p.tokens_k = tokens_of(all, p.hk);
+  return p;
+}
+
+template <bool BF, int G, bool WIDE>
+void launch_rows(const HrParams& p, dim3 grid, bool gradient, hipStream_t stream) {
+  if (gradient) rotate_backward<BF, G, WIDE><<<grid, kThreads, 0, stream>>>(p);
+  else rotate_forward<BF, G, WIDE><<<grid, kThreads, 0, stream>>>(p);
+}
+
+template <bool BF, int G>
+void launch_lanes(const HrParams& p, dim3 grid, bool gradient, hipStream_t stream) {
+  constexpr int U = El<BF>::U;
+  // 16-byte pieces: aligned rows, and no lane whose units lie on both sides of the turned half
+  bool wide = p.q.vec && (p.hk == 0 || p.k.vec) && p.d % U == 0 && (p.neighbours || p.rot / 2 % U == 0);
+  if (gradient) wide = wide && p.gq.vec && (p.hk == 0 || p.gk.vec);
+  if (wide) launch_rows<BF, G, true>(p, grid, gradient, stream);
+  else launch_rows<BF, G, false>(p, grid, gradient, stream);
+}
 
 template <bool BF>
-hipError_t forward(const HrParams& p, hipStream_t stream) {
-  const int tokens = tokens_of(p);
-  const unsigned grid = unsigned((int64_t(p.B) * p.T + tokens - 1) / tokens);
-  if (grid == 0) return hipSuccess;
-  switch (lanes_of(p.d)) {
-    case 4: rotate_forward<BF, 4><<<grid, kThreads, 0, stream>>>(p, tokens); break;
-    case 8: rotate_forward<BF, 8><<<grid, kThreads, 0, stream>>>(p, tokens); break;
-    case 16: rotate_forward<BF, 16><<<grid, kThreads, 0, stream>>>(p, tokens); break;
-    default: rotate_forward<BF, 32><<<grid, kThreads, 0, stream>>>(p, tokens); break;
-  }
-  return hipGetLastError();
-}
-
-template <bool BF>
-hipError_t backward(const HrParams& p, hipStream_t stream) {
-  const int tokens = tokens_of(p), grid = head_rotate_backward_groups(p);
-  const int64_t groups = (int64_t(p.B) * p.T + tokens - 1) / tokens;
-  if (groups > 0) switch (lanes_of(p.d)) {
-    case 4: rotate_backward<BF, 4><<<grid, kThreads, 0, stream>>>(p, tokens, groups); break;
-    case 8: rotate_backward<BF, 8><<<grid, kThreads, 0, stream>>>(p, tokens, groups); break;
-    case 16: rotate_backward<BF, 16><<<grid, kThreads, 0, stream>>>(p, tokens, groups); break;
-    default: rotate_backward<BF, 32><<<grid, kThreads, 0, stream>>>(p, tokens, groups); break;
-  }
-  if (p.gqw || p.gkw) weight_sum<<<dim3((p.d + 63) / 64, 2), kThreads, 0, stream>>>(p, grid);
-  return hipGetLastError();
+void launch_width(const HrParams& p, dim3 grid, bool gradient, hipStream_t stream) {
+  const int need = ((p.d + 1) / 2 + El<BF>::U - 1) / El<BF>::U;
+  if (need <= 2) launch_lanes<BF, 2>(p, grid, gradient, stream);
+  else if (need <= 4) launch_lanes<BF, 4>(p, grid, gradient, stream);
+  else if (need <= 8) launch_lanes<BF, 8>(p, grid, gradient, stream);
+  else if (need <= 16) launch_lanes<BF, 16>(p, grid, gradient, stream);
+  else if constexpr (!BF) launch_lanes<BF, 32>(p, grid, gradient, stream);
 }
 
 }  // namespace
 
-int head_rotate_backward_groups(const HrParams& p) {
-  const int tokens = tokens_of(p);
-  const int64_t groups = (int64_t(p.B) * p.T + tokens - 1) / tokens;
-  return int(std::min<int64_t>(groups, 4 * int64_t(device_cu_count())));
+int head_rotate_backward_groups(const HrParams& given) {
+  return int(std::min<int64_t>(groups_of(with_tokens(given)), 4 * int64_t(device_cu_count())));
 }
 
-hipError_t launch_head_rotate(const HrParams& p, hipStream_t stream) {
-  return p.bf16 ? forward<true>(p, stream) : forward<false>(p, stream);
+hipError_t launch_head_rotate(const HrParams& given, hipStream_t stream) {
+  const HrParams p = with_tokens(given);
+  const dim3 grid(unsigned(groups_of(p)), p.hk > 0 ? 2 : 1);
+  if (p.bf16) launch_width<true>(p, grid, false, stream);
+  else launch_width<false>(p, grid, false, stream);
+  return hipGetLastError();
 }
 
-hipError_t launch_head_rotate_backward(const HrParams& p, hipStream_t stream) {
-  return p.bf16 ? backward<true>(p, stream) : backward<false>(p, stream);
+hipError_t launch_head_rotate_backward(const HrParams& given, hipStream_t stream) {
+  const HrParams p = with_tokens(given);
+  const int groups = head_rotate_backward_groups(p);
+  if (groups > 0) {
+    const dim3 grid(unsigned(groups), 2);
+    if (p.bf16) launch_width<true>(p, grid, true, stream);
+    else launch_width<false>(p, grid, true, stream);
+  }
+  if (p.gqw || p.gkw) weight_sum<<<dim3((p.d + 3) / 4, 2), kThreads, 0, stream>>>(p, groups);
+  return hipGetLastError();
 }
 
 }  // namespace sx

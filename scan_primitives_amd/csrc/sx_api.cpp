@@ -1615,8 +1615,8 @@ struct RotateArgs {
   int neighbours;
 };
 
-sx_status plan_rotate(const char* op, sx_dtype dtype, const RotateArgs& a, bool gradient, sx::HrParams* p) {
-  if (!dtype_ok(dtype))
+sx_status plan_rotate(const char* op, const sx_dtype& dtype, const RotateArgs& a, bool gradient, sx::HrParams* p) {
+  if (!dtype_ok(dtype))  // a reference: a code out of range must not be read as the enum
     return fail(SX_E_DIM_002, "%s: q and k must be f32 or bf16 (dtype code %d)", op, enum_code(dtype));
   for (const HeadArg* x : {&a.q, &a.k}) {
     int64_t n;
@@ -1647,11 +1647,12 @@ sx_status plan_rotate(const char* op, sx_dtype dtype, const RotateArgs& a, bool 
   p->d = int(d);
   p->rot = int(a.rotated);
   const size_t e = dtype == SX_BF16 ? 2 : 4;
-  p->q = head_view(a.q, e, qs[2], 8);
-  p->k = head_view(a.k, e, ks[2], 8);
+  const int64_t piece = 16 / int64_t(e);
+  p->q = head_view(a.q, e, qs[2], piece);
+  p->k = head_view(a.k, e, ks[2], piece);
   if (gradient) {
-    p->gq = head_view(a.gq, e, qs[2], 8);
-    p->gk = head_view(a.gk, e, ks[2], 8);
+    p->gq = head_view(a.gq, e, qs[2], piece);
+    p->gk = head_view(a.gk, e, ks[2], piece);
   }
   p->positions = a.positions;
   p->pos64 = a.positions_i64 ? 1 : 0;
@@ -1716,14 +1717,14 @@ sx_status sx_head_norm_rotate(sx_dtype dtype, const int64_t* q_shape, const int6
   return device_status(sx::launch_head_rotate(p, static_cast<hipStream_t>(stream)), "head-norm-rotate launch");
 }
 
-size_t sx_head_norm_rotate_backward_workspace_bytes(const int64_t* q_shape) {
-  int64_t n;
-  if (!q_shape || !checked_numel(4, q_shape, &n) || q_shape[0] > kMostTokens || q_shape[1] > kMostTokens ||
-      q_shape[0] * q_shape[1] > kMostTokens || q_shape[3] > kMostHeadWidth)
-    return 0;
-  sx::HrParams p{};
-  p.B = int(q_shape[0]);
-  p.T = int(q_shape[1]);
+size_t sx_head_norm_rotate_backward_workspace_bytes(const int64_t* q_shape, const int64_t* k_shape) {
+  RotateArgs a{};
+  a.q.name = "q";
+  a.q.shape = q_shape;
+  a.k.name = "k";
+  a.k.shape = k_shape;
+  sx::HrParams p;
+  if (plan_rotate("head-norm-rotate gradient", SX_F32, a, false, &p) != SX_OK) return 0;
   return size_t(sx::head_rotate_backward_groups(p)) * 2 * size_t(q_shape[3]) * sizeof(float);
 }
 
@@ -1752,7 +1753,7 @@ sx_status sx_head_norm_rotate_backward(sx_dtype dtype, const int64_t* q_shape, c
                      flat_span("grad_k_weight", grad_k_weight, int64_t(p.d) * 4)};
   if ((st = rotate_overlap(op, a, p, to, 4)) != SX_OK) return st;
   if (grad_q_weight || grad_k_weight) {
-    const size_t need = sx_head_norm_rotate_backward_workspace_bytes(q_shape);
+    const size_t need = sx_head_norm_rotate_backward_workspace_bytes(q_shape, k_shape);
     if ((st = check_workspace(op, workspace, workspace_bytes, need)) != SX_OK) return st;
   }
   if (nq + nk == 0 && !grad_q_weight && !grad_k_weight) return ok();

@@ -133,9 +133,10 @@ struct HrParams {
   int bf16;
   void* out_q;          // contiguous [B, T, heads, d]: results, or gradients of q and k
   void* out_k;
-  float* partial;       // backward: [workgroups][2][d]
+  float* partial;       // backward: [2][workgroups][d]
   float* gqw;           // [d] or nullptr
   float* gkw;
+  int tokens_q, tokens_k;  // tokens of a workgroup at a time (set by the launch)
 };
 int head_rotate_backward_groups(const HrParams& p);
 hipError_t launch_head_rotate(const HrParams& p, hipStream_t stream);
