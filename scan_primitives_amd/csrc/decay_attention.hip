@@ -21,6 +21,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ms_mfma.hpp"
 #include "sx_attention.hpp"
@@ -29,8 +30,7 @@
 namespace sx {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
+constexpr int kThreads = 256;  // of the kernels beside the marches
 // Log decays are taken into [-200, 200]: exp(-200) is zero and exp(200) infinite in
 // f32, so the results are those of the whole range, and -inf leaves no inf - inf.
 constexpr float kMostLog = 200.0f;
@@ -40,60 +40,75 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 template <bool BF>
 struct Op;
 
-// bf16 operands. A Frag is four values along the contraction at one row (or
-// column), a Pair two of them (one per 16-wide tile): v_mfma_f32_16x16x32_bf16
-// contracts both tiles at once. Its own order of the 32 does not matter, as
-// both operands use the same one.
+// bf16 operands. A Pair is what a lane brings to a product contracted over 32:
+// the eight values 8g .. 8g + 7 of its row (or column) in lane group g, on
+// v_mfma_f32_16x16x32_bf16. The instruction's own order of the 32 does not
+// matter, as both operands use the same one.
 template <>
 struct Op<true> {
   using E = uint16_t;
   using Pair = uint4;
   static constexpr int C = 64;      // tokens a chunk
   static constexpr int kPiece = 8;  // elements of a 16-byte piece
-  static constexpr int kPad = 8;
   // f32 values enter a product as bf16 parts: three carry all 24 bits, two carry
-  // 16, enough where the result is rounded to bf16 (8 bits) on store.
+  // 17, enough where the result is rounded to bf16 (8 bits) on store.
   static constexpr int kState = 3;
+  static constexpr int kRead = 2;
   static constexpr int kScore = 2;
   static __device__ __forceinline__ f32x4 mma(Pair a, Pair b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                    0, 0);
   }
-  // NP parts of eight f32 values (truncated to bf16 one after the other; the last
-  // of three is what is left, exactly).
+  // NP parts of eight f32 values. Of three, each but the last is truncated and the last is what is
+  // left, exactly; of two, both are rounded to nearest, 2^-18 of the value off at most.
   template <int NP>
   static __device__ __forceinline__ void split(f32x4 a, f32x4 b, Pair (&out)[NP]) {
     float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    uint32_t w[4];
+    if constexpr (NP == 2) {
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      uint32_t u[8];
+      for (int p = 0; p < 2; ++p) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        u[i] = __float_as_uint(v[i]);
-        if (p + 1 < NP) v[i] -= __uint_as_float(u[i] & 0xffff0000u);
+        for (int i = 0; i < 4; ++i) {
+          w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+          if (p == 0) {
+            v[2 * i] -= __uint_as_float(w[i] << 16);
+            v[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+          }
+        }
+        out[p] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      out[p] = make_uint4(upper_halves(u[0], u[1]), upper_halves(u[2], u[3]), upper_halves(u[4], u[5]),
-                          upper_halves(u[6], u[7]));
+    } else {
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        uint32_t u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          u[i] = __float_as_uint(v[i]);
+          if (p + 1 < NP) v[i] -= __uint_as_float(u[i] & 0xffff0000u);
+        }
+        out[p] = make_uint4(upper_halves(u[0], u[1]), upper_halves(u[2], u[3]), upper_halves(u[4], u[5]),
+                            upper_halves(u[6], u[7]));
+      }
     }
   }
-  // rows 16-wide tiles t and t + 1 of the contraction, columns 4g.. of each
+  // columns 8g .. 8g + 7 of a row
   static __device__ __forceinline__ Pair row_pair(const E* row, int g) {
-    const uint2 a = *reinterpret_cast<const uint2*>(row + 4 * g);
-    const uint2 b = *reinterpret_cast<const uint2*>(row + 16 + 4 * g);
-    return make_uint4(a.x, a.y, b.x, b.y);
-  }
-  // the same 32 columns in the other order both operands may share: eight in a row a lane
-  static __device__ __forceinline__ Pair row_pair_any(const E* row, int g) {
     return *reinterpret_cast<const uint4*>(row + 8 * g);
   }
-  // contraction over rows j0 + 4g .. of tile j0 and of tile j0 + 16, at column col0 + c
-  static __device__ __forceinline__ Pair column_pair(const E* tile, int stride, int j0, int col0, int g, int c) {
+  // Rows j0 + 8g .. 8g + 7 of one column a lane, through the transposing read: lane c of a group
+  // addresses four columns of one row and receives column c of four rows. `col`: the lane's four.
+  static __device__ __forceinline__ Pair column_pair(const E* tile, int stride, int j0, int col, int g, int c) {
     typedef s16x4_t __attribute__((address_space(3))) * lds4;
-    const E* p = tile + (j0 + 4 * g + (c >> 2)) * stride + col0 + 4 * (c & 3);
+    const E* p = tile + (j0 + 8 * g + (c >> 2)) * stride + col;
     const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p)));
-    const uint2 b = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 16 * stride)));
+    const uint2 b = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 4 * stride)));
     return make_uint4(a.x, a.y, b.x, b.y);
   }
+  // what column_pair takes for 16 columns in a row from col0 on ...
+  static __device__ __forceinline__ int columns(int col0, int c) { return col0 + 4 * (c & 3); }
+  // ... and for columns 8 (c / 4) + c % 4 from col0 on: the rows of a state tile
+  static __device__ __forceinline__ int state_rows(int col0, int c) { return col0 + 8 * (c & 3); }
   static __device__ __forceinline__ f32x4 low(Pair a) {
     return f32x4{__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u), __uint_as_float(a.y << 16),
                  __uint_as_float(a.y & 0xffff0000u)};
@@ -109,7 +124,7 @@ struct Op<true> {
     return !(bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w));
   }
   // infinities and NaN taken out
-  static __device__ __forceinline__ Pair finite_part(Pair v) {
+  static __device__ __forceinline__ uint4 finite_part(uint4 v) {
     auto f = [](uint32_t u) {
       if ((u & 0x7f800000u) == 0x7f800000u) u &= 0xffffu;
       if ((u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
@@ -132,8 +147,8 @@ struct Op<false> {
   };
   static constexpr int C = 32;
   static constexpr int kPiece = 4;
-  static constexpr int kPad = 4;
   static constexpr int kState = 1;
+  static constexpr int kRead = 1;
   static constexpr int kScore = 1;
   static __device__ __forceinline__ f32x4 mma(Pair a, Pair b, f32x4 c) {
     c = mfma_16x16x16(a.a, b.a, c);
@@ -145,15 +160,15 @@ struct Op<false> {
     out[0] = Pair{a, b};
   }
   static __device__ __forceinline__ Pair row_pair(const E* row, int g) {
-    return Pair{*reinterpret_cast<const f32x4*>(row + 4 * g), *reinterpret_cast<const f32x4*>(row + 16 + 4 * g)};
+    return Pair{*reinterpret_cast<const f32x4*>(row + 8 * g), *reinterpret_cast<const f32x4*>(row + 8 * g + 4)};
   }
-  static __device__ __forceinline__ Pair row_pair_any(const E* row, int g) { return row_pair(row, g); }
-  static __device__ __forceinline__ Pair column_pair(const E* tile, int stride, int j0, int col0, int g, int c) {
-    const E* p = tile + (j0 + 4 * g) * stride + col0 + c;
-    const E* q = p + 16 * stride;
+  static __device__ __forceinline__ Pair column_pair(const E* tile, int stride, int j0, int col, int g, int c) {
+    const E* p = tile + (j0 + 8 * g) * stride + col;
     return Pair{f32x4{p[0], p[stride], p[2 * stride], p[3 * stride]},
-                f32x4{q[0], q[stride], q[2 * stride], q[3 * stride]}};
+                f32x4{p[4 * stride], p[5 * stride], p[6 * stride], p[7 * stride]}};
   }
+  static __device__ __forceinline__ int columns(int col0, int c) { return col0 + c; }
+  static __device__ __forceinline__ int state_rows(int col0, int c) { return col0 + 8 * (c >> 2) + (c & 3); }
   static __device__ __forceinline__ f32x4 low(Pair a) { return a.a; }
   static __device__ __forceinline__ f32x4 high(Pair a) { return a.b; }
   static __device__ __forceinline__ f32x4 four(const E* p) { return *reinterpret_cast<const f32x4*>(p); }
@@ -162,45 +177,64 @@ struct Op<false> {
     auto bad = [](uint32_t u) { return (u & 0x7f800000u) == 0x7f800000u; };
     return !(bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w));
   }
-  static __device__ __forceinline__ Pair finite_part(Pair v) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if ((__float_as_uint(v.a[i]) & 0x7f800000u) == 0x7f800000u) v.a[i] = 0.0f;
-      if ((__float_as_uint(v.b[i]) & 0x7f800000u) == 0x7f800000u) v.b[i] = 0.0f;
-    }
-    return v;
+  static __device__ __forceinline__ uint4 finite_part(uint4 v) {
+    auto f = [](uint32_t u) { return (u & 0x7f800000u) == 0x7f800000u ? 0u : u; };
+    return make_uint4(f(v.x), f(v.y), f(v.z), f(v.w));
   }
   static __device__ __forceinline__ void put4(E* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
   static __device__ __forceinline__ E round(float v) { return v; }
 };
 
-template <bool BF, int NKT, int NV>
+// W waves hold a state of up to 16 NKT rows and 16 NV W columns.
+template <bool BF, int NKT, int NV, int W>
 struct Shape {
   using O = Op<BF>;
   using E = typename O::E;
+  static constexpr int kThreads = W * kWave;
   static constexpr int C = O::C, CT = C / 16;
-  static constexpr int DX = 16 * NKT;       // widest x and y
-  static constexpr int BV = 64 * NV;        // columns of z a workgroup holds: 16 NV a wave
-  static constexpr int SX = DX + O::kPad, SZ = BV + O::kPad, SP = C + O::kPad;
-  static constexpr int NX = C * DX / O::kPiece / kThreads;  // 16-byte pieces a thread of a tile
-  static constexpr int NZ = C * BV / O::kPiece / kThreads;
-  struct Lds {
-    alignas(16) E x[C * SX];
-    alignas(16) E y[C * SX];
-    alignas(16) E z[C * SZ];
-    alignas(16) E score[O::kScore][C * SP];
-    alignas(16) E w[C * SZ];
-    float pairs[C * (C + 1)];
+  static constexpr int TILES = CT * (CT + 1) / 2;  // tiles of scores on and on one side of the diagonal
+  static constexpr int DX = 16 * NKT;              // widest x and y
+  static constexpr int BV = 16 * NV * W;           // columns of z a workgroup holds: 16 NV a wave
+  // Row strides in elements. Tiles read by rows alone: 4 banks past a multiple of 64 bytes, so 16 rows
+  // meet no bank twice; those read by columns too: 12 past (bf16), which spreads the four rows of a
+  // transposing read as well.
+  static constexpr int kRowPad = O::kPiece, kColPad = BF ? 24 : 4;
+  static constexpr int SX = DX + kRowPad, SY = DX + kColPad, SZ = BV + kColPad, SW = BV + kRowPad, SP = C + kRowPad;
+  static constexpr int NX = (C * DX / O::kPiece + kThreads - 1) / kThreads;  // 16-byte pieces a thread of a tile
+  static constexpr int NZ = (C * BV / O::kPiece + kThreads - 1) / kThreads;
+  struct Decays {
     alignas(16) float2 g[C];   // running log2 decay, high and low part
     alignas(16) float row[C];  // decay between the row and the state
     alignas(16) float src[C];  // decay between the source and the next state, times scale_src
-    float part[kWaves][C];
-    float rect[kThreads];
     float total;
-    int odd[2];                // a chunk's z holds an infinity or NaN
   };
-  static_assert(NX >= 1 && NZ >= 1, "tiles smaller than a workgroup");
+  struct Local {  // what a segment's own state takes
+    alignas(16) E y[C * SY];
+    alignas(16) E z[C * SZ];
+    Decays dec[2];
+    int odd[2];   // a chunk's z holds an infinity or NaN
+  };
+  struct Out : Local {
+    alignas(16) E x[C * SX];
+    alignas(16) E score[O::kScore][C * SP];
+  };
+  struct Mass : Out {
+    alignas(16) E w[C * SW];
+    float part[2][W][C];        // a wave's columns of the rows against the state, and w
+    float row_tile[2][CT][C];   // pairs of a row with the sources of a tile, summed
+    float col_tile[2][TILES][16];  // pairs of a tile with their source before the column and their row from it on
+    double cross[W];
+  };
+  template <bool OUT, int MASS>
+  using Lds = std::conditional_t<MASS != 0, Mass, std::conditional_t<OUT, Out, Local>>;
 };
+
+// The same value, as if new: what is formed from it is formed where it is used, not
+// ahead of the loop around it, where it would hold registers through every chunk.
+__device__ __forceinline__ int anew(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
 
 // Base of head h of batch row b, at token 0.
 template <typename E>
@@ -210,18 +244,20 @@ __device__ __forceinline__ const E* head_base(const HeadView& v, int b, int h) {
 
 // A thread's pieces of the tile of C tokens from tb and W columns from c0; zero
 // where a token (from `end` on) or a column (from `d` on) does not exist.
-template <bool BF, int W, int N>
+template <bool BF, int W, int THREADS, int N>
 __device__ __forceinline__ void load_tile(const HeadView& v, const typename Op<BF>::E* base, int d, int c0, int tb,
                                           int end, uint4 (&r)[N]) {
   using E = typename Op<BF>::E;
   constexpr int P = Op<BF>::kPiece, PR = W / P;
+  const E* at = base + int64_t(tb) * v.st;
+  const int tid = anew(int(threadIdx.x));
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    const int q = int(threadIdx.x) + n * kThreads;
-    const int t = tb + q / PR, col = c0 + q % PR * P;
+    const int q = tid + n * THREADS;
+    const int t = q / PR, col = c0 + q % PR * P;
     r[n] = make_uint4(0, 0, 0, 0);
-    if (t < end && col < d) {
-      const E* p = base + int64_t(t) * v.st + int64_t(col) * v.sd;
+    if (tb + t < end && t < Op<BF>::C && col < d) {
+      const E* p = at + int64_t(t) * v.st + int64_t(col) * v.sd;
       if (v.vec) {
         r[n] = *reinterpret_cast<const uint4*>(p);
       } else {
@@ -239,39 +275,75 @@ __device__ __forceinline__ void load_tile(const HeadView& v, const typename Op<B
   }
 }
 
-template <bool BF, int W, int N>
+template <bool BF, int W, int THREADS, int N>
 __device__ __forceinline__ void store_tile(typename Op<BF>::E* tile, int stride, const uint4 (&r)[N]) {
   constexpr int P = Op<BF>::kPiece, PR = W / P;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    const int q = int(threadIdx.x) + n * kThreads;
-    *reinterpret_cast<uint4*>(tile + q / PR * stride + q % PR * P) = r[n];
+    const int q = int(threadIdx.x) + n * THREADS;
+    if (Op<BF>::C * PR % THREADS == 0 || q < Op<BF>::C * PR)
+      *reinterpret_cast<uint4*>(tile + q / PR * stride + q % PR * P) = r[n];
   }
-}
-
-__device__ __forceinline__ double shfl_up_f64(double v, int d) {
-  const long long u = __double_as_longlong(v);
-  const int lo = __shfl_up(int(uint32_t(u)), d), hi = __shfl_up(int(u >> 32), d);
-  return __longlong_as_double((static_cast<long long>(hi) << 32) | uint32_t(lo));
 }
 
 __device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2f(v); }
 
-// A chunk's decays from a lane's log decay gv (wave 0; token tb + lane).
-template <bool REV, int C, typename Lds>
-__device__ __forceinline__ void chunk_decays(Lds& l, float gv, float scale_src, int lane) {
+// v of the lane that CTRL names (DPP), zero where there is none
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const long long u = __double_as_longlong(v);
+  const int lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(u)), CTRL, 0xF, 0xF, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, int(u >> 32), CTRL, 0xF, 0xF, false);
+  return __longlong_as_double((static_cast<long long>(hi) << 32) | uint32_t(lo));
+}
+__device__ __forceinline__ float lane_of(float v, int i) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i));
+}
+__device__ __forceinline__ double lane_of(double v, int i) {
+  const long long u = __double_as_longlong(v);
+  const int lo = __builtin_amdgcn_readlane(int(uint32_t(u)), i), hi = __builtin_amdgcn_readlane(int(u >> 32), i);
+  return __longlong_as_double((static_cast<long long>(hi) << 32) | uint32_t(lo));
+}
+
+// Sum of the lanes up to this one.
+template <typename T>
+__device__ __forceinline__ T prefix_sum(T v, int lane) {
+  v += dpp<0x111>(v);
+  v += dpp<0x112>(v);
+  v += dpp<0x114>(v);
+  v += dpp<0x118>(v);
+  const T a = lane_of(v, 15), b = a + lane_of(v, 31), c = b + lane_of(v, 47);
+  return lane < 16 ? v : v + (lane < 32 ? a : lane < 48 ? b : c);
+}
+// Sum of the lanes from this one on.
+__device__ __forceinline__ float suffix_sum(float v, int lane) {
+  v += dpp<0x101>(v);
+  v += dpp<0x102>(v);
+  v += dpp<0x104>(v);
+  v += dpp<0x108>(v);
+  const float c = lane_of(v, 48), b = lane_of(v, 32) + c, a = lane_of(v, 16) + b;
+  return lane >= 48 ? v : v + (lane >= 32 ? c : lane >= 16 ? b : a);
+}
+// Sum over the 16 lanes of a group, in its last lane.
+__device__ __forceinline__ float group_sum(float v) {
+  v += dpp<0x111>(v);
+  v += dpp<0x112>(v);
+  v += dpp<0x114>(v);
+  return v + dpp<0x118>(v);
+}
+
+// A chunk's decays from a lane's log decay gv (one wave; token tb + lane).
+template <bool REV, int C, typename Decays>
+__device__ __forceinline__ void chunk_decays(Decays& l, float gv, float scale_src, int lane) {
   gv = gv < -kMostLog ? -kMostLog : gv > kMostLog ? kMostLog : gv;
   // 64 bits: the difference of two running sums is the log decay between two tokens, and has to be
   // exact to f32 also behind a token that cut the state.
-  double s = double(gv) * 1.4426950408889634;
-#pragma unroll
-  for (int d = 1; d < C; d *= 2) {
-    const double u = shfl_up_f64(s, d);
-    if (lane >= d) s += u;
-  }
-  const long long all = __double_as_longlong(s);
-  const int tlo = __shfl(int(uint32_t(all)), C - 1), thi = __shfl(int(all >> 32), C - 1);
-  const double total = __longlong_as_double((static_cast<long long>(thi) << 32) | uint32_t(tlo));
+  const double s = prefix_sum(double(gv) * 1.4426950408889634, lane);
+  const double total = lane_of(s, C - 1);
   if (lane < C) {
     const float hi = float(s);
     l.g[lane] = make_float2(hi, float(s - double(hi)));
@@ -282,16 +354,57 @@ __device__ __forceinline__ void chunk_decays(Lds& l, float gv, float scale_src, 
   }
 }
 
+// A chunk's share of the decay's gradient, from the sums its rows and pairs left (one wave).
+// MASS 1: what the rows from a token on take from the state and from sources before the token.
+// MASS 2: what the sources before it give. The sums are taken outright, not as differences of running
+// totals, so a cut leaves an exact zero.
+template <bool REV, int MASS, int CT, int TILES, typename Lds>
+__device__ __forceinline__ void chunk_mass(const DaParams& p, const DaMarch& m, const Lds& l, int buf, int waves,
+                                           int tb, int t1, int cb, int bh, int lane) {
+  constexpr int C = 16 * CT;
+  const int64_t mb = int64_t(cb) * p.B * p.H + bh;
+  float v = 0.0f;
+  if (lane < C)
+    for (int q = 0; q < waves; ++q) v += l.part[buf][q][lane];
+  float mine, all;
+  if constexpr (MASS == 1) {
+    mine = suffix_sum(v, lane);
+    all = lane_of(mine, 0);
+    // pairs: the sources of whole tiles before the token's own ...
+    float before = 0.0f;
+#pragma unroll
+    for (int bt = 1; bt < CT; ++bt) {
+      if (lane < C) before += l.row_tile[buf][bt - 1][lane];
+      const float s = suffix_sum(lane >= 16 * bt ? before : 0.0f, lane);
+      if (lane / 16 == bt) mine += s;
+    }
+    // ... and those of its own
+    if (lane < C) {
+      const int bt = lane / 16;
+      for (int it = bt; it < CT; ++it) mine += l.col_tile[buf][it * (it + 1) / 2 + bt][lane % 16];
+    }
+  } else {
+    const float run = prefix_sum(v, lane);
+    all = lane_of(run, C - 1);
+    mine = __shfl_up(run, 1);
+    if (lane == 0) mine = 0.0f;
+  }
+  const int tok = tb + lane;
+  if (lane < C && tok < t1) m.mass[mb * p.T + tok] = mine;
+  if (lane == 0) m.mass_chunk[mb * ((p.T + C - 1) / C) + tb / C] = all;
+}
+
 // One workgroup's march. MASS: 0 none, 1 the rows' part of the decay's gradient
 // (forward), 2 the sources' part (reverse). OUT false: the segment's own state only.
-template <bool BF, int NKT, int NV, bool REV, int MASS, bool OUT>
+template <typename S, bool BF, int NKT, int NV, int W, bool REV, int MASS, bool OUT>
 __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int block,
-                                      typename Shape<BF, NKT, NV>::Lds& l) {
-  using S = Shape<BF, NKT, NV>;
+                                      typename S::template Lds<OUT, MASS>& l) {
   using O = Op<BF>;
   using E = typename O::E;
   using Pair = typename O::Pair;
-  constexpr int C = S::C, CT = S::CT;
+  constexpr int C = S::C, CT = S::CT, THREADS = S::kThreads;
+  constexpr int kRead = MASS == 0 ? O::kRead : O::kState;  // the decay's gradient is f32
+  constexpr int kDecayWave = W - 1, kMassWave = W - 2;     // they have the fewest tiles of scores
   const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
 
   const int ncb = (m.dz + S::BV - 1) / S::BV, BH = p.B * p.H;
@@ -302,10 +415,10 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
   const int t0 = seg * p.seg_tokens, t1 = min(p.T, t0 + p.seg_tokens);
   int len = p.T;
   if (p.lengths) len = min(max(p.lengths[b], 0), p.T);
-  const int live = max(min(len, t1) - t0, 0);
+  const int live = max(min(len, t1) - t0, 0), end = min(len, t1);
   const int nc = (live + C - 1) / C;
   const int c0 = cb * S::BV, wc0 = 16 * NV * wave;  // first column of the workgroup, and of the wave within it
-  const int nkt = (m.dx + 15) / 16;                 // tiles of x that exist
+  const int nk2 = (m.dx + 31) / 32;                 // pairs of tiles of x that exist
   const int64_t state = int64_t(p.dk) * p.dv;
 
   const E* xb = OUT ? head_base<E>(m.x, b, h) : nullptr;
@@ -314,7 +427,9 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
   const E* wb = MASS ? head_base<E>(m.w, b, h) : nullptr;
   const float* gb = p.g + int64_t(b) * p.gb + int64_t(h) * p.gh;
 
-  // The state: tile kt, rows 16 kt + 4 g + r, column c0 + wc0 + 16 n + c.
+  // The state: tile kt holds rows 32 (kt / 2) + 8 g + 4 (kt % 2) + r, column c0 + wc0 + 16 n + c, so that the
+  // rows of a lane in two tiles are eight in a row, the order of a Pair.
+  auto state_row = [&](int kt, int r) { return 32 * (kt / 2) + 8 * g + 4 * (kt % 2) + r; };
   f32x4 st[NKT][NV];
   {
     const float* from = !OUT ? nullptr : seg_m == 0 ? (m.first ? m.first + bh * state : nullptr)
@@ -325,48 +440,89 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       for (int n = 0; n < NV; ++n)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int row = 16 * kt + 4 * g + r, col = c0 + wc0 + 16 * n + c;
+          const int row = state_row(kt, r), col = c0 + wc0 + 16 * n + c;
           st[kt][n][r] = from && row < m.dx && col < m.dz ? from[row * m.sr + col * m.sc] : 0.0f;
         }
   }
 
   uint4 rx[OUT ? S::NX : 1], ry[S::NX], rz[S::NZ], rw[MASS ? S::NZ : 1];
   float rg = 0.0f;
+  auto first_token = [&](int ci) { return t0 + (REV ? nc - 1 - ci : ci) * C; };
   auto fetch = [&](int ci) {
-    const int tb = t0 + (REV ? nc - 1 - ci : ci) * C, end = min(len, t1);
-    if constexpr (OUT) load_tile<BF, S::DX>(m.x, xb, m.dx, 0, tb, end, rx);
-    load_tile<BF, S::DX>(m.y, yb, m.dx, 0, tb, end, ry);
-    load_tile<BF, S::BV>(m.z, zb, m.dz, c0, tb, end, rz);
-    if constexpr (MASS != 0) load_tile<BF, S::BV>(m.w, wb, m.dz, c0, tb, end, rw);
-    if (wave == 0) rg = lane < C && tb + lane < end ? gb[int64_t(tb + lane) * p.gt] : 0.0f;
+    const int tb = first_token(ci);
+    if constexpr (OUT) load_tile<BF, S::DX, THREADS>(m.x, xb, m.dx, 0, tb, end, rx);
+    load_tile<BF, S::DX, THREADS>(m.y, yb, m.dx, 0, tb, end, ry);
+    load_tile<BF, S::BV, THREADS>(m.z, zb, m.dz, c0, tb, end, rz);
+    if constexpr (MASS != 0) load_tile<BF, S::BV, THREADS>(m.w, wb, m.dz, c0, tb, end, rw);
+  };
+  auto fetch_decay = [&](int ci) {
+    const int t = first_token(ci) + lane;
+    rg = lane < C && t < end ? gb[int64_t(t) * p.gt] : 0.0f;
   };
 
+  if (nc > 0) {
+    fetch(0);
+    if (wave == kDecayWave) fetch_decay(0);
+  }
+  if constexpr (MASS == 1) {
+    // What the decays behind an earlier segment carry in all: the state against its adjoint, both in
+    // memory at the segment's start. Between here and its end the carried sum is kept by differences.
+    if (seg_m > 0) {
+      const float* adj = p.m[1].seg + (int64_t(p.segments - 1 - seg_m) * BH + bh) * state;
+      double s = 0.0;
+#pragma unroll
+      for (int kt = 0; kt < NKT; ++kt)
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = state_row(kt, r), col = c0 + wc0 + 16 * n + c;
+            if (row < m.dx && col < m.dz) s += double(st[kt][n][r]) * double(adj[row * m.sr + col * m.sc]);
+          }
+      s = lane_of(prefix_sum(s, lane), 63);
+      if (lane == 0) l.cross[wave] = s;
+      __syncthreads();
+      if (tid == 0) {
+        s = 0.0;
+        for (int i = 0; i < W; ++i) s += l.cross[i];
+        m.cross[(int64_t(cb) * BH + bh) * p.segments + seg] = s;
+      }
+    }
+  }
   if (tid < 2) l.odd[tid] = 0;
   float decays = 1.0f;
-  if (nc > 0) fetch(0);
+  if (nc > 0 && wave == kDecayWave) {
+    chunk_decays<REV, C>(l.dec[0], rg, m.scale_src, lane);
+    if (nc > 1) fetch_decay(1);
+  }
   for (int ci = 0; ci < nc; ++ci) {
-    const int chunk = REV ? nc - 1 - ci : ci, tb = t0 + chunk * C;
+    const int tb = first_token(ci);
+    typename S::Decays& dec = l.dec[ci & 1];
     __syncthreads();
-    if constexpr (OUT) store_tile<BF, S::DX>(l.x, S::SX, rx);
-    store_tile<BF, S::DX>(l.y, S::SX, ry);
-    store_tile<BF, S::BV>(l.z, S::SZ, rz);
-    if constexpr (MASS != 0) store_tile<BF, S::BV>(l.w, S::SZ, rw);
+    if constexpr (OUT) store_tile<BF, S::DX, THREADS>(l.x, S::SX, rx);
+    store_tile<BF, S::DX, THREADS>(l.y, S::SY, ry);
     if constexpr (OUT) {
+      // An infinity or NaN in z times a score of zero would reach rows that do not see its token: such
+      // values are left out of the products and added at the end to what does see it.
       bool fine = true;
 #pragma unroll
       for (int n = 0; n < S::NZ; ++n) fine = fine && O::finite(rz[n]);
-      if (!fine) l.odd[ci & 1] = 1;
+      if (__builtin_expect(!fine, 0)) {
+        l.odd[ci & 1] = 1;
+#pragma unroll
+        for (int n = 0; n < S::NZ; ++n) rz[n] = O::finite_part(rz[n]);
+      }
     }
-    if (wave == 0) chunk_decays<REV, C>(l, rg, m.scale_src, lane);
+    store_tile<BF, S::BV, THREADS>(l.z, S::SZ, rz);
+    if constexpr (MASS != 0) store_tile<BF, S::BV, THREADS>(l.w, S::SW, rw);
     __syncthreads();
     if (ci + 1 < nc) fetch(ci + 1);
-    const bool odd = OUT && l.odd[ci & 1] != 0;
-    const float total = l.total;
+    const float total = dec.total;
 
     f32x4 acc[OUT ? NV : 1][OUT ? CT : 1];  // out transposed: column wc0 + 16 n + 4 g + r, row 16 it + c
     if constexpr (OUT) {
       // scores: the tiles on and on one side of the diagonal, in turn over the waves, as [row][source]
-      for (int q = wave; q < CT * (CT + 1) / 2; q += kWaves) {
+      for (int q = wave; q < S::TILES; q += W) {
         int hi = 0, lo = q;
         while (lo > hi) lo -= ++hi;
         const int it = REV ? lo : hi, jt = REV ? hi : lo;
@@ -374,14 +530,14 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
         f32x4 s = zero4();
 #pragma unroll
         for (int k2 = 0; k2 < NKT / 2; ++k2)
-          if (2 * k2 < nkt)
-            s = O::mma(O::row_pair_any(l.y + (16 * jt + c) * S::SX + 32 * k2, g),
-                       O::row_pair_any(l.x + row * S::SX + 32 * k2, g), s);
-        const float2 gi = l.g[row];
+          if (k2 < nk2)
+            s = O::mma(O::row_pair(l.y + (16 * jt + c) * S::SY + 32 * k2, g),
+                       O::row_pair(l.x + row * S::SX + 32 * k2, g), s);
+        const float2 gi = dec.g[row];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int j = 16 * jt + 4 * g + r;
-          const float2 gj = l.g[j];
+          const float2 gj = dec.g[j];
           const float d = (gi.x - gj.x) + (gi.y - gj.y);
           const bool seen = REV ? j >= row : j <= row;
           s[r] = seen ? s[r] * m.scale_src * exp2_hw(REV ? -d : d) : 0.0f;
@@ -400,14 +556,35 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
           f32x4 a = zero4();
 #pragma unroll
           for (int k2 = 0; k2 < S::BV / 32; ++k2)
-            a = O::mma(O::row_pair_any(l.z + (16 * jt + c) * S::SZ + 32 * k2, g),
-                       O::row_pair_any(l.w + row * S::SZ + 32 * k2, g), a);
+            a = O::mma(O::row_pair(l.z + (16 * jt + c) * S::SZ + 32 * k2, g),
+                       O::row_pair(l.w + row * S::SW + 32 * k2, g), a);
+          float sum = 0.0f, before[4];  // of the lane's sources, and of those before each
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int j = 16 * jt + 4 * g + r;
-            l.pairs[row * (C + 1) + j] = j < row ? a[r] * s[r] * m.scale_out : 0.0f;
+            before[r] = sum;
+            sum += 16 * jt + 4 * g + r < row ? a[r] * s[r] * m.scale_out : 0.0f;
+          }
+          float to = sum, u = __shfl_up(to, 16);  // ... of the lane groups up to this one
+          if (g >= 1) to += u;
+          u = __shfl_up(to, 32);
+          if (g >= 2) to += u;
+          if (g == 3) l.row_tile[ci & 1][jt][row] = to;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float v = group_sum(16 * jt + 4 * g + r <= row ? (to - sum) + before[r] : 0.0f);
+            if (c == 15) l.col_tile[ci & 1][q][4 * g + r] = v;
           }
         }
+      }
+      if (wave == kDecayWave && ci + 1 < nc) {
+        chunk_decays<REV, C>(l.dec[(ci + 1) & 1], rg, m.scale_src, lane);
+        if (ci + 2 < nc) fetch_decay(ci + 2);
+      }
+      if constexpr (MASS != 0) {
+        if (wave == kMassWave && ci > 0)
+          chunk_mass<REV, MASS, CT, S::TILES>(p, m, l, (ci - 1) & 1, W, first_token(ci - 1), t1, cb, bh, lane);
+        if (m.chunk_decay && cb == 0 && tid == 0)
+          m.chunk_decay[int64_t(bh) * ((p.T + C - 1) / C) + tb / C] = total;
       }
 #pragma unroll
       for (int n = 0; n < NV; ++n)
@@ -416,29 +593,29 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       // rows against the state
 #pragma unroll
       for (int k2 = 0; k2 < NKT / 2; ++k2) {
-        if (2 * k2 < nkt) {
-          Pair sp[NV][O::kState];
+        if (k2 < nk2) {
+          Pair sp[NV][kRead];
 #pragma unroll
-          for (int n = 0; n < NV; ++n) O::template split<O::kState>(st[2 * k2][n], st[2 * k2 + 1][n], sp[n]);
+          for (int n = 0; n < NV; ++n) O::template split<kRead>(st[2 * k2][n], st[2 * k2 + 1][n], sp[n]);
 #pragma unroll
           for (int it = 0; it < CT; ++it) {
             const Pair x = O::row_pair(l.x + (16 * it + c) * S::SX + 32 * k2, g);
 #pragma unroll
             for (int n = 0; n < NV; ++n)
 #pragma unroll
-              for (int q = O::kState - 1; q >= 0; --q) acc[n][it] = O::mma(sp[n][q], x, acc[n][it]);
+              for (int q = kRead - 1; q >= 0; --q) acc[n][it] = O::mma(sp[n][q], x, acc[n][it]);
           }
         }
       }
 #pragma unroll
       for (int it = 0; it < CT; ++it) {
-        const float f = l.row[16 * it + c];
+        const float f = dec.row[16 * it + c];
         float mass = 0.0f;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
           acc[n][it] *= f;
           if constexpr (MASS != 0) {
-            const f32x4 w = O::four(l.w + (16 * it + c) * S::SZ + wc0 + 16 * n + 4 * g);
+            const f32x4 w = O::four(l.w + (16 * it + c) * S::SW + wc0 + 16 * n + 4 * g);
 #pragma unroll
             for (int r = 0; r < 4; ++r) mass += acc[n][it][r] * w[r];
           }
@@ -446,11 +623,15 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
         if constexpr (MASS != 0) {
           mass += __shfl_xor(mass, 16);
           mass += __shfl_xor(mass, 32);
-          if (g == 0) l.part[wave][16 * it + c] = mass * m.scale_out;
+          if (g == 0) l.part[ci & 1][wave][16 * it + c] = mass * m.scale_out;
         }
       }
       __syncthreads();
       if (tid == 0) l.odd[(ci + 1) & 1] = 0;
+      __builtin_amdgcn_sched_barrier(0);
+    } else if (wave == kDecayWave && ci + 1 < nc) {
+      chunk_decays<REV, C>(l.dec[(ci + 1) & 1], rg, m.scale_src, lane);
+      if (ci + 2 < nc) fetch_decay(ci + 2);
     }
 
     // sources: into the rows of the chunk, and into the state
@@ -461,34 +642,25 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     decays *= total;
 #pragma unroll
     for (int j2 = 0; j2 < CT / 2; ++j2) {
+      __builtin_amdgcn_sched_barrier(0);  // one half's reads at a time: both at once do not fit the registers
       Pair z[NV], zs[NV][O::kState];
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
-        z[n] = O::column_pair(l.z, S::SZ, 32 * j2, wc0 + 16 * n, g, c);
-        const f32x4 f0 = *reinterpret_cast<const f32x4*>(l.src + 32 * j2 + 4 * g);
-        const f32x4 f1 = *reinterpret_cast<const f32x4*>(l.src + 32 * j2 + 16 + 4 * g);
+        z[n] = O::column_pair(l.z, S::SZ, 32 * j2, O::columns(wc0 + 16 * n, c), g, c);
+        const f32x4 f0 = *reinterpret_cast<const f32x4*>(dec.src + 32 * j2 + 8 * g);
+        const f32x4 f1 = *reinterpret_cast<const f32x4*>(dec.src + 32 * j2 + 8 * g + 4);
         O::template split<O::kState>(O::low(z[n]) * f0, O::high(z[n]) * f1, zs[n]);
       }
       if constexpr (OUT) {
-        // An infinity or NaN in z times a score of zero would reach rows that do not see its token: such
-        // values are left out here and added below to the rows that do.
-        if (odd)
-          for (int n = 0; n < NV; ++n) z[n] = O::finite_part(z[n]);
 #pragma unroll
         for (int it = 0; it < CT; ++it) {
           if (REV ? it <= 2 * j2 + 1 : it >= 2 * j2) {
             // the one tile of a pair beyond the diagonal was not written
-            const bool half = REV ? it == 2 * j2 + 1 : it == 2 * j2;
+            const bool none = REV ? it == 2 * j2 + 1 && g < 2 : it == 2 * j2 && g >= 2;
 #pragma unroll
             for (int q = O::kScore - 1; q >= 0; --q) {
               Pair s = O::row_pair(l.score[q] + (16 * it + c) * S::SP + 32 * j2, g);
-              if (half) {
-                if constexpr (BF) {
-                  if (REV) s.x = s.y = 0; else s.z = s.w = 0;
-                } else {
-                  if (REV) s.a = zero4(); else s.b = zero4();
-                }
-              }
+              if (none) s = Pair{};
 #pragma unroll
               for (int n = 0; n < NV; ++n) acc[n][it] = O::mma(z[n], s, acc[n][it]);
             }
@@ -497,8 +669,8 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       }
 #pragma unroll
       for (int kt = 0; kt < NKT; ++kt) {
-        if (kt < nkt) {
-          const Pair y = O::column_pair(l.y, S::SX, 32 * j2, 16 * kt, g, c);
+        if (kt / 2 < nk2) {
+          const Pair y = O::column_pair(l.y, S::SY, 32 * j2, O::state_rows(32 * (kt / 2) + 4 * (kt % 2), c), g, c);
 #pragma unroll
           for (int n = 0; n < NV; ++n)
 #pragma unroll
@@ -508,22 +680,38 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     }
 
     if constexpr (OUT) {
-      if (odd) {
-        for (int j = 0; j < C; ++j)
+      if (__builtin_expect(l.odd[ci & 1] != 0, 0)) {
+        const int rare = anew(lane), c = rare & 15, g = rare >> 4, wc0 = 16 * NV * (anew(tid) >> 6);
+        auto state_row = [&](int kt, int r) { return 32 * (kt / 2) + 8 * g + 4 * (kt % 2) + r; };
+        auto value = [&](int j, int col) {
+          return tb + j < end && col < m.dz ? O::one(zb[int64_t(tb + j) * m.z.st + int64_t(col) * m.z.sd]) : 0.0f;
+        };
+        auto odd = [](float v) { return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u; };
+#pragma unroll 1
+        for (int j = 0; j < C; ++j) {
 #pragma unroll
-          for (int n = 0; n < NV; ++n)
+          for (int n = 0; n < NV; ++n) {
+            // selects, not branches: the accumulators in divergent code cost the whole kernel registers
+            const float u = value(j, c0 + wc0 + 16 * n + c), w = dec.src[j] * u;
+#pragma unroll
+            for (int kt = 0; kt < NKT; ++kt)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) st[kt][n][r] += odd(u) ? O::one(l.y[j * S::SY + state_row(kt, r)]) * w : 0.0f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const float v = O::one(l.z[j * S::SZ + wc0 + 16 * n + 4 * g + r]);
-              if ((__float_as_uint(v) & 0x7f800000u) != 0x7f800000u) continue;
+              const float v = value(j, c0 + wc0 + 16 * n + 4 * g + r);
 #pragma unroll
               for (int it = 0; it < CT; ++it) {
                 const int row = 16 * it + c;
-                if (REV ? j >= row : j <= row) acc[n][it][r] += O::one(l.score[0][row * S::SP + j]) * v;
+                const float s = O::one(l.score[0][row * S::SP + j]) * v;
+                acc[n][it][r] += odd(v) && (REV ? j >= row : j <= row) ? s : 0.0f;
               }
             }
+          }
+        }
       }
       const bool whole = (m.dz & 3) == 0;
+      const int again = anew(tid), c = again & 15, g = again >> 4 & 3, wc0 = 16 * NV * (again >> 6);
 #pragma unroll
       for (int it = 0; it < CT; ++it) {
         const int t = tb + 16 * it + c;
@@ -548,68 +736,6 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
           }
         }
       }
-      if constexpr (MASS != 0) {
-        const int64_t mb = (int64_t(cb) * BH + bh);
-        float rect = 0.0f;
-        if constexpr (MASS == 1) {
-          // a token's decay carries every pair of a source before it and a row from it on: sum the
-          // sources of each row, then the rows of each token. Both sums are taken outright, not as
-          // differences of running totals, so a cut leaves an exact zero.
-          constexpr int PARTS = kThreads / C, N = C / PARTS;
-          const int row = tid / PARTS, part = tid % PARTS;
-          float v[N], sum = 0.0f;
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int j = part * N + i;
-            v[i] = sum;
-            if (j < row) sum += l.pairs[row * (C + 1) + j];
-          }
-          float before = sum;
-#pragma unroll
-          for (int d = 1; d < PARTS; d *= 2) {
-            const float u = __shfl_up(before, d);
-            if (part >= d) before += u;
-          }
-          before = __shfl_up(before, 1);
-          if (part == 0) before = 0.0f;
-#pragma unroll
-          for (int i = 0; i < N; ++i) l.pairs[row * (C + 1) + part * N + i] = before + v[i];
-          __syncthreads();
-          const int t = tid % C, from = tid / C;
-          float s = 0.0f;
-          for (int i = from * N; i < from * N + N; ++i)
-            if (i >= t) s += l.pairs[i * (C + 1) + t];
-          l.rect[tid] = s;
-          __syncthreads();
-          if (tid < C)
-            for (int q = 0; q < PARTS; ++q) rect += l.rect[q * C + tid];
-        }
-        if (wave == 0) {
-          float v = 0.0f;
-          if (lane < C)
-            for (int q = 0; q < kWaves; ++q) v += l.part[q][lane];
-          const int tok = tb + lane;
-          // rows from the token on (MASS 1), or sources before it (MASS 2)
-          float run = v;
-#pragma unroll
-          for (int d = 1; d < C; d *= 2) {
-            const float u = MASS == 1 ? __shfl_down(run, d) : __shfl_up(run, d);
-            if (MASS == 1 ? lane + d < C : lane >= d) run += u;
-          }
-          const float all = __shfl(run, MASS == 1 ? 0 : C - 1);
-          float mine = run;
-          if (MASS == 2) {
-            mine = __shfl_up(run, 1);
-            if (lane == 0) mine = 0.0f;
-          }
-          if (lane < C && tok < t1) m.mass[mb * p.T + tok] = mine + rect;
-          if (lane == 0) {
-            const int chunks = (p.T + C - 1) / C;
-            m.mass_chunk[mb * chunks + tb / C] = all;
-            if (m.chunk_decay && cb == 0) m.chunk_decay[int64_t(bh) * chunks + tb / C] = total;
-          }
-        }
-      }
     }
   }
 
@@ -617,7 +743,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     // tokens past the row's length, in chunks that were not marched
     const int from = t0 + nc * C;
     const int width = min(S::BV, m.dz - c0), rest = max(t1 - from, 0);
-    for (int q = tid; q < rest * width; q += kThreads) {
+    for (int q = tid; q < rest * width; q += THREADS) {
       const int64_t at = ((int64_t(b) * p.T + from + q / width) * p.H + h) * m.dz + c0 + q % width;
       if (!BF || m.out_f32) static_cast<float*>(m.out)[at] = 0.0f;
       else static_cast<uint16_t*>(m.out)[at] = 0;
@@ -625,8 +751,13 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     if constexpr (MASS != 0) {
       const int64_t mb = (int64_t(cb) * BH + bh);
       const int chunks = (p.T + C - 1) / C;
-      for (int q = tid; q < rest; q += kThreads) m.mass[mb * p.T + from + q] = 0.0f;
-      for (int q = tid; q < (rest + C - 1) / C; q += kThreads) {
+      if (nc > 0) {
+        __syncthreads();
+        if (wave == kMassWave)
+          chunk_mass<REV, MASS, CT, S::TILES>(p, m, l, (nc - 1) & 1, W, first_token(nc - 1), t1, cb, bh, lane);
+      }
+      for (int q = tid; q < rest; q += THREADS) m.mass[mb * p.T + from + q] = 0.0f;
+      for (int q = tid; q < (rest + C - 1) / C; q += THREADS) {
         m.mass_chunk[mb * chunks + from / C + q] = 0.0f;
         if (m.chunk_decay && cb == 0) m.chunk_decay[int64_t(bh) * chunks + from / C + q] = 1.0f;
       }
@@ -642,35 +773,38 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       for (int n = 0; n < NV; ++n)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int row = 16 * kt + 4 * g + r, col = c0 + wc0 + 16 * n + c;
+          const int row = state_row(kt, r), col = c0 + wc0 + 16 * n + c;
           if (row < m.dx && col < m.dz) to[row * m.sr + col * m.sc] = st[kt][n][r];
         }
   }
   if (!OUT && tid == 0 && cb == 0) m.seg_decay[int64_t(seg_m) * BH + bh] = decays;
 }
 
-// blockIdx.y picks the march of a gradient: 0 grad_q, 1 grad_k, 2 grad_v.
-template <bool BF, int NKT, int NV>
-__global__ __launch_bounds__(kThreads) void march_forward(DaParams p) {
-  __shared__ typename Shape<BF, NKT, NV>::Lds l;
-  march<BF, NKT, NV, false, 0, true>(p, p.m[0], blockIdx.x, l);
+template <bool BF, int NKT, int NV, int W>
+__global__ __launch_bounds__(W * kWave) void march_forward(DaParams p) {
+  using S = Shape<BF, NKT, NV, W>;
+  __shared__ typename S::Out l;
+  march<S, BF, NKT, NV, W, false, 0, true>(p, p.m[0], blockIdx.x, l);
 }
 
-template <bool BF, int NKT, int NV>
-__global__ __launch_bounds__(kThreads) void march_gradient(DaParams p) {
-  __shared__ typename Shape<BF, NKT, NV>::Lds l;
-  if (blockIdx.y == 0) march<BF, NKT, NV, false, 1, true>(p, p.m[0], blockIdx.x, l);
-  else if (blockIdx.y == 1) march<BF, NKT, NV, true, 2, true>(p, p.m[1], blockIdx.x, l);
-  else march<BF, NKT, NV, true, 0, true>(p, p.m[2], blockIdx.x, l);
+// blockIdx.y picks the march of a gradient: 0 grad_q, 1 grad_k, 2 grad_v.
+template <bool BF, int NKT, int NV, int W>
+__global__ __launch_bounds__(W * kWave) void march_gradient(DaParams p) {
+  using S = Shape<BF, NKT, NV, W>;
+  __shared__ typename S::Mass l;
+  if (blockIdx.y == 0) march<S, BF, NKT, NV, W, false, 1, true>(p, p.m[0], blockIdx.x, l);
+  else if (blockIdx.y == 1) march<S, BF, NKT, NV, W, true, 2, true>(p, p.m[1], blockIdx.x, l);
+  else march<S, BF, NKT, NV, W, true, 0, true>(p, p.m[2], blockIdx.x, l);
 }
 
 // Each segment's own state. A gradient needs two: the state (march 0's) and its
 // adjoint (march 1's, which march 2 shares).
-template <bool BF, int NKT, int NV>
-__global__ __launch_bounds__(kThreads) void march_local(DaParams p) {
-  __shared__ typename Shape<BF, NKT, NV>::Lds l;
-  if (blockIdx.y == 0) march<BF, NKT, NV, false, 0, false>(p, p.m[0], blockIdx.x, l);
-  else march<BF, NKT, NV, true, 0, false>(p, p.m[1], blockIdx.x, l);
+template <bool BF, int NKT, int NV, int W>
+__global__ __launch_bounds__(W * kWave) void march_local(DaParams p) {
+  using S = Shape<BF, NKT, NV, W>;
+  __shared__ typename S::Local l;
+  if (blockIdx.y == 0) march<S, BF, NKT, NV, W, false, 0, false>(p, p.m[0], blockIdx.x, l);
+  else march<S, BF, NKT, NV, W, true, 0, false>(p, p.m[1], blockIdx.x, l);
 }
 
 // Segment m's entry, its own state so far, becomes the state at the start of segment m + 1.
@@ -680,11 +814,23 @@ __global__ __launch_bounds__(kThreads) void carry(DaParams p) {
   const int64_t e = int64_t(blockIdx.x) * kThreads + threadIdx.x;
   if (e >= BH * state) return;
   const int64_t bh = e / state;
+  const int n = p.segments - 1;
   float s = m.first ? m.first[e] : 0.0f;
-  for (int i = 0; i < p.segments - 1; ++i) {
-    float* at = m.seg + i * BH * state + e;
-    s = fmaf(m.seg_decay[i * BH + bh], s, *at);
-    *at = s;
+  constexpr int A = 8;  // entries read ahead of the chain
+  for (int i = 0; i < n; i += A) {
+    float v[A], d[A];
+#pragma unroll
+    for (int k = 0; k < A; ++k) {
+      const int j = min(i + k, n - 1);
+      v[k] = m.seg[j * BH * state + e];
+      d[k] = m.seg_decay[j * BH + bh];
+    }
+#pragma unroll
+    for (int k = 0; k < A; ++k) {
+      if (i + k >= n) break;
+      s = fmaf(d[k], s, v[k]);
+      m.seg[(i + k) * BH * state + e] = s;
+    }
   }
 }
 
@@ -706,11 +852,12 @@ __device__ __forceinline__ double block_sum(double v, double* l) {
 // What passes a chunk from before to after it, Y, from what crosses the border
 // before it, Z: Y = Z - (its rows' mass), the next Z = Y + (its sources' mass), and
 // Y is zero outright where the chunk's decays multiply to zero. One workgroup a
-// head; the chunks are scanned as maps Z -> keep Z + add.
+// head and segment, from the segment's own Z; kThreads chunks at a time.
 __global__ __launch_bounds__(kThreads) void decay_grad(DaDecayGrad p) {
   __shared__ double la[kThreads];
-  __shared__ int lk[kThreads];
-  const int bh = blockIdx.x, tid = int(threadIdx.x), b = bh / p.H, h = bh % p.H;
+  __shared__ double ly[kThreads];
+  const int bh = blockIdx.x % (p.B * p.H), seg = blockIdx.x / (p.B * p.H), tid = int(threadIdx.x);
+  const int b = bh / p.H, h = bh % p.H;
   const int64_t BH = int64_t(p.B) * p.H, state = int64_t(p.dk) * p.dv;
   int len = p.T;
   if (p.lengths) len = min(max(p.lengths[b], 0), p.T);
@@ -719,69 +866,59 @@ __global__ __launch_bounds__(kThreads) void decay_grad(DaDecayGrad p) {
     for (int k = 0; k < p.blocks; ++k) s += double(v[(k * BH + bh) * n + i]);
     return s;
   };
-  double z0 = 0.0;
-  if (p.initial) {
+  double z = 0.0;
+  if (seg > 0) {
+    for (int k = 0; k < p.blocks; ++k) z += p.cross[(k * BH + bh) * p.segments + seg];
+  } else if (p.initial) {
     double s = 0.0;
     for (int64_t i = tid; i < state; i += kThreads)
       s += double(p.initial[bh * state + i]) * double(p.grad_initial[bh * state + i]);
-    z0 = block_sum(s, la);
+    z = block_sum(s, la);
   }
-  const int per = (p.chunks + kThreads - 1) / kThreads;
-  const int first = min(tid * per, p.chunks), last = min(first + per, p.chunks);
-  double add = 0.0;
-  int keep = 1;
-  for (int i = first; i < last; ++i) {
-    const bool cut = p.chunk_decay[int64_t(bh) * p.chunks + i] == 0.0f;
-    add = (cut ? 0.0 : add - sum_of(p.rows_chunk, p.chunks, i)) + sum_of(p.sources_chunk, p.chunks, i);
-    if (cut) keep = 0;
-  }
-  la[tid] = add;
-  lk[tid] = keep;
-  __syncthreads();
-  for (int d = 1; d < kThreads; d *= 2) {
-    double a = 0.0;
-    int k = 1;
-    if (tid >= d) {
-      a = la[tid - d];
-      k = lk[tid - d];
-    }
-    __syncthreads();
-    if (tid >= d) {
-      if (lk[tid]) la[tid] += a;
-      lk[tid] &= k;
-    }
-    __syncthreads();
-  }
-  double z = tid == 0 ? z0 : la[tid - 1] + (lk[tid - 1] ? z0 : 0.0);
-  __syncthreads();
+  const int first = seg * (p.seg_tokens / p.chunk), last = min(p.chunks, first + p.seg_tokens / p.chunk);
   double all = 0.0;
-  for (int i = first; i < last; ++i) {
-    const bool cut = p.chunk_decay[int64_t(bh) * p.chunks + i] == 0.0f;
-    const double y = cut ? 0.0 : z - sum_of(p.rows_chunk, p.chunks, i);
-    z = y + sum_of(p.sources_chunk, p.chunks, i);
-    for (int t = i * p.chunk; t < min((i + 1) * p.chunk, p.T); ++t) {
+  for (int i0 = first; i0 < last; i0 += kThreads) {
+    const int n = min(kThreads, last - i0);
+    __syncthreads();
+    if (tid < n) {
+      la[tid] = sum_of(p.sources_chunk, p.chunks, i0 + tid);
+      ly[tid] = sum_of(p.rows_chunk, p.chunks, i0 + tid);
+    }
+    __syncthreads();
+    if (tid == 0)
+      for (int i = 0; i < n; ++i) {
+        const bool cut = p.chunk_decay[int64_t(bh) * p.chunks + i0 + i] == 0.0f;
+        const double y = cut ? 0.0 : z - ly[i];
+        ly[i] = y;
+        z = y + la[i];
+      }
+    __syncthreads();
+    const int t1 = min((i0 + n) * p.chunk, p.T);
+    for (int t = i0 * p.chunk + tid; t < t1; t += kThreads) {
       double v = 0.0;
       if (t < len) {
         const float gv = p.g[int64_t(b) * p.gb + int64_t(t) * p.gt + int64_t(h) * p.gh];
         // exp(g) = 0: nothing passes, and neither does a gradient
-        if (!(gv <= -kMostLog)) v = y + sum_of(p.rows, p.T, t) + sum_of(p.sources, p.T, t);
+        if (!(gv <= -kMostLog)) v = ly[t / p.chunk - i0] + sum_of(p.rows, p.T, t) + sum_of(p.sources, p.T, t);
       }
       if (p.per_head) all += v;
       else p.grad_g[(int64_t(b) * p.T + t) * p.H + h] = float(v);
     }
   }
   if (p.per_head) {
+    __syncthreads();
     all = block_sum(all, la);
-    if (tid == 0) p.partial[bh] = all;
+    if (tid == 0) p.partial[int64_t(seg) * BH + bh] = all;
   }
 }
 
-__global__ void decay_grad_heads(DaDecayGrad p) {
-  const int h = blockIdx.x * blockDim.x + threadIdx.x;
-  if (h >= p.H) return;
+// One wave a head.
+__global__ __launch_bounds__(kWave) void decay_grad_heads(DaDecayGrad p) {
+  const int h = blockIdx.x, lane = int(threadIdx.x);
   double s = 0.0;
-  for (int b = 0; b < p.B; ++b) s += p.partial[int64_t(b) * p.H + h];
-  p.grad_g[h] = float(s);
+  for (int i = lane; i < p.B * p.segments; i += kWave) s += p.partial[int64_t(i) * p.H + h];
+  s = lane_of(prefix_sum(s, lane), 63);
+  if (lane == 0) p.grad_g[h] = float(s);
 }
 
 __global__ __launch_bounds__(kThreads) void share_sum(DaShare p) {
@@ -848,20 +985,21 @@ __global__ __launch_bounds__(kThreads) void step_kernel(DaStep p) {
 
 int tile_class(int d) { return d <= 32 ? 2 : d <= 64 ? 4 : d <= 128 ? 8 : 16; }
 
-template <bool BF, int NKT, int NV>
+template <bool BF, int NKT, int NV, int W>
 hipError_t run_marches(const DaParams& p, hipStream_t stream) {
+  constexpr int BV = 16 * NV * W, kAll = W * kWave;
   const int64_t BH = int64_t(p.B) * p.H;
   int ncb = 1;
-  for (int i = 0; i < p.marches; ++i) ncb = std::max(ncb, (p.m[i].dz + 64 * NV - 1) / (64 * NV));
+  for (int i = 0; i < p.marches; ++i) ncb = std::max(ncb, (p.m[i].dz + BV - 1) / BV);
   const int states = p.marches == 1 ? 1 : 2;
   if (p.segments > 1) {
-    march_local<BF, NKT, NV><<<dim3(unsigned(ncb * BH * (p.segments - 1)), states), kThreads, 0, stream>>>(p);
+    march_local<BF, NKT, NV, W><<<dim3(unsigned(ncb * BH * (p.segments - 1)), states), kAll, 0, stream>>>(p);
     const int64_t n = BH * p.dk * p.dv;
     carry<<<dim3(unsigned((n + kThreads - 1) / kThreads), states), kThreads, 0, stream>>>(p);
   }
   const dim3 grid(unsigned(ncb * BH * p.segments), p.marches);
-  if (p.marches == 1) march_forward<BF, NKT, NV><<<grid, kThreads, 0, stream>>>(p);
-  else march_gradient<BF, NKT, NV><<<grid, kThreads, 0, stream>>>(p);
+  if (p.marches == 1) march_forward<BF, NKT, NV, W><<<grid, kAll, 0, stream>>>(p);
+  else march_gradient<BF, NKT, NV, W><<<grid, kAll, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -869,10 +1007,10 @@ template <bool BF>
 hipError_t run_widths(const DaParams& p, hipStream_t stream) {
   const int wide = std::max(p.dk, p.dv);
   switch (tile_class(wide)) {
-    case 2: return run_marches<BF, 2, 1>(p, stream);
-    case 4: return run_marches<BF, 4, 1>(p, stream);
-    case 8: return run_marches<BF, 8, 2>(p, stream);
-    default: return run_marches<BF, 16, 1>(p, stream);
+    case 2: return run_marches<BF, 2, 1, 4>(p, stream);
+    case 4: return run_marches<BF, 4, 1, 4>(p, stream);
+    case 8: return run_marches<BF, 8, 1, 8>(p, stream);
+    default: return run_marches<BF, 16, 1, 8>(p, stream);
   }
 }
 
@@ -881,7 +1019,7 @@ hipError_t run_widths(const DaParams& p, hipStream_t stream) {
 int decay_attention_chunk(bool bf16) { return bf16 ? Op<true>::C : Op<false>::C; }
 
 int decay_attention_column_blocks(int dx, int dz) {
-  const int bv = tile_class(std::max(dx, dz)) == 8 ? 128 : 64;
+  const int bv = tile_class(std::max(dx, dz)) >= 8 ? 128 : 64;
   return (dz + bv - 1) / bv;
 }
 
@@ -889,8 +1027,9 @@ void decay_attention_split(DaParams& p) {
   const int C = decay_attention_chunk(p.bf16 != 0);
   const int64_t chunks = (int64_t(p.T) + C - 1) / C;
   const int64_t groups = std::max<int64_t>(1, int64_t(p.B) * p.H * decay_attention_column_blocks(p.dk, p.dv));
-  // two workgroups a compute unit, segments of two chunks at least
-  const int64_t want = (2 * device_cu_count() + groups - 1) / groups;
+  // one workgroup a compute unit (two of the narrow states'), segments of two chunks at least
+  const int64_t resident = tile_class(std::max(p.dk, p.dv)) >= 8 ? 1 : 2;
+  const int64_t want = resident * device_cu_count() / groups;
   const int64_t segments = std::max<int64_t>(1, std::min(want, chunks / 2));
   const int64_t per = std::max<int64_t>(1, (chunks + segments - 1) / segments);
   p.seg_tokens = int(per * C);
@@ -902,8 +1041,8 @@ hipError_t launch_decay_attention(const DaParams& p, hipStream_t stream) {
 }
 
 hipError_t launch_decay_grad(const DaDecayGrad& p, hipStream_t stream) {
-  if (p.B > 0) decay_grad<<<unsigned(int64_t(p.B) * p.H), kThreads, 0, stream>>>(p);
-  if (p.per_head) decay_grad_heads<<<(p.H + 63) / 64, 64, 0, stream>>>(p);
+  if (p.B > 0) decay_grad<<<unsigned(int64_t(p.B) * p.H * p.segments), kThreads, 0, stream>>>(p);
+  if (p.per_head) decay_grad_heads<<<p.H, kWave, 0, stream>>>(p);
   return hipGetLastError();
 }
 

@@ -1271,7 +1271,7 @@ void carve_segments(Carve& c, sx::DaParams& p, sx::DaMarch& m) {
 
 struct GradPieces {
   float *rows, *sources, *rows_chunk, *sources_chunk, *chunk_decay;
-  double* partial;
+  double *cross, *partial;
   float *share_q, *share_k, *share_v;
   int chunks, blocks;
 };
@@ -1291,7 +1291,8 @@ GradPieces carve_gradient(Carve& c, const DecayShapes& s, sx::DaParams& p) {
   g.rows_chunk = c.take<float>(g.blocks * BH * g.chunks);
   g.sources_chunk = c.take<float>(g.blocks * BH * g.chunks);
   g.chunk_decay = c.take<float>(BH * g.chunks);
-  g.partial = c.take<double>(BH);
+  g.cross = c.take<double>(g.blocks * BH * p.segments);
+  g.partial = c.take<double>(BH * p.segments);
   // gradients of shared heads are summed over the heads that share them, from f32
   const int64_t n = s.B * s.T * s.H;
   g.share_q = c.take<float>(s.hq == s.H ? 0 : n * s.dk);
@@ -1460,6 +1461,7 @@ sx_status sx_decay_attention_backward(sx_dtype dtype, const int64_t* q_shape, co
   dq.mass = w.rows;
   dq.mass_chunk = w.rows_chunk;
   dq.chunk_decay = w.chunk_decay;
+  dq.cross = w.cross;
   dk.mass = w.sources;
   dk.mass_chunk = w.sources_chunk;
   const hipStream_t str = static_cast<hipStream_t>(stream);
@@ -1501,6 +1503,9 @@ sx_status sx_decay_attention_backward(sx_dtype dtype, const int64_t* q_shape, co
   d.rows_chunk = w.rows_chunk;
   d.sources_chunk = w.sources_chunk;
   d.chunk_decay = w.chunk_decay;
+  d.segments = p.segments;
+  d.seg_tokens = p.seg_tokens;
+  d.cross = w.cross;
   d.initial = initial;
   d.grad_initial = grad_initial;
   d.partial = w.partial;

@@ -47,6 +47,7 @@ struct DaMarch {
   float* seg_decay;     // [segments - 1][B * H]: product of a segment's decays
   float* mass;          // [column blocks][B * H][T]: the part of the decay's gradient that this march sees
   float* mass_chunk;    // [column blocks][B * H][chunks]: a chunk's mass against the state it entered with
+  double* cross;        // [column blocks][B * H][segments]: the state at a segment's start against its adjoint there
   float* chunk_decay;   // [B * H][chunks]: product of a chunk's decays (written by column block 0; nullptr: no)
 };
 
@@ -83,9 +84,11 @@ struct DaDecayGrad {
   const float* rows_chunk;     // [blocks][B * H][chunks]
   const float* sources_chunk;
   const float* chunk_decay;    // [B * H][chunks]
+  int segments, seg_tokens;
+  const double* cross;         // [blocks][B * H][segments], of segments but the first
   const float* initial;        // nullptr: zero
   const float* grad_initial;
-  double* partial;             // per_head: [B * H]
+  double* partial;             // per_head: [segments][B * H]
   float* grad_g;
   int per_head;
 };
