@@ -3,809 +3,16 @@
 //
 //   S[t] = exp(g[t]) S[t-1] + k[t] v[t]^T,   o[t] = scale S[t]^T q[t]
 //
-// Prompts and gradients run as marches (DaMarch in sx_attention.hpp) over
-// chunks of C tokens. With G the running sum of g inside a chunk, and S the
-// state the chunk is entered with,
-//   out_i = scale (exp(G_i) S^T x_i + sum_{j <= i} exp(G_i - G_j) (x_i . y_j) z_j)
-//   S    <- exp(G_C) S + sum_j exp(G_C - G_j) y_j z_j^T
-// Every exponent is the log decay between two tokens, never its two halves
-// apart, so nothing overflows however strong the decay, and a decay of zero
-// (g = -inf) cuts exactly. A workgroup keeps S in its accumulators: the wave
-// layout of a 16x16 MFMA result (four rows of one column a lane) is the layout
-// of an operand contracted over those rows, so S feeds x S without leaving the
-// registers.
-//
+// Prompts and gradients run as marches over chunks of tokens (decay_march.hpp).
 // Long sequences with few heads are split into segments: a first pass forms
 // each segment's state from its own tokens, a carry joins them, and the second
 // pass marches all segments at once from their true states.
-#include <hip/hip_runtime.h>
-
-#include <algorithm>
-#include <type_traits>
-
-#include "ms_mfma.hpp"
-#include "sx_attention.hpp"
-#include "sx_common.hpp"
+#include "decay_march.hpp"
 
 namespace sx {
 namespace {
 
-constexpr int kThreads = 256;  // of the kernels beside the marches
-// Log decays are taken into [-200, 200]: exp(-200) is zero and exp(200) infinite in
-// f32, so the results are those of the whole range, and -inf leaves no inf - inf.
-constexpr float kMostLog = 200.0f;
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-template <bool BF>
-struct Op;
-
-// bf16 operands. A Pair is what a lane brings to a product contracted over 32:
-// the eight values 8g .. 8g + 7 of its row (or column) in lane group g, on
-// v_mfma_f32_16x16x32_bf16. The instruction's own order of the 32 does not
-// matter, as both operands use the same one.
-template <>
-struct Op<true> {
-  using E = uint16_t;
-  using Pair = uint4;
-  static constexpr int C = 64;      // tokens a chunk
-  static constexpr int kPiece = 8;  // elements of a 16-byte piece
-  // f32 values enter a product as bf16 parts: three carry all 24 bits, two carry
-  // 17, enough where the result is rounded to bf16 (8 bits) on store.
-  static constexpr int kState = 3;
-  static constexpr int kRead = 2;
-  static constexpr int kScore = 2;
-  static __device__ __forceinline__ f32x4 mma(Pair a, Pair b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
-                                                   0, 0);
-  }
-  // NP parts of eight f32 values. Of three, each but the last is truncated and the last is what is
-  // left, exactly; of two, both are rounded to nearest, 2^-18 of the value off at most.
-  template <int NP>
-  static __device__ __forceinline__ void split(f32x4 a, f32x4 b, Pair (&out)[NP]) {
-    float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-    uint32_t w[4];
-    if constexpr (NP == 2) {
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-          if (p == 0) {
-            v[2 * i] -= __uint_as_float(w[i] << 16);
-            v[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
-          }
-        }
-        out[p] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    } else {
-#pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        uint32_t u[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          u[i] = __float_as_uint(v[i]);
-          if (p + 1 < NP) v[i] -= __uint_as_float(u[i] & 0xffff0000u);
-        }
-        out[p] = make_uint4(upper_halves(u[0], u[1]), upper_halves(u[2], u[3]), upper_halves(u[4], u[5]),
-                            upper_halves(u[6], u[7]));
-      }
-    }
-  }
-  // columns 8g .. 8g + 7 of a row
-  static __device__ __forceinline__ Pair row_pair(const E* row, int g) {
-    return *reinterpret_cast<const uint4*>(row + 8 * g);
-  }
-  // Rows j0 + 8g .. 8g + 7 of one column a lane, through the transposing read: lane c of a group
-  // addresses four columns of one row and receives column c of four rows. `col`: the lane's four.
-  static __device__ __forceinline__ Pair column_pair(const E* tile, int stride, int j0, int col, int g, int c) {
-    typedef s16x4_t __attribute__((address_space(3))) * lds4;
-    const E* p = tile + (j0 + 8 * g + (c >> 2)) * stride + col;
-    const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p)));
-    const uint2 b = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 4 * stride)));
-    return make_uint4(a.x, a.y, b.x, b.y);
-  }
-  // what column_pair takes for 16 columns in a row from col0 on ...
-  static __device__ __forceinline__ int columns(int col0, int c) { return col0 + 4 * (c & 3); }
-  // ... and for columns 8 (c / 4) + c % 4 from col0 on: the rows of a state tile
-  static __device__ __forceinline__ int state_rows(int col0, int c) { return col0 + 8 * (c & 3); }
-  static __device__ __forceinline__ f32x4 low(Pair a) {
-    return f32x4{__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u), __uint_as_float(a.y << 16),
-                 __uint_as_float(a.y & 0xffff0000u)};
-  }
-  static __device__ __forceinline__ f32x4 high(Pair a) { return low(make_uint4(a.z, a.w, 0, 0)); }
-  static __device__ __forceinline__ f32x4 four(const E* p) {
-    const uint2 a = *reinterpret_cast<const uint2*>(p);
-    return low(make_uint4(a.x, a.y, 0, 0));
-  }
-  static __device__ __forceinline__ float one(E v) { return bf16_to_f32(v); }
-  static __device__ __forceinline__ bool finite(uint4 v) {
-    auto bad = [](uint32_t u) { return (u & 0x7f800000u) == 0x7f800000u || (u & 0x7f80u) == 0x7f80u; };
-    return !(bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w));
-  }
-  // infinities and NaN taken out
-  static __device__ __forceinline__ uint4 finite_part(uint4 v) {
-    auto f = [](uint32_t u) {
-      if ((u & 0x7f800000u) == 0x7f800000u) u &= 0xffffu;
-      if ((u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
-      return u;
-    };
-    return make_uint4(f(v.x), f(v.y), f(v.z), f(v.w));
-  }
-  static __device__ __forceinline__ void put4(E* p, f32x4 v) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-  }
-  static __device__ __forceinline__ E round(float v) { return f32_to_bf16_rne(v); }
-};
-
-// f32 operands on v_mfma_f32_16x16x4_f32, four contracted at a time.
-template <>
-struct Op<false> {
-  using E = float;
-  struct Pair {
-    f32x4 a, b;
-  };
-  static constexpr int C = 32;
-  static constexpr int kPiece = 4;
-  static constexpr int kState = 1;
-  static constexpr int kRead = 1;
-  static constexpr int kScore = 1;
-  static __device__ __forceinline__ f32x4 mma(Pair a, Pair b, f32x4 c) {
-    c = mfma_16x16x16(a.a, b.a, c);
-    return mfma_16x16x16(a.b, b.b, c);
-  }
-  template <int NP>
-  static __device__ __forceinline__ void split(f32x4 a, f32x4 b, Pair (&out)[NP]) {
-    static_assert(NP == 1, "f32 operands are whole");
-    out[0] = Pair{a, b};
-  }
-  static __device__ __forceinline__ Pair row_pair(const E* row, int g) {
-    return Pair{*reinterpret_cast<const f32x4*>(row + 8 * g), *reinterpret_cast<const f32x4*>(row + 8 * g + 4)};
-  }
-  static __device__ __forceinline__ Pair column_pair(const E* tile, int stride, int j0, int col, int g, int c) {
-    const E* p = tile + (j0 + 8 * g) * stride + col;
-    return Pair{f32x4{p[0], p[stride], p[2 * stride], p[3 * stride]},
-                f32x4{p[4 * stride], p[5 * stride], p[6 * stride], p[7 * stride]}};
-  }
-  static __device__ __forceinline__ int columns(int col0, int c) { return col0 + c; }
-  static __device__ __forceinline__ int state_rows(int col0, int c) { return col0 + 8 * (c >> 2) + (c & 3); }
-  static __device__ __forceinline__ f32x4 low(Pair a) { return a.a; }
-  static __device__ __forceinline__ f32x4 high(Pair a) { return a.b; }
-  static __device__ __forceinline__ f32x4 four(const E* p) { return *reinterpret_cast<const f32x4*>(p); }
-  static __device__ __forceinline__ float one(E v) { return v; }
-  static __device__ __forceinline__ bool finite(uint4 v) {
-    auto bad = [](uint32_t u) { return (u & 0x7f800000u) == 0x7f800000u; };
-    return !(bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w));
-  }
-  static __device__ __forceinline__ uint4 finite_part(uint4 v) {
-    auto f = [](uint32_t u) { return (u & 0x7f800000u) == 0x7f800000u ? 0u : u; };
-    return make_uint4(f(v.x), f(v.y), f(v.z), f(v.w));
-  }
-  static __device__ __forceinline__ void put4(E* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
-  static __device__ __forceinline__ E round(float v) { return v; }
-};
-
-// W waves hold a state of up to 16 NKT rows and 16 NV W columns.
-template <bool BF, int NKT, int NV, int W>
-struct Shape {
-  using O = Op<BF>;
-  using E = typename O::E;
-  static constexpr int kThreads = W * kWave;
-  static constexpr int C = O::C, CT = C / 16;
-  static constexpr int TILES = CT * (CT + 1) / 2;  // tiles of scores on and on one side of the diagonal
-  static constexpr int DX = 16 * NKT;              // widest x and y
-  static constexpr int BV = 16 * NV * W;           // columns of z a workgroup holds: 16 NV a wave
-  // Row strides in elements. Tiles read by rows alone: 4 banks past a multiple of 64 bytes, so 16 rows
-  // meet no bank twice; those read by columns too: 12 past (bf16), which spreads the four rows of a
-  // transposing read as well.
-  static constexpr int kRowPad = O::kPiece, kColPad = BF ? 24 : 4;
-  static constexpr int SX = DX + kRowPad, SY = DX + kColPad, SZ = BV + kColPad, SW = BV + kRowPad, SP = C + kRowPad;
-  static constexpr int NX = (C * DX / O::kPiece + kThreads - 1) / kThreads;  // 16-byte pieces a thread of a tile
-  static constexpr int NZ = (C * BV / O::kPiece + kThreads - 1) / kThreads;
-  struct Decays {
-    alignas(16) float2 g[C];   // running log2 decay, high and low part
-    alignas(16) float row[C];  // decay between the row and the state
-    alignas(16) float src[C];  // decay between the source and the next state, times scale_src
-    float total;
-  };
-  struct Local {  // what a segment's own state takes
-    alignas(16) E y[C * SY];
-    alignas(16) E z[C * SZ];
-    Decays dec[2];
-    int odd[2];   // a chunk's z holds an infinity or NaN
-  };
-  struct Out : Local {
-    alignas(16) E x[C * SX];
-    alignas(16) E score[O::kScore][C * SP];
-  };
-  struct Mass : Out {
-    alignas(16) E w[C * SW];
-    float part[2][W][C];        // a wave's columns of the rows against the state, and w
-    float row_tile[2][CT][C];   // pairs of a row with the sources of a tile, summed
-    float col_tile[2][TILES][16];  // pairs of a tile with their source before the column and their row from it on
-    double cross[W];
-  };
-  template <bool OUT, int MASS>
-  using Lds = std::conditional_t<MASS != 0, Mass, std::conditional_t<OUT, Out, Local>>;
-};
-
-// The same value, as if new: what is formed from it is formed where it is used, not
-// ahead of the loop around it, where it would hold registers through every chunk.
-__device__ __forceinline__ int anew(int v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
-
-// Base of head h of batch row b, at token 0.
-template <typename E>
-__device__ __forceinline__ const E* head_base(const HeadView& v, int b, int h) {
-  return static_cast<const E*>(v.p) + int64_t(b) * v.sb + int64_t(h / v.rep) * v.sh;
-}
-
-// A thread's pieces of the tile of C tokens from tb and W columns from c0; zero
-// where a token (from `end` on) or a column (from `d` on) does not exist.
-template <bool BF, int W, int THREADS, int N>
-__device__ __forceinline__ void load_tile(const HeadView& v, const typename Op<BF>::E* base, int d, int c0, int tb,
-                                          int end, uint4 (&r)[N]) {
-  using E = typename Op<BF>::E;
-  constexpr int P = Op<BF>::kPiece, PR = W / P;
-  const E* at = base + int64_t(tb) * v.st;
-  const int tid = anew(int(threadIdx.x));
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const int q = tid + n * THREADS;
-    const int t = q / PR, col = c0 + q % PR * P;
-    r[n] = make_uint4(0, 0, 0, 0);
-    if (tb + t < end && t < Op<BF>::C && col < d) {
-      const E* p = at + int64_t(t) * v.st + int64_t(col) * v.sd;
-      if (v.vec) {
-        r[n] = *reinterpret_cast<const uint4*>(p);
-      } else {
-        uint32_t u[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int e = 0; e < P; ++e) {
-          if (col + e < d) {
-            if constexpr (BF) u[e / 2] |= uint32_t(p[e * v.sd]) << (16 * (e & 1));
-            else u[e] = __float_as_uint(p[e * v.sd]);
-          }
-        }
-        r[n] = make_uint4(u[0], u[1], u[2], u[3]);
-      }
-    }
-  }
-}
-
-template <bool BF, int W, int THREADS, int N>
-__device__ __forceinline__ void store_tile(typename Op<BF>::E* tile, int stride, const uint4 (&r)[N]) {
-  constexpr int P = Op<BF>::kPiece, PR = W / P;
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const int q = int(threadIdx.x) + n * THREADS;
-    if (Op<BF>::C * PR % THREADS == 0 || q < Op<BF>::C * PR)
-      *reinterpret_cast<uint4*>(tile + q / PR * stride + q % PR * P) = r[n];
-  }
-}
-
-__device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2f(v); }
-
-// v of the lane that CTRL names (DPP), zero where there is none
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
-}
-template <int CTRL>
-__device__ __forceinline__ double dpp(double v) {
-  const long long u = __double_as_longlong(v);
-  const int lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(u)), CTRL, 0xF, 0xF, false);
-  const int hi = __builtin_amdgcn_update_dpp(0, int(u >> 32), CTRL, 0xF, 0xF, false);
-  return __longlong_as_double((static_cast<long long>(hi) << 32) | uint32_t(lo));
-}
-__device__ __forceinline__ float lane_of(float v, int i) {
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i));
-}
-__device__ __forceinline__ double lane_of(double v, int i) {
-  const long long u = __double_as_longlong(v);
-  const int lo = __builtin_amdgcn_readlane(int(uint32_t(u)), i), hi = __builtin_amdgcn_readlane(int(u >> 32), i);
-  return __longlong_as_double((static_cast<long long>(hi) << 32) | uint32_t(lo));
-}
-
-// Sum of the lanes up to this one.
-template <typename T>
-__device__ __forceinline__ T prefix_sum(T v, int lane) {
-  v += dpp<0x111>(v);
-  v += dpp<0x112>(v);
-  v += dpp<0x114>(v);
-  v += dpp<0x118>(v);
-  const T a = lane_of(v, 15), b = a + lane_of(v, 31), c = b + lane_of(v, 47);
-  return lane < 16 ? v : v + (lane < 32 ? a : lane < 48 ? b : c);
-}
-// Sum of the lanes from this one on.
-__device__ __forceinline__ float suffix_sum(float v, int lane) {
-  v += dpp<0x101>(v);
-  v += dpp<0x102>(v);
-  v += dpp<0x104>(v);
-  v += dpp<0x108>(v);
-  const float c = lane_of(v, 48), b = lane_of(v, 32) + c, a = lane_of(v, 16) + b;
-  return lane >= 48 ? v : v + (lane >= 32 ? c : lane >= 16 ? b : a);
-}
-// Sum over the 16 lanes of a group, in its last lane.
-__device__ __forceinline__ float group_sum(float v) {
-  v += dpp<0x111>(v);
-  v += dpp<0x112>(v);
-  v += dpp<0x114>(v);
-  return v + dpp<0x118>(v);
-}
-
-// A chunk's decays from a lane's log decay gv (one wave; token tb + lane).
-template <bool REV, int C, typename Decays>
-__device__ __forceinline__ void chunk_decays(Decays& l, float gv, float scale_src, int lane) {
-  gv = gv < -kMostLog ? -kMostLog : gv > kMostLog ? kMostLog : gv;
-  // 64 bits: the difference of two running sums is the log decay between two tokens, and has to be
-  // exact to f32 also behind a token that cut the state.
-  const double s = prefix_sum(double(gv) * 1.4426950408889634, lane);
-  const double total = lane_of(s, C - 1);
-  if (lane < C) {
-    const float hi = float(s);
-    l.g[lane] = make_float2(hi, float(s - double(hi)));
-    const float from_start = exp2_hw(hi), to_end = exp2_hw(float(total - s));
-    l.row[lane] = REV ? to_end : from_start;
-    l.src[lane] = (REV ? from_start : to_end) * scale_src;
-    if (lane == 0) l.total = exp2_hw(float(total));
-  }
-}
-
-// A chunk's share of the decay's gradient, from the sums its rows and pairs left (one wave).
-// MASS 1: what the rows from a token on take from the state and from sources before the token.
-// MASS 2: what the sources before it give. The sums are taken outright, not as differences of running
-// totals, so a cut leaves an exact zero.
-template <bool REV, int MASS, int CT, int TILES, typename Lds>
-__device__ __forceinline__ void chunk_mass(const DaParams& p, const DaMarch& m, const Lds& l, int buf, int waves,
-                                           int tb, int t1, int cb, int bh, int lane) {
-  constexpr int C = 16 * CT;
-  const int64_t mb = int64_t(cb) * p.B * p.H + bh;
-  float v = 0.0f;
-  if (lane < C)
-    for (int q = 0; q < waves; ++q) v += l.part[buf][q][lane];
-  float mine, all;
-  if constexpr (MASS == 1) {
-    mine = suffix_sum(v, lane);
-    all = lane_of(mine, 0);
-    // pairs: the sources of whole tiles before the token's own ...
-    float before = 0.0f;
-#pragma unroll
-    for (int bt = 1; bt < CT; ++bt) {
-      if (lane < C) before += l.row_tile[buf][bt - 1][lane];
-      const float s = suffix_sum(lane >= 16 * bt ? before : 0.0f, lane);
-      if (lane / 16 == bt) mine += s;
-    }
-    // ... and those of its own
-    if (lane < C) {
-      const int bt = lane / 16;
-      for (int it = bt; it < CT; ++it) mine += l.col_tile[buf][it * (it + 1) / 2 + bt][lane % 16];
-    }
-  } else {
-    const float run = prefix_sum(v, lane);
-    all = lane_of(run, C - 1);
-    mine = __shfl_up(run, 1);
-    if (lane == 0) mine = 0.0f;
-  }
-  const int tok = tb + lane;
-  if (lane < C && tok < t1) m.mass[mb * p.T + tok] = mine;
-  if (lane == 0) m.mass_chunk[mb * ((p.T + C - 1) / C) + tb / C] = all;
-}
-
-// One workgroup's march. MASS: 0 none, 1 the rows' part of the decay's gradient
-// (forward), 2 the sources' part (reverse). OUT false: the segment's own state only.
-template <typename S, bool BF, int NKT, int NV, int W, bool REV, int MASS, bool OUT>
-__device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int block,
-                                      typename S::template Lds<OUT, MASS>& l) {
-  using O = Op<BF>;
-  using E = typename O::E;
-  using Pair = typename O::Pair;
-  constexpr int C = S::C, CT = S::CT, THREADS = S::kThreads;
-  constexpr int kRead = MASS == 0 ? O::kRead : O::kState;  // the decay's gradient is f32
-  constexpr int kDecayWave = W - 1, kMassWave = W - 2;     // they have the fewest tiles of scores
-  const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
-
-  const int ncb = (m.dz + S::BV - 1) / S::BV, BH = p.B * p.H;
-  const int cb = block % ncb, bh = block / ncb % BH, seg_m = block / ncb / BH;
-  if (seg_m >= (OUT ? p.segments : p.segments - 1)) return;
-  const int b = bh / p.H, h = bh % p.H;
-  const int seg = REV ? p.segments - 1 - seg_m : seg_m;
-  const int t0 = seg * p.seg_tokens, t1 = min(p.T, t0 + p.seg_tokens);
-  int len = p.T;
-  if (p.lengths) len = min(max(p.lengths[b], 0), p.T);
-  const int live = max(min(len, t1) - t0, 0), end = min(len, t1);
-  const int nc = (live + C - 1) / C;
-  const int c0 = cb * S::BV, wc0 = 16 * NV * wave;  // first column of the workgroup, and of the wave within it
-  const int nk2 = (m.dx + 31) / 32;                 // pairs of tiles of x that exist
-  const int64_t state = int64_t(p.dk) * p.dv;
-
-  const E* xb = OUT ? head_base<E>(m.x, b, h) : nullptr;
-  const E* yb = head_base<E>(m.y, b, h);
-  const E* zb = head_base<E>(m.z, b, h);
-  const E* wb = MASS ? head_base<E>(m.w, b, h) : nullptr;
-  const float* gb = p.g + int64_t(b) * p.gb + int64_t(h) * p.gh;
-
-  // The state: tile kt holds rows 32 (kt / 2) + 8 g + 4 (kt % 2) + r, column c0 + wc0 + 16 n + c, so that the
-  // rows of a lane in two tiles are eight in a row, the order of a Pair.
-  auto state_row = [&](int kt, int r) { return 32 * (kt / 2) + 8 * g + 4 * (kt % 2) + r; };
-  f32x4 st[NKT][NV];
-  {
-    const float* from = !OUT ? nullptr : seg_m == 0 ? (m.first ? m.first + bh * state : nullptr)
-                                                    : m.seg + (int64_t(seg_m - 1) * BH + bh) * state;
-#pragma unroll
-    for (int kt = 0; kt < NKT; ++kt)
-#pragma unroll
-      for (int n = 0; n < NV; ++n)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = state_row(kt, r), col = c0 + wc0 + 16 * n + c;
-          st[kt][n][r] = from && row < m.dx && col < m.dz ? from[row * m.sr + col * m.sc] : 0.0f;
-        }
-  }
-
-  uint4 rx[OUT ? S::NX : 1], ry[S::NX], rz[S::NZ], rw[MASS ? S::NZ : 1];
-  float rg = 0.0f;
-  auto first_token = [&](int ci) { return t0 + (REV ? nc - 1 - ci : ci) * C; };
-  auto fetch = [&](int ci) {
-    const int tb = first_token(ci);
-    if constexpr (OUT) load_tile<BF, S::DX, THREADS>(m.x, xb, m.dx, 0, tb, end, rx);
-    load_tile<BF, S::DX, THREADS>(m.y, yb, m.dx, 0, tb, end, ry);
-    load_tile<BF, S::BV, THREADS>(m.z, zb, m.dz, c0, tb, end, rz);
-    if constexpr (MASS != 0) load_tile<BF, S::BV, THREADS>(m.w, wb, m.dz, c0, tb, end, rw);
-  };
-  auto fetch_decay = [&](int ci) {
-    const int t = first_token(ci) + lane;
-    rg = lane < C && t < end ? gb[int64_t(t) * p.gt] : 0.0f;
-  };
-
-  if (nc > 0) {
-    fetch(0);
-    if (wave == kDecayWave) fetch_decay(0);
-  }
-  if constexpr (MASS == 1) {
-    // What the decays behind an earlier segment carry in all: the state against its adjoint, both in
-    // memory at the segment's start. Between here and its end the carried sum is kept by differences.
-    if (seg_m > 0) {
-      const float* adj = p.m[1].seg + (int64_t(p.segments - 1 - seg_m) * BH + bh) * state;
-      double s = 0.0;
-#pragma unroll
-      for (int kt = 0; kt < NKT; ++kt)
-#pragma unroll
-        for (int n = 0; n < NV; ++n)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int row = state_row(kt, r), col = c0 + wc0 + 16 * n + c;
-            if (row < m.dx && col < m.dz) s += double(st[kt][n][r]) * double(adj[row * m.sr + col * m.sc]);
-          }
-      s = lane_of(prefix_sum(s, lane), 63);
-      if (lane == 0) l.cross[wave] = s;
-      __syncthreads();
-      if (tid == 0) {
-        s = 0.0;
-        for (int i = 0; i < W; ++i) s += l.cross[i];
-        m.cross[(int64_t(cb) * BH + bh) * p.segments + seg] = s;
-      }
-    }
-  }
-  if (tid < 2) l.odd[tid] = 0;
-  float decays = 1.0f;
-  if (nc > 0 && wave == kDecayWave) {
-    chunk_decays<REV, C>(l.dec[0], rg, m.scale_src, lane);
-    if (nc > 1) fetch_decay(1);
-  }
-  for (int ci = 0; ci < nc; ++ci) {
-    const int tb = first_token(ci);
-    typename S::Decays& dec = l.dec[ci & 1];
-    __syncthreads();
-    if constexpr (OUT) store_tile<BF, S::DX, THREADS>(l.x, S::SX, rx);
-    store_tile<BF, S::DX, THREADS>(l.y, S::SY, ry);
-    if constexpr (OUT) {
-      // An infinity or NaN in z times a score of zero would reach rows that do not see its token: such
-      // values are left out of the products and added at the end to what does see it.
-      bool fine = true;
-#pragma unroll
-      for (int n = 0; n < S::NZ; ++n) fine = fine && O::finite(rz[n]);
-      if (__builtin_expect(!fine, 0)) {
-        l.odd[ci & 1] = 1;
-#pragma unroll
-        for (int n = 0; n < S::NZ; ++n) rz[n] = O::finite_part(rz[n]);
-      }
-    }
-    store_tile<BF, S::BV, THREADS>(l.z, S::SZ, rz);
-    if constexpr (MASS != 0) store_tile<BF, S::BV, THREADS>(l.w, S::SW, rw);
-    __syncthreads();
-    if (ci + 1 < nc) fetch(ci + 1);
-    const float total = dec.total;
-
-    f32x4 acc[OUT ? NV : 1][OUT ? CT : 1];  // out transposed: column wc0 + 16 n + 4 g + r, row 16 it + c
-    if constexpr (OUT) {
-      // scores: the tiles on and on one side of the diagonal, in turn over the waves, as [row][source]
-      for (int q = wave; q < S::TILES; q += W) {
-        int hi = 0, lo = q;
-        while (lo > hi) lo -= ++hi;
-        const int it = REV ? lo : hi, jt = REV ? hi : lo;
-        const int row = 16 * it + c;
-        f32x4 s = zero4();
-#pragma unroll
-        for (int k2 = 0; k2 < NKT / 2; ++k2)
-          if (k2 < nk2)
-            s = O::mma(O::row_pair(l.y + (16 * jt + c) * S::SY + 32 * k2, g),
-                       O::row_pair(l.x + row * S::SX + 32 * k2, g), s);
-        const float2 gi = dec.g[row];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = 16 * jt + 4 * g + r;
-          const float2 gj = dec.g[j];
-          const float d = (gi.x - gj.x) + (gi.y - gj.y);
-          const bool seen = REV ? j >= row : j <= row;
-          s[r] = seen ? s[r] * m.scale_src * exp2_hw(REV ? -d : d) : 0.0f;
-        }
-        if constexpr (BF) {
-          Pair parts[O::kScore];
-          O::template split<O::kScore>(s, s, parts);
-#pragma unroll
-          for (int n = 0; n < O::kScore; ++n)
-            *reinterpret_cast<uint2*>(l.score[n] + row * S::SP + 16 * jt + 4 * g) = make_uint2(parts[n].x, parts[n].y);
-        } else {
-          O::put4(l.score[0] + row * S::SP + 16 * jt + 4 * g, s);
-        }
-        if constexpr (MASS == 1) {
-          // what a row takes from a source: decay (x_i . y_j) (w_i . z_j), this workgroup's columns of the second
-          f32x4 a = zero4();
-#pragma unroll
-          for (int k2 = 0; k2 < S::BV / 32; ++k2)
-            a = O::mma(O::row_pair(l.z + (16 * jt + c) * S::SZ + 32 * k2, g),
-                       O::row_pair(l.w + row * S::SW + 32 * k2, g), a);
-          float sum = 0.0f, before[4];  // of the lane's sources, and of those before each
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            before[r] = sum;
-            sum += 16 * jt + 4 * g + r < row ? a[r] * s[r] * m.scale_out : 0.0f;
-          }
-          float to = sum, u = __shfl_up(to, 16);  // ... of the lane groups up to this one
-          if (g >= 1) to += u;
-          u = __shfl_up(to, 32);
-          if (g >= 2) to += u;
-          if (g == 3) l.row_tile[ci & 1][jt][row] = to;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float v = group_sum(16 * jt + 4 * g + r <= row ? (to - sum) + before[r] : 0.0f);
-            if (c == 15) l.col_tile[ci & 1][q][4 * g + r] = v;
-          }
-        }
-      }
-      if (wave == kDecayWave && ci + 1 < nc) {
-        chunk_decays<REV, C>(l.dec[(ci + 1) & 1], rg, m.scale_src, lane);
-        if (ci + 2 < nc) fetch_decay(ci + 2);
-      }
-      if constexpr (MASS != 0) {
-        if (wave == kMassWave && ci > 0)
-          chunk_mass<REV, MASS, CT, S::TILES>(p, m, l, (ci - 1) & 1, W, first_token(ci - 1), t1, cb, bh, lane);
-        if (m.chunk_decay && cb == 0 && tid == 0)
-          m.chunk_decay[int64_t(bh) * ((p.T + C - 1) / C) + tb / C] = total;
-      }
-#pragma unroll
-      for (int n = 0; n < NV; ++n)
-#pragma unroll
-        for (int it = 0; it < CT; ++it) acc[n][it] = zero4();
-      // rows against the state
-#pragma unroll
-      for (int k2 = 0; k2 < NKT / 2; ++k2) {
-        if (k2 < nk2) {
-          Pair sp[NV][kRead];
-#pragma unroll
-          for (int n = 0; n < NV; ++n) O::template split<kRead>(st[2 * k2][n], st[2 * k2 + 1][n], sp[n]);
-#pragma unroll
-          for (int it = 0; it < CT; ++it) {
-            const Pair x = O::row_pair(l.x + (16 * it + c) * S::SX + 32 * k2, g);
-#pragma unroll
-            for (int n = 0; n < NV; ++n)
-#pragma unroll
-              for (int q = kRead - 1; q >= 0; --q) acc[n][it] = O::mma(sp[n][q], x, acc[n][it]);
-          }
-        }
-      }
-#pragma unroll
-      for (int it = 0; it < CT; ++it) {
-        const float f = dec.row[16 * it + c];
-        float mass = 0.0f;
-#pragma unroll
-        for (int n = 0; n < NV; ++n) {
-          acc[n][it] *= f;
-          if constexpr (MASS != 0) {
-            const f32x4 w = O::four(l.w + (16 * it + c) * S::SW + wc0 + 16 * n + 4 * g);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) mass += acc[n][it][r] * w[r];
-          }
-        }
-        if constexpr (MASS != 0) {
-          mass += __shfl_xor(mass, 16);
-          mass += __shfl_xor(mass, 32);
-          if (g == 0) l.part[ci & 1][wave][16 * it + c] = mass * m.scale_out;
-        }
-      }
-      __syncthreads();
-      if (tid == 0) l.odd[(ci + 1) & 1] = 0;
-      __builtin_amdgcn_sched_barrier(0);
-    } else if (wave == kDecayWave && ci + 1 < nc) {
-      chunk_decays<REV, C>(l.dec[(ci + 1) & 1], rg, m.scale_src, lane);
-      if (ci + 2 < nc) fetch_decay(ci + 2);
-    }
-
-    // sources: into the rows of the chunk, and into the state
-#pragma unroll
-    for (int kt = 0; kt < NKT; ++kt)
-#pragma unroll
-      for (int n = 0; n < NV; ++n) st[kt][n] *= total;
-    decays *= total;
-#pragma unroll
-    for (int j2 = 0; j2 < CT / 2; ++j2) {
-      __builtin_amdgcn_sched_barrier(0);  // one half's reads at a time: both at once do not fit the registers
-      Pair z[NV], zs[NV][O::kState];
-#pragma unroll
-      for (int n = 0; n < NV; ++n) {
-        z[n] = O::column_pair(l.z, S::SZ, 32 * j2, O::columns(wc0 + 16 * n, c), g, c);
-        const f32x4 f0 = *reinterpret_cast<const f32x4*>(dec.src + 32 * j2 + 8 * g);
-        const f32x4 f1 = *reinterpret_cast<const f32x4*>(dec.src + 32 * j2 + 8 * g + 4);
-        O::template split<O::kState>(O::low(z[n]) * f0, O::high(z[n]) * f1, zs[n]);
-      }
-      if constexpr (OUT) {
-#pragma unroll
-        for (int it = 0; it < CT; ++it) {
-          if (REV ? it <= 2 * j2 + 1 : it >= 2 * j2) {
-            // the one tile of a pair beyond the diagonal was not written
-            const bool none = REV ? it == 2 * j2 + 1 && g < 2 : it == 2 * j2 && g >= 2;
-#pragma unroll
-            for (int q = O::kScore - 1; q >= 0; --q) {
-              Pair s = O::row_pair(l.score[q] + (16 * it + c) * S::SP + 32 * j2, g);
-              if (none) s = Pair{};
-#pragma unroll
-              for (int n = 0; n < NV; ++n) acc[n][it] = O::mma(z[n], s, acc[n][it]);
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int kt = 0; kt < NKT; ++kt) {
-        if (kt / 2 < nk2) {
-          const Pair y = O::column_pair(l.y, S::SY, 32 * j2, O::state_rows(32 * (kt / 2) + 4 * (kt % 2), c), g, c);
-#pragma unroll
-          for (int n = 0; n < NV; ++n)
-#pragma unroll
-            for (int q = O::kState - 1; q >= 0; --q) st[kt][n] = O::mma(y, zs[n][q], st[kt][n]);
-        }
-      }
-    }
-
-    if constexpr (OUT) {
-      if (__builtin_expect(l.odd[ci & 1] != 0, 0)) {
-        const int rare = anew(lane), c = rare & 15, g = rare >> 4, wc0 = 16 * NV * (anew(tid) >> 6);
-        auto state_row = [&](int kt, int r) { return 32 * (kt / 2) + 8 * g + 4 * (kt % 2) + r; };
-        auto value = [&](int j, int col) {
-          return tb + j < end && col < m.dz ? O::one(zb[int64_t(tb + j) * m.z.st + int64_t(col) * m.z.sd]) : 0.0f;
-        };
-        auto odd = [](float v) { return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u; };
-#pragma unroll 1
-        for (int j = 0; j < C; ++j) {
-#pragma unroll
-          for (int n = 0; n < NV; ++n) {
-            // selects, not branches: the accumulators in divergent code cost the whole kernel registers
-            const float u = value(j, c0 + wc0 + 16 * n + c), w = dec.src[j] * u;
-#pragma unroll
-            for (int kt = 0; kt < NKT; ++kt)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) st[kt][n][r] += odd(u) ? O::one(l.y[j * S::SY + state_row(kt, r)]) * w : 0.0f;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float v = value(j, c0 + wc0 + 16 * n + 4 * g + r);
-#pragma unroll
-              for (int it = 0; it < CT; ++it) {
-                const int row = 16 * it + c;
-                const float s = O::one(l.score[0][row * S::SP + j]) * v;
-                acc[n][it][r] += odd(v) && (REV ? j >= row : j <= row) ? s : 0.0f;
-              }
-            }
-          }
-        }
-      }
-      const bool whole = (m.dz & 3) == 0;
-      const int again = anew(tid), c = again & 15, g = again >> 4 & 3, wc0 = 16 * NV * (again >> 6);
-#pragma unroll
-      for (int it = 0; it < CT; ++it) {
-        const int t = tb + 16 * it + c;
-        if (t < t1) {
-          const int64_t at = ((int64_t(b) * p.T + t) * p.H + h) * m.dz;
-#pragma unroll
-          for (int n = 0; n < NV; ++n) {
-            const int col = c0 + wc0 + 16 * n + 4 * g;
-            f32x4 v = acc[n][it] * m.scale_out;
-            if (t >= len) v = zero4();
-            if (whole && col < m.dz) {
-              if (!BF || m.out_f32) *reinterpret_cast<f32x4*>(static_cast<float*>(m.out) + at + col) = v;
-              else Op<true>::put4(static_cast<uint16_t*>(m.out) + at + col, v);
-            } else {
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                if (col + r < m.dz) {
-                  if (!BF || m.out_f32) static_cast<float*>(m.out)[at + col + r] = v[r];
-                  else static_cast<uint16_t*>(m.out)[at + col + r] = f32_to_bf16_rne(v[r]);
-                }
-            }
-          }
-        }
-      }
-    }
-  }
-
-  if constexpr (OUT) {
-    // tokens past the row's length, in chunks that were not marched
-    const int from = t0 + nc * C;
-    const int width = min(S::BV, m.dz - c0), rest = max(t1 - from, 0);
-    for (int q = tid; q < rest * width; q += THREADS) {
-      const int64_t at = ((int64_t(b) * p.T + from + q / width) * p.H + h) * m.dz + c0 + q % width;
-      if (!BF || m.out_f32) static_cast<float*>(m.out)[at] = 0.0f;
-      else static_cast<uint16_t*>(m.out)[at] = 0;
-    }
-    if constexpr (MASS != 0) {
-      const int64_t mb = (int64_t(cb) * BH + bh);
-      const int chunks = (p.T + C - 1) / C;
-      if (nc > 0) {
-        __syncthreads();
-        if (wave == kMassWave)
-          chunk_mass<REV, MASS, CT, S::TILES>(p, m, l, (nc - 1) & 1, W, first_token(nc - 1), t1, cb, bh, lane);
-      }
-      for (int q = tid; q < rest; q += THREADS) m.mass[mb * p.T + from + q] = 0.0f;
-      for (int q = tid; q < (rest + C - 1) / C; q += THREADS) {
-        m.mass_chunk[mb * chunks + from / C + q] = 0.0f;
-        if (m.chunk_decay && cb == 0) m.chunk_decay[int64_t(bh) * chunks + from / C + q] = 1.0f;
-      }
-    }
-  }
-
-  float* to = OUT ? (seg_m == p.segments - 1 && m.last ? m.last + bh * state : nullptr)
-                  : m.seg + (int64_t(seg_m) * BH + bh) * state;
-  if (to) {
-#pragma unroll
-    for (int kt = 0; kt < NKT; ++kt)
-#pragma unroll
-      for (int n = 0; n < NV; ++n)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = state_row(kt, r), col = c0 + wc0 + 16 * n + c;
-          if (row < m.dx && col < m.dz) to[row * m.sr + col * m.sc] = st[kt][n][r];
-        }
-  }
-  if (!OUT && tid == 0 && cb == 0) m.seg_decay[int64_t(seg_m) * BH + bh] = decays;
-}
-
-template <bool BF, int NKT, int NV, int W>
-__global__ __launch_bounds__(W * kWave) void march_forward(DaParams p) {
-  using S = Shape<BF, NKT, NV, W>;
-  __shared__ typename S::Out l;
-  march<S, BF, NKT, NV, W, false, 0, true>(p, p.m[0], blockIdx.x, l);
-}
-
-// blockIdx.y picks the march of a gradient: 0 grad_q, 1 grad_k, 2 grad_v.
-template <bool BF, int NKT, int NV, int W>
-__global__ __launch_bounds__(W * kWave) void march_gradient(DaParams p) {
-  using S = Shape<BF, NKT, NV, W>;
-  __shared__ typename S::Mass l;
-  if (blockIdx.y == 0) march<S, BF, NKT, NV, W, false, 1, true>(p, p.m[0], blockIdx.x, l);
-  else if (blockIdx.y == 1) march<S, BF, NKT, NV, W, true, 2, true>(p, p.m[1], blockIdx.x, l);
-  else march<S, BF, NKT, NV, W, true, 0, true>(p, p.m[2], blockIdx.x, l);
-}
-
-// Each segment's own state. A gradient needs two: the state (march 0's) and its
-// adjoint (march 1's, which march 2 shares).
-template <bool BF, int NKT, int NV, int W>
-__global__ __launch_bounds__(W * kWave) void march_local(DaParams p) {
-  using S = Shape<BF, NKT, NV, W>;
-  __shared__ typename S::Local l;
-  if (blockIdx.y == 0) march<S, BF, NKT, NV, W, false, 0, false>(p, p.m[0], blockIdx.x, l);
-  else march<S, BF, NKT, NV, W, true, 0, false>(p, p.m[1], blockIdx.x, l);
-}
+constexpr int kThreads = 256;
 
 // Segment m's entry, its own state so far, becomes the state at the start of segment m + 1.
 __global__ __launch_bounds__(kThreads) void carry(DaParams p) {
@@ -983,52 +190,24 @@ __global__ __launch_bounds__(kThreads) void step_kernel(DaStep p) {
 
 // ---------------------------------------------------------------- launches
 
-int tile_class(int d) { return d <= 32 ? 2 : d <= 64 ? 4 : d <= 128 ? 8 : 16; }
-
-template <bool BF, int NKT, int NV, int W>
-hipError_t run_marches(const DaParams& p, hipStream_t stream) {
-  constexpr int BV = 16 * NV * W, kAll = W * kWave;
-  const int64_t BH = int64_t(p.B) * p.H;
-  int ncb = 1;
-  for (int i = 0; i < p.marches; ++i) ncb = std::max(ncb, (p.m[i].dz + BV - 1) / BV);
-  const int states = p.marches == 1 ? 1 : 2;
-  if (p.segments > 1) {
-    march_local<BF, NKT, NV, W><<<dim3(unsigned(ncb * BH * (p.segments - 1)), states), kAll, 0, stream>>>(p);
-    const int64_t n = BH * p.dk * p.dv;
-    carry<<<dim3(unsigned((n + kThreads - 1) / kThreads), states), kThreads, 0, stream>>>(p);
-  }
-  const dim3 grid(unsigned(ncb * BH * p.segments), p.marches);
-  if (p.marches == 1) march_forward<BF, NKT, NV, W><<<grid, kAll, 0, stream>>>(p);
-  else march_gradient<BF, NKT, NV, W><<<grid, kAll, 0, stream>>>(p);
-  return hipGetLastError();
-}
-
-template <bool BF>
-hipError_t run_widths(const DaParams& p, hipStream_t stream) {
-  const int wide = std::max(p.dk, p.dv);
-  switch (tile_class(wide)) {
-    case 2: return run_marches<BF, 2, 1, 4>(p, stream);
-    case 4: return run_marches<BF, 4, 1, 4>(p, stream);
-    case 8: return run_marches<BF, 8, 1, 8>(p, stream);
-    default: return run_marches<BF, 16, 1, 8>(p, stream);
-  }
-}
-
 }  // namespace
 
 int decay_attention_chunk(bool bf16) { return bf16 ? Op<true>::C : Op<false>::C; }
 
-int decay_attention_column_blocks(int dx, int dz) {
-  const int bv = tile_class(std::max(dx, dz)) >= 8 ? 128 : 64;
+int march_tiles(int dx) { return dx <= 32 ? 2 : dx <= 64 ? 4 : dx <= 128 ? 8 : 16; }
+int march_waves(int dz) { return dz <= 64 ? 4 : 8; }
+
+int decay_attention_column_blocks(int dz) {
+  const int bv = 16 * march_waves(dz);
   return (dz + bv - 1) / bv;
 }
 
 void decay_attention_split(DaParams& p) {
   const int C = decay_attention_chunk(p.bf16 != 0);
   const int64_t chunks = (int64_t(p.T) + C - 1) / C;
-  const int64_t groups = std::max<int64_t>(1, int64_t(p.B) * p.H * decay_attention_column_blocks(p.dk, p.dv));
-  // one workgroup a compute unit (two of the narrow states'), segments of two chunks at least
-  const int64_t resident = tile_class(std::max(p.dk, p.dv)) >= 8 ? 1 : 2;
+  const int64_t groups = std::max<int64_t>(1, int64_t(p.B) * p.H * decay_attention_column_blocks(p.dv));
+  // one workgroup a compute unit (two of four waves), segments of two chunks at least
+  const int64_t resident = march_waves(p.dv) == 8 ? 1 : 2;
   const int64_t want = resident * device_cu_count() / groups;
   const int64_t segments = std::max<int64_t>(1, std::min(want, chunks / 2));
   const int64_t per = std::max<int64_t>(1, (chunks + segments - 1) / segments);
@@ -1037,7 +216,30 @@ void decay_attention_split(DaParams& p) {
 }
 
 hipError_t launch_decay_attention(const DaParams& p, hipStream_t stream) {
-  return p.bf16 ? run_widths<true>(p, stream) : run_widths<false>(p, stream);
+  // 16-byte pieces at 32-bit offsets within a chunk
+  const int64_t e = p.bf16 ? 2 : 4, chunk = decay_attention_chunk(p.bf16 != 0), most = int64_t(1) << 31;
+  bool vec = true;
+  for (int i = 0; i < p.marches; ++i) {
+    for (const HeadView* v : {&p.m[i].x, &p.m[i].y, &p.m[i].z, &p.m[i].w})
+      vec = vec && (!v->p || (v->vec && v->st >= 0 && v->st < most / (chunk * e)));
+    vec = vec && int64_t(p.H) * p.m[i].dz < most / (chunk * 4);
+  }
+  const auto launch = p.bf16 ? (vec ? launch_marches_bf16 : launch_marches_bf16_any)
+                             : (vec ? launch_marches_f32 : launch_marches_f32_any);
+  hipError_t err = hipSuccess;
+  if (p.segments > 1) {
+    const int states = p.marches == 1 ? 1 : 2;
+    err = launch(p, 0, states, true, stream);
+    const int64_t n = int64_t(p.B) * p.H * p.dk * p.dv;
+    if (err == hipSuccess) carry<<<dim3(unsigned((n + kThreads - 1) / kThreads), states), kThreads, 0, stream>>>(p);
+  }
+  if (err != hipSuccess) return err;
+  if (p.marches == 1) return launch(p, 0, 1, false, stream);
+  // grad_v's march holds the state the other way round: the same kernel where keys and values are of one class
+  if (march_tiles(p.dk) == march_tiles(p.dv) && march_waves(p.dk) == march_waves(p.dv))
+    return launch(p, 0, 3, false, stream);
+  err = launch(p, 0, 2, false, stream);
+  return err == hipSuccess ? launch(p, 2, 1, false, stream) : err;
 }
 
 hipError_t launch_decay_grad(const DaDecayGrad& p, hipStream_t stream) {

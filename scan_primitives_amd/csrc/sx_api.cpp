@@ -1285,7 +1285,7 @@ GradPieces carve_gradient(Carve& c, const DecayShapes& s, sx::DaParams& p) {
   const int chunk = sx::decay_attention_chunk(p.bf16 != 0);
   const int64_t BH = s.B * s.H;
   g.chunks = int((s.T + chunk - 1) / chunk);
-  g.blocks = sx::decay_attention_column_blocks(p.dv, p.dk);
+  g.blocks = sx::decay_attention_column_blocks(p.dk);
   g.rows = c.take<float>(g.blocks * BH * s.T);
   g.sources = c.take<float>(g.blocks * BH * s.T);
   g.rows_chunk = c.take<float>(g.blocks * BH * g.chunks);

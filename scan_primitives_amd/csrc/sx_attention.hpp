@@ -65,8 +65,15 @@ struct DaParams {
 };
 
 int decay_attention_chunk(bool bf16);
-// Columns of z that one workgroup holds, and workgroups a head needs for `dz` columns.
-int decay_attention_column_blocks(int dx, int dz);
+// Workgroups a head needs for `dz` columns.
+int decay_attention_column_blocks(int dz);
+// A march's shape: 16-row tiles of the state (2, 4, 8 or 16), and waves of 16 columns (4 or 8).
+int march_tiles(int dx);
+int march_waves(int dz);
+hipError_t launch_marches_bf16(const DaParams& p, int first, int count, bool local, hipStream_t stream);
+hipError_t launch_marches_bf16_any(const DaParams& p, int first, int count, bool local, hipStream_t stream);
+hipError_t launch_marches_f32(const DaParams& p, int first, int count, bool local, hipStream_t stream);
+hipError_t launch_marches_f32_any(const DaParams& p, int first, int count, bool local, hipStream_t stream);
 // How the tokens are split: sets segments and seg_tokens.
 void decay_attention_split(DaParams& p);
 hipError_t launch_decay_attention(const DaParams& p, hipStream_t stream);
