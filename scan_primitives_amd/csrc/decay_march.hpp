@@ -241,110 +241,71 @@ __device__ __forceinline__ const E* head_base(const HeadView& v, int b, int h) {
 }
 
 // A workgroup's tile of C tokens and W columns from c0, on its way from memory to LDS: a thread's
-// share of it in registers. Zero where a token or a column (from `d` on) does not exist. VEC: 16-byte
-// pieces at 32-bit offsets from the tile's first token, else one element at a time.
+// share of it in registers. Zero where a token or a column (from `d` on) does not exist: there the
+// load reads the last token or the first columns instead, and `store` writes zero. (A load under a
+// condition would have to be waited for where its lanes join the others again.) VEC: 16-byte pieces
+// at 32-bit offsets from the tile's first token, else one element at a time.
 template <bool BF, int W, int THREADS, bool VEC>
-struct Tile;
-
-template <bool BF, int W, int THREADS>
-struct Tile<BF, W, THREADS, true> {
+struct Tile {
   using O = Op<BF>;
   using E = typename O::E;
-  static constexpr int PR = W / O::kPiece, STEP = THREADS / PR, N = (O::C + STEP - 1) / STEP;
+  using R = std::conditional_t<VEC, uint4, E>;
+  static constexpr int PIECE = VEC ? O::kPiece : 1, PR = W / PIECE, STEP = THREADS / PR;
+  static constexpr int N = (O::C + STEP - 1) / STEP;
   static_assert(THREADS % PR == 0);
   const char* base;
-  int64_t st;      // bytes a token
-  uint32_t off;    // of the thread's first piece
-  int row, col;    // row, and column within the tile
-  bool ok;
-  uint4 r[N];
+  int64_t st;        // bytes a token
+  int64_t col_any;   // bytes to the thread's column
+  int row, col;      // of the thread's first piece in the tile
+  bool ok;           // its columns exist
+  R r[N];
 
   __device__ __forceinline__ void init(const HeadView& v, int b, int h, int d, int c0) {
     base = reinterpret_cast<const char*>(head_base<E>(v, b, h));
     st = v.st * int64_t(sizeof(E));
     row = int(threadIdx.x) / PR;
-    col = int(threadIdx.x) % PR * O::kPiece;
+    col = int(threadIdx.x) % PR * PIECE;
     ok = c0 + col < d;
-    off = uint32_t(row) * uint32_t(st) + uint32_t(c0 + col) * uint32_t(sizeof(E));
-#pragma unroll
-    for (int n = 0; n < N; ++n) r[n] = make_uint4(0, 0, 0, 0);
+    col_any = ok ? int64_t(c0 + col) * (VEC ? 1 : v.sd) * int64_t(sizeof(E)) : 0;
   }
-  // tokens tb .. of which `left` exist
+  // tokens tb .. of which `left` > 0 exist
   __device__ __forceinline__ void fetch(int tb, int left) {
     const char* at = base + tb * st;
-    if (left >= O::C) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int t = min(row + n * STEP, left - 1);
+      if constexpr (VEC) r[n] = *reinterpret_cast<const R*>(at + (uint32_t(t) * uint32_t(st) + uint32_t(col_any)));
+      else r[n] = *reinterpret_cast<const R*>(at + t * st + col_any);
+    }
+  }
+  __device__ __forceinline__ void mend(int left, bool columns) {
+    if (left < O::C || columns) {
 #pragma unroll
       for (int n = 0; n < N; ++n)
-        if (ok && (O::C % STEP == 0 || row + n * STEP < O::C))
-          r[n] = *reinterpret_cast<const uint4*>(at + n * STEP * st + off);
-    } else {
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        r[n] = make_uint4(0, 0, 0, 0);
-        if (ok && row + n * STEP < left) r[n] = *reinterpret_cast<const uint4*>(at + n * STEP * st + off);
-      }
+        if (!ok || row + n * STEP >= left) r[n] = R{};
     }
   }
   __device__ __forceinline__ void store(E* tile, int stride) const {
 #pragma unroll
     for (int n = 0; n < N; ++n)
       if (O::C % STEP == 0 || row + n * STEP < O::C)
-        *reinterpret_cast<uint4*>(tile + (row + n * STEP) * stride + col) = r[n];
+        *reinterpret_cast<R*>(tile + (row + n * STEP) * stride + col) = r[n];
   }
   __device__ __forceinline__ bool finite() const {
     bool fine = true;
-#pragma unroll
-    for (int n = 0; n < N; ++n) fine = fine && O::finite(r[n]);
-    return fine;
-  }
-  __device__ __forceinline__ void keep_finite() {
-#pragma unroll
-    for (int n = 0; n < N; ++n) r[n] = O::finite_part(r[n]);
-  }
-};
-
-template <bool BF, int W, int THREADS>
-struct Tile<BF, W, THREADS, false> {
-  using O = Op<BF>;
-  using E = typename O::E;
-  static constexpr int STEP = THREADS / W, N = (O::C + STEP - 1) / STEP;
-  static_assert(THREADS % W == 0);
-  const E* base;
-  int64_t st;
-  int row, col;
-  bool ok;
-  E r[N];
-
-  __device__ __forceinline__ void init(const HeadView& v, int b, int h, int d, int c0) {
-    row = int(threadIdx.x) / W;
-    col = int(threadIdx.x) % W;
-    ok = c0 + col < d;
-    st = v.st;
-    base = head_base<E>(v, b, h) + int64_t(c0 + col) * v.sd;
-  }
-  __device__ __forceinline__ void fetch(int tb, int left) {
-    const E* at = base + int64_t(tb + row) * st;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      r[n] = E(0);
-      if (ok && row + n * STEP < min(left, O::C)) r[n] = at[int64_t(n * STEP) * st];
+      if constexpr (VEC) fine = fine && O::finite(r[n]);
+      else fine = fine && (__float_as_uint(O::one(r[n])) & 0x7f800000u) != 0x7f800000u;
     }
-  }
-  __device__ __forceinline__ void store(E* tile, int stride) const {
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-      if (O::C % STEP == 0 || row + n * STEP < O::C) tile[(row + n * STEP) * stride + col] = r[n];
-  }
-  __device__ __forceinline__ bool finite() const {
-    bool fine = true;
-#pragma unroll
-    for (int n = 0; n < N; ++n) fine = fine && (__float_as_uint(O::one(r[n])) & 0x7f800000u) != 0x7f800000u;
     return fine;
   }
   __device__ __forceinline__ void keep_finite() {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      if ((__float_as_uint(O::one(r[n])) & 0x7f800000u) == 0x7f800000u) r[n] = E(0);
+    for (int n = 0; n < N; ++n) {
+      if constexpr (VEC) r[n] = O::finite_part(r[n]);
+      else if ((__float_as_uint(O::one(r[n])) & 0x7f800000u) == 0x7f800000u) r[n] = E(0);
+    }
   }
 };
 
@@ -488,6 +449,12 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
   // The state: tile kt holds rows 32 (kt / 2) + 8 g + 4 (kt % 2) + r, column c0 + wc0 + 16 n + c, so that the
   // rows of a lane in two tiles are eight in a row, the order of a Pair.
   auto state_row = [&](int kt, int r) { return 32 * (kt / 2) + 8 * g + 4 * (kt % 2) + r; };
+  const uint32_t sr = uint32_t(m.sr), sc = uint32_t(m.sc);  // of at most 256 x 256 floats
+  const uint32_t st_at = 8 * uint32_t(g) * sr + uint32_t(c0 + wc0 + c) * sc;
+  auto state_at = [&](int kt, int n, int r) {
+    return st_at + (32 * (kt / 2) + 4 * (kt % 2) + r) * sr + 16 * n * sc;
+  };
+  auto state_is = [&](int kt, int n, int r) { return state_row(kt, r) < m.dx && c0 + wc0 + 16 * n + c < m.dz; };
   f32x4 st[NKT][NV];
   {
     const float* from = !OUT ? nullptr : seg_m == 0 ? (m.first ? m.first + bh * state : nullptr)
@@ -497,10 +464,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
 #pragma unroll
       for (int n = 0; n < NV; ++n)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = state_row(kt, r), col = c0 + wc0 + 16 * n + c;
-          st[kt][n][r] = from && row < m.dx && col < m.dz ? from[row * m.sr + col * m.sc] : 0.0f;
-        }
+        for (int r = 0; r < 4; ++r) st[kt][n][r] = from && state_is(kt, n, r) ? from[state_at(kt, n, r)] : 0.0f;
   }
 
   Tile<BF, S::DX, THREADS, VEC> tx, ty;
@@ -538,10 +502,8 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
 #pragma unroll
         for (int n = 0; n < NV; ++n)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int row = state_row(kt, r), col = c0 + wc0 + 16 * n + c;
-            if (row < m.dx && col < m.dz) s += double(st[kt][n][r]) * double(adj[row * m.sr + col * m.sc]);
-          }
+          for (int r = 0; r < 4; ++r)
+            if (state_is(kt, n, r)) s += double(st[kt][n][r]) * double(adj[state_at(kt, n, r)]);
       s = lane_of(prefix_sum(s, lane), 63);
       if (lane == 0) l.cross[wave] = s;
       __syncthreads();
@@ -562,8 +524,14 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     const int tb = first_token(ci);
     typename S::Decays& dec = l.dec[ci & 1];
     __syncthreads();
-    if constexpr (OUT) tx.store(l.x, S::SX);
+    const int left = end - tb;
+    if constexpr (OUT) {
+      tx.mend(left, m.dx < S::DX);
+      tx.store(l.x, S::SX);
+    }
+    ty.mend(left, m.dx < S::DX);
     ty.store(l.y, S::SY);
+    tz.mend(left, m.dz < c0 + S::BV);
     if constexpr (OUT) {
       // An infinity or NaN in z times a score of zero would reach rows that do not see its token: such
       // values are left out of the products and added at the end to what does see it.
@@ -573,7 +541,10 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       }
     }
     tz.store(l.z, S::SZ);
-    if constexpr (MASS != 0) tw.store(l.w, S::SW);
+    if constexpr (MASS != 0) {
+      tw.mend(left, m.dz < c0 + S::BV);
+      tw.store(l.w, S::SW);
+    }
     __syncthreads();
     if (ci + 1 < nc) fetch(ci + 1);
     const float total = dec.total;
@@ -845,10 +816,8 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
 #pragma unroll
       for (int n = 0; n < NV; ++n)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = state_row(kt, r), col = c0 + wc0 + 16 * n + c;
-          if (row < m.dx && col < m.dz) to[row * m.sr + col * m.sc] = st[kt][n][r];
-        }
+        for (int r = 0; r < 4; ++r)
+          if (state_is(kt, n, r)) to[state_at(kt, n, r)] = st[kt][n][r];
   }
   if (!OUT && tid == 0 && cb == 0) m.seg_decay[int64_t(seg_m) * BH + bh] = decays;
 }
