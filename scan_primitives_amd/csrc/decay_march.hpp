@@ -40,10 +40,10 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 template <bool BF>
 struct Op;
 
-// bf16 operands. A Pair is what a lane brings to a product contracted over 32:
-// the eight values 8g .. 8g + 7 of its row (or column) in lane group g, on
-// v_mfma_f32_16x16x32_bf16. The instruction's own order of the 32 does not
-// matter, as both operands use the same one.
+// bf16 operands. A Pair is what a lane brings to a product contracted over 32 on
+// v_mfma_f32_16x16x32_bf16: in lane group g the values 4g .. 4g + 3 of each of two
+// 16-wide tiles. The instruction's own order of the 32 does not matter, as both
+// operands use the same one.
 template <>
 struct Op<true> {
   using E = uint16_t;
@@ -92,23 +92,36 @@ struct Op<true> {
       }
     }
   }
-  // columns 8g .. 8g + 7 of a row
+  // 32 columns of a row from two tiles
   static __device__ __forceinline__ Pair row_pair(const E* row, int g) {
-    return *reinterpret_cast<const uint4*>(row + 8 * g);
-  }
-  // Rows j0 + 8g .. 8g + 7 of one column a lane, through the transposing read: lane c of a group
-  // addresses four columns of one row and receives column c of four rows. `col`: the lane's four.
-  static __device__ __forceinline__ Pair column_pair(const E* tile, int stride, int j0, int col, int g, int c) {
-    typedef s16x4_t __attribute__((address_space(3))) * lds4;
-    const E* p = tile + (j0 + 8 * g + (c >> 2)) * stride + col;
-    const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p)));
-    const uint2 b = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 4 * stride)));
+    const uint2 a = *reinterpret_cast<const uint2*>(row + 4 * g);
+    const uint2 b = *reinterpret_cast<const uint2*>(row + 16 + 4 * g);
     return make_uint4(a.x, a.y, b.x, b.y);
   }
-  // what column_pair takes for 16 columns in a row from col0 on ...
-  static __device__ __forceinline__ int columns(int col0, int c) { return col0 + 4 * (c & 3); }
-  // ... and for columns 8 (c / 4) + c % 4 from col0 on: the rows of a state tile
-  static __device__ __forceinline__ int state_rows(int col0, int c) { return col0 + 8 * (c & 3); }
+  // Where column `col` of x and of the scores stands in LDS: a lane's two fours side by side, so that a
+  // row is read by 16 bytes.
+  static __device__ __forceinline__ int paired(int col) {
+    return (col & ~31) | (col >> 2 & 3) * 8 | (col >> 4 & 1) * 4 | (col & 3);
+  }
+  static __device__ __forceinline__ void store_paired(E* row, int col, uint4 v) {
+    E* p = row + paired(col);
+    *reinterpret_cast<uint2*>(p) = make_uint2(v.x, v.y);
+    *reinterpret_cast<uint2*>(p + 8) = make_uint2(v.z, v.w);
+  }
+  static __device__ __forceinline__ Pair paired_row(const E* row, int g) { return row_eight(row, g); }
+  // 32 columns in the other order two rows may share: eight in a row a lane
+  static __device__ __forceinline__ Pair row_eight(const E* row, int g) {
+    return *reinterpret_cast<const uint4*>(row + 8 * g);
+  }
+  // Rows 4g .. of the tiles at j0 and j0 + 16, column col0 + c, through the transposing read: lane c of a
+  // group addresses four columns of one row and receives column c of four rows.
+  static __device__ __forceinline__ Pair column_pair(const E* tile, int stride, int j0, int col0, int g, int c) {
+    typedef s16x4_t __attribute__((address_space(3))) * lds4;
+    const E* p = tile + (j0 + 4 * g + (c >> 2)) * stride + col0 + 4 * (c & 3);
+    const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p)));
+    const uint2 b = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 16 * stride)));
+    return make_uint4(a.x, a.y, b.x, b.y);
+  }
   static __device__ __forceinline__ f32x4 low(Pair a) {
     return f32x4{__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u), __uint_as_float(a.y << 16),
                  __uint_as_float(a.y & 0xffff0000u)};
@@ -119,9 +132,17 @@ struct Op<true> {
     return low(make_uint4(a.x, a.y, 0, 0));
   }
   static __device__ __forceinline__ float one(E v) { return bf16_to_f32(v); }
-  static __device__ __forceinline__ bool finite(uint4 v) {
-    auto bad = [](uint32_t u) { return (u & 0x7f800000u) == 0x7f800000u || (u & 0x7f80u) == 0x7f80u; };
-    return !(bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w));
+  // the larger magnitudes of what was seen and of a piece, half by half, as bit patterns
+  typedef uint16_t halves __attribute__((ext_vector_type(2)));
+  static __device__ __forceinline__ uint32_t larger(uint32_t seen, uint4 v) {
+    auto most = [](uint32_t a, uint32_t b) {
+      return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(halves, a),
+                                                                    __builtin_bit_cast(halves, b & 0x7fff7fffu)));
+    };
+    return most(most(most(most(seen, v.x), v.y), v.z), v.w);
+  }
+  static __device__ __forceinline__ bool finite(uint32_t seen) {
+    return (seen & 0xffffu) < 0x7f80u && seen < 0x7f800000u;
   }
   // infinities and NaN taken out
   static __device__ __forceinline__ uint4 finite_part(uint4 v) {
@@ -160,23 +181,29 @@ struct Op<false> {
     out[0] = Pair{a, b};
   }
   static __device__ __forceinline__ Pair row_pair(const E* row, int g) {
-    return Pair{*reinterpret_cast<const f32x4*>(row + 8 * g), *reinterpret_cast<const f32x4*>(row + 8 * g + 4)};
+    return Pair{*reinterpret_cast<const f32x4*>(row + 4 * g), *reinterpret_cast<const f32x4*>(row + 16 + 4 * g)};
   }
-  static __device__ __forceinline__ Pair column_pair(const E* tile, int stride, int j0, int col, int g, int c) {
-    const E* p = tile + (j0 + 8 * g) * stride + col;
+  static __device__ __forceinline__ int paired(int col) { return col; }
+  static __device__ __forceinline__ void store_paired(E* row, int col, uint4 v) {
+    *reinterpret_cast<uint4*>(row + col) = v;
+  }
+  static __device__ __forceinline__ Pair paired_row(const E* row, int g) { return row_pair(row, g); }
+  static __device__ __forceinline__ Pair row_eight(const E* row, int g) { return row_pair(row, g); }
+  static __device__ __forceinline__ Pair column_pair(const E* tile, int stride, int j0, int col0, int g, int c) {
+    const E* p = tile + (j0 + 4 * g) * stride + col0 + c;
+    const E* q = p + 16 * stride;
     return Pair{f32x4{p[0], p[stride], p[2 * stride], p[3 * stride]},
-                f32x4{p[4 * stride], p[5 * stride], p[6 * stride], p[7 * stride]}};
+                f32x4{q[0], q[stride], q[2 * stride], q[3 * stride]}};
   }
-  static __device__ __forceinline__ int columns(int col0, int c) { return col0 + c; }
-  static __device__ __forceinline__ int state_rows(int col0, int c) { return col0 + 8 * (c >> 2) + (c & 3); }
   static __device__ __forceinline__ f32x4 low(Pair a) { return a.a; }
   static __device__ __forceinline__ f32x4 high(Pair a) { return a.b; }
   static __device__ __forceinline__ f32x4 four(const E* p) { return *reinterpret_cast<const f32x4*>(p); }
   static __device__ __forceinline__ float one(E v) { return v; }
-  static __device__ __forceinline__ bool finite(uint4 v) {
-    auto bad = [](uint32_t u) { return (u & 0x7f800000u) == 0x7f800000u; };
-    return !(bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w));
+  static __device__ __forceinline__ uint32_t larger(uint32_t seen, uint4 v) {
+    auto most = [](uint32_t a, uint32_t b) { return max(a, b & 0x7fffffffu); };
+    return most(most(most(most(seen, v.x), v.y), v.z), v.w);
   }
+  static __device__ __forceinline__ bool finite(uint32_t seen) { return seen < 0x7f800000u; }
   static __device__ __forceinline__ uint4 finite_part(uint4 v) {
     auto f = [](uint32_t u) { return (u & 0x7f800000u) == 0x7f800000u ? 0u : u; };
     return make_uint4(f(v.x), f(v.y), f(v.z), f(v.w));
@@ -195,20 +222,22 @@ struct Shape {
   static constexpr int TILES = CT * (CT + 1) / 2;  // tiles of scores on and on one side of the diagonal
   static constexpr int DX = 16 * NKT;              // widest x and y
   static constexpr int BV = 16 * NV * W;           // columns of z a workgroup holds: 16 NV a wave
-  // Row strides in elements. Tiles read by rows alone: 4 banks past a multiple of 64 bytes, so 16 rows
-  // meet no bank twice; those read by columns too: 12 past (bf16), which spreads the four rows of a
-  // transposing read as well.
-  static constexpr int kRowPad = O::kPiece, kColPad = BF ? 24 : 4;
+  // Row strides in elements. 64 banks of 4 bytes: with rows 4 banks past a multiple of 64, 16 rows read by
+  // 16 bytes meet no bank twice; with bf16 rows 8 past, neither do the eight rows of 32 bytes that half a
+  // wave's transposing read touches.
+  static constexpr int kRowPad = O::kPiece, kColPad = BF ? 16 : 4;
   static constexpr int SX = DX + kRowPad, SY = DX + kColPad, SZ = BV + kColPad, SW = BV + kRowPad, SP = C + kRowPad;
+  // y and z of two chunks at once, where they fit: the next chunk's arrive while this one's are read
+  static constexpr int NB = NKT == 16 ? 1 : 2;
   struct Decays {
     alignas(16) float2 g[C];   // running log2 decay, high and low part
-    alignas(16) float row[C];  // decay between the row and the state
+    alignas(16) float row[C];  // decay between the row and the state, times scale_out
     alignas(16) float src[C];  // decay between the source and the next state, times scale_src
     float total;
   };
   struct Local {  // what a segment's own state takes
-    alignas(16) E y[C * SY];
-    alignas(16) E z[C * SZ];
+    alignas(16) E y[NB][C * SY];
+    alignas(16) E z[NB][C * SZ];
     Decays dec[2];
     int odd[2];   // a chunk's z holds an infinity or NaN
   };
@@ -285,20 +314,24 @@ struct Tile {
         if (!ok || row + n * STEP >= left) r[n] = R{};
     }
   }
+  template <bool PAIRED = false>
   __device__ __forceinline__ void store(E* tile, int stride) const {
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      if (O::C % STEP == 0 || row + n * STEP < O::C)
-        *reinterpret_cast<R*>(tile + (row + n * STEP) * stride + col) = r[n];
+      if (O::C % STEP == 0 || row + n * STEP < O::C) {
+        E* to = tile + (row + n * STEP) * stride;
+        if constexpr (PAIRED && VEC) O::store_paired(to, col, r[n]);
+        else *reinterpret_cast<R*>(to + (PAIRED ? O::paired(col) : col)) = r[n];
+      }
   }
   __device__ __forceinline__ bool finite() const {
-    bool fine = true;
+    uint32_t seen = 0;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      if constexpr (VEC) fine = fine && O::finite(r[n]);
-      else fine = fine && (__float_as_uint(O::one(r[n])) & 0x7f800000u) != 0x7f800000u;
+      if constexpr (VEC) seen = O::larger(seen, r[n]);
+      else seen = max(seen, __float_as_uint(O::one(r[n])) & 0x7fffffffu);
     }
-    return fine;
+    return VEC ? O::finite(seen) : seen < 0x7f800000u;
   }
   __device__ __forceinline__ void keep_finite() {
 #pragma unroll
@@ -361,7 +394,7 @@ __device__ __forceinline__ float group_sum(float v) {
 
 // A chunk's decays from a lane's log decay gv (one wave; token tb + lane).
 template <bool REV, int C, typename Decays>
-__device__ __forceinline__ void chunk_decays(Decays& l, float gv, float scale_src, int lane) {
+__device__ __forceinline__ void chunk_decays(Decays& l, float gv, float scale_out, float scale_src, int lane) {
   gv = gv < -kMostLog ? -kMostLog : gv > kMostLog ? kMostLog : gv;
   // 64 bits: the difference of two running sums is the log decay between two tokens, and has to be
   // exact to f32 also behind a token that cut the state.
@@ -371,7 +404,7 @@ __device__ __forceinline__ void chunk_decays(Decays& l, float gv, float scale_sr
     const float hi = float(s);
     l.g[lane] = make_float2(hi, float(s - double(hi)));
     const float from_start = exp2_hw(hi), to_end = exp2_hw(float(total - s));
-    l.row[lane] = REV ? to_end : from_start;
+    l.row[lane] = (REV ? to_end : from_start) * scale_out;
     l.src[lane] = (REV ? from_start : to_end) * scale_src;
     if (lane == 0) l.total = exp2_hw(float(total));
   }
@@ -446,14 +479,11 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
 
   const float* gb = p.g + int64_t(b) * p.gb + int64_t(h) * p.gh;
 
-  // The state: tile kt holds rows 32 (kt / 2) + 8 g + 4 (kt % 2) + r, column c0 + wc0 + 16 n + c, so that the
-  // rows of a lane in two tiles are eight in a row, the order of a Pair.
-  auto state_row = [&](int kt, int r) { return 32 * (kt / 2) + 8 * g + 4 * (kt % 2) + r; };
+  // The state: tile kt holds rows 16 kt + 4 g + r, column c0 + wc0 + 16 n + c.
+  auto state_row = [&](int kt, int r) { return 16 * kt + 4 * g + r; };
   const uint32_t sr = uint32_t(m.sr), sc = uint32_t(m.sc);  // of at most 256 x 256 floats
-  const uint32_t st_at = 8 * uint32_t(g) * sr + uint32_t(c0 + wc0 + c) * sc;
-  auto state_at = [&](int kt, int n, int r) {
-    return st_at + (32 * (kt / 2) + 4 * (kt % 2) + r) * sr + 16 * n * sc;
-  };
+  const uint32_t st_at = 4 * uint32_t(g) * sr + uint32_t(c0 + wc0 + c) * sc;
+  auto state_at = [&](int kt, int n, int r) { return st_at + (16 * kt + r) * sr + 16 * n * sc; };
   auto state_is = [&](int kt, int n, int r) { return state_row(kt, r) < m.dx && c0 + wc0 + 16 * n + c < m.dz; };
   f32x4 st[NKT][NV];
   {
@@ -514,23 +544,15 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       }
     }
   }
-  if (tid < 2) l.odd[tid] = 0;
-  float decays = 1.0f;
-  if (nc > 0 && wave == kDecayWave) {
-    chunk_decays<REV, C>(l.dec[0], rg, m.scale_src, lane);
-    if (nc > 1) fetch_decay(1);
-  }
-  for (int ci = 0; ci < nc; ++ci) {
-    const int tb = first_token(ci);
-    typename S::Decays& dec = l.dec[ci & 1];
-    __syncthreads();
-    const int left = end - tb;
+  // chunk ci's tiles from registers to LDS: x and w, which only the first half of a chunk reads, and y and z
+  auto put = [&](int ci) {
+    const int left = end - first_token(ci), buf = ci % S::NB;
     if constexpr (OUT) {
       tx.mend(left, m.dx < S::DX);
-      tx.store(l.x, S::SX);
+      tx.template store<true>(l.x, S::SX);
     }
     ty.mend(left, m.dx < S::DX);
-    ty.store(l.y, S::SY);
+    ty.store(l.y[buf], S::SY);
     tz.mend(left, m.dz < c0 + S::BV);
     if constexpr (OUT) {
       // An infinity or NaN in z times a score of zero would reach rows that do not see its token: such
@@ -540,73 +562,109 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
         tz.keep_finite();
       }
     }
-    tz.store(l.z, S::SZ);
+    tz.store(l.z[buf], S::SZ);
     if constexpr (MASS != 0) {
       tw.mend(left, m.dz < c0 + S::BV);
       tw.store(l.w, S::SW);
     }
+  };
+  if (tid < 2) l.odd[tid] = 0;
+  float decays = 1.0f;
+  __syncthreads();
+  if (nc > 0) {
+    if (wave == kDecayWave) {
+      chunk_decays<REV, C>(l.dec[0], rg, m.scale_out, m.scale_src, lane);
+      if (nc > 1) fetch_decay(1);
+    }
+    put(0);
+    if (nc > 1) fetch(1);
     __syncthreads();
-    if (ci + 1 < nc) fetch(ci + 1);
+  }
+  for (int ci = 0; ci < nc; ++ci) {
+    const int tb = first_token(ci);
+    typename S::Decays& dec = l.dec[ci & 1];
+    E* const ly = l.y[ci % S::NB];
+    E* const lz = l.z[ci % S::NB];
     const float total = dec.total;
 
     f32x4 acc[OUT ? NV : 1][OUT ? CT : 1];  // out transposed: column wc0 + 16 n + 4 g + r, row 16 it + c
     if constexpr (OUT) {
-      // scores: the tiles on and on one side of the diagonal, in turn over the waves, as [row][source]
-      for (int q = wave; q < S::TILES; q += W) {
-        int hi = 0, lo = q;
-        while (lo > hi) lo -= ++hi;
-        const int it = REV ? lo : hi, jt = REV ? hi : lo;
-        const int row = 16 * it + c;
-        f32x4 s = zero4();
+      if (tid == 0) l.odd[(ci + 1) & 1] = 0;
+      // scores: the tiles on and on one side of the diagonal, in turn over the waves, as [row][source]; a
+      // wave's tiles side by side
+      constexpr int kTurns = (S::TILES + W - 1) / W;
+      auto tiles = [&](auto count) {
+        constexpr int N = decltype(count)::value;
+        int it[N], jt[N];
+        f32x4 s[N], a[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          int hi = 0, lo = wave + i * W;
+          while (lo > hi) lo -= ++hi;
+          it[i] = REV ? lo : hi;
+          jt[i] = REV ? hi : lo;
+          s[i] = a[i] = zero4();
+        }
 #pragma unroll
         for (int k2 = 0; k2 < NKT / 2; ++k2)
-          s = O::mma(O::row_pair(l.y + (16 * jt + c) * S::SY + 32 * k2, g),
-                     O::row_pair(l.x + row * S::SX + 32 * k2, g), s);
-        const float2 gi = dec.g[row];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = 16 * jt + 4 * g + r;
-          const float2 gj = dec.g[j];
-          const float d = (gi.x - gj.x) + (gi.y - gj.y);
-          const bool seen = REV ? j >= row : j <= row;
-          s[r] = seen ? s[r] * m.scale_src * exp2_hw(REV ? -d : d) : 0.0f;
-        }
-        if constexpr (BF) {
-          Pair parts[O::kScore];
-          O::template split<O::kScore>(s, s, parts);
-#pragma unroll
-          for (int n = 0; n < O::kScore; ++n)
-            *reinterpret_cast<uint2*>(l.score[n] + row * S::SP + 16 * jt + 4 * g) = make_uint2(parts[n].x, parts[n].y);
-        } else {
-          O::put4(l.score[0] + row * S::SP + 16 * jt + 4 * g, s);
-        }
+          for (int i = 0; i < N; ++i)
+            s[i] = O::mma(O::row_pair(ly + (16 * jt[i] + c) * S::SY + 32 * k2, g),
+                          O::paired_row(l.x + (16 * it[i] + c) * S::SX + 32 * k2, g), s[i]);
         if constexpr (MASS == 1) {
           // what a row takes from a source: decay (x_i . y_j) (w_i . z_j), this workgroup's columns of the second
-          f32x4 a = zero4();
 #pragma unroll
           for (int k2 = 0; k2 < S::BV / 32; ++k2)
-            a = O::mma(O::row_pair(l.z + (16 * jt + c) * S::SZ + 32 * k2, g),
-                       O::row_pair(l.w + row * S::SW + 32 * k2, g), a);
-          float sum = 0.0f, before[4];  // of the lane's sources, and of those before each
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              a[i] = O::mma(O::row_eight(lz + (16 * jt[i] + c) * S::SZ + 32 * k2, g),
+                            O::row_eight(l.w + (16 * it[i] + c) * S::SW + 32 * k2, g), a[i]);
+        }
+        const float scale = m.scale_src * m.scale_out;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int row = 16 * it[i] + c, j0 = 16 * jt[i] + 4 * g;
+          const float2 gi = dec.g[row];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            before[r] = sum;
-            sum += 16 * jt + 4 * g + r < row ? a[r] * s[r] * m.scale_out : 0.0f;
+            const float2 gj = dec.g[j0 + r];
+            const float d = (gi.x - gj.x) + (gi.y - gj.y);
+            const bool seen = REV ? j0 + r >= row : j0 + r <= row;
+            s[i][r] = seen ? s[i][r] * scale * exp2_hw(REV ? -d : d) : 0.0f;
           }
-          float to = sum, u = __shfl_up(to, 16);  // ... of the lane groups up to this one
-          if (g >= 1) to += u;
-          u = __shfl_up(to, 32);
-          if (g >= 2) to += u;
-          if (g == 3) l.row_tile[ci & 1][jt][row] = to;
+          if constexpr (BF) {
+            Pair parts[O::kScore];
+            O::template split<O::kScore>(s[i], s[i], parts);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float v = group_sum(16 * jt + 4 * g + r <= row ? (to - sum) + before[r] : 0.0f);
-            if (c == 15) l.col_tile[ci & 1][q][4 * g + r] = v;
+            for (int n = 0; n < O::kScore; ++n)
+              *reinterpret_cast<uint2*>(l.score[n] + row * S::SP + O::paired(j0)) = make_uint2(parts[n].x, parts[n].y);
+          } else {
+            O::put4(l.score[0] + row * S::SP + O::paired(j0), s[i]);
+          }
+          if constexpr (MASS == 1) {
+            float sum = 0.0f, before[4];  // of the lane's sources, and of those before each
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              before[r] = sum;
+              sum += j0 + r < row ? a[i][r] * s[i][r] : 0.0f;
+            }
+            float to = sum, u = __shfl_up(to, 16);  // ... of the lane groups up to this one
+            if (g >= 1) to += u;
+            u = __shfl_up(to, 32);
+            if (g >= 2) to += u;
+            if (g == 3) l.row_tile[ci & 1][jt[i]][row] = to;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float v = group_sum(j0 + r <= row ? (to - sum) + before[r] : 0.0f);
+              if (c == 15) l.col_tile[ci & 1][wave + i * W][4 * g + r] = v;
+            }
           }
         }
-      }
+      };
+      if (wave + (kTurns - 1) * W < S::TILES) tiles(std::integral_constant<int, kTurns>{});
+      else if constexpr (kTurns > 1) tiles(std::integral_constant<int, kTurns - 1>{});
       if (wave == kDecayWave && ci + 1 < nc) {
-        chunk_decays<REV, C>(l.dec[(ci + 1) & 1], rg, m.scale_src, lane);
+        chunk_decays<REV, C>(l.dec[(ci + 1) & 1], rg, m.scale_out, m.scale_src, lane);
         if (ci + 2 < nc) fetch_decay(ci + 2);
       }
       if constexpr (MASS != 0) {
@@ -627,7 +685,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
         for (int n = 0; n < NV; ++n) O::template split<kRead>(st[2 * k2][n], st[2 * k2 + 1][n], sp[n]);
         Pair x[CT];
 #pragma unroll
-        for (int it = 0; it < CT; ++it) x[it] = O::row_pair(l.x + (16 * it + c) * S::SX + 32 * k2, g);
+        for (int it = 0; it < CT; ++it) x[it] = O::paired_row(l.x + (16 * it + c) * S::SX + 32 * k2, g);
 #pragma unroll
         for (int q = kRead - 1; q >= 0; --q)
 #pragma unroll
@@ -651,17 +709,19 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
         if constexpr (MASS != 0) {
           mass += __shfl_xor(mass, 16);
           mass += __shfl_xor(mass, 32);
-          if (g == 0) l.part[ci & 1][wave][16 * it + c] = mass * m.scale_out;
+          if (g == 0) l.part[ci & 1][wave][16 * it + c] = mass;
         }
       }
       __syncthreads();
-      if (tid == 0) l.odd[(ci + 1) & 1] = 0;
-      __builtin_amdgcn_sched_barrier(0);
     } else if (wave == kDecayWave && ci + 1 < nc) {
-      chunk_decays<REV, C>(l.dec[(ci + 1) & 1], rg, m.scale_src, lane);
+      chunk_decays<REV, C>(l.dec[(ci + 1) & 1], rg, m.scale_out, m.scale_src, lane);
       if (ci + 2 < nc) fetch_decay(ci + 2);
     }
 
+    if (S::NB == 2 && ci + 1 < nc) {
+      put(ci + 1);
+      if (ci + 2 < nc) fetch(ci + 2);
+    }
     // sources: into the rows of the chunk, and into the state
 #pragma unroll
     for (int kt = 0; kt < NKT; ++kt)
@@ -674,9 +734,9 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       Pair z[NV], zs[NV][O::kState];
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
-        z[n] = O::column_pair(l.z, S::SZ, 32 * j2, O::columns(wc0 + 16 * n, c), g, c);
-        const f32x4 f0 = *reinterpret_cast<const f32x4*>(dec.src + 32 * j2 + 8 * g);
-        const f32x4 f1 = *reinterpret_cast<const f32x4*>(dec.src + 32 * j2 + 8 * g + 4);
+        z[n] = O::column_pair(lz, S::SZ, 32 * j2, wc0 + 16 * n, g, c);
+        const f32x4 f0 = *reinterpret_cast<const f32x4*>(dec.src + 32 * j2 + 4 * g);
+        const f32x4 f1 = *reinterpret_cast<const f32x4*>(dec.src + 32 * j2 + 16 + 4 * g);
         O::template split<O::kState>(O::low(z[n]) * f0, O::high(z[n]) * f1, zs[n]);
       }
       if constexpr (OUT) {
@@ -684,11 +744,17 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
         for (int it = 0; it < CT; ++it) {
           if (REV ? it <= 2 * j2 + 1 : it >= 2 * j2) {
             // the one tile of a pair beyond the diagonal was not written
-            const bool none = REV ? it == 2 * j2 + 1 && g < 2 : it == 2 * j2 && g >= 2;
+            const bool half = REV ? it == 2 * j2 + 1 : it == 2 * j2;
 #pragma unroll
             for (int q = O::kScore - 1; q >= 0; --q) {
-              Pair s = O::row_pair(l.score[q] + (16 * it + c) * S::SP + 32 * j2, g);
-              if (none) s = Pair{};
+              Pair s = O::paired_row(l.score[q] + (16 * it + c) * S::SP + 32 * j2, g);
+              if (half) {
+                if constexpr (BF) {
+                  if (REV) s.x = s.y = 0; else s.z = s.w = 0;
+                } else {
+                  if (REV) s.a = zero4(); else s.b = zero4();
+                }
+              }
 #pragma unroll
               for (int n = 0; n < NV; ++n) acc[n][it] = O::mma(z[n], s, acc[n][it]);
             }
@@ -699,7 +765,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       for (int kt = 0; kt < NKT; kt += 2) {
         Pair y[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) y[i] = O::column_pair(l.y, S::SY, 32 * j2, O::state_rows(16 * kt + 4 * i, c), g, c);
+        for (int i = 0; i < 2; ++i) y[i] = O::column_pair(ly, S::SY, 32 * j2, 16 * (kt + i), g, c);
 #pragma unroll
         for (int q = O::kState - 1; q >= 0; --q)
 #pragma unroll
@@ -712,7 +778,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     if constexpr (OUT) {
       if (__builtin_expect(l.odd[ci & 1] != 0, 0)) {
         const int rare = anew(lane), c = rare & 15, g = rare >> 4, wc0 = 16 * NV * (anew(tid) >> 6);
-        auto state_row = [&](int kt, int r) { return 32 * (kt / 2) + 8 * g + 4 * (kt % 2) + r; };
+        auto state_row = [&](int kt, int r) { return 16 * kt + 4 * g + r; };
         const E* zb = head_base<E>(m.z, b, h);
         auto value = [&](int j, int col) {
           return tb + j < end && col < m.dz ? O::one(zb[int64_t(tb + j) * m.z.st + int64_t(col) * m.z.sd]) : 0.0f;
@@ -727,14 +793,14 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
 #pragma unroll
             for (int kt = 0; kt < NKT; ++kt)
 #pragma unroll
-              for (int r = 0; r < 4; ++r) st[kt][n][r] += odd(u) ? O::one(l.y[j * S::SY + state_row(kt, r)]) * w : 0.0f;
+              for (int r = 0; r < 4; ++r) st[kt][n][r] += odd(u) ? O::one(ly[j * S::SY + state_row(kt, r)]) * w : 0.0f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float v = value(j, c0 + wc0 + 16 * n + 4 * g + r);
 #pragma unroll
               for (int it = 0; it < CT; ++it) {
                 const int row = 16 * it + c;
-                const float s = O::one(l.score[0][row * S::SP + j]) * v;
+                const float s = O::one(l.score[0][row * S::SP + O::paired(j)]) * v;
                 acc[n][it][r] += odd(v) && (REV ? j >= row : j <= row) ? s : 0.0f;
               }
             }
@@ -753,7 +819,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
           char* row = to + 16 * it * row_bytes;
 #pragma unroll
           for (int n = 0; n < NV; ++n) {
-            f32x4 v = acc[n][it] * m.scale_out;
+            f32x4 v = acc[n][it];
             if (tb + 16 * it + c >= len) v = zero4();
             if (tb + 16 * it + c < t1 && c0 + col + 16 * n < m.dz) {
               if (!BF || m.out_f32) *reinterpret_cast<f32x4*>(row + (off + 4 * uint32_t(col + 16 * n))) = v;
@@ -772,7 +838,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const int at = wc0 + 16 * n + 4 * g + r;
-              const float v = t >= len ? 0.0f : acc[n][it][r] * m.scale_out;
+              const float v = t >= len ? 0.0f : acc[n][it][r];
               if (t < t1 && c0 + at < m.dz) {
                 if (!BF || m.out_f32) reinterpret_cast<float*>(row)[at] = v;
                 else reinterpret_cast<uint16_t*>(row)[at] = f32_to_bf16_rne(v);
@@ -780,6 +846,12 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
             }
         }
       }
+    }
+    __syncthreads();
+    if (S::NB == 1 && ci + 1 < nc) {
+      put(ci + 1);
+      if (ci + 2 < nc) fetch(ci + 2);
+      __syncthreads();
     }
   }
 
@@ -795,11 +867,8 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     if constexpr (MASS != 0) {
       const int64_t mb = (int64_t(cb) * BH + bh);
       const int chunks = (p.T + C - 1) / C;
-      if (nc > 0) {
-        __syncthreads();
-        if (wave == kMassWave)
-          chunk_mass<REV, MASS, CT, S::TILES>(p, m, l, (nc - 1) & 1, W, first_token(nc - 1), t1, cb, bh, lane);
-      }
+      if (nc > 0 && wave == kMassWave)
+        chunk_mass<REV, MASS, CT, S::TILES>(p, m, l, (nc - 1) & 1, W, first_token(nc - 1), t1, cb, bh, lane);
       for (int q = tid; q < rest; q += THREADS) m.mass[mb * p.T + from + q] = 0.0f;
       for (int q = tid; q < (rest + C - 1) / C; q += THREADS) {
         m.mass_chunk[mb * chunks + from / C + q] = 0.0f;
