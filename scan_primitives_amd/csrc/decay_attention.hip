@@ -63,6 +63,8 @@ __device__ __forceinline__ double block_sum(double v, double* l) {
 __global__ __launch_bounds__(kThreads) void decay_grad(DaDecayGrad p) {
   __shared__ double la[kThreads];
   __shared__ double ly[kThreads];
+  __shared__ double lw[kThreads];
+  __shared__ bool cuts[kThreads];
   const int bh = blockIdx.x % (p.B * p.H), seg = blockIdx.x / (p.B * p.H), tid = int(threadIdx.x);
   const int b = bh / p.H, h = bh % p.H;
   const int64_t BH = int64_t(p.B) * p.H, state = int64_t(p.dk) * p.dv;
@@ -75,13 +77,16 @@ __global__ __launch_bounds__(kThreads) void decay_grad(DaDecayGrad p) {
   };
   double z = 0.0;
   if (seg > 0) {
-    for (int k = 0; k < p.blocks; ++k) z += p.cross[(k * BH + bh) * p.segments + seg];
+    for (int k = 0; k < p.blocks; ++k) z += p.cross[(k * BH + bh) * (p.segments + 1) + seg];
   } else if (p.initial) {
     double s = 0.0;
     for (int64_t i = tid; i < state; i += kThreads)
       s += double(p.initial[bh * state + i]) * double(p.grad_initial[bh * state + i]);
     z = block_sum(s, la);
   }
+  // cross: [blocks][B * H][segments + 1], at the start of each segment but the first, and at the end
+  double end = 0.0;
+  for (int k = 0; k < p.blocks; ++k) end += p.cross[(k * BH + bh) * (p.segments + 1) + seg + 1];
   const int first = seg * (p.seg_tokens / p.chunk), last = min(p.chunks, first + p.seg_tokens / p.chunk);
   double all = 0.0;
   for (int i0 = first; i0 < last; i0 += kThreads) {
@@ -90,15 +95,32 @@ __global__ __launch_bounds__(kThreads) void decay_grad(DaDecayGrad p) {
     if (tid < n) {
       la[tid] = sum_of(p.sources_chunk, p.chunks, i0 + tid);
       ly[tid] = sum_of(p.rows_chunk, p.chunks, i0 + tid);
+      cuts[tid] = p.chunk_decay[int64_t(bh) * p.chunks + i0 + tid] == 0.0f;
     }
     __syncthreads();
-    if (tid == 0)
+    if (tid == 0) {
+      // `sum`: what was added up since the last cut, the scale of the rounding errors in z
+      double sum = fabs(z);
+      int from = 0;
       for (int i = 0; i < n; ++i) {
-        const bool cut = p.chunk_decay[int64_t(bh) * p.chunks + i0 + i] == 0.0f;
-        const double y = cut ? 0.0 : z - ly[i];
+        if (cuts[i]) {
+          from = i;
+          sum = 0.0;
+        } else {
+          sum += fabs(ly[i]);
+        }
+        const double y = cuts[i] ? 0.0 : z - ly[i];
+        lw[i] = sum;
         ly[i] = y;
         z = y + la[i];
+        sum += fabs(la[i]);
       }
+      // The carried sum at the segment's end is known outright as well: what rounding has put between
+      // the two is taken off again, in proportion to what had been added up.
+      const double off = z - end;
+      if (n == last - first && sum > 0.0 && fabs(off) <= 1e-4 * sum)
+        for (int i = from; i < n; ++i) ly[i] -= cuts[i] ? 0.0 : off * (lw[i] / sum);
+    }
     __syncthreads();
     const int t1 = min((i0 + n) * p.chunk, p.T);
     for (int t = i0 * p.chunk + tid; t < t1; t += kThreads) {
@@ -141,54 +163,92 @@ __global__ __launch_bounds__(kThreads) void share_sum(DaShare p) {
 
 // ---------------------------------------------------------------- one token
 
-// One workgroup a request, head and block of kStepCols columns: 8 threads of 4
-// columns, 32 rows at a time.
-constexpr int kStepCols = 32;
+// One workgroup a request, head and block of 4 CG columns: CG threads of four columns, kThreads / CG
+// rows at a time, and of a thread's rows kStepRows on their way at once. VEC: the state by 16 bytes.
+constexpr int kStepRows = 8;
 
-template <bool BF>
+template <bool BF, int CG, bool VEC>
 __global__ __launch_bounds__(kThreads) void step_kernel(DaStep p) {
   using O = Op<BF>;
   using E = typename O::E;
-  __shared__ float sum[kThreads / 8][kStepCols];
-  const int tid = int(threadIdx.x), cols = (p.dv + kStepCols - 1) / kStepCols;
-  const int cb = blockIdx.x % cols, bh = blockIdx.x / cols, b = bh / p.H, h = bh % p.H;
+  constexpr int RG = kThreads / CG;
+  __shared__ float lq[256], lk[256];
+  __shared__ alignas(16) float sum[RG][4 * CG];
+  const int tid = int(threadIdx.x), blocks = (p.dv + 4 * CG - 1) / (4 * CG);
+  const int cb = blockIdx.x % blocks, bh = blockIdx.x / blocks, b = bh / p.H, h = bh % p.H;
   const int64_t slot = p.slots ? int64_t(p.slots[b]) : int64_t(b);
   const bool used = slot >= 0 && slot < p.slots_in_pool;
-  const int col = cb * kStepCols + (tid & 7) * 4, r0 = tid >> 3;
+  const int cg = tid % CG, r0 = tid / CG, col = 4 * (cb * CG + cg);
   f32x4 o = zero4();
   if (used) {
-    const E* q = head_base<E>(p.q, b, h);
-    const E* k = head_base<E>(p.k, b, h);
+    float* s = p.state + slot * p.ss + int64_t(h) * p.sh + col;
     const E* v = head_base<E>(p.v, b, h);
-    const float decay = expf(p.g[int64_t(b) * p.gb + int64_t(h) * p.gh]);
-    f32x4 vv = zero4();
+    f32x4 old[kStepRows], vv = zero4();
+    auto load = [&](int r1) {
+#pragma unroll
+      for (int i = 0; i < kStepRows; ++i) {
+        // rows and columns that do not exist: an existing one, not written back
+        const float* from = s + int64_t(min(r1 + i * RG, p.dk - 1)) * p.dv;
+        if constexpr (VEC) {
+          old[i] = *reinterpret_cast<const f32x4*>(col < p.dv ? from : from - col);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) old[i][e] = from[col + e < p.dv ? e : -col];
+        }
+      }
+    };
+    load(r0);
+    if (tid < p.dk) {
+      lq[tid] = O::one(head_base<E>(p.q, b, h)[int64_t(tid) * p.q.sd]);
+      lk[tid] = O::one(head_base<E>(p.k, b, h)[int64_t(tid) * p.k.sd]);
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (col + e < p.dv) vv[e] = O::one(v[int64_t(col + e) * p.v.sd]);
-    float* s = p.state + slot * p.ss + int64_t(h) * p.sh;
-    for (int r = r0; r < p.dk; r += kThreads / 8) {
-      const float kr = O::one(k[int64_t(r) * p.k.sd]), qr = O::one(q[int64_t(r) * p.q.sd]);
+    const float decay = expf(p.g[int64_t(b) * p.gb + int64_t(h) * p.gh]);
+    __syncthreads();
+    for (int r1 = r0; r1 < p.dk; r1 += kStepRows * RG) {
+      if (r1 != r0) load(r1);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (col + e < p.dv) {
-          const float n = fmaf(decay, s[int64_t(r) * p.dv + col + e], kr * vv[e]);
-          s[int64_t(r) * p.dv + col + e] = n;
-          o[e] = fmaf(qr, n, o[e]);
+      for (int i = 0; i < kStepRows; ++i) {
+        const int r = r1 + i * RG;
+        if (r < p.dk) {
+          const float kr = lk[r], qr = lq[r];
+          f32x4 n;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            n[e] = fmaf(decay, old[i][e], kr * vv[e]);
+            o[e] = fmaf(qr, n[e], o[e]);
+          }
+          float* to = s + int64_t(r) * p.dv;
+          if constexpr (VEC) {
+            if (col < p.dv) *reinterpret_cast<f32x4*>(to) = n;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (col + e < p.dv) to[e] = n[e];
+          }
         }
+      }
     }
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) sum[r0][(tid & 7) * 4 + e] = o[e];
+  *reinterpret_cast<f32x4*>(&sum[r0][4 * cg]) = o;
   __syncthreads();
-  if (tid < kStepCols && cb * kStepCols + tid < p.dv) {
+  const int at = 4 * CG * cb + tid;
+  if (tid < 4 * CG && at < p.dv) {
     float t = 0.0f;
-    for (int r = 0; r < kThreads / 8; ++r) t += sum[r][tid];
-    const int64_t at = int64_t(bh) * p.dv + cb * kStepCols + tid;
-    static_cast<E*>(p.out)[at] = O::round(t * p.scale);
+#pragma unroll
+    for (int r = 0; r < RG; ++r) t += sum[r][tid];
+    static_cast<E*>(p.out)[int64_t(bh) * p.dv + at] = O::round(t * p.scale);
   }
 }
 
-// ---------------------------------------------------------------- launches
+template <bool BF, int CG>
+void launch_step(const DaStep& p, bool vec, hipStream_t stream) {
+  const unsigned grid = unsigned(int64_t(p.B) * p.H * ((p.dv + 4 * CG - 1) / (4 * CG)));
+  if (vec) step_kernel<BF, CG, true><<<grid, kThreads, 0, stream>>>(p);
+  else step_kernel<BF, CG, false><<<grid, kThreads, 0, stream>>>(p);
+}
 
 }  // namespace
 
@@ -257,9 +317,16 @@ hipError_t launch_share_sum(const DaShare& p, hipStream_t stream) {
 }
 
 hipError_t launch_decay_step(const DaStep& p, hipStream_t stream) {
-  const unsigned grid = unsigned(int64_t(p.B) * p.H * ((p.dv + kStepCols - 1) / kStepCols));
-  if (p.bf16) step_kernel<true><<<grid, kThreads, 0, stream>>>(p);
-  else step_kernel<false><<<grid, kThreads, 0, stream>>>(p);
+  const bool vec = p.dv % 4 == 0 && p.ss % 4 == 0 && p.sh % 4 == 0 && (reinterpret_cast<uintptr_t>(p.state) & 15u) == 0;
+  // 128 columns a workgroup where that fills the device, else 32
+  const bool wide = p.dv > 32 && int64_t(p.B) * p.H * ((p.dv + 127) / 128) >= 2 * int64_t(device_cu_count());
+  if (p.bf16) {
+    if (wide) launch_step<true, 32>(p, vec, stream);
+    else launch_step<true, 8>(p, vec, stream);
+  } else {
+    if (wide) launch_step<false, 32>(p, vec, stream);
+    else launch_step<false, 8>(p, vec, stream);
+  }
   return hipGetLastError();
 }
 

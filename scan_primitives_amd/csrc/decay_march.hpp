@@ -517,32 +517,38 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     rg = lane < C && t < end ? gb[int64_t(t) * p.gt] : 0.0f;
   };
 
-  if (nc > 0) {
-    fetch(0);
-    if (wave == kDecayWave) fetch_decay(0);
-  }
-  if constexpr (MASS == 1) {
-    // What the decays behind an earlier segment carry in all: the state against its adjoint, both in
-    // memory at the segment's start. Between here and its end the carried sum is kept by differences.
-    if (seg_m > 0) {
-      const float* adj = p.m[1].seg + (int64_t(p.segments - 1 - seg_m) * BH + bh) * state;
+  // What a decay carries in all at a segment's border: the state against its adjoint there, `adj`.
+  auto carried = [&](const float* adj, int border) {
+    if constexpr (MASS == 1) {
       double s = 0.0;
+      if (adj) {
 #pragma unroll
-      for (int kt = 0; kt < NKT; ++kt)
+        for (int kt = 0; kt < NKT; ++kt)
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
+          for (int n = 0; n < NV; ++n)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (state_is(kt, n, r)) s += double(st[kt][n][r]) * double(adj[state_at(kt, n, r)]);
+            for (int r = 0; r < 4; ++r)
+              if (state_is(kt, n, r)) s += double(st[kt][n][r]) * double(adj[state_at(kt, n, r)]);
+      }
       s = lane_of(prefix_sum(s, lane), 63);
       if (lane == 0) l.cross[wave] = s;
       __syncthreads();
       if (tid == 0) {
         s = 0.0;
         for (int i = 0; i < W; ++i) s += l.cross[i];
-        m.cross[(int64_t(cb) * BH + bh) * p.segments + seg] = s;
+        m.cross[(int64_t(cb) * BH + bh) * (p.segments + 1) + border] = s;
       }
+      __syncthreads();
     }
+  };
+
+  if (nc > 0) {
+    fetch(0);
+    if (wave == kDecayWave) fetch_decay(0);
+  }
+  if constexpr (MASS == 1) {
+    // Between here and the segment's end the carried sum is kept by differences.
+    if (seg_m > 0) carried(p.m[1].seg + (int64_t(p.segments - 1 - seg_m) * BH + bh) * state, seg);
   }
   // chunk ci's tiles from registers to LDS: x and w, which only the first half of a chunk reads, and y and z
   auto put = [&](int ci) {
@@ -877,6 +883,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     }
   }
 
+  if (MASS == 1 && seg == p.segments - 1) carried(p.m[1].first ? p.m[1].first + bh * state : nullptr, p.segments);
   float* to = OUT ? (seg_m == p.segments - 1 && m.last ? m.last + bh * state : nullptr)
                   : m.seg + (int64_t(seg_m) * BH + bh) * state;
   if (to) {

@@ -1291,7 +1291,7 @@ GradPieces carve_gradient(Carve& c, const DecayShapes& s, sx::DaParams& p) {
   g.rows_chunk = c.take<float>(g.blocks * BH * g.chunks);
   g.sources_chunk = c.take<float>(g.blocks * BH * g.chunks);
   g.chunk_decay = c.take<float>(BH * g.chunks);
-  g.cross = c.take<double>(g.blocks * BH * p.segments);
+  g.cross = c.take<double>(g.blocks * BH * (p.segments + 1));
   g.partial = c.take<double>(BH * p.segments);
   // gradients of shared heads are summed over the heads that share them, from f32
   const int64_t n = s.B * s.T * s.H;

@@ -47,7 +47,8 @@ struct DaMarch {
   float* seg_decay;     // [segments - 1][B * H]: product of a segment's decays
   float* mass;          // [column blocks][B * H][T]: the part of the decay's gradient that this march sees
   float* mass_chunk;    // [column blocks][B * H][chunks]: a chunk's mass against the state it entered with
-  double* cross;        // [column blocks][B * H][segments]: the state at a segment's start against its adjoint there
+  double* cross;        // [column blocks][B * H][segments + 1]: the state against its adjoint at the segments' borders
+                        // (but the first)
   float* chunk_decay;   // [B * H][chunks]: product of a chunk's decays (written by column block 0; nullptr: no)
 };
 
@@ -92,7 +93,7 @@ struct DaDecayGrad {
   const float* sources_chunk;
   const float* chunk_decay;    // [B * H][chunks]
   int segments, seg_tokens;
-  const double* cross;         // [blocks][B * H][segments], of segments but the first
+  const double* cross;         // [blocks][B * H][segments + 1], but of the first border
   const float* initial;        // nullptr: zero
   const float* grad_initial;
   double* partial;             // per_head: [segments][B * H]
