@@ -570,8 +570,41 @@ def _matrix_dims_contiguous(t: torch.Tensor) -> bool:
 # ---------------------------------------------------------------- linear attention
 #
 # A single token's call takes the GPU a few microseconds, so what the binding
-# does in Python counts: shape and stride arrays are kept by value, and the
-# device is switched only when another one is current.
+# does on the host counts. Calls whose tensors are as the library takes them go
+# the short way (csrc/py_marshal.cpp), which answers None to any other; those go
+# the long way below, which checks everything by name, converts, records for
+# autograd and switches devices.
+
+_marshal = None
+
+
+def _load_marshal():
+    """The short way, bound to the loaded library."""
+    global _marshal
+    from importlib import machinery, util
+
+    lib = load_library()
+    path = os.path.join(HERE, "_sx_marshal.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is not built; run `python -m scan_primitives_amd.build_lib`")
+    loader = machinery.ExtensionFileLoader("_sx_marshal", path)
+    module = util.module_from_spec(util.spec_from_loader("_sx_marshal", loader))
+    loader.exec_module(module)
+    names = ("sx_decay_attention", "sx_decay_attention_workspace_bytes", "sx_decay_attention_backward",
+             "sx_decay_attention_backward_workspace_bytes", "sx_decay_attention_step", "sx_head_norm_rotate",
+             "sx_head_norm_rotate_backward", "sx_head_norm_rotate_backward_workspace_bytes")
+    module.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
+                torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    _marshal = module
+    return module
+
+
+def _done(answer):
+    """The results of the short way; its status raises."""
+    if type(answer) is int:
+        _check(answer)
+    return answer
+
 
 @functools.lru_cache(maxsize=4096)
 def _i64(values: tuple) -> ctypes.Array:
@@ -702,6 +735,9 @@ def decay_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay
     ``[B, T, H, dv]``, and the last state too when ``return_state``. When autograd
     records, the gradient runs through ``decay_attention_backward``.
     """
+    got = (_marshal or _load_marshal()).decay_attention(q, k, v, log_decay, initial, lengths, scale, return_state)
+    if got is not None:
+        return _done(got) if return_state else _done(got)[0]
     if _records(q, k, v, log_decay, initial):
         out, state = _DecayAttentionFunction.apply(q, k, v, log_decay, initial, lengths, scale, return_state)
     else:
@@ -738,6 +774,10 @@ def decay_attention_backward(q, k, v, log_decay, grad_out, initial=None, lengths
     Each gradient has its operand's shape and dtype; ``grad_initial`` is the
     gradient of the state before the first token, also when that was zero.
     """
+    got = (_marshal or _load_marshal()).decay_attention_backward(q, k, v, log_decay, grad_out, initial, lengths, scale,
+                                                                 grad_state)
+    if got is not None:
+        return _done(got)
     op = "decay-attention gradient"
     code, heads, index = _decay_operands(op, q, k, v, log_decay, 2, (("grad_out", grad_out),),
                                          (("initial", initial), ("lengths", lengths), ("grad_state", grad_state)))
@@ -795,6 +835,9 @@ def decay_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_
     whose slot lies outside the pool is idle: zero out, no state changed; two
     rows of one slot race. Returns out ``[B, H, dv]``. No gradient is recorded.
     """
+    got = (_marshal or _load_marshal()).decay_attention_step(q, k, v, log_decay, state, slots, scale)
+    if got is not None:
+        return _done(got)[0]
     op = "decay-attention step"
     code, heads, index = _decay_operands(op, q, k, v, log_decay, 1, (("state", state),), (("slots", slots),))
     b, _, dk = q.shape
@@ -859,6 +902,9 @@ def head_norm_rotate(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, 
     dtype. When autograd records, the gradient runs through
     ``head_norm_rotate_backward``.
     """
+    got = (_marshal or _load_marshal()).head_norm_rotate(q, k, positions, turns, q_weight, k_weight, eps, neighbours)
+    if got is not None:
+        return _done(got)
     if _records(q, k, q_weight, k_weight):
         return _HeadNormRotateFunction.apply(q, k, positions, turns, q_weight, k_weight, eps, neighbours)
     return _head_norm_rotate_forward(q, k, positions, turns, q_weight, k_weight, eps, neighbours)
@@ -881,6 +927,10 @@ def head_norm_rotate_backward(q, k, positions, turns, grad_out_q, grad_out_k, q_
     """Gradients ``(grad_q, grad_k, grad_q_weight, grad_k_weight)`` of a loss through
     ``head_norm_rotate(q, k, positions, turns, q_weight, k_weight, eps, neighbours)``, given its gradients with
     respect to the two results (their shapes, q's dtype). A weight that is None has None for its gradient."""
+    got = (_marshal or _load_marshal()).head_norm_rotate_backward(q, k, positions, turns, grad_out_q, grad_out_k,
+                                                                  q_weight, k_weight, eps, neighbours)
+    if got is not None:
+        return _done(got)
     op = "head-norm-rotate gradient"
     code, index, positions, turns, q_weight, k_weight = _rotate_operands(
         op, q, k, positions, turns, q_weight, k_weight, (("grad_out_q", grad_out_q), ("grad_out_k", grad_out_k)))

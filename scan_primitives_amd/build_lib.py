@@ -18,6 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libsx_scan.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
+# The binding's short way into the library: a CPython extension over torch's headers (host code only).
+MARSHAL_PATH = os.path.join(HERE, "_sx_marshal.so")
 
 SOURCES = ["sx_api.cpp", "element_scan.hip", "normcap_quad.hip", "matrix_scan.hip", "matrix_scan_grad.hip",
            "table_scan.hip", "decay_attention.hip", "decay_march_bf16.hip", "decay_march_bf16_any.hip",
@@ -45,6 +47,19 @@ def link_command(objs: list[str], out_path: str) -> list[str]:
     return [hipcc_path(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", out_path, *objs]
 
 
+def marshal_command(out_path: str) -> list[str]:
+    import importlib.util
+    import sysconfig
+
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    libs = os.path.join(torch_dir, "lib")
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch_dir, "include"),
+            "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), "-o", out_path,
+            os.path.join(CSRC, "py_marshal.cpp"), "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
+            f"-Wl,-rpath,{libs}"]
+
+
 def _run(cmd: list[str]) -> tuple[int, list[str]]:
     proc = subprocess.run(cmd, capture_output=True, text=True)
     # hipcc's host pass does not know the device-only feature flag and says so; that is harmless.
@@ -63,17 +78,20 @@ def build(verbose: bool = False) -> str:
     os.makedirs(objdir, exist_ok=True)
     jobs = [(src, os.path.join(objdir, os.path.splitext(src)[0] + ".o")) for src in SOURCES]
     cmds = [compile_command(src, obj) for src, obj in jobs]
+    marshal_tmp = MARSHAL_PATH + ".tmp"
+    cmds.append(marshal_command(marshal_tmp))
     if verbose:
         for cmd in cmds:
             print(" ".join(cmd), flush=True)
     workers = max(1, min(len(cmds), os.cpu_count() or 1, 8))
     with ThreadPoolExecutor(max_workers=workers) as pool:
         results = list(pool.map(_run, cmds))
-    errors = [(src, msgs) for (src, _), (rc, msgs) in zip(jobs, results) if rc != 0]
+    sources = [src for src, _ in jobs] + ["py_marshal.cpp"]
+    errors = [(src, msgs) for src, (rc, msgs) in zip(sources, results) if rc != 0]
     if errors:
-        raise RuntimeError("hipcc failed:\n" + "\n".join(f"{src}:\n" + "\n".join(msgs) for src, msgs in errors))
+        raise RuntimeError("compilation failed:\n" + "\n".join(f"{src}:\n" + "\n".join(msgs) for src, msgs in errors))
     if verbose:
-        for (src, _), (_, msgs) in zip(jobs, results):
+        for _, msgs in results:
             if msgs:
                 print("\n".join(msgs))
     tmp = LIB_PATH + ".tmp"
@@ -81,6 +99,7 @@ def build(verbose: bool = False) -> str:
     if rc != 0:
         raise RuntimeError("hipcc link failed:\n" + "\n".join(msgs))
     os.replace(tmp, LIB_PATH)
+    os.replace(marshal_tmp, MARSHAL_PATH)
     return LIB_PATH
 
 

@@ -320,6 +320,30 @@ def test_replays_of_a_graph_and_another_stream():
         assert torch.equal(a, b)
 
 
+def test_both_ways_into_the_library():
+    # an operand that has to be converted, or a scale that is no float, takes the binding's long way
+    s = make(t=90, h=4, initial=True, lengths=[90, 40])
+    want = (*_forward(s), *_backward(s))
+    s["initial"] = s["initial"].transpose(2, 3).contiguous().transpose(2, 3)
+    s["gs"] = s["gs"].transpose(0, 1).contiguous().transpose(0, 1)
+    for a, b in zip(want, (*_forward(s), *_backward(s))):
+        assert torch.equal(a, b)
+    s["scale"] = 1.0
+    want = _forward(s)
+    s["scale"] = 1
+    assert torch.equal(want[0], _forward(s)[0])
+    one = make_step()
+    kept = one["state"].clone()
+    want = sx.decay_attention_step(one["q"], one["k"], one["v"], one["g"], kept, slots=one["slots"], scale=1.0)
+    got = sx.decay_attention_step(one["q"], one["k"], one["v"], one["g"], one["state"], slots=one["slots"], scale=1)
+    assert torch.equal(want, got) and torch.equal(kept, one["state"])
+    for bad in (dict(log_decay=s["g"].double()), dict(v=s["v"].float()), dict(lengths=s["lengths"].long()),
+                dict(initial=s["initial"][:1]), dict(q=s["q"][0]), dict(k=s["k"][:, :, :, :3]), dict(q=None)):
+        args = dict(q=s["q"], k=s["k"], v=s["v"], log_decay=s["g"], initial=s["initial"], lengths=s["lengths"])
+        with pytest.raises(sx.SxError):
+            sx.decay_attention(**{**args, **bad})
+
+
 def test_far_apart_rows():
     # batch rows more than 2^31 elements apart in one buffer
     base = make(b=2, t=70, h=2, dk=32, dv=32)
