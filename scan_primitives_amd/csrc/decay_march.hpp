@@ -239,9 +239,10 @@ struct Shape {
     alignas(16) E y[NB][C * SY];
     alignas(16) E z[NB][C * SZ];
     Decays dec[2];
-    int odd[2];   // a chunk's z holds an infinity or NaN
   };
   struct Out : Local {
+    int odd[2];       // a chunk's z holds an infinity or NaN:
+    int from[2][BV];  // the first token of each column that does (in the march's order; C and more: none)
     alignas(16) E x[C * SX];
     alignas(16) E score[O::kScore][C * SP];
   };
@@ -333,12 +334,26 @@ struct Tile {
     }
     return VEC ? O::finite(seen) : seen < 0x7f800000u;
   }
-  __device__ __forceinline__ void keep_finite() {
+  // Infinities and NaN taken out; `from` of their columns holds the first token of each (the last: `rev`).
+  __device__ __forceinline__ void keep_finite(int* from, bool rev) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
+      const int t = row + n * STEP;
+#pragma unroll
+      for (int e = 0; e < PIECE; ++e) {
+        uint32_t u;
+        if constexpr (!VEC) u = __float_as_uint(O::one(r[n]));
+        else if constexpr (BF) u = (e & 1) ? word(n, e / 2) : word(n, e / 2) << 16;
+        else u = word(n, e);
+        if ((u & 0x7f800000u) == 0x7f800000u) atomicMin(from + col + e, rev ? O::C - 1 - t : t);
+      }
       if constexpr (VEC) r[n] = O::finite_part(r[n]);
       else if ((__float_as_uint(O::one(r[n])) & 0x7f800000u) == 0x7f800000u) r[n] = E(0);
     }
+  }
+  __device__ __forceinline__ uint32_t word(int n, int i) const {
+    if constexpr (VEC) return i == 0 ? r[n].x : i == 1 ? r[n].y : i == 2 ? r[n].z : r[n].w;
+    else return 0;
   }
 };
 
@@ -562,10 +577,10 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     tz.mend(left, m.dz < c0 + S::BV);
     if constexpr (OUT) {
       // An infinity or NaN in z times a score of zero would reach rows that do not see its token: such
-      // values are left out of the products and added at the end to what does see it.
+      // values are left out of the products, and what does see them turns into NaN at the end.
       if (__builtin_expect(!tz.finite(), 0)) {
         l.odd[ci & 1] = 1;
-        tz.keep_finite();
+        tz.keep_finite(l.from[ci & 1], REV);
       }
     }
     tz.store(l.z[buf], S::SZ);
@@ -574,7 +589,10 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       tw.store(l.w, S::SW);
     }
   };
-  if (tid < 2) l.odd[tid] = 0;
+  if constexpr (OUT) {
+    if (tid < 2) l.odd[tid] = 0;
+    for (int i = tid; i < 2 * S::BV; i += THREADS) l.from[i / S::BV][i % S::BV] = C;
+  }
   float decays = 1.0f;
   __syncthreads();
   if (nc > 0) {
@@ -587,7 +605,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     __syncthreads();
   }
   for (int ci = 0; ci < nc; ++ci) {
-    const int tb = first_token(ci);
+    const int tb = first_token(ci), left = end - tb;
     typename S::Decays& dec = l.dec[ci & 1];
     E* const ly = l.y[ci % S::NB];
     E* const lz = l.z[ci % S::NB];
@@ -611,32 +629,62 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
           jt[i] = REV ? hi : lo;
           s[i] = a[i] = zero4();
         }
+        float2 gi[N];
+        f32x4 gj[N][2];
 #pragma unroll
-        for (int k2 = 0; k2 < NKT / 2; ++k2)
+        for (int i = 0; i < N; ++i) {
+          gi[i] = dec.g[16 * it[i] + c];
+          gj[i][0] = *reinterpret_cast<const f32x4*>(&dec.g[16 * jt[i] + 4 * g]);
+          gj[i][1] = *reinterpret_cast<const f32x4*>(&dec.g[16 * jt[i] + 4 * g + 2]);
+        }
+        constexpr int A = NKT / 2 < 4 ? NKT / 2 : N == 1 ? 4 : 2;  // products whose operands are read at once
 #pragma unroll
-          for (int i = 0; i < N; ++i)
-            s[i] = O::mma(O::row_pair(ly + (16 * jt[i] + c) * S::SY + 32 * k2, g),
-                          O::paired_row(l.x + (16 * it[i] + c) * S::SX + 32 * k2, g), s[i]);
+        for (int k2 = 0; k2 < NKT / 2; k2 += A) {
+          Pair y[A][N], x[A][N];
+#pragma unroll
+          for (int k = 0; k < A; ++k)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              y[k][i] = O::row_pair(ly + (16 * jt[i] + c) * S::SY + 32 * (k2 + k), g);
+              x[k][i] = O::paired_row(l.x + (16 * it[i] + c) * S::SX + 32 * (k2 + k), g);
+            }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int k = 0; k < A; ++k)
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i] = O::mma(y[k][i], x[k][i], s[i]);
+        }
         if constexpr (MASS == 1) {
           // what a row takes from a source: decay (x_i . y_j) (w_i . z_j), this workgroup's columns of the second
 #pragma unroll
-          for (int k2 = 0; k2 < S::BV / 32; ++k2)
+          for (int k2 = 0; k2 < S::BV / 32; k2 += 2) {
+            Pair z[2][N], w[2][N];
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-              a[i] = O::mma(O::row_eight(lz + (16 * jt[i] + c) * S::SZ + 32 * k2, g),
-                            O::row_eight(l.w + (16 * it[i] + c) * S::SW + 32 * k2, g), a[i]);
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int i = 0; i < N; ++i) {
+                z[k][i] = O::row_eight(lz + (16 * jt[i] + c) * S::SZ + 32 * (k2 + k), g);
+                w[k][i] = O::row_eight(l.w + (16 * it[i] + c) * S::SW + 32 * (k2 + k), g);
+              }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int i = 0; i < N; ++i) a[i] = O::mma(z[k][i], w[k][i], a[i]);
+          }
         }
         const float scale = m.scale_src * m.scale_out;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int row = 16 * it[i] + c, j0 = 16 * jt[i] + 4 * g;
-          const float2 gi = dec.g[row];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float2 gj = dec.g[j0 + r];
-            const float d = (gi.x - gj.x) + (gi.y - gj.y);
-            const bool seen = REV ? j0 + r >= row : j0 + r <= row;
-            s[i][r] = seen ? s[i][r] * scale * exp2_hw(REV ? -d : d) : 0.0f;
+            const float d = (gi[i].x - gj[i][r / 2][2 * (r & 1)]) + (gi[i].y - gj[i][r / 2][2 * (r & 1) + 1]);
+            s[i][r] *= scale * exp2_hw(REV ? -d : d);
+          }
+          if (it[i] == jt[i]) {  // the tiles on the diagonal: sources a row does not see
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[i][r] = (REV ? j0 + r >= row : j0 + r <= row) ? s[i][r] : 0.0f;
           }
           if constexpr (BF) {
             Pair parts[O::kScore];
@@ -683,21 +731,26 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       for (int n = 0; n < NV; ++n)
 #pragma unroll
         for (int it = 0; it < CT; ++it) acc[n][it] = zero4();
-      // rows against the state
+      // rows against the state, each product's rows read ahead of the one before
+      Pair x[2][CT];
+      auto rows_of = [&](int k2) {
+#pragma unroll
+        for (int it = 0; it < CT; ++it) x[k2 & 1][it] = O::paired_row(l.x + (16 * it + c) * S::SX + 32 * k2, g);
+      };
+      rows_of(0);
 #pragma unroll
       for (int k2 = 0; k2 < NKT / 2; ++k2) {
+        if (k2 + 1 < NKT / 2) rows_of(k2 + 1);
+        __builtin_amdgcn_sched_barrier(0);
         Pair sp[NV][kRead];
 #pragma unroll
         for (int n = 0; n < NV; ++n) O::template split<kRead>(st[2 * k2][n], st[2 * k2 + 1][n], sp[n]);
-        Pair x[CT];
-#pragma unroll
-        for (int it = 0; it < CT; ++it) x[it] = O::paired_row(l.x + (16 * it + c) * S::SX + 32 * k2, g);
 #pragma unroll
         for (int q = kRead - 1; q >= 0; --q)
 #pragma unroll
           for (int it = 0; it < CT; ++it)
 #pragma unroll
-            for (int n = 0; n < NV; ++n) acc[n][it] = O::mma(sp[n][q], x[it], acc[n][it]);
+            for (int n = 0; n < NV; ++n) acc[n][it] = O::mma(sp[n][q], x[k2 & 1][it], acc[n][it]);
       }
 #pragma unroll
       for (int it = 0; it < CT; ++it) {
@@ -724,94 +777,99 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       if (ci + 2 < nc) fetch_decay(ci + 2);
     }
 
-    if (S::NB == 2 && ci + 1 < nc) {
-      put(ci + 1);
-      if (ci + 2 < nc) fetch(ci + 2);
-    }
-    // sources: into the rows of the chunk, and into the state
-#pragma unroll
-    for (int kt = 0; kt < NKT; ++kt)
-#pragma unroll
-      for (int n = 0; n < NV; ++n) st[kt][n] *= total;
-    decays *= total;
+    // sources: into the rows of the chunk, and into the state, half a chunk at a time; what a product
+    // reads is on its way while the ones before it run
+    constexpr int YA = NKT < 4 ? NKT : 4;  // columns of y read at once
 #pragma unroll
     for (int j2 = 0; j2 < CT / 2; ++j2) {
-      __builtin_amdgcn_sched_barrier(0);  // one half's reads at a time: both at once do not fit the registers
-      Pair z[NV], zs[NV][O::kState];
+      Pair z[NV], zs[NV][O::kState], y[2][YA];
+      Pair sc[OUT ? CT : 1][O::kScore];
+      f32x4 f0, f1;
+      auto columns_of = [&](int kt) {
 #pragma unroll
-      for (int n = 0; n < NV; ++n) {
-        z[n] = O::column_pair(lz, S::SZ, 32 * j2, wc0 + 16 * n, g, c);
-        const f32x4 f0 = *reinterpret_cast<const f32x4*>(dec.src + 32 * j2 + 4 * g);
-        const f32x4 f1 = *reinterpret_cast<const f32x4*>(dec.src + 32 * j2 + 16 + 4 * g);
-        O::template split<O::kState>(O::low(z[n]) * f0, O::high(z[n]) * f1, zs[n]);
-      }
+        for (int i = 0; i < YA; ++i) y[kt / YA & 1][i] = O::column_pair(ly, S::SY, 32 * j2, 16 * (kt + i), g, c);
+      };
+#pragma unroll
+      for (int n = 0; n < NV; ++n) z[n] = O::column_pair(lz, S::SZ, 32 * j2, wc0 + 16 * n, g, c);
+      f0 = *reinterpret_cast<const f32x4*>(dec.src + 32 * j2 + 4 * g);
+      f1 = *reinterpret_cast<const f32x4*>(dec.src + 32 * j2 + 16 + 4 * g);
       if constexpr (OUT) {
 #pragma unroll
-        for (int it = 0; it < CT; ++it) {
+        for (int it = 0; it < CT; ++it)
           if (REV ? it <= 2 * j2 + 1 : it >= 2 * j2) {
-            // the one tile of a pair beyond the diagonal was not written
-            const bool half = REV ? it == 2 * j2 + 1 : it == 2 * j2;
 #pragma unroll
-            for (int q = O::kScore - 1; q >= 0; --q) {
-              Pair s = O::paired_row(l.score[q] + (16 * it + c) * S::SP + 32 * j2, g);
-              if (half) {
+            for (int q = 0; q < O::kScore; ++q)
+              sc[it][q] = O::paired_row(l.score[q] + (16 * it + c) * S::SP + 32 * j2, g);
+          }
+      }
+      columns_of(0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (j2 == 0) {
+#pragma unroll
+        for (int kt = 0; kt < NKT; ++kt)
+#pragma unroll
+          for (int n = 0; n < NV; ++n) st[kt][n] *= total;
+        decays *= total;
+      }
+#pragma unroll
+      for (int n = 0; n < NV; ++n) O::template split<O::kState>(O::low(z[n]) * f0, O::high(z[n]) * f1, zs[n]);
+      if constexpr (OUT) {
+#pragma unroll
+        for (int q = O::kScore - 1; q >= 0; --q)
+#pragma unroll
+          for (int it = 0; it < CT; ++it) {
+            if (REV ? it <= 2 * j2 + 1 : it >= 2 * j2) {
+              // the one tile of a pair beyond the diagonal was not written
+              if (REV ? it == 2 * j2 + 1 : it == 2 * j2) {
                 if constexpr (BF) {
-                  if (REV) s.x = s.y = 0; else s.z = s.w = 0;
+                  if (REV) sc[it][q].x = sc[it][q].y = 0; else sc[it][q].z = sc[it][q].w = 0;
                 } else {
-                  if (REV) s.a = zero4(); else s.b = zero4();
+                  if (REV) sc[it][q].a = zero4(); else sc[it][q].b = zero4();
                 }
               }
 #pragma unroll
-              for (int n = 0; n < NV; ++n) acc[n][it] = O::mma(z[n], s, acc[n][it]);
+              for (int n = 0; n < NV; ++n) acc[n][it] = O::mma(z[n], sc[it][q], acc[n][it]);
             }
           }
-        }
       }
 #pragma unroll
-      for (int kt = 0; kt < NKT; kt += 2) {
-        Pair y[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) y[i] = O::column_pair(ly, S::SY, 32 * j2, 16 * (kt + i), g, c);
+      for (int kt = 0; kt < NKT; kt += YA) {
+        if (kt + YA < NKT) columns_of(kt + YA);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int q = O::kState - 1; q >= 0; --q)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < YA; ++i)
 #pragma unroll
-            for (int n = 0; n < NV; ++n) st[kt + i][n] = O::mma(y[i], zs[n][q], st[kt + i][n]);
+            for (int n = 0; n < NV; ++n) st[kt + i][n] = O::mma(y[kt / YA & 1][i], zs[n][q], st[kt + i][n]);
+      }
+      if (j2 == 0 && S::NB == 2 && ci + 1 < nc) {
+        put(ci + 1);
+        if (ci + 2 < nc) fetch(ci + 2);
       }
     }
 
     if constexpr (OUT) {
       if (__builtin_expect(l.odd[ci & 1] != 0, 0)) {
-        const int rare = anew(lane), c = rare & 15, g = rare >> 4, wc0 = 16 * NV * (anew(tid) >> 6);
-        auto state_row = [&](int kt, int r) { return 16 * kt + 4 * g + r; };
-        const E* zb = head_base<E>(m.z, b, h);
-        auto value = [&](int j, int col) {
-          return tb + j < end && col < m.dz ? O::one(zb[int64_t(tb + j) * m.z.st + int64_t(col) * m.z.sd]) : 0.0f;
-        };
-        auto odd = [](float v) { return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u; };
-#pragma unroll 1
-        for (int j = 0; j < C; ++j) {
+        int* from = l.from[ci & 1] + wc0;  // this wave's own columns
 #pragma unroll
-          for (int n = 0; n < NV; ++n) {
-            // selects, not branches: the accumulators in divergent code cost the whole kernel registers
-            const float u = value(j, c0 + wc0 + 16 * n + c), w = dec.src[j] * u;
+        for (int n = 0; n < NV; ++n) {
+          const bool lost = from[16 * n + c] < C;
 #pragma unroll
-            for (int kt = 0; kt < NKT; ++kt)
+          for (int kt = 0; kt < NKT; ++kt)
 #pragma unroll
-              for (int r = 0; r < 4; ++r) st[kt][n][r] += odd(u) ? O::one(ly[j * S::SY + state_row(kt, r)]) * w : 0.0f;
+            for (int r = 0; r < 4; ++r) st[kt][n][r] = lost ? NAN : st[kt][n][r];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float v = value(j, c0 + wc0 + 16 * n + 4 * g + r);
+          for (int r = 0; r < 4; ++r) {
+            const int first = from[16 * n + 4 * g + r];
 #pragma unroll
-              for (int it = 0; it < CT; ++it) {
-                const int row = 16 * it + c;
-                const float s = O::one(l.score[0][row * S::SP + O::paired(j)]) * v;
-                acc[n][it][r] += odd(v) && (REV ? j >= row : j <= row) ? s : 0.0f;
-              }
+            for (int it = 0; it < CT; ++it) {
+              const int row = REV ? C - 1 - (16 * it + c) : 16 * it + c;
+              acc[n][it][r] = row >= first ? NAN : acc[n][it][r];
             }
           }
         }
+        for (int i = lane; i < 16 * NV; i += kWave) from[i] = C;
       }
       // a token's rows of out
       const int64_t row_bytes = int64_t(p.H) * m.dz * (!BF || m.out_f32 ? 4 : 2);
@@ -821,15 +879,26 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       if (VEC) {
         const uint32_t off = uint32_t(c) * uint32_t(row_bytes);
 #pragma unroll
-        for (int it = 0; it < CT; ++it) {
-          char* row = to + 16 * it * row_bytes;
+        for (int n = 0; n < NV; ++n) {
+          const uint32_t at = uint32_t(col + 16 * n);
+          if (c0 + int(at) < m.dz) {
+            if (left >= C) {
 #pragma unroll
-          for (int n = 0; n < NV; ++n) {
-            f32x4 v = acc[n][it];
-            if (tb + 16 * it + c >= len) v = zero4();
-            if (tb + 16 * it + c < t1 && c0 + col + 16 * n < m.dz) {
-              if (!BF || m.out_f32) *reinterpret_cast<f32x4*>(row + (off + 4 * uint32_t(col + 16 * n))) = v;
-              else Op<true>::put4(reinterpret_cast<uint16_t*>(row + (off + 2 * uint32_t(col + 16 * n))), v);
+              for (int it = 0; it < CT; ++it) {
+                char* row = to + 16 * it * row_bytes;
+                if (!BF || m.out_f32) *reinterpret_cast<f32x4*>(row + (off + 4 * at)) = acc[n][it];
+                else Op<true>::put4(reinterpret_cast<uint16_t*>(row + (off + 2 * at)), acc[n][it]);
+              }
+            } else {
+#pragma unroll
+              for (int it = 0; it < CT; ++it) {
+                char* row = to + 16 * it * row_bytes;
+                const f32x4 v = 16 * it + c < left ? acc[n][it] : zero4();
+                if (tb + 16 * it + c < t1) {
+                  if (!BF || m.out_f32) *reinterpret_cast<f32x4*>(row + (off + 4 * at)) = v;
+                  else Op<true>::put4(reinterpret_cast<uint16_t*>(row + (off + 2 * at)), v);
+                }
+              }
             }
           }
         }
