@@ -999,7 +999,9 @@ __global__ __launch_bounds__(W * kWave) void march_local(DaParams p) {
 template <bool BF, int NKT, int W, bool VEC>
 void launch_shape(const DaParams& p, int first, int count, bool local, hipStream_t stream) {
   constexpr int BV = 16 * W;
-  const int64_t blocks = int64_t((p.m[first].dz + BV - 1) / BV) * p.B * p.H * (local ? p.segments - 1 : p.segments);
+  int64_t columns = 0;
+  for (int i = first; i < first + count; ++i) columns = std::max<int64_t>(columns, (p.m[i].dz + BV - 1) / BV);
+  const int64_t blocks = columns * p.B * p.H * (local ? p.segments - 1 : p.segments);
   const dim3 grid{unsigned(blocks), unsigned(count), 1};
   if (local) march_local<BF, NKT, 1, W, VEC><<<grid, W * kWave, 0, stream>>>(p);
   else if (p.marches == 1) march_forward<BF, NKT, 1, W, VEC><<<grid, W * kWave, 0, stream>>>(p);
@@ -1008,8 +1010,14 @@ void launch_shape(const DaParams& p, int first, int count, bool local, hipStream
 
 template <bool BF, bool VEC>
 hipError_t launch_marches(const DaParams& p, int first, int count, bool local, hipStream_t stream) {
-  const int tiles = march_tiles(p.m[first].dx);
-  if (march_waves(p.m[first].dz) == 4) {
+  // the class of the widest: marches launched together may differ
+  int dx = 0, dz = 0;
+  for (int i = first; i < first + count; ++i) {
+    dx = std::max(dx, p.m[i].dx);
+    dz = std::max(dz, p.m[i].dz);
+  }
+  const int tiles = march_tiles(dx);
+  if (march_waves(dz) == 4) {
     if (tiles == 2) launch_shape<BF, 2, 4, VEC>(p, first, count, local, stream);
     else if (tiles == 4) launch_shape<BF, 4, 4, VEC>(p, first, count, local, stream);
     else if (tiles == 8) launch_shape<BF, 8, 4, VEC>(p, first, count, local, stream);

@@ -1471,18 +1471,19 @@ sx_status sx_decay_attention_backward(sx_dtype dtype, const int64_t* q_shape, co
     if (err != hipSuccess) return device_status(err, "decay-attention gradient launch");
     const struct { const float* src; void* to; int64_t heads, d; } shared[3] = {
         {w.share_q, grad_q, s.hq, s.dk}, {w.share_k, grad_k, s.hk, s.dk}, {w.share_v, grad_v, s.hv, s.dv}};
+    sx::DaShares sums{};
     for (const auto& x : shared) {
       if (!x.src) continue;
-      sx::DaShare sh{};
+      sx::DaShare& sh = sums.s[sums.count++];
       sh.src = x.src;
       sh.out = x.to;
       sh.rows = s.B * s.T * x.heads;
       sh.rep = int(s.H / x.heads);
       sh.d = int(x.d);
       sh.bf16 = p.bf16;
-      err = sx::launch_share_sum(sh, str);
-      if (err != hipSuccess) return device_status(err, "decay-attention gradient launch");
     }
+    err = sx::launch_share_sums(sums, str);
+    if (err != hipSuccess) return device_status(err, "decay-attention gradient launch");
   }
   sx::DaDecayGrad d{};
   d.B = p.B;

@@ -110,7 +110,11 @@ struct DaShare {
   int rep, d;
   int bf16;
 };
-hipError_t launch_share_sum(const DaShare& p, hipStream_t stream);
+struct DaShares {
+  DaShare s[3];
+  int count;
+};
+hipError_t launch_share_sums(const DaShares& p, hipStream_t stream);
 
 // One token of many requests.
 struct DaStep {
