@@ -491,6 +491,12 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
   const int nc = (live + C - 1) / C;
   const int c0 = cb * S::BV, wc0 = 16 * NV * wave;  // first column of the workgroup, and of the wave within it
   const int64_t state = int64_t(p.dk) * p.dv;
+  // Tiles of x, y and the state that hold nothing, and waves without columns, are left out where a product
+  // is dear (f32: 32 cycles a 16x16x4; 333 tokens of 48 x 80: gradient 25 us, 32 without); with bf16 the
+  // branches cost more than the products (8192 tokens of 128 x 128: 53 us, 56 with).
+  const int pairs = BF ? NKT / 2 : (m.dx + 31) / 32;
+  const int busy = BF ? W : min(W, (m.dz - c0 + 16 * NV - 1) / (16 * NV));
+  const bool mine = BF || wave < busy;
 
   const float* gb = p.g + int64_t(b) * p.gb + int64_t(h) * p.gh;
 
@@ -640,6 +646,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
         constexpr int A = NKT / 2 < 4 ? NKT / 2 : N == 1 ? 4 : 2;  // products whose operands are read at once
 #pragma unroll
         for (int k2 = 0; k2 < NKT / 2; k2 += A) {
+          if (!BF && k2 >= pairs) continue;
           Pair y[A][N], x[A][N];
 #pragma unroll
           for (int k = 0; k < A; ++k)
@@ -658,6 +665,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
           // what a row takes from a source: decay (x_i . y_j) (w_i . z_j), this workgroup's columns of the second
 #pragma unroll
           for (int k2 = 0; k2 < S::BV / 32; k2 += 2) {
+            if (!BF && c0 + 32 * k2 >= m.dz) continue;
             Pair z[2][N], w[2][N];
 #pragma unroll
             for (int k = 0; k < 2; ++k)
@@ -723,7 +731,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       }
       if constexpr (MASS != 0) {
         if (wave == kMassWave && ci > 0)
-          chunk_mass<REV, MASS, CT, S::TILES>(p, m, l, (ci - 1) & 1, W, first_token(ci - 1), t1, cb, bh, lane);
+          chunk_mass<REV, MASS, CT, S::TILES>(p, m, l, (ci - 1) & 1, busy, first_token(ci - 1), t1, cb, bh, lane);
         if (m.chunk_decay && cb == 0 && tid == 0)
           m.chunk_decay[int64_t(bh) * ((p.T + C - 1) / C) + tb / C] = total;
       }
@@ -732,43 +740,46 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
 #pragma unroll
         for (int it = 0; it < CT; ++it) acc[n][it] = zero4();
       // rows against the state, each product's rows read ahead of the one before
-      Pair x[2][CT];
-      auto rows_of = [&](int k2) {
+      if (mine) {
+        Pair x[2][CT];
+        auto rows_of = [&](int k2) {
 #pragma unroll
-        for (int it = 0; it < CT; ++it) x[k2 & 1][it] = O::paired_row(l.x + (16 * it + c) * S::SX + 32 * k2, g);
-      };
-      rows_of(0);
+          for (int it = 0; it < CT; ++it) x[k2 & 1][it] = O::paired_row(l.x + (16 * it + c) * S::SX + 32 * k2, g);
+        };
+        rows_of(0);
 #pragma unroll
-      for (int k2 = 0; k2 < NKT / 2; ++k2) {
-        if (k2 + 1 < NKT / 2) rows_of(k2 + 1);
-        __builtin_amdgcn_sched_barrier(0);
-        Pair sp[NV][kRead];
+        for (int k2 = 0; k2 < NKT / 2; ++k2) {
+          if (!BF && k2 >= pairs) continue;
+          if (k2 + 1 < NKT / 2) rows_of(k2 + 1);
+          __builtin_amdgcn_sched_barrier(0);
+          Pair sp[NV][kRead];
 #pragma unroll
-        for (int n = 0; n < NV; ++n) O::template split<kRead>(st[2 * k2][n], st[2 * k2 + 1][n], sp[n]);
+          for (int n = 0; n < NV; ++n) O::template split<kRead>(st[2 * k2][n], st[2 * k2 + 1][n], sp[n]);
 #pragma unroll
-        for (int q = kRead - 1; q >= 0; --q)
+          for (int q = kRead - 1; q >= 0; --q)
 #pragma unroll
-          for (int it = 0; it < CT; ++it)
+            for (int it = 0; it < CT; ++it)
 #pragma unroll
-            for (int n = 0; n < NV; ++n) acc[n][it] = O::mma(sp[n][q], x[k2 & 1][it], acc[n][it]);
-      }
-#pragma unroll
-      for (int it = 0; it < CT; ++it) {
-        const float f = dec.row[16 * it + c];
-        float mass = 0.0f;
-#pragma unroll
-        for (int n = 0; n < NV; ++n) {
-          acc[n][it] *= f;
-          if constexpr (MASS != 0) {
-            const f32x4 w = O::four(l.w + (16 * it + c) * S::SW + wc0 + 16 * n + 4 * g);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) mass += acc[n][it][r] * w[r];
-          }
+              for (int n = 0; n < NV; ++n) acc[n][it] = O::mma(sp[n][q], x[k2 & 1][it], acc[n][it]);
         }
-        if constexpr (MASS != 0) {
-          mass += __shfl_xor(mass, 16);
-          mass += __shfl_xor(mass, 32);
-          if (g == 0) l.part[ci & 1][wave][16 * it + c] = mass;
+#pragma unroll
+        for (int it = 0; it < CT; ++it) {
+          const float f = dec.row[16 * it + c];
+          float mass = 0.0f;
+#pragma unroll
+          for (int n = 0; n < NV; ++n) {
+            acc[n][it] *= f;
+            if constexpr (MASS != 0) {
+              const f32x4 w = O::four(l.w + (16 * it + c) * S::SW + wc0 + 16 * n + 4 * g);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) mass += acc[n][it][r] * w[r];
+            }
+          }
+          if constexpr (MASS != 0) {
+            mass += __shfl_xor(mass, 16);
+            mass += __shfl_xor(mass, 32);
+            if (g == 0) l.part[ci & 1][wave][16 * it + c] = mass;
+          }
         }
       }
       __syncthreads();
@@ -780,68 +791,71 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     // sources: into the rows of the chunk, and into the state, half a chunk at a time; what a product
     // reads is on its way while the ones before it run
     constexpr int YA = NKT < 4 ? NKT : 4;  // columns of y read at once
+    decays *= total;
 #pragma unroll
     for (int j2 = 0; j2 < CT / 2; ++j2) {
-      Pair z[NV], zs[NV][O::kState], y[2][YA];
-      Pair sc[OUT ? CT : 1][O::kScore];
-      f32x4 f0, f1;
-      auto columns_of = [&](int kt) {
+      if (mine) {
+        Pair z[NV], zs[NV][O::kState], y[2][YA];
+        Pair sc[OUT ? CT : 1][O::kScore];
+        f32x4 f0, f1;
+        auto columns_of = [&](int kt) {
 #pragma unroll
-        for (int i = 0; i < YA; ++i) y[kt / YA & 1][i] = O::column_pair(ly, S::SY, 32 * j2, 16 * (kt + i), g, c);
-      };
+          for (int i = 0; i < YA; ++i) y[kt / YA & 1][i] = O::column_pair(ly, S::SY, 32 * j2, 16 * (kt + i), g, c);
+        };
 #pragma unroll
-      for (int n = 0; n < NV; ++n) z[n] = O::column_pair(lz, S::SZ, 32 * j2, wc0 + 16 * n, g, c);
-      f0 = *reinterpret_cast<const f32x4*>(dec.src + 32 * j2 + 4 * g);
-      f1 = *reinterpret_cast<const f32x4*>(dec.src + 32 * j2 + 16 + 4 * g);
-      if constexpr (OUT) {
+        for (int n = 0; n < NV; ++n) z[n] = O::column_pair(lz, S::SZ, 32 * j2, wc0 + 16 * n, g, c);
+        f0 = *reinterpret_cast<const f32x4*>(dec.src + 32 * j2 + 4 * g);
+        f1 = *reinterpret_cast<const f32x4*>(dec.src + 32 * j2 + 16 + 4 * g);
+        if constexpr (OUT) {
 #pragma unroll
-        for (int it = 0; it < CT; ++it)
-          if (REV ? it <= 2 * j2 + 1 : it >= 2 * j2) {
-#pragma unroll
-            for (int q = 0; q < O::kScore; ++q)
-              sc[it][q] = O::paired_row(l.score[q] + (16 * it + c) * S::SP + 32 * j2, g);
-          }
-      }
-      columns_of(0);
-      __builtin_amdgcn_sched_barrier(0);
-      if (j2 == 0) {
-#pragma unroll
-        for (int kt = 0; kt < NKT; ++kt)
-#pragma unroll
-          for (int n = 0; n < NV; ++n) st[kt][n] *= total;
-        decays *= total;
-      }
-#pragma unroll
-      for (int n = 0; n < NV; ++n) O::template split<O::kState>(O::low(z[n]) * f0, O::high(z[n]) * f1, zs[n]);
-      if constexpr (OUT) {
-#pragma unroll
-        for (int q = O::kScore - 1; q >= 0; --q)
-#pragma unroll
-          for (int it = 0; it < CT; ++it) {
+          for (int it = 0; it < CT; ++it)
             if (REV ? it <= 2 * j2 + 1 : it >= 2 * j2) {
-              // the one tile of a pair beyond the diagonal was not written
-              if (REV ? it == 2 * j2 + 1 : it == 2 * j2) {
-                if constexpr (BF) {
-                  if (REV) sc[it][q].x = sc[it][q].y = 0; else sc[it][q].z = sc[it][q].w = 0;
-                } else {
-                  if (REV) sc[it][q].a = zero4(); else sc[it][q].b = zero4();
-                }
-              }
 #pragma unroll
-              for (int n = 0; n < NV; ++n) acc[n][it] = O::mma(z[n], sc[it][q], acc[n][it]);
+              for (int q = 0; q < O::kScore; ++q)
+                sc[it][q] = O::paired_row(l.score[q] + (16 * it + c) * S::SP + 32 * j2, g);
             }
-          }
-      }
-#pragma unroll
-      for (int kt = 0; kt < NKT; kt += YA) {
-        if (kt + YA < NKT) columns_of(kt + YA);
+        }
+        columns_of(0);
         __builtin_amdgcn_sched_barrier(0);
+        if (j2 == 0) {
 #pragma unroll
-        for (int q = O::kState - 1; q >= 0; --q)
+          for (int kt = 0; kt < NKT; ++kt)
 #pragma unroll
-          for (int i = 0; i < YA; ++i)
+            for (int n = 0; n < NV; ++n) st[kt][n] *= total;
+        }
 #pragma unroll
-            for (int n = 0; n < NV; ++n) st[kt + i][n] = O::mma(y[kt / YA & 1][i], zs[n][q], st[kt + i][n]);
+        for (int n = 0; n < NV; ++n) O::template split<O::kState>(O::low(z[n]) * f0, O::high(z[n]) * f1, zs[n]);
+        if constexpr (OUT) {
+#pragma unroll
+          for (int q = O::kScore - 1; q >= 0; --q)
+#pragma unroll
+            for (int it = 0; it < CT; ++it) {
+              if (REV ? it <= 2 * j2 + 1 : it >= 2 * j2) {
+                // the one tile of a pair beyond the diagonal was not written
+                if (REV ? it == 2 * j2 + 1 : it == 2 * j2) {
+                  if constexpr (BF) {
+                    if (REV) sc[it][q].x = sc[it][q].y = 0; else sc[it][q].z = sc[it][q].w = 0;
+                  } else {
+                    if (REV) sc[it][q].a = zero4(); else sc[it][q].b = zero4();
+                  }
+                }
+#pragma unroll
+                for (int n = 0; n < NV; ++n) acc[n][it] = O::mma(z[n], sc[it][q], acc[n][it]);
+              }
+            }
+        }
+#pragma unroll
+        for (int kt = 0; kt < NKT; kt += YA) {
+          if (!BF && kt / 2 >= pairs) continue;
+          if (kt + YA < NKT) columns_of(kt + YA);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int q = O::kState - 1; q >= 0; --q)
+#pragma unroll
+            for (int i = 0; i < YA; ++i)
+#pragma unroll
+              for (int n = 0; n < NV; ++n) st[kt + i][n] = O::mma(y[kt / YA & 1][i], zs[n][q], st[kt + i][n]);
+        }
       }
       if (j2 == 0 && S::NB == 2 && ci + 1 < nc) {
         put(ci + 1);
@@ -943,7 +957,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       const int64_t mb = (int64_t(cb) * BH + bh);
       const int chunks = (p.T + C - 1) / C;
       if (nc > 0 && wave == kMassWave)
-        chunk_mass<REV, MASS, CT, S::TILES>(p, m, l, (nc - 1) & 1, W, first_token(nc - 1), t1, cb, bh, lane);
+        chunk_mass<REV, MASS, CT, S::TILES>(p, m, l, (nc - 1) & 1, busy, first_token(nc - 1), t1, cb, bh, lane);
       for (int q = tid; q < rest; q += THREADS) m.mass[mb * p.T + from + q] = 0.0f;
       for (int q = tid; q < (rest + C - 1) / C; q += THREADS) {
         m.mass_chunk[mb * chunks + from / C + q] = 0.0f;
