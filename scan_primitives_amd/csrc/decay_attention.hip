@@ -75,19 +75,39 @@ __global__ __launch_bounds__(kThreads) void decay_grad(DaDecayGrad p) {
     for (int k = 0; k < p.blocks; ++k) s += double(v[(k * BH + bh) * n + i]);
     return s;
   };
-  double z = 0.0;
-  if (seg > 0) {
-    for (int k = 0; k < p.blocks; ++k) z += p.cross[(k * BH + bh) * (p.segments + 1) + seg];
-  } else if (p.initial) {
+  const int first = seg * (p.seg_tokens / p.chunk), last = min(p.chunks, first + p.seg_tokens / p.chunk);
+  // What a token's decay carries within its chunk, and whether anything passes at all: where exp(g) = 0
+  // neither does a gradient.
+  struct Within {
+    double v;
+    bool passes;
+  };
+  auto within = [&](int t) {
+    if (t >= len) return Within{0.0, false};
+    const float gv = p.g[int64_t(b) * p.gb + int64_t(t) * p.gt + int64_t(h) * p.gh];
+    return Within{sum_of(p.rows, p.T, t) + sum_of(p.sources, p.T, t), !(gv <= -kMostLog)};
+  };
+  // the first tokens' on their way before anything is waited for
+  constexpr int A = 2;
+  Within ahead[A];
+#pragma unroll
+  for (int i = 0; i < A; ++i) {
+    const int t = first * p.chunk + i * kThreads + tid;
+    ahead[i] = t < min(last * p.chunk, p.T) ? within(t) : Within{0.0, false};
+  }
+  // cross: [blocks][B * H][segments + 1], at the start of each segment but the first, and at the end
+  double z = 0.0, end = 0.0;
+  for (int k = 0; k < p.blocks; ++k) {
+    const double* at = p.cross + (k * BH + bh) * (p.segments + 1) + seg;
+    if (seg > 0) z += at[0];
+    end += at[1];
+  }
+  if (seg == 0 && p.initial) {
     double s = 0.0;
     for (int64_t i = tid; i < state; i += kThreads)
       s += double(p.initial[bh * state + i]) * double(p.grad_initial[bh * state + i]);
     z = block_sum(s, la);
   }
-  // cross: [blocks][B * H][segments + 1], at the start of each segment but the first, and at the end
-  double end = 0.0;
-  for (int k = 0; k < p.blocks; ++k) end += p.cross[(k * BH + bh) * (p.segments + 1) + seg + 1];
-  const int first = seg * (p.seg_tokens / p.chunk), last = min(p.chunks, first + p.seg_tokens / p.chunk);
   double all = 0.0;
   for (int i0 = first; i0 < last; i0 += kThreads) {
     const int n = min(kThreads, last - i0);
@@ -118,21 +138,25 @@ __global__ __launch_bounds__(kThreads) void decay_grad(DaDecayGrad p) {
       // The carried sum at the segment's end is known outright as well: what rounding has put between
       // the two is taken off again, in proportion to what had been added up.
       const double off = z - end;
-      if (n == last - first && sum > 0.0 && fabs(off) <= 1e-4 * sum)
-        for (int i = from; i < n; ++i) ly[i] -= cuts[i] ? 0.0 : off * (lw[i] / sum);
+      if (n == last - first && sum > 0.0 && fabs(off) <= 1e-4 * sum) {
+        const double share = off / sum;
+        for (int i = from; i < n; ++i) ly[i] -= cuts[i] ? 0.0 : share * lw[i];
+      }
     }
     __syncthreads();
-    const int t1 = min((i0 + n) * p.chunk, p.T);
-    for (int t = i0 * p.chunk + tid; t < t1; t += kThreads) {
-      double v = 0.0;
-      if (t < len) {
-        const float gv = p.g[int64_t(b) * p.gb + int64_t(t) * p.gt + int64_t(h) * p.gh];
-        // exp(g) = 0: nothing passes, and neither does a gradient
-        if (!(gv <= -kMostLog)) v = ly[t / p.chunk - i0] + sum_of(p.rows, p.T, t) + sum_of(p.sources, p.T, t);
-      }
+    const int t0 = i0 * p.chunk, t1 = min((i0 + n) * p.chunk, p.T);
+    auto put = [&](int t, Within in) {
+      const double v = in.passes ? ly[t / p.chunk - i0] + in.v : 0.0;
       if (p.per_head) all += v;
       else p.grad_g[(int64_t(b) * p.T + t) * p.H + h] = float(v);
+    };
+    int t = t0 + tid;
+    if (i0 == first) {
+#pragma unroll
+      for (int i = 0; i < A; ++i, t += kThreads)
+        if (t < t1) put(t, ahead[i]);
     }
+    for (; t < t1; t += kThreads) put(t, within(t));
   }
   if (p.per_head) {
     __syncthreads();
