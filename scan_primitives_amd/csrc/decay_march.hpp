@@ -245,6 +245,7 @@ struct Shape {
     int from[2][BV];  // the first token of each column that does (in the march's order; C and more: none)
     alignas(16) E x[C * SX];
     alignas(16) E score[O::kScore][C * SP];
+    alignas(16) E out[C * SW];  // a chunk's rows of out, on their way to memory
   };
   struct Mass : Out {
     alignas(16) E w[C * SW];
@@ -595,6 +596,37 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       tw.store(l.w, S::SW);
     }
   };
+  // Results of the operands' type leave through LDS, a chunk late, by whole rows and past the caches: a
+  // wave's 16 columns alone are 32 bytes of a bf16 row, and lines the L2s still held at the kernel's end
+  // would have to be written then (8192 tokens of 128 x 128: 78.0 us, 81.8 straight from the accumulators).
+  constexpr int PR = S::BV / O::kPiece, STEP = THREADS / PR, NO = (C + STEP - 1) / STEP;
+  const bool staged = VEC && OUT && !(BF && m.out_f32);
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 held[NO];
+  auto out_read = [&] {
+    if constexpr (OUT) {
+      if (!staged) return;
+#pragma unroll
+      for (int n = 0; n < NO; ++n)
+        held[n] = *reinterpret_cast<const u32x4*>(l.out + min(tid / PR + n * STEP, C - 1) * S::SW +
+                                                  tid % PR * O::kPiece);
+    }
+  };
+  auto out_write = [&](int ci) {
+    if constexpr (OUT) {
+      const int tb = first_token(ci), col = tid % PR * O::kPiece;
+      if (!staged || c0 + col >= m.dz) return;
+      const int64_t row_bytes = int64_t(p.H) * m.dz * int64_t(sizeof(E));
+      char* to = static_cast<char*>(m.out) + (((int64_t(b) * p.T + tb) * p.H + h) * m.dz + c0) * int64_t(sizeof(E));
+      const uint32_t off = uint32_t(tid / PR) * uint32_t(row_bytes) + uint32_t(col) * uint32_t(sizeof(E));
+#pragma unroll
+      for (int n = 0; n < NO; ++n) {
+        const int t = tid / PR + n * STEP;
+        if (tb + C > end && t >= end - tb) held[n] = u32x4{0, 0, 0, 0};
+        if (t < C && tb + t < t1) st_stream(reinterpret_cast<u32x4*>(to + n * STEP * row_bytes + off), held[n]);
+      }
+    }
+  };
   if constexpr (OUT) {
     if (tid < 2) l.odd[tid] = 0;
     for (int i = tid; i < 2 * S::BV; i += THREADS) l.from[i / S::BV][i % S::BV] = C;
@@ -611,7 +643,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     __syncthreads();
   }
   for (int ci = 0; ci < nc; ++ci) {
-    const int tb = first_token(ci), left = end - tb;
+    const int tb = first_token(ci);
     typename S::Decays& dec = l.dec[ci & 1];
     E* const ly = l.y[ci % S::NB];
     E* const lz = l.z[ci % S::NB];
@@ -620,6 +652,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     f32x4 acc[OUT ? NV : 1][OUT ? CT : 1];  // out transposed: column wc0 + 16 n + 4 g + r, row 16 it + c
     if constexpr (OUT) {
       if (tid == 0) l.odd[(ci + 1) & 1] = 0;
+      if (ci > 0) out_read();
       // scores: the tiles on and on one side of the diagonal, in turn over the waves, as [row][source]; a
       // wave's tiles side by side
       constexpr int kTurns = (S::TILES + W - 1) / W;
@@ -725,6 +758,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       };
       if (wave + (kTurns - 1) * W < S::TILES) tiles(std::integral_constant<int, kTurns>{});
       else if constexpr (kTurns > 1) tiles(std::integral_constant<int, kTurns - 1>{});
+      if (ci > 0) out_write(ci - 1);
       if (wave == kDecayWave && ci + 1 < nc) {
         chunk_decays<REV, C>(l.dec[(ci + 1) & 1], rg, m.scale_out, m.scale_src, lane);
         if (ci + 2 < nc) fetch_decay(ci + 2);
@@ -886,53 +920,33 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
         for (int i = lane; i < 16 * NV; i += kWave) from[i] = C;
       }
       // a token's rows of out
-      const int64_t row_bytes = int64_t(p.H) * m.dz * (!BF || m.out_f32 ? 4 : 2);
-      char* to = static_cast<char*>(m.out) +
-                 (((int64_t(b) * p.T + tb) * p.H + h) * m.dz + c0) * (!BF || m.out_f32 ? 4 : 2);
-      const int col = wc0 + 4 * g;
-      if (VEC) {
-        const uint32_t off = uint32_t(c) * uint32_t(row_bytes);
+      if (staged) {
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-          const uint32_t at = uint32_t(col + 16 * n);
-          if (c0 + int(at) < m.dz) {
-            if (left >= C) {
+        for (int it = 0; it < CT; ++it)
 #pragma unroll
-              for (int it = 0; it < CT; ++it) {
-                char* row = to + 16 * it * row_bytes;
-                if (!BF || m.out_f32) *reinterpret_cast<f32x4*>(row + (off + 4 * at)) = acc[n][it];
-                else Op<true>::put4(reinterpret_cast<uint16_t*>(row + (off + 2 * at)), acc[n][it]);
-              }
-            } else {
-#pragma unroll
-              for (int it = 0; it < CT; ++it) {
-                char* row = to + 16 * it * row_bytes;
-                const f32x4 v = 16 * it + c < left ? acc[n][it] : zero4();
-                if (tb + 16 * it + c < t1) {
-                  if (!BF || m.out_f32) *reinterpret_cast<f32x4*>(row + (off + 4 * at)) = v;
-                  else Op<true>::put4(reinterpret_cast<uint16_t*>(row + (off + 2 * at)), v);
-                }
-              }
-            }
-          }
-        }
+          for (int n = 0; n < NV; ++n) O::put4(l.out + (16 * it + c) * S::SW + wc0 + 16 * n + 4 * g, acc[n][it]);
       } else {
         const int again = anew(tid), c = again & 15, g = again >> 4 & 3;
 #pragma unroll
         for (int it = 0; it < CT; ++it) {
           const int t = tb + 16 * it + c;
-          char* row = to + int64_t(16 * it + c) * row_bytes;
+          const int64_t row = ((int64_t(b) * p.T + t) * p.H + h) * m.dz + c0;
 #pragma unroll
-          for (int n = 0; n < NV; ++n)
+          for (int n = 0; n < NV; ++n) {
+            const int at = wc0 + 16 * n + 4 * g;
+            const f32x4 v = t >= len ? zero4() : acc[n][it];
+            if (VEC) {  // f32 results of bf16 operands, for a sum over the heads that share them
+              if (t < t1 && c0 + at < m.dz) *reinterpret_cast<f32x4*>(static_cast<float*>(m.out) + row + at) = v;
+              continue;
+            }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const int at = wc0 + 16 * n + 4 * g + r;
-              const float v = t >= len ? 0.0f : acc[n][it][r];
-              if (t < t1 && c0 + at < m.dz) {
-                if (!BF || m.out_f32) reinterpret_cast<float*>(row)[at] = v;
-                else reinterpret_cast<uint16_t*>(row)[at] = f32_to_bf16_rne(v);
+              if (t < t1 && c0 + at + r < m.dz) {
+                if (!BF || m.out_f32) static_cast<float*>(m.out)[row + at + r] = v[r];
+                else static_cast<uint16_t*>(m.out)[row + at + r] = f32_to_bf16_rne(v[r]);
               }
             }
+          }
         }
       }
     }
@@ -944,6 +958,10 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     }
   }
 
+  if (OUT && nc > 0) {
+    out_read();
+    out_write(nc - 1);
+  }
   if constexpr (OUT) {
     // tokens past the row's length, in chunks that were not marched
     const int from = t0 + nc * C;
