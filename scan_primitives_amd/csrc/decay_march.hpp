@@ -400,6 +400,23 @@ __device__ __forceinline__ float suffix_sum(float v, int lane) {
   const float c = lane_of(v, 48), b = lane_of(v, 32) + c, a = lane_of(v, 16) + b;
   return lane >= 48 ? v : v + (lane >= 32 ? c : lane >= 16 ? b : a);
 }
+// v of the even and of the odd one of a pair of lane groups, and of the lower and upper half of the wave.
+struct Two {
+  float a, b;
+};
+__device__ __forceinline__ Two of_pair(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return {__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+__device__ __forceinline__ Two of_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return {__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+// Sum over the four lanes, one a group, of a column.
+__device__ __forceinline__ float groups_sum(float v) {
+  const Two p = of_pair(v), h = of_halves(p.a + p.b);
+  return h.a + h.b;
+}
 // Sum over the 16 lanes of a group, in its last lane.
 __device__ __forceinline__ float group_sum(float v) {
   v += dpp<0x111>(v);
@@ -743,14 +760,13 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
               before[r] = sum;
               sum += j0 + r < row ? a[i][r] * s[i][r] : 0.0f;
             }
-            float to = sum, u = __shfl_up(to, 16);  // ... of the lane groups up to this one
-            if (g >= 1) to += u;
-            u = __shfl_up(to, 32);
-            if (g >= 2) to += u;
-            if (g == 3) l.row_tile[ci & 1][jt[i]][row] = to;
+            // ... of the lane groups before this one
+            const Two two = of_pair(sum), halves = of_halves(two.a + two.b);
+            const float groups = (g & 1 ? two.a : 0.0f) + (g >= 2 ? halves.a : 0.0f);
+            if (g == 3) l.row_tile[ci & 1][jt[i]][row] = halves.a + halves.b;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const float v = group_sum(j0 + r <= row ? (to - sum) + before[r] : 0.0f);
+              const float v = group_sum(j0 + r <= row ? groups + before[r] : 0.0f);
               if (c == 15) l.col_tile[ci & 1][wave + i * W][4 * g + r] = v;
             }
           }
@@ -810,8 +826,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
             }
           }
           if constexpr (MASS != 0) {
-            mass += __shfl_xor(mass, 16);
-            mass += __shfl_xor(mass, 32);
+            mass = groups_sum(mass);
             if (g == 0) l.part[ci & 1][wave][16 * it + c] = mass;
           }
         }
