@@ -417,8 +417,9 @@ sx_status sx_table_scan(int states, int nsym, const int32_t* table, int rank, co
  *   S[t] = exp(g[t]) S[t-1] + k[t] v[t]^T,   out[t] = scale * S[t]^T q[t].
  * States, running sums and products are f32 (and finer) for f32 and bf16
  * operands alike; out is rounded to bf16 to nearest even once, on store. With
- * bf16 operands the state enters its products as three bf16 parts that carry
- * all of it, and the scores q[t] . k[s] as two that carry 16 bits.
+ * bf16 operands f32 values enter a product as bf16 parts: three that carry all
+ * 24 bits into the state, two that carry 17 (the scores q[t] . k[s], and the
+ * state where it is read for out).
  *
  *  dtype         SX_F32 or SX_BF16, shared by q, k, v and out.
  *  q, k, v       [B, T, heads, width]: shape (4 entries), strides (NULL for
@@ -441,7 +442,8 @@ sx_status sx_table_scan(int states, int nsym, const int32_t* table, int rank, co
  *                aligned; may hold anything; may be NULL when that is 0.
  *
  * An infinity or NaN of one token reaches that token's own row and later ones of
- * its head, never earlier ones (an infinity may come out as NaN). out and
+ * its head (past a cut as well), never earlier ones; an infinity may come out as
+ * NaN. out and
  * final_state are 16-byte aligned (else SX_E_UNSUPPORTED) and overlap no input
  * and not each other (SX_E_ALIAS). Errors otherwise as the scans: E-DIM-001 shapes,
  * E-DIM-002 dtypes, E-DIM-003 a NULL tensor that has elements, SX_E_UNSUPPORTED
