@@ -322,7 +322,7 @@ hipError_t launch_decay_attention(const DaParams& p, hipStream_t stream) {
   bool vec = true;
   for (int i = 0; i < p.marches; ++i) {
     for (const HeadView* v : {&p.m[i].x, &p.m[i].y, &p.m[i].z, &p.m[i].w})
-      vec = vec && (!v->p || (v->vec && v->st >= 0 && v->st < most / (chunk * e)));
+      vec = vec && (!v->p || (v->unit && v->st >= 0 && v->st < most / (chunk * e)));
     vec = vec && int64_t(p.H) * p.m[i].dz < most / (chunk * 4);
   }
   const auto launch = p.bf16 ? (vec ? launch_marches_bf16 : launch_marches_bf16_any)

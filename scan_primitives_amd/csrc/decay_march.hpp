@@ -155,6 +155,14 @@ struct Op<true> {
   static __device__ __forceinline__ bool finite(uint32_t seen) {
     return (seen & 0xffffu) < 0x7f80u && seen < 0x7f800000u;
   }
+  // a piece without its first n elements, zeros behind
+  static __device__ __forceinline__ uint4 shifted(uint4 v, int n) {
+    if (n & 4) v = make_uint4(v.z, v.w, 0, 0);
+    if (n & 2) v = make_uint4(v.y, v.z, v.w, 0);
+    if (n & 1)
+      v = make_uint4(v.x >> 16 | v.y << 16, v.y >> 16 | v.z << 16, v.z >> 16 | v.w << 16, v.w >> 16);
+    return v;
+  }
   // infinities and NaN taken out
   static __device__ __forceinline__ uint4 finite_part(uint4 v) {
     auto f = [](uint32_t u) {
@@ -215,6 +223,11 @@ struct Op<false> {
     return most(most(most(most(seen, v.x), v.y), v.z), v.w);
   }
   static __device__ __forceinline__ bool finite(uint32_t seen) { return seen < 0x7f800000u; }
+  static __device__ __forceinline__ uint4 shifted(uint4 v, int n) {
+    if (n & 2) v = make_uint4(v.z, v.w, 0, 0);
+    if (n & 1) v = make_uint4(v.y, v.z, v.w, 0);
+    return v;
+  }
   static __device__ __forceinline__ uint4 finite_part(uint4 v) {
     auto f = [](uint32_t u) { return (u & 0x7f800000u) == 0x7f800000u ? 0u : u; };
     return make_uint4(f(v.x), f(v.y), f(v.z), f(v.w));
@@ -285,8 +298,9 @@ __device__ __forceinline__ const E* head_base(const HeadView& v, int b, int h) {
 // A workgroup's tile of C tokens and W columns from c0, on its way from memory to LDS: a thread's
 // share of it in registers. Zero where a token or a column (from `d` on) does not exist: there the
 // load reads the last token or the first columns instead, and `store` writes zero. (A load under a
-// condition would have to be waited for where its lanes join the others again.) VEC: 16-byte pieces
-// at 32-bit offsets from the tile's first token, else one element at a time.
+// condition would have to be waited for where its lanes join the others again.) VEC: 16-byte pieces of
+// rows of any alignment, at 32-bit offsets from the tile's first token; a row's last piece, where it is
+// not whole, is read up to the row's end and shifted into place. Else one element at a time.
 template <bool BF, int W, int THREADS, bool VEC>
 struct Tile {
   using O = Op<BF>;
@@ -300,6 +314,7 @@ struct Tile {
   int64_t col_any;   // bytes to the thread's column
   int row, col;      // of the thread's first piece in the tile
   bool ok;           // its columns exist
+  int shift;         // VEC: elements that the thread's piece is read early
   R r[N];
 
   __device__ __forceinline__ void init(const HeadView& v, int b, int h, int d, int c0) {
@@ -308,7 +323,9 @@ struct Tile {
     row = int(threadIdx.x) / PR;
     col = int(threadIdx.x) % PR * PIECE;
     ok = c0 + col < d;
-    col_any = ok ? int64_t(c0 + col) * (VEC ? 1 : v.sd) * int64_t(sizeof(E)) : 0;
+    const int from = VEC ? min(c0 + col, d - PIECE) : c0 + col;
+    shift = ok ? c0 + col - from : 0;
+    col_any = ok ? int64_t(from) * (VEC ? 1 : v.sd) * int64_t(sizeof(E)) : 0;
   }
   // tokens tb .. of which `left` > 0 exist
   __device__ __forceinline__ void fetch(int tb, int left) {
@@ -316,11 +333,18 @@ struct Tile {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int t = min(row + n * STEP, left - 1);
-      if constexpr (VEC) r[n] = *reinterpret_cast<const R*>(at + (uint32_t(t) * uint32_t(st) + uint32_t(col_any)));
+      if constexpr (VEC) __builtin_memcpy(&r[n], at + (uint32_t(t) * uint32_t(st) + uint32_t(col_any)), 16);
       else r[n] = *reinterpret_cast<const R*>(at + t * st + col_any);
     }
   }
-  __device__ __forceinline__ void mend(int left, bool columns) {
+  // `columns`: the tile is wider than the tensor; `part`: the tensor's width is no whole number of pieces
+  __device__ __forceinline__ void mend(int left, bool columns, bool part) {
+    if constexpr (VEC) {
+      if (part) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) r[n] = O::shifted(r[n], shift);
+      }
+    }
     if (left < O::C || columns) {
 #pragma unroll
       for (int n = 0; n < N; ++n)
@@ -604,12 +628,12 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
   auto put = [&](int ci) {
     const int left = end - first_token(ci), buf = ci % S::NB;
     if constexpr (OUT) {
-      tx.mend(left, m.dx < S::DX);
+      tx.mend(left, m.dx < S::DX, m.dx % O::kPiece != 0);
       tx.template store<true>(l.x, S::SX);
     }
-    ty.mend(left, m.dx < S::DX);
+    ty.mend(left, m.dx < S::DX, m.dx % O::kPiece != 0);
     ty.store(l.y[buf], S::SY);
-    tz.mend(left, m.dz < c0 + S::BV);
+    tz.mend(left, m.dz < c0 + S::BV, m.dz % O::kPiece != 0);
     if constexpr (OUT) {
       // An infinity or NaN in z times a score of zero would reach rows that do not see its token: such
       // values are left out of the products, and what does see them turns into NaN at the end.
@@ -620,7 +644,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     }
     tz.store(l.z[buf], S::SZ);
     if constexpr (MASS != 0) {
-      tw.mend(left, m.dz < c0 + S::BV);
+      tw.mend(left, m.dz < c0 + S::BV, m.dz % O::kPiece != 0);
       tw.store(l.w, S::SW);
     }
   };
@@ -651,7 +675,20 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       for (int n = 0; n < NO; ++n) {
         const int t = tid / PR + n * STEP;
         if (tb + C > end && t >= end - tb) held[n] = u32x4{0, 0, 0, 0};
-        if (t < C && tb + t < t1) st_stream(reinterpret_cast<u32x4*>(to + n * STEP * row_bytes + off), held[n]);
+        if (t >= C || tb + t >= t1) continue;
+        char* at = to + n * STEP * row_bytes + off;
+        const int exist = m.dz - (c0 + col);
+        if (m.dz % O::kPiece == 0) {
+          st_stream(reinterpret_cast<u32x4*>(at), held[n]);
+        } else if (exist >= O::kPiece) {
+          __builtin_memcpy(at, &held[n], 16);  // at any alignment
+        } else {
+#pragma unroll
+          for (int e = 0; e < O::kPiece - 1; ++e) {
+            const uint32_t w = BF ? held[n][e / 2] >> 16 * (e & 1) : held[n][e];
+            if (e < exist) reinterpret_cast<E*>(at)[e] = BF ? E(uint16_t(w)) : E(__uint_as_float(w));
+          }
+        }
       }
     }
   };
@@ -961,7 +998,8 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
           for (int n = 0; n < NV; ++n) {
             const int at = wc0 + 16 * n + 4 * g;
             const f32x4 v = t >= len ? zero4() : acc[n][it];
-            if (VEC) {  // f32 results of bf16 operands, for a sum over the heads that share them
+            // (VEC: f32 results of bf16 operands, for a sum over the heads that share them)
+            if (VEC && m.dz % 4 == 0) {
               if (t < t1 && c0 + at < m.dz) *reinterpret_cast<f32x4*>(static_cast<float*>(m.out) + row + at) = v;
               continue;
             }

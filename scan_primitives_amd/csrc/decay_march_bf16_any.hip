@@ -1,4 +1,4 @@
-// decay_march_bf16_any.hip: the marches of decay attention for bf16 operands, rows of any stride and alignment.
+// decay_march_bf16_any.hip: the marches of decay attention for bf16 operands, an element at a time (rows of any stride).
 #include "decay_march.hpp"
 
 namespace sx {

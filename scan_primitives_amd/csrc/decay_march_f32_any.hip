@@ -1,4 +1,4 @@
-// decay_march_f32_any.hip: the marches of decay attention for f32 operands, rows of any stride and alignment.
+// decay_march_f32_any.hip: the marches of decay attention for f32 operands, an element at a time (rows of any stride).
 #include "decay_march.hpp"
 
 namespace sx {

@@ -1133,6 +1133,7 @@ sx::HeadView head_view(const HeadArg& a, size_t elem, int64_t heads, int64_t pie
   v.sd = st[3];
   v.rep = int(heads / std::max<int64_t>(a.shape[2], 1));
   auto whole = [&](int64_t n, int64_t s) { return n <= 1 || (s * int64_t(elem)) % 16 == 0; };
+  v.unit = st[3] == 1 && a.shape[3] * int64_t(elem) >= 16;
   v.vec = st[3] == 1 && a.shape[3] % piece == 0 && (reinterpret_cast<uintptr_t>(a.data) & 15u) == 0 &&
           whole(a.shape[0], st[0]) && whole(a.shape[1], st[1]) && whole(a.shape[2], st[2]);
   return v;
