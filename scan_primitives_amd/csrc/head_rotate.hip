@@ -8,11 +8,13 @@
 //
 // A row (one head of one token) is cut into units of two components that turn
 // together: (i, i + rot/2) or (2i, 2i+1), and neighbours behind `rot` that do not
-// turn. A lane holds U units of a row, so a pair never leaves its lane: where
-// alignment allows it U consecutive ones (two 16-byte loads a row), else every
-// G-th one, so that a load's lanes touch neighbouring elements. A workgroup takes
-// some tokens of the queries or of the keys; their cosines and sines are formed
-// once for all its heads, through LDS, while its first rows are on their way.
+// turn. A lane holds U units of a row, so a pair never leaves its lane: U
+// consecutive ones (two 16-byte pieces a row, at any alignment) where elements
+// are next to each other, else every G-th one. The gradient of 7 x 2481 tokens
+// of 4 + 2 heads of 194, 12 of them turned, in bf16 takes 53 us in pieces, 112
+// by elements. A workgroup takes some tokens of the queries or of the keys;
+// their cosines and sines are formed once for all its heads, through LDS, while
+// its first rows are on their way.
 // The angle is reduced in 64 bits: position times turns, its nearest whole
 // number taken off; 32 bits would lose the angle of far positions.
 //
@@ -48,6 +50,7 @@ template <>
 struct El<true> {
   using E = uint16_t;
   static constexpr int U = 8;  // units a lane
+  typedef uint32_t piece_t __attribute__((ext_vector_type(4), aligned(2)));  // of a row of any alignment
   static __device__ __forceinline__ float get(E v) { return bf16_to_f32(v); }
   static __device__ __forceinline__ E put(float v) { return f32_to_bf16_rne(v); }
   static __device__ __forceinline__ void open(u32x4 a, float* v) {
@@ -57,6 +60,13 @@ struct El<true> {
       v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
     }
   }
+  // a piece without its first n elements
+  static __device__ __forceinline__ u32x4 shifted(u32x4 v, int n) {
+    if (n & 4) v = u32x4{v[2], v[3], 0, 0};
+    if (n & 2) v = u32x4{v[1], v[2], v[3], 0};
+    if (n & 1) v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+    return v;
+  }
   static __device__ __forceinline__ u32x4 close(const float* v) {
     return u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
   }
@@ -65,45 +75,68 @@ template <>
 struct El<false> {
   using E = float;
   static constexpr int U = 4;
+  typedef uint32_t piece_t __attribute__((ext_vector_type(4), aligned(4)));
   static __device__ __forceinline__ float get(E v) { return v; }
   static __device__ __forceinline__ E put(float v) { return v; }
   static __device__ __forceinline__ void open(u32x4 a, float* v) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(a[i]);
   }
+  static __device__ __forceinline__ u32x4 shifted(u32x4 v, int n) {
+    if (n & 2) v = u32x4{v[2], v[3], 0, 0};
+    if (n & 1) v = u32x4{v[1], v[2], v[3], 0};
+    return v;
+  }
   static __device__ __forceinline__ u32x4 close(const float* v) {
     return u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
   }
 };
 
-// Which components a lane holds. WIDE: U consecutive units (16-byte pieces), else every G-th.
-template <bool BF, int G, bool WIDE>
+// Which components of a row a lane holds: every G-th unit, an element at a time (Elements); or two pieces of U
+// consecutive components (16 bytes), of U units that are either halves apart or neighbours. The last pieces of
+// either kind may hold fewer, and are read early where the row ends (Cut). Where none does (Whole) the gradient
+// of 2 x 2048 tokens of 16 + 4 heads of 128 takes 19.0 us, 20.4 with the cuts looked for.
+enum class Rows { Elements, Cut, Whole };
+
+template <bool BF, int G, Rows R>
 struct Lane {
+  static constexpr bool WIDE = R != Rows::Elements, whole = R == Rows::Whole;
   using T = El<BF>;
   using E = typename T::E;
   static constexpr int U = T::U;
+  using piece_t = typename T::piece_t;
   int lr, half, d;
-  bool split;  // pairs are halves apart, not neighbours
+  bool split;   // pairs are halves apart, not neighbours
+  // WIDE:
+  bool apart;   // ... and so are this lane's
+  int unit0;    // its first unit
+  int at[2], count[2];
 
   __device__ __forceinline__ Lane(const HrParams& p, int lane_in_row)
-      : lr(lane_in_row), half(p.rot / 2), d(p.d), split(!p.neighbours) {}
-  __device__ __forceinline__ int unit(int i) const { return WIDE ? U * lr + i : lr + G * i; }
-  __device__ __forceinline__ int first(int i) const {
-    const int k = unit(i);
-    return split && k < half ? k : 2 * k;
+      : lr(lane_in_row), half(p.rot / 2), d(p.d), split(!p.neighbours) {
+    const int turned = split ? (half + U - 1) / U : 0;  // lanes of units halves apart
+    apart = lr < turned;
+    unit0 = apart ? U * lr : (split ? half : 0) + U * (lr - turned);
+    at[0] = apart ? unit0 : 2 * unit0;
+    at[1] = at[0] + (apart ? half : U);
+    const int end0 = apart ? half : d;
+    count[0] = min(max(end0 - at[0], 0), U);
+    count[1] = apart ? count[0] : min(max(d - at[1], 0), U);
   }
-  __device__ __forceinline__ int second(int i) const {
-    const int k = unit(i);
-    return split && k < half ? k + half : 2 * k + 1;
+  __device__ __forceinline__ int unit(int i) const { return WIDE ? unit0 + i : lr + G * i; }
+  // where its angle is, if it turns
+  __device__ __forceinline__ int angle(int i) const {
+    return WIDE ? min(unit0, kMaxUnits - U) + i : min(unit(i), kMaxUnits - 1);
   }
-  // WIDE: the first components of the lane's two pieces; all U units lie on one side of `half`
-  __device__ __forceinline__ bool apart() const { return split && U * lr < half; }
-  __device__ __forceinline__ int piece(int i) const {
-    return apart() ? U * lr + i * half : 2 * U * lr + i * U;
+  // component of the first (j = 0) or second of unit i, d and more where there is none
+  __device__ __forceinline__ int component(int i, int j) const {
+    const int k = unit(i);
+    if (WIDE && apart) return i < count[0] ? k + j * half : d;
+    return !WIDE && split && k < half ? k + j * half : 2 * k + j;
   }
 
   struct Raw {
-    u32x4 a, b;          // WIDE
+    u32x4 v[2];          // WIDE
     E x[U], y[U];        // not
   };
   // STREAM: past the caches, which a forward pass gains by (4 x 4096 tokens of 16 + 16 heads: 59.1 us, 60.7
@@ -111,28 +144,37 @@ struct Lane {
   template <bool STREAM>
   __device__ __forceinline__ void load(const E* row, int64_t sd, Raw& r) const {
     if constexpr (WIDE) {
-      const u32x4 none = {0, 0, 0, 0};
-      const u32x4* a = reinterpret_cast<const u32x4*>(row + piece(0));
-      const u32x4* b = reinterpret_cast<const u32x4*>(row + piece(1));
-      r.a = piece(0) < d ? (STREAM ? ld_stream(a) : *a) : none;
-      r.b = piece(1) < d ? (STREAM ? ld_stream(b) : *b) : none;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const piece_t* from = reinterpret_cast<const piece_t*>(row + min(at[j], d - U));
+        const u32x4 none = {0, 0, 0, 0};
+        r.v[j] = count[j] > 0 ? u32x4(STREAM ? __builtin_nontemporal_load(from) : *from) : none;
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        r.x[i] = first(i) < d ? row[first(i) * sd] : E(0);
-        r.y[i] = second(i) < d ? row[second(i) * sd] : E(0);
+        r.x[i] = component(i, 0) < d ? row[component(i, 0) * sd] : E(0);
+        r.y[i] = component(i, 1) < d ? row[component(i, 1) * sd] : E(0);
       }
     }
   }
   __device__ __forceinline__ void open(const Raw& r, float (&x)[U], float (&y)[U]) const {
     if constexpr (WIDE) {
-      float v[2 * U];
-      T::open(r.a, v);
-      T::open(r.b, v + U);
+      float v[2][U];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        u32x4 w = r.v[j];
+        if constexpr (!whole) w = T::shifted(w, max(at[j] - (d - U), 0) % U);
+        T::open(w, v[j]);
+        if constexpr (!whole) {
+#pragma unroll
+          for (int i = 0; i < U; ++i) v[j][i] = i < count[j] ? v[j][i] : 0.0f;
+        }
+      }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        x[i] = apart() ? v[i] : v[2 * i];
-        y[i] = apart() ? v[U + i] : v[2 * i + 1];
+        x[i] = apart ? v[0][i] : v[2 * i / U][2 * i % U];
+        y[i] = apart ? v[1][i] : v[2 * i / U][2 * i % U + 1];
       }
     } else {
 #pragma unroll
@@ -144,28 +186,36 @@ struct Lane {
   }
   __device__ __forceinline__ void store(E* row, const float (&x)[U], const float (&y)[U]) const {
     if constexpr (WIDE) {
-      float v[2 * U];
+      float v[2][U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        v[i] = apart() ? x[i] : (i & 1 ? y[i / 2] : x[i / 2]);
-        v[U + i] = apart() ? y[i] : (i & 1 ? y[(U + i) / 2] : x[(U + i) / 2]);
+        v[0][i] = apart ? x[i] : (i & 1 ? y[i / 2] : x[i / 2]);
+        v[1][i] = apart ? y[i] : (i & 1 ? y[(U + i) / 2] : x[(U + i) / 2]);
       }
-      // streamed: what the L2s still held at the kernel's end would have to be written then (63.1 us without)
-      if (piece(0) < d) st_stream(reinterpret_cast<u32x4*>(row + piece(0)), T::close(v));
-      if (piece(1) < d) st_stream(reinterpret_cast<u32x4*>(row + piece(1)), T::close(v + U));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        // streamed: what the L2s still held at the kernel's end would have to be written then (63.1 us without)
+        if (count[j] == U) {
+          __builtin_nontemporal_store(piece_t(T::close(v[j])), reinterpret_cast<piece_t*>(row + at[j]));
+        } else if constexpr (!whole) {
+#pragma unroll
+          for (int i = 0; i < U - 1; ++i)
+            if (i < count[j]) row[at[j] + i] = T::put(v[j][i]);
+        }
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        if (first(i) < d) row[first(i)] = T::put(x[i]);
-        if (second(i) < d) row[second(i)] = T::put(y[i]);
+        if (component(i, 0) < d) row[component(i, 0)] = T::put(x[i]);
+        if (component(i, 1) < d) row[component(i, 1)] = T::put(y[i]);
       }
     }
   }
   __device__ __forceinline__ void weights(const float* w, float (&x)[U], float (&y)[U]) const {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      x[i] = first(i) < d ? (w ? w[first(i)] : 1.0f) : 0.0f;
-      y[i] = second(i) < d ? (w ? w[second(i)] : 1.0f) : 0.0f;
+      x[i] = component(i, 0) < d ? (w ? w[component(i, 0)] : 1.0f) : 0.0f;
+      y[i] = component(i, 1) < d ? (w ? w[component(i, 1)] : 1.0f) : 0.0f;
     }
   }
 };
@@ -178,22 +228,18 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// Cosine and sine of `count` tokens' units from token tok0 on, into cs[token][unit].
+// Cosine and sine of `count` tokens' units that turn, from token tok0 on, into cs[token][unit].
 __device__ __forceinline__ void angles(const HrParams& p, uint32_t tok0, int count, float2 (*cs)[kMaxUnits]) {
-  const int half = p.rot / 2, units = (p.d + 1) / 2;
-  for (int q = int(threadIdx.x); q < count * units; q += kThreads) {
-    const int t = q / units, i = q % units;
-    float2 v = make_float2(1.0f, 0.0f);
-    if (i < half) {
-      const uint32_t tok = tok0 + uint32_t(t), b = tok / uint32_t(p.T);
-      const int64_t at = int64_t(b) * p.pb + int64_t(tok - b * uint32_t(p.T)) * p.pt;
-      const double pos = p.pos64 ? double(static_cast<const int64_t*>(p.positions)[at])
-                                 : double(static_cast<const int32_t*>(p.positions)[at]);
-      const double turn = pos * p.turns[i];
-      const float f = float(turn - rint(turn));
-      v = make_float2(cospif(2.0f * f), sinpif(2.0f * f));
-    }
-    cs[t][i] = v;
+  const int half = p.rot / 2;
+  for (int q = int(threadIdx.x); q < count * half; q += kThreads) {
+    const int t = q / half, i = q % half;
+    const uint32_t tok = tok0 + uint32_t(t), b = tok / uint32_t(p.T);
+    const int64_t at = int64_t(b) * p.pb + int64_t(tok - b * uint32_t(p.T)) * p.pt;
+    const double pos = p.pos64 ? double(static_cast<const int64_t*>(p.positions)[at])
+                               : double(static_cast<const int32_t*>(p.positions)[at]);
+    const double turn = pos * p.turns[i];
+    const float f = float(turn - rint(turn));
+    cs[t][i] = make_float2(cospif(2.0f * f), sinpif(2.0f * f));
   }
 }
 
@@ -206,9 +252,9 @@ __device__ __forceinline__ const E* row_of(const HrParams& p, const HeadView& v,
 }
 
 // blockIdx.y: queries or keys. G lanes a row.
-template <bool BF, int G, bool WIDE>
+template <bool BF, int G, Rows R>
 __global__ __launch_bounds__(kThreads) void rotate_forward(HrParams p) {
-  using L = Lane<BF, G, WIDE>;
+  using L = Lane<BF, G, R>;
   using E = typename L::E;
   constexpr int U = L::U, kSlots = kThreads / G;
   __shared__ float2 cs[kMostTokens][kMaxUnits];
@@ -222,7 +268,6 @@ __global__ __launch_bounds__(kThreads) void rotate_forward(HrParams p) {
   const int count = int(min(uint32_t(tokens), all - tok0)), rows = count * heads;
   const int slot = int(threadIdx.x) / G;
   const L l(p, int(threadIdx.x) % G);
-  const int units = (p.d + 1) / 2;
   typename L::Raw raw;
   if (slot < rows) l.template load<true>(row_of<E>(p, v, tok0, heads, slot), v.sd, raw);
   float w0[U], w1[U];
@@ -242,19 +287,20 @@ __global__ __launch_bounds__(kThreads) void rotate_forward(HrParams p) {
     const float2* turn = cs[q / heads];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const float2 z = l.unit(i) < units ? turn[l.unit(i)] : make_float2(1.0f, 0.0f);
+      const float2 z = turn[l.angle(i)];
+      const bool turns = l.unit(i) < l.half;
       const float a = x[i] * r * w0[i], c = y[i] * r * w1[i];
-      x[i] = a * z.x - c * z.y;
-      y[i] = a * z.y + c * z.x;
+      x[i] = turns ? a * z.x - c * z.y : a;
+      y[i] = turns ? a * z.y + c * z.x : c;
     }
     l.store(out + int64_t(q) * p.d, x, y);
   }
 }
 
 // A workgroup takes every gridDim.x-th group of tokens and leaves one partial sum of the weight's gradient.
-template <bool BF, int G, bool WIDE>
+template <bool BF, int G, Rows R>
 __global__ __launch_bounds__(kThreads) void rotate_backward(HrParams p) {
-  using L = Lane<BF, G, WIDE>;
+  using L = Lane<BF, G, R>;
   using E = typename L::E;
   constexpr int U = L::U, kSlots = kThreads / G;
   __shared__ union {
@@ -268,7 +314,6 @@ __global__ __launch_bounds__(kThreads) void rotate_backward(HrParams p) {
   const uint32_t all = uint32_t(p.B) * uint32_t(p.T);
   const int slot = int(threadIdx.x) / G;
   const L l(p, int(threadIdx.x) % G);
-  const int units = (p.d + 1) / 2;
   float w0[U], w1[U], g0[U], g1[U];
   l.weights(isq ? p.qw : p.kw, w0, w1);
 #pragma unroll
@@ -298,10 +343,11 @@ __global__ __launch_bounds__(kThreads) void rotate_backward(HrParams p) {
       float s = 0.0f, dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const float2 z = l.unit(i) < units ? turn[l.unit(i)] : make_float2(1.0f, 0.0f);
+        const float2 z = turn[l.angle(i)];
+        const bool turns = l.unit(i) < l.half;
         const float e = a[i], f = c[i];
-        a[i] = e * z.x + f * z.y;  // the gradient of u
-        c[i] = f * z.x - e * z.y;
+        a[i] = turns ? e * z.x + f * z.y : e;  // the gradient of u
+        c[i] = turns ? f * z.x - e * z.y : f;
         s = fmaf(x[i], x[i], fmaf(y[i], y[i], s));
         dot = fmaf(a[i] * w0[i], x[i], fmaf(c[i] * w1[i], y[i], dot));
       }
@@ -330,7 +376,7 @@ __global__ __launch_bounds__(kThreads) void rotate_backward(HrParams p) {
     float s = 0.0f;
     for (int i = 0; i < kSlots; ++i) s += lds.sums[i][q];
     const L w(p, q / (2 * U));
-    const int i = q % U, col = q % (2 * U) < U ? w.first(i) : w.second(i);
+    const int col = w.component(q % U, q % (2 * U) < U ? 0 : 1);
     if (col < p.d) partial[col] = s;
   }
 }
@@ -377,30 +423,35 @@ HrParams with_tokens(const HrParams& given, int per_cu) {
   return p;
 }
 
-template <bool BF, int G, bool WIDE>
+template <bool BF, int G, Rows R>
 void launch_rows(const HrParams& p, dim3 grid, bool gradient, hipStream_t stream) {
-  if (gradient) rotate_backward<BF, G, WIDE><<<grid, kThreads, 0, stream>>>(p);
-  else rotate_forward<BF, G, WIDE><<<grid, kThreads, 0, stream>>>(p);
+  if (gradient) rotate_backward<BF, G, R><<<grid, kThreads, 0, stream>>>(p);
+  else rotate_forward<BF, G, R><<<grid, kThreads, 0, stream>>>(p);
 }
 
 template <bool BF, int G>
 void launch_lanes(const HrParams& p, dim3 grid, bool gradient, hipStream_t stream) {
+  bool wide = p.q.unit && (p.hk == 0 || p.k.unit);
+  if (gradient) wide = wide && p.gq.unit && (p.hk == 0 || p.gk.unit);
   constexpr int U = El<BF>::U;
-  // 16-byte pieces: aligned rows, and no lane whose units lie on both sides of the turned half
-  bool wide = p.q.vec && (p.hk == 0 || p.k.vec) && p.d % U == 0 && (p.neighbours || p.rot / 2 % U == 0);
-  if (gradient) wide = wide && p.gq.vec && (p.hk == 0 || p.gk.vec);
-  if (wide) launch_rows<BF, G, true>(p, grid, gradient, stream);
-  else launch_rows<BF, G, false>(p, grid, gradient, stream);
+  const bool whole = p.d % U == 0 && (p.neighbours || p.rot / 2 % U == 0);
+  if (!wide) return launch_rows<BF, G, Rows::Elements>(p, grid, gradient, stream);
+  if constexpr (G * U <= kMaxUnits)  // else only cut rows take so many lanes
+    if (whole) return launch_rows<BF, G, Rows::Whole>(p, grid, gradient, stream);
+  launch_rows<BF, G, Rows::Cut>(p, grid, gradient, stream);
 }
 
 template <bool BF>
 void launch_width(const HrParams& p, dim3 grid, bool gradient, hipStream_t stream) {
-  const int need = ((p.d + 1) / 2 + El<BF>::U - 1) / El<BF>::U;
+  constexpr int U = El<BF>::U;
+  const int half = p.neighbours ? 0 : p.rot / 2;
+  const int need = (half + U - 1) / U + (p.d - 2 * half + 2 * U - 1) / (2 * U);
   if (need <= 2) launch_lanes<BF, 2>(p, grid, gradient, stream);
   else if (need <= 4) launch_lanes<BF, 4>(p, grid, gradient, stream);
   else if (need <= 8) launch_lanes<BF, 8>(p, grid, gradient, stream);
   else if (need <= 16) launch_lanes<BF, 16>(p, grid, gradient, stream);
-  else if constexpr (!BF) launch_lanes<BF, 32>(p, grid, gradient, stream);
+  else if (BF || need <= 32) launch_lanes<BF, 32>(p, grid, gradient, stream);
+  else if constexpr (!BF) launch_lanes<BF, 64>(p, grid, gradient, stream);
 }
 
 }  // namespace

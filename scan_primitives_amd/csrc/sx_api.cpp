@@ -1121,8 +1121,7 @@ void head_strides(const HeadArg& a, int64_t* st) {
   if (a.strides) std::copy(a.strides, a.strides + 4, st); else contiguous_strides(4, a.shape, st);
 }
 
-// `piece`: elements that have to divide d for rows to be read 16 bytes at a time.
-sx::HeadView head_view(const HeadArg& a, size_t elem, int64_t heads, int64_t piece) {
+sx::HeadView head_view(const HeadArg& a, size_t elem, int64_t heads) {
   int64_t st[4];
   head_strides(a, st);
   sx::HeadView v{};
@@ -1132,10 +1131,7 @@ sx::HeadView head_view(const HeadArg& a, size_t elem, int64_t heads, int64_t pie
   v.sh = st[2];
   v.sd = st[3];
   v.rep = int(heads / std::max<int64_t>(a.shape[2], 1));
-  auto whole = [&](int64_t n, int64_t s) { return n <= 1 || (s * int64_t(elem)) % 16 == 0; };
   v.unit = st[3] == 1 && a.shape[3] * int64_t(elem) >= 16;
-  v.vec = st[3] == 1 && a.shape[3] % piece == 0 && (reinterpret_cast<uintptr_t>(a.data) & 15u) == 0 &&
-          whole(a.shape[0], st[0]) && whole(a.shape[1], st[1]) && whole(a.shape[2], st[2]);
   return v;
 }
 
@@ -1357,11 +1353,10 @@ sx_status sx_decay_attention(sx_dtype dtype, const int64_t* q_shape, const int64
   sx::DaMarch& m = p.m[0];
   carve_segments(c, p, m);
   if ((st = check_workspace(op, workspace, workspace_bytes, c.used)) != SX_OK) return st;
-  const int64_t piece = 16 / int64_t(e);
   p.marches = 1;
-  m.x = head_view(qa, e, s.H, piece);
-  m.y = head_view(ka, e, s.H, piece);
-  m.z = head_view(va, e, s.H, piece);
+  m.x = head_view(qa, e, s.H);
+  m.y = head_view(ka, e, s.H);
+  m.z = head_view(va, e, s.H);
   m.dx = p.dk;
   m.dz = p.dv;
   m.scale_out = scale;
@@ -1429,9 +1424,8 @@ sx_status sx_decay_attention_backward(sx_dtype dtype, const int64_t* q_shape, co
   const GradPieces w = carve_gradient(c, s, p);
   if ((st = check_workspace(op, workspace, workspace_bytes, c.used)) != SX_OK) return st;
 
-  const int64_t piece = 16 / int64_t(e);
-  const sx::HeadView qv = head_view(qa, e, s.H, piece), kv = head_view(ka, e, s.H, piece),
-                     vv = head_view(va, e, s.H, piece), ov = head_view(oa, e, s.H, piece);
+  const sx::HeadView qv = head_view(qa, e, s.H), kv = head_view(ka, e, s.H),
+                     vv = head_view(va, e, s.H), ov = head_view(oa, e, s.H);
   p.marches = 3;
   sx::DaMarch &dq = p.m[0], &dk = p.m[1], &dv = p.m[2];
   dq.x = ov; dq.y = vv; dq.z = kv; dq.w = qv;
@@ -1589,9 +1583,9 @@ sx_status sx_decay_attention_step(sx_dtype dtype, const int64_t* q_shape, const 
   p.H = int(s.H);
   p.dk = int(s.dk);
   p.dv = int(s.dv);
-  p.q = head_view(qa, e, s.H, 4);
-  p.k = head_view(ka, e, s.H, 4);
-  p.v = head_view(va, e, s.H, 4);
+  p.q = head_view(qa, e, s.H);
+  p.k = head_view(ka, e, s.H);
+  p.v = head_view(va, e, s.H);
   p.g = log_decay;
   p.gb = s.gb;
   p.gh = s.gh;
@@ -1654,12 +1648,11 @@ sx_status plan_rotate(const char* op, const sx_dtype& dtype, const RotateArgs& a
   p->d = int(d);
   p->rot = int(a.rotated);
   const size_t e = dtype == SX_BF16 ? 2 : 4;
-  const int64_t piece = 16 / int64_t(e);
-  p->q = head_view(a.q, e, qs[2], piece);
-  p->k = head_view(a.k, e, ks[2], piece);
+  p->q = head_view(a.q, e, qs[2]);
+  p->k = head_view(a.k, e, ks[2]);
   if (gradient) {
-    p->gq = head_view(a.gq, e, qs[2], piece);
-    p->gk = head_view(a.gk, e, ks[2], piece);
+    p->gq = head_view(a.gq, e, qs[2]);
+    p->gk = head_view(a.gk, e, ks[2]);
   }
   p->positions = a.positions;
   p->pos64 = a.positions_i64 ? 1 : 0;

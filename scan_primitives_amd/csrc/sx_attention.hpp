@@ -16,8 +16,7 @@ struct HeadView {
   const void* p;
   int64_t sb, st, sh, sd;
   int rep;
-  int unit; // unit sd, and a row holds 16 bytes at least: pieces of it can be read at any alignment
-  int vec;  // rows can be read 16 bytes at a time: unit sd, 16-byte aligned base and strides, D whole pieces
+  int unit;  // unit sd, and a row holds 16 bytes at least: pieces of it can be read at any alignment
 };
 
 // ---------------------------------------------------------------- decay attention

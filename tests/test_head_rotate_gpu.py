@@ -170,6 +170,53 @@ def test_infinities_stay_in_their_row():
         assert torch.equal(got, want)
 
 
+# Rows whose pieces are cut by the turned half, by the row's end or by both, down to a row of one piece, and the
+# widest rows of few turned pairs, which take the most lanes.
+WIDTHS = {
+    "one piece": dict(d=8, rot=8),
+    "one piece f32": dict(d=4, rot=2, type=F32),
+    "one piece and one": dict(d=9, rot=2),
+    "half cut": dict(d=64, rot=36, layout="aligned"),
+    "half and end cut": dict(d=114, rot=46),
+    "half cut, odd end": dict(d=75, rot=74, layout="odd offset"),
+    "end cut, neighbours": dict(d=121, rot=30, near=True),
+    "end cut f32": dict(d=58, rot=22, type=F32, layout="odd offset"),
+    "odd end f32, neighbours": dict(d=101, rot=100, near=True, type=F32),
+    "widest, two turned": dict(d=256, rot=2),
+    "widest, two turned f32": dict(d=256, rot=2, type=F32),
+    "widest, two turned, every other f32": dict(d=256, rot=2, type=F32, layout="every other"),
+    "many tokens, half cut": dict(b=3, t=401, hq=5, hk=1, d=90, rot=12),
+}
+
+
+@pytest.mark.parametrize("name", WIDTHS)
+def test_cut_pieces(name):
+    print(f"\n[case] head norm + rotation, cut pieces: {name}", flush=True)
+    s = make(**WIDTHS[name], seed=50)
+    out, grad = _forward(s), _backward(s)
+    for i, (x, w) in enumerate((("q", "qw"), ("k", "kw"))):
+        args = (_np(s[x]), _positions(s), _np(s["turns"]), _np(s[w]))
+        ref = oa.head_norm_rotate(*args, neighbours=s["near"])
+        size = oa.head_norm_rotate(*args, neighbours=s["near"], size=True)
+        _close(x, out[i], ref, np.abs(size), s[x].dtype == BF)
+        args = args[:3] + (_np(s["g" + x]), args[3])
+        ref = oa.head_norm_rotate_vjp(*args, neighbours=s["near"])
+        size = oa.head_norm_rotate_vjp(*args, neighbours=s["near"], size=True)
+        _close("grad_" + x, grad[i], ref[0], size[0], s[x].dtype == BF)
+        _close("grad_" + w, grad[2 + i], ref[1], size[1], False, rows=s[x].shape[0] * s[x].shape[1] * s[x].shape[2])
+
+
+@pytest.mark.parametrize("type", [BF, F32])
+@pytest.mark.parametrize("near", [False, True])
+def test_an_infinity_behind_the_turned_part_stays_alone(type, near):
+    s = make(type=type, rot=10, near=near)
+    s["q"][1, 3, 2, 20] = float("inf")
+    row = _forward(s)[0][1, 3, 2].clone()
+    assert torch.isnan(row[20])  # infinity times a root of zero
+    row[20] = 0
+    assert not row.any()
+
+
 def test_autograd_gives_the_backward_call():
     s = make(t=30, type=F32)
     leaves = [s[n].clone().requires_grad_() for n in ("q", "k", "qw", "kw")]
