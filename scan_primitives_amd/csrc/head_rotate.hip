@@ -11,7 +11,7 @@
 // turn. A lane holds U units of a row, so a pair never leaves its lane: U
 // consecutive ones (two 16-byte pieces a row, at any alignment) where elements
 // are next to each other, else every G-th one. The gradient of 7 x 2481 tokens
-// of 4 + 2 heads of 194, 12 of them turned, in bf16 takes 53 us in pieces, 112
+// of 4 + 2 heads of 194, 12 of them turned, in bf16 takes 51 us in pieces, 112
 // by elements. A workgroup takes some tokens of the queries or of the keys;
 // their cosines and sines are formed once for all its heads, through LDS, while
 // its first rows are on their way.
@@ -43,6 +43,8 @@ constexpr int kForwardPerCu = 4, kGradPerCu = 1;
 constexpr int kSumRows = 64;     // partial sums of a weight's gradient that are read at once
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t words_t __attribute__((ext_vector_type(2), aligned(2)));  // of a row of any alignment
+typedef uint32_t word_t __attribute__((aligned(2)));
 
 template <bool BF>
 struct El;
@@ -194,13 +196,29 @@ struct Lane {
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        // streamed: what the L2s still held at the kernel's end would have to be written then (63.1 us without)
+        // streamed where rows end on 16-byte borders: what the L2s still held at the kernel's end would have to
+        // be written then (63.1 us without). Others write parts of lines, which the caches join (3 x 2947 tokens
+        // of 8 + 8 heads of 228: 46.3 us, 49.9 streamed), the last components by words (48.4 one by one).
         if (count[j] == U) {
-          __builtin_nontemporal_store(piece_t(T::close(v[j])), reinterpret_cast<piece_t*>(row + at[j]));
+          piece_t* to = reinterpret_cast<piece_t*>(row + at[j]);
+          if constexpr (whole) __builtin_nontemporal_store(piece_t(T::close(v[j])), to);
+          else *to = T::close(v[j]);
         } else if constexpr (!whole) {
-#pragma unroll
-          for (int i = 0; i < U - 1; ++i)
-            if (i < count[j]) row[at[j] + i] = T::put(v[j][i]);
+          constexpr int W = 4 / sizeof(E);  // elements a word
+          u32x4 w = T::close(v[j]);
+          E* to = row + at[j];
+          if (count[j] & 2 * W) {
+            *reinterpret_cast<words_t*>(to) = words_t{w[0], w[1]};
+            to += 2 * W;
+            w[0] = w[2];
+            w[1] = w[3];
+          }
+          if (count[j] & W) {
+            *reinterpret_cast<word_t*>(to) = w[0];
+            to += W;
+            w[0] = w[1];
+          }
+          if (W > 1 && (count[j] & 1)) *to = E(w[0]);
         }
       }
     } else {
