@@ -319,14 +319,15 @@ void decay_attention_split(DaParams& p) {
 hipError_t launch_decay_attention(const DaParams& p, hipStream_t stream) {
   // 16-byte pieces at 32-bit offsets within a chunk
   const int64_t e = p.bf16 ? 2 : 4, chunk = decay_attention_chunk(p.bf16 != 0), most = int64_t(1) << 31;
-  bool vec = true;
+  bool vec = true, whole = true;  // whole: rows that are whole pieces cost the least
   for (int i = 0; i < p.marches; ++i) {
     for (const HeadView* v : {&p.m[i].x, &p.m[i].y, &p.m[i].z, &p.m[i].w})
       vec = vec && (!v->p || (v->unit && v->st >= 0 && v->st < most / (chunk * e)));
+    whole = whole && p.m[i].dx * e % 16 == 0 && p.m[i].dz * e % 16 == 0;
     vec = vec && int64_t(p.H) * p.m[i].dz < most / (chunk * 4);
   }
-  const auto launch = p.bf16 ? (vec ? launch_marches_bf16 : launch_marches_bf16_any)
-                             : (vec ? launch_marches_f32 : launch_marches_f32_any);
+  const auto launch = p.bf16 ? (!vec ? launch_marches_bf16_any : whole ? launch_marches_bf16 : launch_marches_bf16_cut)
+                             : (!vec ? launch_marches_f32_any : whole ? launch_marches_f32 : launch_marches_f32_cut);
   hipError_t err = hipSuccess;
   if (p.segments > 1) {
     const int states = p.marches == 1 ? 1 : 2;

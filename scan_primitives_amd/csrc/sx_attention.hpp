@@ -72,8 +72,10 @@ int decay_attention_column_blocks(int dz);
 int march_tiles(int dx);
 int march_waves(int dz);
 hipError_t launch_marches_bf16(const DaParams& p, int first, int count, bool local, hipStream_t stream);
+hipError_t launch_marches_bf16_cut(const DaParams& p, int first, int count, bool local, hipStream_t stream);
 hipError_t launch_marches_bf16_any(const DaParams& p, int first, int count, bool local, hipStream_t stream);
 hipError_t launch_marches_f32(const DaParams& p, int first, int count, bool local, hipStream_t stream);
+hipError_t launch_marches_f32_cut(const DaParams& p, int first, int count, bool local, hipStream_t stream);
 hipError_t launch_marches_f32_any(const DaParams& p, int first, int count, bool local, hipStream_t stream);
 // How the tokens are split: sets segments and seg_tokens.
 void decay_attention_split(DaParams& p);
