@@ -200,6 +200,39 @@ def test_backward(name):
     check_backward(make(**SHAPES[name]), grad_state=SHAPES[name].get("initial", False))
 
 
+# Rows whose last 16-byte piece holds fewer elements: one piece, one and an element, several column blocks, segments,
+# shared heads (f32 results before their sum), rows off any 16-byte border.
+CUT = {
+    "one piece": dict(dk=8, dv=8, layout="odd offset"),
+    "one piece and one": dict(dk=9, dv=9, initial=True),
+    "one piece and one f32": dict(dk=5, dv=5, type=F32, initial=True),
+    "keys cut": dict(dk=70, dv=64, t=140),
+    "values cut": dict(dk=64, dv=70, t=140),
+    "two column blocks": dict(dk=31, dv=133, t=80, layout="odd offset"),
+    "segments": dict(b=1, t=700, h=2, dk=59, dv=101, initial=True),
+    "ragged segments f32": dict(b=2, t=500, h=2, lengths=[500, 77], dk=43, dv=61, type=F32, layout="odd offset"),
+    "shared heads": dict(h=6, hq=2, hk=3, hv=1, dk=27, dv=42, t=130, initial=True),
+    "shared heads f32": dict(h=6, hq=1, hk=6, hv=2, dk=26, dv=41, type=F32),
+}
+
+
+@pytest.mark.parametrize("name", CUT)
+def test_cut_rows(name):
+    print(f"\n[case] decay attention, cut rows: {name}", flush=True)
+    s = make(**CUT[name], seed=50)
+    check_forward(s)
+    check_backward(s, grad_state=CUT[name].get("initial", False))
+
+
+def test_an_infinity_in_a_cut_row():
+    s = make(b=1, t=150, h=2, dk=35, dv=37)
+    clean = _forward(s)[0]
+    s["v"][0, 77, 0, 36] = float("inf")
+    out = _forward(s)[0]
+    assert torch.equal(out[..., :36], clean[..., :36]) and torch.equal(out[:, :, 1], clean[:, :, 1])
+    assert torch.equal(out[:, :77], clean[:, :77]) and not torch.isfinite(out[0, 77:, 0, 36]).any()
+
+
 @pytest.mark.parametrize("type", [BF, F32])
 def test_no_tokens(type):
     s = make(t=0, type=type, initial=True)
