@@ -138,7 +138,7 @@ bool decay_args(Call& c, PyObject* const* a, int64_t rank, DecayArgs* d) {
 PyObject* decay_attention(PyObject* const* a, Py_ssize_t n) {
   Call c;
   DecayArgs d;
-  if (n != 8 || !decay_args(c, a, 4, &d)) return the_long_way();
+  if (n != 8 || (a[7] != Py_True && a[7] != Py_False) || !decay_args(c, a, 4, &d)) return the_long_way();
   const int64_t b = d.q->size(0), t = d.q->size(1), dk = d.q->size(3), dv = d.v->size(3);
   const void* initial = c.optional(a[4], at::kFloat, {b, d.heads, dk, dv});
   const void* lengths = c.optional(a[5], at::kInt, {b});
