@@ -833,13 +833,18 @@ def decay_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_
     ``[H]`` or ``[B, H]``. ``state`` (f32 ``[pool, H, dk, dv]``) is updated in
     place; row b uses state ``slots[b]`` (int32 ``[B]``; state b when None). A row
     whose slot lies outside the pool is idle: zero out, no state changed; two
-    rows of one slot race. Returns out ``[B, H, dv]``. No gradient is recorded.
+    rows of one slot race. Returns out ``[B, H, dv]``. No gradient is recorded,
+    so a ``state`` that autograd records is refused; one that it has saved is
+    marked as modified in place.
     """
     got = (_marshal or _load_marshal()).decay_attention_step(q, k, v, log_decay, state, slots, scale)
     if got is not None:
         return _done(got)[0]
     op = "decay-attention step"
     code, heads, index = _decay_operands(op, q, k, v, log_decay, 1, (("state", state),), (("slots", slots),))
+    if _records(state):
+        raise SxError(SX_E_UNSUPPORTED, f"{op}: state requires grad, and a step records none; detach it, or call the "
+                                        "step under torch.no_grad()")
     b, _, dk = q.shape
     dv = v.shape[-1]
     if state.dim() != 4 or state.shape[1:] != (heads, dk, dv):
@@ -851,6 +856,7 @@ def decay_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_
     _enqueue(index, load_library().sx_decay_attention_step, code, *_args(q), *_args(k), *_args(v), log_decay.dim(),
              *_args(log_decay), state.shape[0], _i64(state.stride()), state.data_ptr(), _ptr(slots), float(scale),
              out.data_ptr())
+    torch.autograd.graph.increment_version(state)
     return out
 
 

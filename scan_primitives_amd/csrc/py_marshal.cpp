@@ -198,14 +198,15 @@ PyObject* decay_attention_step(PyObject* const* a, Py_ssize_t n) {
   const double scale = c.number(a[6]);
   if (!c.here() || state->size(1) != d.heads || state->size(2) != dk || state->size(3) != dv) return the_long_way();
   const at::Tensor out = at::empty({b, d.heads, dv}, d.q->options());
-  return answer(lib.decay_attention_step(
-                    d.code, d.q->sizes().data(), d.q->strides().data(), d.q->data_ptr(), d.k->sizes().data(),
-                    d.k->strides().data(), d.k->data_ptr(), d.v->sizes().data(), d.v->strides().data(),
-                    d.v->data_ptr(), int(d.g->dim()), d.g->sizes().data(), d.g->strides().data(),
-                    static_cast<const float*>(d.g->data_ptr()), state->size(0), state->strides().data(),
-                    static_cast<float*>(state->data_ptr()), static_cast<const int32_t*>(slots), float(scale),
-                    out.data_ptr(), c.stream()),
-                out);
+  const sx_status st = lib.decay_attention_step(
+      d.code, d.q->sizes().data(), d.q->strides().data(), d.q->data_ptr(), d.k->sizes().data(), d.k->strides().data(),
+      d.k->data_ptr(), d.v->sizes().data(), d.v->strides().data(), d.v->data_ptr(), int(d.g->dim()),
+      d.g->sizes().data(), d.g->strides().data(), static_cast<const float*>(d.g->data_ptr()), state->size(0),
+      state->strides().data(), static_cast<float*>(state->data_ptr()), static_cast<const int32_t*>(slots),
+      float(scale), out.data_ptr(), c.stream());
+  // autograd tells by the version that a state it saved has been written to (a state of inference mode has none)
+  if (st == SX_OK && !state->is_inference()) state->unsafeGetTensorImpl()->bump_version();
+  return answer(st, out);
 }
 
 struct RotateArgs {

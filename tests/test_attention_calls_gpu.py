@@ -1,13 +1,16 @@
-"""How decay attention and head norm + rotation are called: optional values of any truth."""
+"""How decay attention and head norm + rotation are called: optional values of any truth, states that are
+written in place."""
 
 import numpy as np
 import pytest
 import torch
 
 import scan_primitives_amd as sx
-from tests.test_decay_attention_gpu import make
+from scan_primitives_amd import _binding as B
+from tests.test_decay_attention_gpu import make, make_step
 
 pytestmark = pytest.mark.gpu
+F32 = torch.float32
 
 
 @pytest.mark.parametrize("true,false", [(1, 0), (np.bool_(True), np.bool_(False)), ("yes", "")])
@@ -18,3 +21,42 @@ def test_whether_the_state_is_wanted_goes_by_truth(true, false):
     got = sx.decay_attention(s["q"], s["k"], s["v"], s["g"], return_state=true, **args)
     assert torch.equal(got[0], out) and torch.equal(got[1], state)
     assert torch.equal(sx.decay_attention(s["q"], s["k"], s["v"], s["g"], return_state=false, **args), out)
+
+
+def _step(s, scale=1.0):
+    return sx.decay_attention_step(s["q"], s["k"], s["v"], s["g"], s["state"], slots=s["slots"], scale=scale)
+
+
+@pytest.mark.parametrize("scale", [1.0, 1])  # the binding's short way and its long one
+def test_a_step_on_a_saved_state_is_noticed(scale):
+    p, s = make(t=20, type=F32, initial=True), make_step(b=2, pool=2, type=F32)
+    q = p["q"].clone().requires_grad_()
+    s["state"], s["slots"] = p["initial"], None
+    before = s["state"]._version
+    loss = sx.decay_attention(q, p["k"], p["v"], p["g"], initial=s["state"]).sum()
+    _step(s, scale)
+    assert s["state"]._version > before
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+@pytest.mark.parametrize("scale", [1.0, 1])
+def test_a_step_does_not_overwrite_a_state_that_autograd_records(scale):
+    s = make_step(type=F32)
+    kept = s["state"].clone()
+    s["state"] = s["state"].requires_grad_()
+    with pytest.raises(sx.SxError) as e:
+        _step(s, scale)
+    assert e.value.code == B.SX_E_UNSUPPORTED and torch.equal(s["state"], kept)
+    with torch.no_grad():  # as torch's own operations in place
+        _step(s, scale)
+    assert not torch.equal(s["state"], kept)
+
+
+@pytest.mark.parametrize("scale", [1.0, 1])
+def test_a_step_on_a_state_made_in_inference_mode(scale):
+    s, e = make_step(), make_step()
+    with torch.inference_mode():
+        s["state"] = s["state"].clone()
+    got, want = _step(s, scale), _step(e, scale)
+    assert torch.equal(got, want) and torch.equal(s["state"], e["state"])
