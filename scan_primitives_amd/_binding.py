@@ -14,6 +14,7 @@ import math
 import os
 
 import torch
+import torch.autograd.forward_ad as forward_ad
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # SX_SCAN_LIB selects another build of the same library (the host-sanitized one the
@@ -212,6 +213,15 @@ def set_lookback_spin_limit(limit: int) -> None:
     load_library().sx_set_lookback_spin_limit(int(limit))
 
 
+def _require_no_tangent(*tensors) -> None:
+    """Forward-mode derivatives are not carried: a tensor with a tangent is refused, not taken without it."""
+    if forward_ad._current_level < 0:  # outside of every dual_level() no tensor has one
+        return
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+            raise SxError(SX_E_UNSUPPORTED, "forward-mode differentiation (a tensor with a tangent) is not supported")
+
+
 def _require_device_tensor(name: str, t) -> None:
     if not isinstance(t, torch.Tensor):
         raise SxError(SX_E_DIM_003, f"{name}: a tensor was expected, got {type(t).__name__}")
@@ -230,6 +240,7 @@ def element_scan(body: str, initial: torch.Tensor, sequences, axis: int = 0, sta
     ``element_scan_backward``.
     """
     seqs = list(sequences)
+    _require_no_tangent(initial, *seqs)
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in [initial] + seqs):
         if len(seqs) != 2:
             raise SxError(SX_E_DIM_001, f"element-scan: the {body} body takes two sequences, got {len(seqs)}")
@@ -304,6 +315,7 @@ def element_scan_backward(body: str, initial: torch.Tensor, sequences, h: torch.
     if len(seqs) != 2:
         raise SxError(SX_E_DIM_001, f"element-scan gradient: the {body} body takes two sequences, got {len(seqs)}")
     x, s = seqs
+    _require_no_tangent(initial, x, s, h, g)
     for name, t in (("initial", initial), ("x", x), ("sequence 2", s), ("h", h), ("g", g)):
         _require_device_tensor(name, t)
         if t.dtype != torch.float32:
@@ -361,6 +373,7 @@ def matrix_scan(a: torch.Tensor, b: torch.Tensor, axis: int = 0, reverse: bool =
     otherwise. Computation is f32. When autograd records (an input requires
     grad), the gradient runs through ``matrix_scan_backward``.
     """
+    _require_no_tangent(a, b)
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (a, b)):
         return _MatrixScanFunction.apply(a, b, axis, reverse, out_dtype, projective)
     return _matrix_scan_forward(a, b, axis, reverse, out_dtype, projective)
@@ -414,6 +427,7 @@ def linear_scan(a, b, axis: int = 0, reverse: bool = False, out_dtype=None) -> t
     result has the broadcast shape and that dtype unless ``out_dtype`` says
     otherwise. Computation is f32.
     """
+    _require_no_tangent(a, b)
     ta = a if isinstance(a, torch.Tensor) else None
     tb = b if isinstance(b, torch.Tensor) else None
     if ta is None and tb is None:
@@ -493,6 +507,7 @@ def matrix_scan_backward(a: torch.Tensor, b_shape, h: torch.Tensor, g: torch.Ten
     ``grad_b`` have the shapes of ``a`` and ``b`` (summed over broadcast dims)
     and ``grad_dtype`` (default: a's dtype). The adjoint is computed in f32.
     """
+    _require_no_tangent(a, h, g)
     for name, t in (("a", a), ("h", h), ("g", g)):
         _require_device_tensor(name, t)
     if not (a.dtype == h.dtype == g.dtype) or a.dtype not in _DTYPES:
@@ -738,6 +753,7 @@ def decay_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay
     got = (_marshal or _load_marshal()).decay_attention(q, k, v, log_decay, initial, lengths, scale, return_state)
     if got is not None:
         return _done(got) if return_state else _done(got)[0]
+    _require_no_tangent(q, k, v, log_decay, initial)
     if _records(q, k, v, log_decay, initial):
         out, state = _DecayAttentionFunction.apply(q, k, v, log_decay, initial, lengths, scale, return_state)
     else:
@@ -778,6 +794,7 @@ def decay_attention_backward(q, k, v, log_decay, grad_out, initial=None, lengths
                                                                  grad_state)
     if got is not None:
         return _done(got)
+    _require_no_tangent(q, k, v, log_decay, grad_out, initial, grad_state)
     op = "decay-attention gradient"
     code, heads, index = _decay_operands(op, q, k, v, log_decay, 2, (("grad_out", grad_out),),
                                          (("initial", initial), ("lengths", lengths), ("grad_state", grad_state)))
@@ -840,6 +857,7 @@ def decay_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_
     got = (_marshal or _load_marshal()).decay_attention_step(q, k, v, log_decay, state, slots, scale)
     if got is not None:
         return _done(got)[0]
+    _require_no_tangent(q, k, v, log_decay, state)
     op = "decay-attention step"
     code, heads, index = _decay_operands(op, q, k, v, log_decay, 1, (("state", state),), (("slots", slots),))
     if _records(state):
@@ -911,6 +929,7 @@ def head_norm_rotate(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, 
     got = (_marshal or _load_marshal()).head_norm_rotate(q, k, positions, turns, q_weight, k_weight, eps, neighbours)
     if got is not None:
         return _done(got)
+    _require_no_tangent(q, k, q_weight, k_weight)
     if _records(q, k, q_weight, k_weight):
         return _HeadNormRotateFunction.apply(q, k, positions, turns, q_weight, k_weight, eps, neighbours)
     return _head_norm_rotate_forward(q, k, positions, turns, q_weight, k_weight, eps, neighbours)
@@ -937,6 +956,7 @@ def head_norm_rotate_backward(q, k, positions, turns, grad_out_q, grad_out_k, q_
                                                                   q_weight, k_weight, eps, neighbours)
     if got is not None:
         return _done(got)
+    _require_no_tangent(q, k, grad_out_q, grad_out_k, q_weight, k_weight)
     op = "head-norm-rotate gradient"
     code, index, positions, turns, q_weight, k_weight = _rotate_operands(
         op, q, k, positions, turns, q_weight, k_weight, (("grad_out_q", grad_out_q), ("grad_out_k", grad_out_k)))

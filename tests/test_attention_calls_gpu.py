@@ -1,13 +1,15 @@
 """How decay attention and head norm + rotation are called: optional values of any truth, states that are
-written in place."""
+written in place, tensors that carry more than their numbers."""
 
 import numpy as np
 import pytest
 import torch
+import torch.autograd.forward_ad as forward_ad
 
 import scan_primitives_amd as sx
 from scan_primitives_amd import _binding as B
-from tests.test_decay_attention_gpu import make, make_step
+from tests import test_head_rotate_gpu as rotate
+from tests.test_decay_attention_gpu import _forward, make, make_step
 
 pytestmark = pytest.mark.gpu
 F32 = torch.float32
@@ -60,3 +62,34 @@ def test_a_step_on_a_state_made_in_inference_mode(scale):
         s["state"] = s["state"].clone()
     got, want = _step(s, scale), _step(e, scale)
     assert torch.equal(got, want) and torch.equal(s["state"], e["state"])
+
+
+def _scan_calls(x):
+    """Every scan and its gradient on tensors made from x [4, 16]."""
+    init = torch.zeros(16, device="cuda")
+    a = x.reshape(4, 4, 4)
+    return [lambda: sx.element_scan("tanh_affine", init, [x, torch.ones_like(init).expand(4, 16)]),
+            lambda: sx.element_scan_backward("tanh_affine", init, [x, x], torch.zeros_like(init).expand(4, 16), x),
+            lambda: sx.matrix_scan(a, a), lambda: sx.linear_scan(0.5, x), lambda: sx.cumsum(x),
+            lambda: sx.matrix_scan_backward(a, a.shape, a, a)]
+
+
+def test_tangents_are_refused():
+    s, r, one = make(t=20, type=F32), rotate.make(type=F32), make_step(type=F32)
+    with forward_ad.dual_level():
+        dual = lambda x: forward_ad.make_dual(x, torch.ones_like(x))  # noqa: E731
+        calls = [lambda: sx.decay_attention(dual(s["q"]), s["k"], s["v"], s["g"]),
+                 lambda: sx.decay_attention(s["q"], s["k"], s["v"], dual(s["g"]), scale=1),
+                 lambda: sx.decay_attention(s["q"], s["k"], s["v"], s["g"], initial=dual(s["gs"])),
+                 lambda: sx.decay_attention_backward(s["q"], s["k"], s["v"], s["g"], dual(s["go"])),
+                 lambda: sx.decay_attention_step(one["q"], dual(one["k"]), one["v"], one["g"], one["state"]),
+                 lambda: sx.decay_attention_step(one["q"], one["k"], one["v"], one["g"], dual(one["state"])),
+                 lambda: sx.head_norm_rotate(r["q"], dual(r["k"]), r["positions"], r["turns"]),
+                 lambda: sx.head_norm_rotate(r["q"], r["k"], r["positions"], r["turns"], k_weight=dual(r["kw"])),
+                 lambda: sx.head_norm_rotate_backward(r["q"], r["k"], r["positions"], r["turns"], dual(r["gq"]), r["gk"])]
+        for i, call in enumerate(calls + _scan_calls(dual(torch.rand(4, 16, device="cuda")))):
+            with pytest.raises(sx.SxError) as e:
+                call()
+            assert e.value.code == B.SX_E_UNSUPPORTED, i
+        # tensors without a tangent are as ever
+        assert torch.equal(sx.decay_attention(s["q"], s["k"], s["v"], s["g"], scale=s["scale"]), _forward(s)[0])
