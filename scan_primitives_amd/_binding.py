@@ -222,6 +222,11 @@ def _require_no_tangent(*tensors) -> None:
             raise SxError(SX_E_UNSUPPORTED, "forward-mode differentiation (a tensor with a tangent) is not supported")
 
 
+def _signed(*tensors):
+    """The tensors with lazily negated views (the imaginary part of a conjugate) as tensors of the values they have."""
+    return [t.resolve_neg() if isinstance(t, torch.Tensor) and t.is_neg() else t for t in tensors]
+
+
 def _require_device_tensor(name: str, t) -> None:
     if not isinstance(t, torch.Tensor):
         raise SxError(SX_E_DIM_003, f"{name}: a tensor was expected, got {type(t).__name__}")
@@ -241,6 +246,7 @@ def element_scan(body: str, initial: torch.Tensor, sequences, axis: int = 0, sta
     """
     seqs = list(sequences)
     _require_no_tangent(initial, *seqs)
+    initial, *seqs = _signed(initial, *seqs)
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in [initial] + seqs):
         if len(seqs) != 2:
             raise SxError(SX_E_DIM_001, f"element-scan: the {body} body takes two sequences, got {len(seqs)}")
@@ -316,6 +322,7 @@ def element_scan_backward(body: str, initial: torch.Tensor, sequences, h: torch.
         raise SxError(SX_E_DIM_001, f"element-scan gradient: the {body} body takes two sequences, got {len(seqs)}")
     x, s = seqs
     _require_no_tangent(initial, x, s, h, g)
+    initial, x, s, h, g = _signed(initial, x, s, h, g)
     for name, t in (("initial", initial), ("x", x), ("sequence 2", s), ("h", h), ("g", g)):
         _require_device_tensor(name, t)
         if t.dtype != torch.float32:
@@ -374,6 +381,7 @@ def matrix_scan(a: torch.Tensor, b: torch.Tensor, axis: int = 0, reverse: bool =
     grad), the gradient runs through ``matrix_scan_backward``.
     """
     _require_no_tangent(a, b)
+    a, b = _signed(a, b)
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (a, b)):
         return _MatrixScanFunction.apply(a, b, axis, reverse, out_dtype, projective)
     return _matrix_scan_forward(a, b, axis, reverse, out_dtype, projective)
@@ -428,6 +436,7 @@ def linear_scan(a, b, axis: int = 0, reverse: bool = False, out_dtype=None) -> t
     otherwise. Computation is f32.
     """
     _require_no_tangent(a, b)
+    a, b = _signed(a, b)
     ta = a if isinstance(a, torch.Tensor) else None
     tb = b if isinstance(b, torch.Tensor) else None
     if ta is None and tb is None:
@@ -508,6 +517,7 @@ def matrix_scan_backward(a: torch.Tensor, b_shape, h: torch.Tensor, g: torch.Ten
     and ``grad_dtype`` (default: a's dtype). The adjoint is computed in f32.
     """
     _require_no_tangent(a, h, g)
+    a, h, g = _signed(a, h, g)
     for name, t in (("a", a), ("h", h), ("g", g)):
         _require_device_tensor(name, t)
     if not (a.dtype == h.dtype == g.dtype) or a.dtype not in _DTYPES:
@@ -754,6 +764,7 @@ def decay_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay
     if got is not None:
         return _done(got) if return_state else _done(got)[0]
     _require_no_tangent(q, k, v, log_decay, initial)
+    q, k, v, log_decay, initial = _signed(q, k, v, log_decay, initial)
     if _records(q, k, v, log_decay, initial):
         out, state = _DecayAttentionFunction.apply(q, k, v, log_decay, initial, lengths, scale, return_state)
     else:
@@ -795,6 +806,7 @@ def decay_attention_backward(q, k, v, log_decay, grad_out, initial=None, lengths
     if got is not None:
         return _done(got)
     _require_no_tangent(q, k, v, log_decay, grad_out, initial, grad_state)
+    q, k, v, log_decay, grad_out, initial, grad_state = _signed(q, k, v, log_decay, grad_out, initial, grad_state)
     op = "decay-attention gradient"
     code, heads, index = _decay_operands(op, q, k, v, log_decay, 2, (("grad_out", grad_out),),
                                          (("initial", initial), ("lengths", lengths), ("grad_state", grad_state)))
@@ -858,8 +870,11 @@ def decay_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_
     if got is not None:
         return _done(got)[0]
     _require_no_tangent(q, k, v, log_decay, state)
+    q, k, v, log_decay = _signed(q, k, v, log_decay)
     op = "decay-attention step"
     code, heads, index = _decay_operands(op, q, k, v, log_decay, 1, (("state", state),), (("slots", slots),))
+    if state.is_neg():
+        raise SxError(SX_E_UNSUPPORTED, f"{op}: state is a lazily negated view, which cannot be written in place")
     if _records(state):
         raise SxError(SX_E_UNSUPPORTED, f"{op}: state requires grad, and a step records none; detach it, or call the "
                                         "step under torch.no_grad()")
@@ -930,6 +945,7 @@ def head_norm_rotate(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, 
     if got is not None:
         return _done(got)
     _require_no_tangent(q, k, q_weight, k_weight)
+    q, k, turns, q_weight, k_weight = _signed(q, k, turns, q_weight, k_weight)
     if _records(q, k, q_weight, k_weight):
         return _HeadNormRotateFunction.apply(q, k, positions, turns, q_weight, k_weight, eps, neighbours)
     return _head_norm_rotate_forward(q, k, positions, turns, q_weight, k_weight, eps, neighbours)
@@ -957,6 +973,8 @@ def head_norm_rotate_backward(q, k, positions, turns, grad_out_q, grad_out_k, q_
     if got is not None:
         return _done(got)
     _require_no_tangent(q, k, grad_out_q, grad_out_k, q_weight, k_weight)
+    q, k, turns, grad_out_q, grad_out_k, q_weight, k_weight = _signed(q, k, turns, grad_out_q, grad_out_k, q_weight,
+                                                                      k_weight)
     op = "head-norm-rotate gradient"
     code, index, positions, turns, q_weight, k_weight = _rotate_operands(
         op, q, k, positions, turns, q_weight, k_weight, (("grad_out_q", grad_out_q), ("grad_out_k", grad_out_k)))

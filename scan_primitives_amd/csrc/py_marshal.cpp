@@ -3,7 +3,7 @@
 //
 // Each function takes what the binding's function of the same name takes, in
 // order. Where every tensor is a plain one on the current device, of the expected
-// type and shape and without a tangent, and autograd does not record, it allocates
+// type and shape, without a tangent or a lazy sign, and autograd does not record, it allocates
 // the results, calls the C entry on the current stream and returns them (or the
 // entry's status where that is not zero). Anything else returns None: the binding then goes the long
 // way, which converts, records, switches devices and names what is wrong. The two
@@ -41,7 +41,7 @@ struct Call {
   const at::Tensor* take(PyObject* o) {
     if (!fit || !THPVariable_CheckExact(o)) return fit = false, nullptr;
     const at::Tensor& t = THPVariable_Unpack(o);
-    if (!t.is_cuda() || (records && t.requires_grad()) || t._fw_grad(0).defined() ||
+    if (!t.is_cuda() || (records && t.requires_grad()) || t._fw_grad(0).defined() || t.is_neg() ||
         (index >= 0 && t.get_device() != index))
       return fit = false, nullptr;
     index = int(t.get_device());

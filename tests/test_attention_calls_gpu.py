@@ -9,7 +9,7 @@ import torch.autograd.forward_ad as forward_ad
 import scan_primitives_amd as sx
 from scan_primitives_amd import _binding as B
 from tests import test_head_rotate_gpu as rotate
-from tests.test_decay_attention_gpu import _forward, make, make_step
+from tests.test_decay_attention_gpu import _backward, _forward, make, make_step
 
 pytestmark = pytest.mark.gpu
 F32 = torch.float32
@@ -93,3 +93,46 @@ def test_tangents_are_refused():
             assert e.value.code == B.SX_E_UNSUPPORTED, i
         # tensors without a tangent are as ever
         assert torch.equal(sx.decay_attention(s["q"], s["k"], s["v"], s["g"], scale=s["scale"]), _forward(s)[0])
+
+
+def _negated(x):
+    """A lazily negated view with the values of x."""
+    view = torch.complex(torch.zeros_like(x), -x).conj().imag
+    assert view.is_neg() and torch.equal(view, x)
+    return view
+
+
+def test_lazily_negated_views_are_read_with_their_sign():
+    s, r, one = make(t=40, type=F32, initial=True), rotate.make(type=F32), make_step(type=F32)
+    want = (*_forward(s), *_backward(s))
+    for n in ("q", "k", "v", "g", "initial", "go", "gs"):
+        kept, s[n] = s[n], _negated(s[n])
+        for a, b in zip((*_forward(s), *_backward(s)), want):
+            torch.testing.assert_close(a, b, rtol=1e-4, atol=1e-4, msg=n)  # other strides, another order of the sums
+        s[n] = kept
+    want = (*rotate._forward(r), *rotate._backward(r))
+    for n in ("q", "k", "turns", "qw", "kw", "gq", "gk"):
+        kept, r[n] = r[n], _negated(r[n])
+        for a, b in zip((*rotate._forward(r), *rotate._backward(r)), want):
+            torch.testing.assert_close(a, b, rtol=1e-4, atol=1e-4, msg=n)
+        r[n] = kept
+    x = torch.rand(4, 16, device="cuda")
+    for i, (a, b) in enumerate(zip(_scan_calls(_negated(x)), _scan_calls(x))):
+        torch.testing.assert_close(a(), b(), msg=str(i))
+    state, one["k"] = one["state"].clone(), _negated(one["k"])
+    got = sx.decay_attention_step(one["q"], one["k"], one["v"], one["g"], one["state"], slots=one["slots"])
+    want = sx.decay_attention_step(one["q"], one["k"].clone(), one["v"], one["g"], state, slots=one["slots"])
+    assert torch.equal(got, want) and torch.equal(one["state"], state)
+    with pytest.raises(sx.SxError) as e:  # a state is written: its numbers have to be what is in memory
+        sx.decay_attention_step(one["q"], one["k"], one["v"], one["g"], _negated(state))
+    assert e.value.code == B.SX_E_UNSUPPORTED
+
+
+@pytest.mark.parametrize("name,at", [("q", 0), ("k", 1), ("v", 2)])
+def test_autograd_of_a_lazily_negated_view(name, at):
+    s = make(t=40, type=F32)
+    x = torch.complex(torch.zeros_like(s[name]), -s[name]).requires_grad_()
+    out = sx.decay_attention(*(x.conj().imag if n == name else s[n] for n in ("q", "k", "v", "g")), scale=s["scale"])
+    torch.testing.assert_close(out, _forward(s)[0], rtol=1e-4, atol=1e-4)
+    out.backward(s["go"])
+    torch.testing.assert_close(-x.grad.imag, _backward(s, grad_state=False)[at], rtol=1e-4, atol=1e-4)
