@@ -507,7 +507,8 @@ size_t sx_decay_attention_backward_workspace_bytes(sx_dtype dtype, const int64_t
  *  pool, state_strides, state
  *                f32 states [pool, H, dk, dv]; each head's dk-by-dv block
  *                row-major contiguous (else SX_E_UNSUPPORTED), no two blocks
- *                overlapping.
+ *                overlapping; any strides and start otherwise (on 16-byte borders
+ *                throughout they are read and written in larger pieces).
  *  slots         int32 [B]: the state of each row, or NULL (row b uses state b;
  *                pool >= B then). A row whose slot lies outside [0, pool) is
  *                idle: its row of out is zero and no state changes. Two rows with

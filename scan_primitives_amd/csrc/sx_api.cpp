@@ -1140,6 +1140,7 @@ int64_t numel4(const int64_t* s) { return s[0] * s[1] * s[2] * s[3]; }
 struct Span {
   const char* name;
   uintptr_t lo, hi;
+  unsigned align = 16;  // of an output: bytes
 };
 
 Span head_span(const HeadArg& a, size_t elem) {
@@ -1165,8 +1166,8 @@ sx_status no_overlap(const char* op, const Span* in, int nin, const Span* out, i
     for (int j = i + 1; j < nout; ++j)
       if (overlaps(out[i].lo, out[i].hi, out[j].lo, out[j].hi))
         return fail(SX_E_ALIAS, "%s: %s overlaps %s", op, out[i].name, out[j].name);
-    if ((out[i].lo & 15u) != 0)
-      return fail(SX_E_UNSUPPORTED, "%s: %s must be 16-byte aligned", op, out[i].name);
+    if (out[i].lo % out[i].align != 0)
+      return fail(SX_E_UNSUPPORTED, "%s: %s must be %u-byte aligned", op, out[i].name, out[i].align);
   }
   return ok();
 }
@@ -1575,7 +1576,8 @@ sx_status sx_decay_attention_step(sx_dtype dtype, const int64_t* q_shape, const 
   const size_t e = dtype == SX_BF16 ? 2 : 4;
   const Span in[] = {head_span(qa, e), head_span(ka, e), head_span(va, e), decay_span(s, log_decay),
                      flat_span("slots", slots, s.B * 4)};
-  Span to[] = {flat_span("out", out, s.B * s.H * s.dv * int64_t(e)), {"state", 0, 0}};
+  // the state may be a view of a wider pool: any element of it
+  Span to[] = {flat_span("out", out, s.B * s.H * s.dv * int64_t(e)), {"state", 0, 0, sizeof(float)}};
   if (state && numel > 0) span_bytes(state, 4, pool_shape, ps, sizeof(float), &to[1].lo, &to[1].hi);
   if ((st = no_overlap(op, in, 5, to, 2)) != SX_OK) return st;
   sx::DaStep p{};

@@ -222,3 +222,15 @@ def test_rotation_turns():
     assert sx.rotation_turns(0).numel() == 0
     with pytest.raises(sx.SxError):
         sx.rotation_turns(3)
+
+
+def test_decay_attention_step_state_alignment(lib):
+    assert _step(lib, state=_at(4) + 2) == B.SX_E_UNSUPPORTED  # inside an f32
+    assert b"4-byte aligned" in lib.sx_last_error()
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are no memory: the call must not reach a GPU")
+@pytest.mark.parametrize("at", [4, 8, 12])
+def test_decay_attention_step_takes_a_state_off_16_byte_borders(lib, at):
+    # what is left to refuse it is that there is no device
+    assert _step(lib, state=_at(4) + at) == _step(lib) == B.SX_E_DEVICE, lib.sx_last_error()

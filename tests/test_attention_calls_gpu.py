@@ -1,5 +1,5 @@
 """How decay attention and head norm + rotation are called: optional values of any truth, states that are
-written in place, tensors that carry more than their numbers."""
+written in place, tensors that carry more than their numbers, states at any alignment."""
 
 import numpy as np
 import pytest
@@ -136,3 +136,21 @@ def test_autograd_of_a_lazily_negated_view(name, at):
     torch.testing.assert_close(out, _forward(s)[0], rtol=1e-4, atol=1e-4)
     out.backward(s["go"])
     torch.testing.assert_close(-x.grad.imag, _backward(s, grad_state=False)[at], rtol=1e-4, atol=1e-4)
+
+
+@pytest.mark.parametrize("name,room,view,dk,dv", [
+    ("slots from the second on", (5, 1, 33, 33), lambda x: x[1:], 33, 33),
+    ("heads from the second on", (4, 3, 33, 47), lambda x: x[:, 1:], 33, 47),
+    ("states a word past a 16-byte border", (4, 2, 32 * 32 + 4), lambda x: x[..., 1:-3].unflatten(-1, (32, 32)), 32, 32),
+])
+def test_a_step_on_a_view_of_a_pool(name, room, view, dk, dv):
+    room = torch.randn(room, device="cuda")
+    state = view(room)
+    s = make_step(b=3, pool=4, h=state.shape[1], dk=dk, dv=dv, slots=None)
+    kept, alone = room.clone(), state.clone(memory_format=torch.contiguous_format)
+    assert state.data_ptr() % 16 != 0 and alone.data_ptr() % 16 == 0
+    got = sx.decay_attention_step(s["q"], s["k"], s["v"], s["g"], state, scale=s["scale"])
+    assert torch.equal(got, sx.decay_attention_step(s["q"], s["k"], s["v"], s["g"], alone, scale=s["scale"]))
+    assert torch.equal(state, alone)
+    view(kept).copy_(state)
+    assert torch.equal(room, kept)  # nothing else of the buffer has changed
