@@ -110,9 +110,8 @@ __global__ __launch_bounds__(kThreads) void decay_grad(DaDecayGrad p) {
       s += double(p.initial[bh * state + i]) * double(p.grad_initial[bh * state + i]);
     z = block_sum(s, la);
   }
-  double all = 0.0;
-  for (int i0 = first; i0 < last; i0 += kThreads) {
-    const int n = min(kThreads, last - i0);
+  // the sums of n chunks from i0 on
+  auto load = [&](int i0, int n) {
     __syncthreads();
     if (tid < n) {
       la[tid] = sum_of(p.sources_chunk, p.chunks, i0 + tid);
@@ -120,29 +119,51 @@ __global__ __launch_bounds__(kThreads) void decay_grad(DaDecayGrad p) {
       cuts[tid] = p.chunk_decay[int64_t(bh) * p.chunks + i0 + tid] == 0.0f;
     }
     __syncthreads();
-    if (tid == 0) {
-      // `sum`: what was added up since the last cut, the scale of the rounding errors in z
-      double sum = fabs(z);
-      int from = 0;
-      for (int i = 0; i < n; ++i) {
-        if (cuts[i]) {
-          from = i;
-          sum = 0.0;
-        } else {
-          sum += fabs(ly[i]);
-        }
-        const double y = cuts[i] ? 0.0 : z - ly[i];
-        lw[i] = sum;
-        ly[i] = y;
-        z = y + la[i];
-        sum += fabs(la[i]);
+  };
+  // `sum`: what was added up since the last cut, the chunk `from`: the scale of the rounding errors in z
+  struct Carried {
+    double z, sum;
+    int from;
+  };
+  // carries c over them (one thread): what passes each of them to ly, the sum by then to lw
+  auto carry_over = [&](Carried& c, int i0, int n) {
+    for (int i = 0; i < n; ++i) {
+      if (cuts[i]) {
+        c.from = i0 + i;
+        c.sum = 0.0;
+      } else {
+        c.sum += fabs(ly[i]);
       }
-      // The carried sum at the segment's end is known outright as well: what rounding has put between
-      // the two is taken off again, in proportion to what had been added up.
-      const double off = z - end;
-      if (n == last - first && sum > 0.0 && fabs(off) <= 1e-4 * sum) {
-        const double share = off / sum;
-        for (int i = from; i < n; ++i) ly[i] -= cuts[i] ? 0.0 : share * lw[i];
+      const double y = cuts[i] ? 0.0 : c.z - ly[i];
+      lw[i] = c.sum;
+      ly[i] = y;
+      c.z = y + la[i];
+      c.sum += fabs(la[i]);
+    }
+  };
+  // The carried sum at the segment's end is known outright as well: what rounding has put between the two
+  // is taken off again, in proportion to what had been added up. So the end comes first: where a segment has
+  // more chunks than are read at a time, they are read twice.
+  Carried at = {z, fabs(z), first}, at_end = at;
+  const bool twice = last - first > kThreads;
+  if (twice) {
+    for (int i0 = first; i0 < last; i0 += kThreads) {
+      const int n = min(kThreads, last - i0);
+      load(i0, n);
+      if (tid == 0) carry_over(at_end, i0, n);
+    }
+  }
+  double all = 0.0;
+  for (int i0 = first; i0 < last; i0 += kThreads) {
+    const int n = min(kThreads, last - i0);
+    load(i0, n);
+    if (tid == 0) {
+      carry_over(at, i0, n);
+      if (!twice) at_end = at;
+      const double off = at_end.z - end;
+      if (at_end.sum > 0.0 && fabs(off) <= 1e-4 * at_end.sum) {
+        const double share = off / at_end.sum;
+        for (int i = max(at_end.from - i0, 0); i < n; ++i) ly[i] -= cuts[i] ? 0.0 : share * lw[i];
       }
     }
     __syncthreads();

@@ -1,5 +1,6 @@
 """How decay attention and head norm + rotation are called: optional values of any truth, states that are
-written in place, tensors that carry more than their numbers, states at any alignment."""
+written in place, tensors that carry more than their numbers, states at any alignment, long
+segments."""
 
 import numpy as np
 import pytest
@@ -9,10 +10,11 @@ import torch.autograd.forward_ad as forward_ad
 import scan_primitives_amd as sx
 from scan_primitives_amd import _binding as B
 from tests import test_head_rotate_gpu as rotate
-from tests.test_decay_attention_gpu import _backward, _forward, make, make_step
+from tests.test_decay_attention_gpu import (_backward, _close, _forward, _np, _oracle_vjp, _roundings, make,
+                                            make_step)
 
 pytestmark = pytest.mark.gpu
-F32 = torch.float32
+BF, F32 = torch.bfloat16, torch.float32
 
 
 @pytest.mark.parametrize("true,false", [(1, 0), (np.bool_(True), np.bool_(False)), ("yes", "")])
@@ -154,3 +156,48 @@ def test_a_step_on_a_view_of_a_pool(name, room, view, dk, dv):
     assert torch.equal(state, alone)
     view(kept).copy_(state)
     assert torch.equal(room, kept)  # nothing else of the buffer has changed
+
+
+def _whole_numbers(b=1, t=200, h=4, dk=16, dv=16, type=F32, cuts=False, lengths=None, hq=None, seed=0):
+    """Operands of -1, 0 and 1 and decays of one or nothing: every product and sum is a whole number."""
+    s = make(b=b, t=t, h=h, hq=hq, dk=dk, dv=dv, type=type, initial=True, lengths=lengths, seed=seed,
+             decay="cuts" if cuts else "none")
+    if cuts:
+        s["g"] = torch.where(torch.isinf(s["g"]), s["g"], torch.zeros_like(s["g"]))
+    for n in ("q", "k", "v", "go", "initial", "gs"):
+        s[n] = s[n].float().round().clamp(-1, 1).to(s[n].dtype)
+    s["scale"] = 1.0
+    return s
+
+
+@pytest.mark.parametrize("type", [BF, F32])
+@pytest.mark.parametrize("name,kwargs", [
+    ("one chunk", dict(t=20)), ("chunks", dict(t=200)), ("segments", dict(t=1000, h=2)), ("cuts", dict(t=300, cuts=True)),
+    ("segments, cuts", dict(t=1000, h=2, cuts=True)), ("two column blocks", dict(t=150, dk=130, dv=8)),
+    ("shared", dict(t=150, h=6, hq=2)), ("ragged", dict(b=3, t=300, lengths=[300, 0, 77], cuts=True)),
+])
+def test_the_decays_gradient_of_whole_numbers_is_exact(type, name, kwargs):
+    s = _whole_numbers(type=type, **kwargs)
+    # no sum of absolute values that enters a result reaches 2^24: in 32 bits nothing is rounded
+    ref = _oracle_vjp(s)
+    assert np.abs(ref[3]).max() < 2.0 ** 22
+    assert np.array_equal(_np(_backward(s)[3]), ref[3])
+
+
+@pytest.mark.parametrize("type,t", [(F32, 1000), (BF, 1500), (F32, 8300), (BF, 16500)])
+def test_what_large_tokens_leave_is_taken_off_at_a_segments_end(type, t):
+    # Heads enough that each is one segment (the last two lengths: of more than 256 chunks). The first quarter's
+    # values and gradients are 2^10 times the others', and a decay of exp(-0.05) a token leaves nothing of them 512
+    # tokens on: but the roundings of the sums that are carried, which only the sum that is known at the end takes off.
+    # Without it they are about 2^-24 (2^10)^2 times a chunk's sums of the other tokens.
+    s = make(b=1, t=t, h=260, dk=2, dv=2, type=type)
+    s["g"] = torch.full_like(s["g"], -0.05)
+    s["v"][:, :t // 4] *= 1024
+    s["go"][:, :t // 4] *= 1024
+    tail = t // 4 + 512
+    got = _backward(s, grad_state=False)[3]
+    ref, size = _oracle_vjp(s, grad_state=False), _oracle_vjp(s, grad_state=False, size=True)
+    # a chunk of 64 tokens' sums of q . grad_q and k . grad_k, as everywhere
+    mass = (np.abs(_np(s["q"])) * size[0]).sum(-1) + (np.abs(_np(s["k"])) * size[1]).sum(-1)
+    floor = 64.0 * mass[:, tail:].max()
+    _close("grad_log_decay", got[:, tail:], ref[3][:, tail:], size[3][:, tail:], _roundings(s), False, floor=floor)
