@@ -269,3 +269,30 @@ def test_far_apart_rows():
         for a, b in zip(want, (*_forward(s), *_backward(s))):
             assert torch.equal(a, b)
         s[name] = kept
+
+
+# One token in f32, and token groups enough that a workgroup of the gradient takes several (1024 of them at most take
+# part on 256 compute units; with 130 heads a group is one token).
+MORE = {
+    "one token f32": dict(b=1, t=1, type=F32),
+    "one token f32, far": dict(b=1, t=1, type=F32, first=1 << 20, layout="aligned", d=128),
+    "one token f32 neighbours, odd width": dict(b=1, t=1, type=F32, near=True, d=33, rot=20),
+    "several groups a workgroup": dict(b=2, t=1300, hq=130, hk=2, d=8, layout="aligned"),
+    "several groups a workgroup f32": dict(b=1, t=2100, hq=2, hk=130, d=10, rot=6, type=F32),
+}
+
+
+@pytest.mark.parametrize("name", MORE)
+def test_single_tokens_and_many_groups(name):
+    print(f"\n[case] head norm + rotation: {name}", flush=True)
+    s = make(**MORE[name], seed=70)
+    out, grad = _forward(s), _backward(s)
+    for i, (x, w) in enumerate((("q", "qw"), ("k", "kw"))):
+        args = (_np(s[x]), _positions(s), _np(s["turns"]), _np(s[w]))
+        size = oa.head_norm_rotate(*args, neighbours=s["near"], size=True)
+        _close(x, out[i], oa.head_norm_rotate(*args, neighbours=s["near"]), np.abs(size), s[x].dtype == BF)
+        args = args[:3] + (_np(s["g" + x]), args[3])
+        ref = oa.head_norm_rotate_vjp(*args, neighbours=s["near"])
+        size = oa.head_norm_rotate_vjp(*args, neighbours=s["near"], size=True)
+        _close("grad_" + x, grad[i], ref[0], size[0], s[x].dtype == BF)
+        _close("grad_" + w, grad[2 + i], ref[1], size[1], False, rows=s[x].shape[0] * s[x].shape[1] * s[x].shape[2])
