@@ -442,12 +442,13 @@ sx_status sx_table_scan(int states, int nsym, const int32_t* table, int rank, co
  *                aligned; may hold anything; may be NULL when that is 0.
  *
  * An infinity or NaN of one token reaches that token's own row and later ones of
- * its head (past a cut as well), never earlier ones; an infinity may come out as
- * NaN. out and
- * final_state are 16-byte aligned (else SX_E_UNSUPPORTED) and overlap no input
- * and not each other (SX_E_ALIAS). Errors otherwise as the scans: E-DIM-001 shapes,
- * E-DIM-002 dtypes, E-DIM-003 a NULL tensor that has elements, SX_E_UNSUPPORTED
- * heads wider than 256.
+ * its head (it may past a cut as well), never earlier ones; an infinity may come
+ * out as NaN. One of `initial` reaches no row from a cut on (a token whose decay is
+ * zero in f32); where the decays of several tokens multiply to zero it may be left
+ * behind too. out and final_state are 16-byte aligned (else SX_E_UNSUPPORTED) and
+ * overlap no input and not each other (SX_E_ALIAS). Errors otherwise as the scans:
+ * E-DIM-001 shapes, E-DIM-002 dtypes, E-DIM-003 a NULL tensor that has elements,
+ * SX_E_UNSUPPORTED heads wider than 256.
  */
 sx_status sx_decay_attention(sx_dtype dtype, const int64_t* q_shape, const int64_t* q_strides, const void* q,
                              const int64_t* k_shape, const int64_t* k_strides, const void* k, const int64_t* v_shape,
@@ -513,7 +514,8 @@ size_t sx_decay_attention_backward_workspace_bytes(sx_dtype dtype, const int64_t
  *                pool >= B then). A row whose slot lies outside [0, pool) is
  *                idle: its row of out is zero and no state changes. Two rows with
  *                the same slot race: that state and those rows of out are then
- *                undefined.
+ *                undefined. A token whose decay is zero in f32 starts from a state
+ *                of zeros, whatever the slot holds.
  *  out           contiguous [B, H, dv], 16-byte aligned.
  *
  * No workspace. Errors as sx_decay_attention.

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(kThreads) void carry(DaParams p) {
 #pragma unroll
     for (int k = 0; k < A; ++k) {
       if (i + k >= n) break;
-      s = fmaf(d[k], s, v[k]);
+      s = d[k] == 0.0f ? v[k] : fmaf(d[k], s, v[k]);  // nothing is left, of a state that is not finite either
       m.seg[(i + k) * BH * state + e] = s;
     }
   }
@@ -266,6 +266,7 @@ __global__ __launch_bounds__(kThreads) void step_kernel(DaStep p) {
     for (int e = 0; e < 4; ++e)
       if (col + e < p.dv) vv[e] = O::one(v[int64_t(col + e) * p.v.sd]);
     const float decay = expf(p.g[int64_t(b) * p.gb + int64_t(h) * p.gh]);
+    const bool clears = decay == 0.0f;  // nothing of the state is left, whatever it holds
     __syncthreads();
     for (int r1 = r0; r1 < p.dk; r1 += kStepRows * RG) {
       if (r1 != r0) load(r1);
@@ -277,7 +278,7 @@ __global__ __launch_bounds__(kThreads) void step_kernel(DaStep p) {
           f32x4 n;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            n[e] = fmaf(decay, old[i][e], kr * vv[e]);
+            n[e] = fmaf(decay, clears ? 0.0f : old[i][e], kr * vv[e]);
             o[e] = fmaf(qr, n[e], o[e]);
           }
           float* to = s + int64_t(r) * p.dv;

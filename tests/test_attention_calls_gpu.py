@@ -1,6 +1,6 @@
 """How decay attention and head norm + rotation are called: optional values of any truth, states that are
 written in place, tensors that carry more than their numbers, states at any alignment, long
-segments."""
+segments, states that are not finite."""
 
 import numpy as np
 import pytest
@@ -201,3 +201,47 @@ def test_what_large_tokens_leave_is_taken_off_at_a_segments_end(type, t):
     mass = (np.abs(_np(s["q"])) * size[0]).sum(-1) + (np.abs(_np(s["k"])) * size[1]).sum(-1)
     floor = 64.0 * mass[:, tail:].max()
     _close("grad_log_decay", got[:, tail:], ref[3][:, tail:], size[3][:, tail:], _roundings(s), False, floor=floor)
+
+
+@pytest.mark.parametrize("type", [BF, F32])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("t,at", [(1, 0), (40, 0), (150, 70), (150, 64), (1000, 0), (1000, 700)])
+def test_a_cut_clears_a_state_that_is_not_finite(type, value, t, at):
+    s = make(b=1, t=t, h=2, dk=40, dv=24, type=type, initial=True)
+    s["g"][:, at] = -float("inf")
+    clean, grads = _forward(s), _backward(s)
+    s["initial"][0, 0, 3], s["initial"][0, 1, :, 5] = value, value
+    out, last = _forward(s)
+    assert torch.equal(out[:, at:], clean[0][:, at:]) and torch.equal(last, clean[1])
+    assert at == 0 or not torch.isfinite(out[:, :at, 0]).any()
+    gq, gk, gv, gg, gi = _backward(s)
+    assert torch.equal(gq[:, at:], grads[0][:, at:])
+    for a, b in ((gk, grads[1]), (gv, grads[2]), (gi, grads[4])):
+        assert torch.equal(a, b)
+    if at == 0:
+        # what is carried over the borders is kept by differences: another start, other roundings of them
+        torch.testing.assert_close(gg, grads[3], rtol=1e-4, atol=1e-3)
+    assert torch.isfinite(gg[:, at:]).all() and not gg[:, at].any()
+
+
+@pytest.mark.parametrize("type", [BF, F32])
+def test_a_cut_clears_a_gradient_of_the_state_that_is_not_finite(type):
+    s = make(b=1, t=150, h=2, dk=40, dv=24, type=type, initial=True)
+    s["g"][:, 70] = -float("inf")
+    clean = _backward(s)
+    s["gs"][0, 0, 3, 4] = float("nan")
+    got = _backward(s)
+    assert torch.equal(got[0], clean[0]) and torch.equal(got[4], clean[4])
+    assert torch.equal(got[1][:, :70], clean[1][:, :70]) and torch.equal(got[2][:, :70], clean[2][:, :70])
+
+
+@pytest.mark.parametrize("dv", [24, 33, 128])
+@pytest.mark.parametrize("g", [-float("inf"), -150.0])
+def test_a_first_token_that_cuts_starts_on_an_uncleared_slot(dv, g):
+    s, e = (make_step(b=5, pool=8, dk=40, dv=dv, slots="all used") for _ in range(2))
+    s["g"][2] = e["g"][2] = g
+    slot = s["slots"][2].long()
+    s["state"][slot], e["state"][slot] = float("nan"), 0.0
+    s["state"][slot, 1] = float("inf")
+    got, want = (sx.decay_attention_step(x["q"], x["k"], x["v"], x["g"], x["state"], slots=x["slots"]) for x in (s, e))
+    assert torch.equal(got, want) and torch.equal(s["state"], e["state"])
