@@ -12,6 +12,7 @@ import ctypes
 import functools
 import math
 import os
+import warnings
 
 import torch
 import torch.autograd.forward_ad as forward_ad
@@ -600,6 +601,19 @@ def _matrix_dims_contiguous(t: torch.Tensor) -> bool:
 # the long way below, which checks everything by name, converts, records for
 # autograd and switches devices.
 
+MARSHAL_PATH = os.path.join(HERE, "_sx_marshal.so")
+
+
+class _LongWay:
+    """In the place of the short way where that is not built or does not load: every call goes the long one."""
+
+    def _none(*args):
+        return None
+
+    decay_attention = decay_attention_backward = decay_attention_step = _none
+    head_norm_rotate = head_norm_rotate_backward = _none
+
+
 _marshal = None
 
 
@@ -609,12 +623,15 @@ def _load_marshal():
     from importlib import machinery, util
 
     lib = load_library()
-    path = os.path.join(HERE, "_sx_marshal.so")
-    if not os.path.exists(path):
-        raise RuntimeError(f"{path} is not built; run `python -m scan_primitives_amd.build_lib`")
-    loader = machinery.ExtensionFileLoader("_sx_marshal", path)
-    module = util.module_from_spec(util.spec_from_loader("_sx_marshal", loader))
-    loader.exec_module(module)
+    loader = machinery.ExtensionFileLoader("_sx_marshal", MARSHAL_PATH)
+    try:
+        module = util.module_from_spec(util.spec_from_loader("_sx_marshal", loader))
+        loader.exec_module(module)
+    except ImportError as e:
+        warnings.warn(f"{MARSHAL_PATH} is not built or does not load ({e}): linear-attention calls cost more on the "
+                      "host; run `python -m scan_primitives_amd.build_lib`", RuntimeWarning, stacklevel=3)
+        _marshal = _LongWay()
+        return _marshal
     names = ("sx_decay_attention", "sx_decay_attention_workspace_bytes", "sx_decay_attention_backward",
              "sx_decay_attention_backward_workspace_bytes", "sx_decay_attention_step", "sx_head_norm_rotate",
              "sx_head_norm_rotate_backward", "sx_head_norm_rotate_backward_workspace_bytes")

@@ -62,17 +62,35 @@ def marshal_command(out_path: str) -> list[str]:
 
 
 def _run(cmd: list[str]) -> tuple[int, list[str]]:
-    proc = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        proc = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:  # no such compiler
+        return 127, [str(e)]
     # hipcc's host pass does not know the device-only feature flag and says so; that is harmless.
     noise = "'-packed-fp32-ops' is not a recognized feature"
     return proc.returncode, [ln for ln in (proc.stdout + proc.stderr).splitlines() if noise not in ln]
+
+
+def _put_marshal(tmp: str, rc: int, msgs: list[str]) -> bool:
+    """The binding's extension as compiled to `tmp`. The library does not need it: where it does not compile (it
+    takes g++ and the headers of torch and CPython) an older one goes, and the binding's calls take its long way."""
+    if rc == 0:
+        os.replace(tmp, MARSHAL_PATH)
+        return True
+    print("\n".join(["py_marshal.cpp did not compile: single-token calls will cost more on the host", *msgs]),
+          flush=True)
+    for path in (tmp, MARSHAL_PATH):
+        if os.path.exists(path):
+            os.remove(path)
+    return False
 
 
 def build(verbose: bool = False) -> str:
     """Compile the library (always, even when one is already there) and return its path.
 
     Each source compiles to an object of its own, in parallel, under a build
-    folder next to this file; then one link step writes the library."""
+    folder next to this file; then one link step writes the library. The
+    binding's extension is compiled beside them."""
     from concurrent.futures import ThreadPoolExecutor
 
     objdir = os.path.join(HERE, "_build")
@@ -87,8 +105,8 @@ def build(verbose: bool = False) -> str:
     workers = max(1, min(len(cmds), os.cpu_count() or 1, 8))
     with ThreadPoolExecutor(max_workers=workers) as pool:
         results = list(pool.map(_run, cmds))
-    sources = [src for src, _ in jobs] + ["py_marshal.cpp"]
-    errors = [(src, msgs) for src, (rc, msgs) in zip(sources, results) if rc != 0]
+    marshal = results.pop()
+    errors = [(src, msgs) for (src, _), (rc, msgs) in zip(jobs, results) if rc != 0]
     if errors:
         raise RuntimeError("compilation failed:\n" + "\n".join(f"{src}:\n" + "\n".join(msgs) for src, msgs in errors))
     if verbose:
@@ -100,7 +118,7 @@ def build(verbose: bool = False) -> str:
     if rc != 0:
         raise RuntimeError("hipcc link failed:\n" + "\n".join(msgs))
     os.replace(tmp, LIB_PATH)
-    os.replace(marshal_tmp, MARSHAL_PATH)
+    _put_marshal(marshal_tmp, *marshal)
     return LIB_PATH
 
 

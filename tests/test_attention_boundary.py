@@ -234,3 +234,27 @@ def test_decay_attention_step_state_alignment(lib):
 def test_decay_attention_step_takes_a_state_off_16_byte_borders(lib, at):
     # what is left to refuse it is that there is no device
     assert _step(lib, state=_at(4) + at) == _step(lib) == B.SX_E_DEVICE, lib.sx_last_error()
+
+
+def test_the_binding_without_its_extension(monkeypatch, tmp_path):
+    monkeypatch.setattr(B, "_marshal", None)
+    monkeypatch.setattr(B, "MARSHAL_PATH", str(tmp_path / "_sx_marshal.so"))
+    with pytest.warns(RuntimeWarning, match="not built or does not load"):
+        test_binding_refuses_host_tensors()
+    (tmp_path / "_sx_marshal.so").write_bytes(b"another machine's")
+    monkeypatch.setattr(B, "_marshal", None)
+    with pytest.warns(RuntimeWarning, match="not built or does not load"):
+        test_binding_refuses_host_tensors()
+
+
+def test_the_library_is_built_where_the_extension_does_not_compile(monkeypatch, tmp_path):
+    from scan_primitives_amd import build_lib
+
+    old, tmp = tmp_path / "_sx_marshal.so", tmp_path / "_sx_marshal.so.tmp"
+    old.write_bytes(b"of other sources")
+    monkeypatch.setattr(build_lib, "MARSHAL_PATH", str(old))
+    rc, msgs = build_lib._run([str(tmp_path / "no compiler"), "-c"])
+    assert rc != 0 and msgs
+    assert build_lib._put_marshal(str(tmp), rc, msgs) is False and not old.exists()
+    tmp.write_bytes(b"of these")
+    assert build_lib._put_marshal(str(tmp), 0, []) is True and old.read_bytes() == b"of these" and not tmp.exists()

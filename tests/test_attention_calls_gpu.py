@@ -27,6 +27,15 @@ def test_whether_the_state_is_wanted_goes_by_truth(true, false):
     assert torch.equal(sx.decay_attention(s["q"], s["k"], s["v"], s["g"], return_state=false, **args), out)
 
 
+def test_every_call_without_the_bindings_extension(monkeypatch):
+    s, r, one, other = make(t=70, initial=True, lengths=[70, 9]), rotate.make(), make_step(), make_step()
+    want = (*_forward(s), *_backward(s), *rotate._forward(r), *rotate._backward(r), _step(one), one["state"])
+    monkeypatch.setattr(B, "_marshal", B._LongWay())
+    got = (*_forward(s), *_backward(s), *rotate._forward(r), *rotate._backward(r), _step(other), other["state"])
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
 def _step(s, scale=1.0):
     return sx.decay_attention_step(s["q"], s["k"], s["v"], s["g"], s["state"], slots=s["slots"], scale=scale)
 
@@ -88,7 +97,8 @@ def test_tangents_are_refused():
                  lambda: sx.decay_attention_step(one["q"], one["k"], one["v"], one["g"], dual(one["state"])),
                  lambda: sx.head_norm_rotate(r["q"], dual(r["k"]), r["positions"], r["turns"]),
                  lambda: sx.head_norm_rotate(r["q"], r["k"], r["positions"], r["turns"], k_weight=dual(r["kw"])),
-                 lambda: sx.head_norm_rotate_backward(r["q"], r["k"], r["positions"], r["turns"], dual(r["gq"]), r["gk"])]
+                 lambda: sx.head_norm_rotate_backward(r["q"], r["k"], r["positions"], r["turns"], dual(r["gq"]),
+                                                      r["gk"])]
         for i, call in enumerate(calls + _scan_calls(dual(torch.rand(4, 16, device="cuda")))):
             with pytest.raises(sx.SxError) as e:
                 call()
@@ -143,7 +153,8 @@ def test_autograd_of_a_lazily_negated_view(name, at):
 @pytest.mark.parametrize("name,room,view,dk,dv", [
     ("slots from the second on", (5, 1, 33, 33), lambda x: x[1:], 33, 33),
     ("heads from the second on", (4, 3, 33, 47), lambda x: x[:, 1:], 33, 47),
-    ("states a word past a 16-byte border", (4, 2, 32 * 32 + 4), lambda x: x[..., 1:-3].unflatten(-1, (32, 32)), 32, 32),
+    ("states a word past a 16-byte border", (4, 2, 32 * 32 + 4), lambda x: x[..., 1:-3].unflatten(-1, (32, 32)), 32,
+     32),
 ])
 def test_a_step_on_a_view_of_a_pool(name, room, view, dk, dv):
     room = torch.randn(room, device="cuda")
@@ -172,7 +183,8 @@ def _whole_numbers(b=1, t=200, h=4, dk=16, dv=16, type=F32, cuts=False, lengths=
 
 @pytest.mark.parametrize("type", [BF, F32])
 @pytest.mark.parametrize("name,kwargs", [
-    ("one chunk", dict(t=20)), ("chunks", dict(t=200)), ("segments", dict(t=1000, h=2)), ("cuts", dict(t=300, cuts=True)),
+    ("one chunk", dict(t=20)), ("chunks", dict(t=200)), ("segments", dict(t=1000, h=2)),
+    ("cuts", dict(t=300, cuts=True)),
     ("segments, cuts", dict(t=1000, h=2, cuts=True)), ("two column blocks", dict(t=150, dk=130, dv=8)),
     ("shared", dict(t=150, h=6, hq=2)), ("ragged", dict(b=3, t=300, lengths=[300, 0, 77], cuts=True)),
 ])
