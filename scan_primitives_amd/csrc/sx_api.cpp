@@ -1436,7 +1436,6 @@ sx_status sx_decay_attention_backward(sx_dtype dtype, const int64_t* q_shape, co
   dq.dz = dk.dz = p.dk;
   dv.dx = p.dk;
   dv.dz = p.dv;
-  dk.reverse = dv.reverse = 1;
   dq.scale_out = scale;
   dq.scale_src = 1.0f;
   dk.scale_out = dv.scale_out = 1.0f;

@@ -35,7 +35,6 @@ struct DaMarch {
   HeadView x, y, z;
   HeadView w;           // grad_q: q; grad_k: k: the row each output meets in the decay's gradient (p == nullptr: none)
   int dx, dz;
-  int reverse;
   float scale_out, scale_src;
   void* out;            // element (b, t, h, d) at ((b * T + t) * H + h) * dz + d; nullptr: states only
   int out_f32;          // out is f32 whatever the inputs' type
