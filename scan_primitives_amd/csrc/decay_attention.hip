@@ -13,6 +13,10 @@ namespace sx {
 namespace {
 
 constexpr int kThreads = 256;
+// Chunks over which the gradient of a decay is carried by differences. Of one decay a head, summed over 4096 tokens of
+// 8 rows of 64 heads of 16 x 16 in f32, 3.8e-7 is lost against 64 bits, 8.7e-6 where spans are whole segments (128
+// chunks); the marks cost 32 x 4096 tokens of 8 heads of 128 in bf16 1285 us for 1217.
+constexpr int kSpanChunks = 8;
 
 // Segment m's entry, its own state so far, becomes the state at the start of segment m + 1. Bound by
 // memory: each entry is read and written once, eight read ahead of the chain (15 entries of 16 states of
@@ -58,17 +62,40 @@ __device__ __forceinline__ double block_sum(double v, double* l) {
   return v;
 }
 
+// The state against its adjoint at the spans' borders within segments, from the marks that two marches left of
+// them. One workgroup a border.
+__global__ __launch_bounds__(kThreads) void span_cross(DaDecayGrad p) {
+  __shared__ double l[kThreads];
+  const int inner = p.segments * (p.spans - 1), tid = int(threadIdx.x);
+  const int64_t at = blockIdx.x, bh = at / inner, BH = int64_t(p.B) * p.H, n = mark_floats(p.dk, p.dv);
+  const int seg = int(at % inner) / (p.spans - 1), k = int(at % inner) % (p.spans - 1) + 1;
+  const f32x4* s = reinterpret_cast<const f32x4*>(p.states + at * n);
+  const f32x4* a = reinterpret_cast<const f32x4*>(p.adjoints + at * n);
+  double v = 0.0;
+#pragma unroll 4
+  for (int64_t i = tid; i < n / 4; i += kThreads) {
+    const f32x4 x = s[i], y = a[i];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v += double(x[e]) * double(y[e]);
+  }
+  v = block_sum(v, l);
+  if (tid < p.blocks)
+    p.cross[(tid * BH + bh) * (int64_t(p.segments) * p.spans + 1) + seg * p.spans + k] = tid == 0 ? v : 0.0;
+}
+
 // What passes a chunk from before to after it, Y, from what crosses the border
 // before it, Z: Y = Z - (its rows' mass), the next Z = Y + (its sources' mass), and
 // Y is zero outright where the chunk's decays multiply to zero. One workgroup a
-// head and segment, from the segment's own Z; kThreads chunks at a time.
+// head and span, from the span's own Z. A span is few chunks (kSpanChunks), for
+// what the two sums are rounded by adds up in Z, and stays when the state that
+// it was rounded in has long decayed.
 __global__ __launch_bounds__(kThreads) void decay_grad(DaDecayGrad p) {
   __shared__ double la[kThreads];
-  __shared__ double ly[kThreads];
-  __shared__ double lw[kThreads];
-  __shared__ bool cuts[kThreads];
-  const int bh = blockIdx.x % (p.B * p.H), seg = blockIdx.x / (p.B * p.H), tid = int(threadIdx.x);
-  const int b = bh / p.H, h = bh % p.H;
+  __shared__ double ly[kSpanChunks];
+  __shared__ double lw[kSpanChunks];
+  __shared__ bool cuts[kSpanChunks];
+  const int bh = blockIdx.x % (p.B * p.H), span = blockIdx.x / (p.B * p.H), tid = int(threadIdx.x);
+  const int b = bh / p.H, h = bh % p.H, spans = p.segments * p.spans;
   const int64_t BH = int64_t(p.B) * p.H, state = int64_t(p.dk) * p.dv;
   int len = p.T;
   if (p.lengths) len = min(max(p.lengths[b], 0), p.T);
@@ -77,7 +104,11 @@ __global__ __launch_bounds__(kThreads) void decay_grad(DaDecayGrad p) {
     for (int k = 0; k < p.blocks; ++k) s += double(v[(k * BH + bh) * n + i]);
     return s;
   };
-  const int first = seg * (p.seg_tokens / p.chunk), last = min(p.chunks, first + p.seg_tokens / p.chunk);
+  // its chunks (none, where the last segment is shorter)
+  const int seg_chunks = p.seg_tokens / p.chunk, seg = span / p.spans;
+  const int first = min(p.chunks, seg * seg_chunks + span % p.spans * p.span_chunks);
+  const int last = min(p.chunks, min((seg + 1) * seg_chunks, first + p.span_chunks)), n = last - first;
+  const int t0 = first * p.chunk, t1 = min(last * p.chunk, p.T);
   // What a token's decay carries within its chunk, and whether anything passes at all: where exp(g) = 0
   // neither does a gradient.
   struct Within {
@@ -94,97 +125,68 @@ __global__ __launch_bounds__(kThreads) void decay_grad(DaDecayGrad p) {
   Within ahead[A];
 #pragma unroll
   for (int i = 0; i < A; ++i) {
-    const int t = first * p.chunk + i * kThreads + tid;
-    ahead[i] = t < min(last * p.chunk, p.T) ? within(t) : Within{0.0, false};
+    const int t = t0 + i * kThreads + tid;
+    ahead[i] = t < t1 ? within(t) : Within{0.0, false};
   }
-  // cross: [blocks][B * H][segments + 1], at the start of each segment but the first, and at the end
+  // cross: [blocks][B * H][spans + 1], at the start of each span but the first, and at the end
   double z = 0.0, end = 0.0;
   for (int k = 0; k < p.blocks; ++k) {
-    const double* at = p.cross + (k * BH + bh) * (p.segments + 1) + seg;
-    if (seg > 0) z += at[0];
-    end += at[1];
+    const double* at = p.cross + (k * BH + bh) * (spans + 1);
+    if (span > 0 && n > 0) z += at[span];
+    if (n > 0) end += at[last == p.chunks ? spans : span + 1];
   }
-  if (seg == 0 && p.initial) {
+  if (span == 0 && p.initial) {
     double s = 0.0;
     for (int64_t i = tid; i < state; i += kThreads)
       s += double(p.initial[bh * state + i]) * double(p.grad_initial[bh * state + i]);
     z = block_sum(s, la);
   }
-  // the sums of n chunks from i0 on
-  auto load = [&](int i0, int n) {
-    __syncthreads();
-    if (tid < n) {
-      la[tid] = sum_of(p.sources_chunk, p.chunks, i0 + tid);
-      ly[tid] = sum_of(p.rows_chunk, p.chunks, i0 + tid);
-      cuts[tid] = p.chunk_decay[int64_t(bh) * p.chunks + i0 + tid] == 0.0f;
-    }
-    __syncthreads();
-  };
-  // `sum`: what was added up since the last cut, the chunk `from`: the scale of the rounding errors in z
-  struct Carried {
-    double z, sum;
-    int from;
-  };
-  // carries c over them (one thread): what passes each of them to ly, the sum by then to lw
-  auto carry_over = [&](Carried& c, int i0, int n) {
+  if (tid < n) {
+    la[tid] = sum_of(p.sources_chunk, p.chunks, first + tid);
+    ly[tid] = sum_of(p.rows_chunk, p.chunks, first + tid);
+    cuts[tid] = p.chunk_decay[int64_t(bh) * p.chunks + first + tid] == 0.0f;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    // `sum`: what was added up since the last cut, the scale of the rounding errors in z
+    double sum = fabs(z);
+    int from = 0;
     for (int i = 0; i < n; ++i) {
       if (cuts[i]) {
-        c.from = i0 + i;
-        c.sum = 0.0;
+        from = i;
+        sum = 0.0;
       } else {
-        c.sum += fabs(ly[i]);
+        sum += fabs(ly[i]);
       }
-      const double y = cuts[i] ? 0.0 : c.z - ly[i];
-      lw[i] = c.sum;
+      const double y = cuts[i] ? 0.0 : z - ly[i];
+      lw[i] = sum;
       ly[i] = y;
-      c.z = y + la[i];
-      c.sum += fabs(la[i]);
+      z = y + la[i];
+      sum += fabs(la[i]);
     }
-  };
-  // The carried sum at the segment's end is known outright as well: what rounding has put between the two
-  // is taken off again, in proportion to what had been added up. So the end comes first: where a segment has
-  // more chunks than are read at a time, they are read twice.
-  Carried at = {z, fabs(z), first}, at_end = at;
-  const bool twice = last - first > kThreads;
-  if (twice) {
-    for (int i0 = first; i0 < last; i0 += kThreads) {
-      const int n = min(kThreads, last - i0);
-      load(i0, n);
-      if (tid == 0) carry_over(at_end, i0, n);
+    // The carried sum at the span's end is known outright as well: what rounding has put between
+    // the two is taken off again, in proportion to what had been added up.
+    const double off = z - end;
+    if (sum > 0.0 && fabs(off) <= 1e-4 * sum) {
+      const double share = off / sum;
+      for (int i = from; i < n; ++i) ly[i] -= cuts[i] ? 0.0 : share * lw[i];
     }
   }
+  __syncthreads();
   double all = 0.0;
-  for (int i0 = first; i0 < last; i0 += kThreads) {
-    const int n = min(kThreads, last - i0);
-    load(i0, n);
-    if (tid == 0) {
-      carry_over(at, i0, n);
-      if (!twice) at_end = at;
-      const double off = at_end.z - end;
-      if (at_end.sum > 0.0 && fabs(off) <= 1e-4 * at_end.sum) {
-        const double share = off / at_end.sum;
-        for (int i = max(at_end.from - i0, 0); i < n; ++i) ly[i] -= cuts[i] ? 0.0 : share * lw[i];
-      }
-    }
-    __syncthreads();
-    const int t0 = i0 * p.chunk, t1 = min((i0 + n) * p.chunk, p.T);
-    auto put = [&](int t, Within in) {
-      const double v = in.passes ? ly[t / p.chunk - i0] + in.v : 0.0;
-      if (p.per_head) all += v;
-      else p.grad_g[(int64_t(b) * p.T + t) * p.H + h] = float(v);
-    };
-    int t = t0 + tid;
-    if (i0 == first) {
+  auto put = [&](int t, Within in) {
+    const double v = in.passes ? ly[t / p.chunk - first] + in.v : 0.0;
+    if (p.per_head) all += v;
+    else p.grad_g[(int64_t(b) * p.T + t) * p.H + h] = float(v);
+  };
+  int t = t0 + tid;
 #pragma unroll
-      for (int i = 0; i < A; ++i, t += kThreads)
-        if (t < t1) put(t, ahead[i]);
-    }
-    for (; t < t1; t += kThreads) put(t, within(t));
-  }
+  for (int i = 0; i < A; ++i, t += kThreads)
+    if (t < t1) put(t, ahead[i]);
+  for (; t < t1; t += kThreads) put(t, within(t));
   if (p.per_head) {
-    __syncthreads();
     all = block_sum(all, la);
-    if (tid == 0) p.partial[int64_t(seg) * BH + bh] = all;
+    if (tid == 0) p.partial[int64_t(span) * BH + bh] = all;
   }
 }
 
@@ -192,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void decay_grad(DaDecayGrad p) {
 __global__ __launch_bounds__(kWave) void decay_grad_heads(DaDecayGrad p) {
   const int h = blockIdx.x, lane = int(threadIdx.x);
   double s = 0.0;
-  for (int i = lane; i < p.B * p.segments; i += kWave) s += p.partial[int64_t(i) * p.H + h];
+  for (int64_t i = lane; i < int64_t(p.B) * p.segments * p.spans; i += kWave) s += p.partial[i * p.H + h];
   s = lane_of(prefix_sum(s, lane), 63);
   if (lane == 0) p.grad_g[h] = float(s);
 }
@@ -336,6 +338,9 @@ void decay_attention_split(DaParams& p) {
   const int64_t per = std::max<int64_t>(1, (chunks + segments - 1) / segments);
   p.seg_tokens = int(per * C);
   p.segments = int(std::max<int64_t>(1, (chunks + per - 1) / per));
+  const int64_t spans = (per + kSpanChunks - 1) / kSpanChunks;
+  p.span_chunks = int((per + spans - 1) / spans);
+  p.spans = int((per + p.span_chunks - 1) / p.span_chunks);
 }
 
 hipError_t launch_decay_attention(const DaParams& p, hipStream_t stream) {
@@ -369,7 +374,11 @@ hipError_t launch_decay_attention(const DaParams& p, hipStream_t stream) {
 }
 
 hipError_t launch_decay_grad(const DaDecayGrad& p, hipStream_t stream) {
-  if (p.B > 0) decay_grad<<<unsigned(int64_t(p.B) * p.H * p.segments), kThreads, 0, stream>>>(p);
+  const int64_t BH = int64_t(p.B) * p.H;
+  if (BH > 0) {
+    if (p.spans > 1) span_cross<<<unsigned(BH * p.segments * (p.spans - 1)), kThreads, 0, stream>>>(p);
+    decay_grad<<<unsigned(BH * p.segments * p.spans), kThreads, 0, stream>>>(p);
+  }
   if (p.per_head) decay_grad_heads<<<p.H, kWave, 0, stream>>>(p);
   return hipGetLastError();
 }

@@ -609,6 +609,20 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     rg = lane < C && t < end ? gb[int64_t(t) * p.gt] : 0.0f;
   };
 
+  // The state at the start of span k of the segment, to be met by its adjoint there (marches 0 and 1 hold both
+  // alike, transposed: a lane's four rows are next to each other).
+  auto mark = [&](int k) {
+    if constexpr (MASS != 0) {
+      const int pitch = (m.dx + 3) & ~3, col = c0 + wc0 + c;
+      float* to = m.marks + ((int64_t(bh) * p.segments + seg) * (p.spans - 1) + (k - 1)) * mark_floats(p.dk, p.dv);
+#pragma unroll
+      for (int kt = 0; kt < NKT; ++kt)
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+          if (16 * kt + 4 * g < pitch && col + 16 * n < m.dz)
+            *reinterpret_cast<f32x4*>(to + (col + 16 * n) * pitch + 16 * kt + 4 * g) = st[kt][n];
+    }
+  };
   // What a decay carries in all at a segment's border: the state against its adjoint there, `adj`.
   auto carried = [&](const float* adj, int border) {
     if constexpr (MASS == 1) {
@@ -628,7 +642,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
       if (tid == 0) {
         s = 0.0;
         for (int i = 0; i < W; ++i) s += l.cross[i];
-        m.cross[(int64_t(cb) * BH + bh) * (p.segments + 1) + border] = s;
+        m.cross[(int64_t(cb) * BH + bh) * (int64_t(p.segments) * p.spans + 1) + border] = s;
       }
       __syncthreads();
     }
@@ -640,7 +654,7 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
   }
   if constexpr (MASS == 1) {
     // Between here and the segment's end the carried sum is kept by differences.
-    if (seg_m > 0) carried(p.m[1].seg + (int64_t(p.segments - 1 - seg_m) * BH + bh) * state, seg);
+    if (seg_m > 0) carried(p.m[1].seg + (int64_t(p.segments - 1 - seg_m) * BH + bh) * state, seg * p.spans);
   }
   // chunk ci's tiles from registers to LDS: x and w, which only the first half of a chunk reads, and y and z
   auto put = [&](int ci) {
@@ -715,6 +729,11 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     for (int i = tid; i < 2 * S::BV; i += THREADS) l.from[i / S::BV][i % S::BV] = C;
   }
   float decays = 1.0f;
+  int next_k = REV ? p.spans - 1 : 1;  // the next span's border on the way, and its chunk
+  if constexpr (MASS == 2) {  // (those behind the row's last token)
+    for (; next_k > 0 && next_k * p.span_chunks >= nc; --next_k) mark(next_k);
+  }
+  int next_mark = next_k > 0 && next_k < p.spans ? next_k * p.span_chunks : -1;
   __syncthreads();
   if (nc > 0) {
     if (wave == kDecayWave) {
@@ -1005,6 +1024,13 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
         }
         for (int i = lane; i < 16 * NV; i += kWave) from[i] = C;
       }
+      if constexpr (MASS != 0) {
+        if ((REV ? nc - 1 - ci : ci + 1) == next_mark) {
+          mark(next_k);
+          next_k += REV ? -1 : 1;
+          next_mark = next_k > 0 && next_k < p.spans ? next_k * p.span_chunks : -1;
+        }
+      }
       // a token's rows of out
       if (staged) {
 #pragma unroll
@@ -1071,7 +1097,11 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
     }
   }
 
-  if (MASS == 1 && seg == p.segments - 1) carried(p.m[1].first ? p.m[1].first + bh * state : nullptr, p.segments);
+  if constexpr (MASS == 1) {
+    for (int k = p.spans - 1; k > 0 && k * p.span_chunks > nc; --k) mark(k);  // (those behind the row's last token)
+  }
+  if (MASS == 1 && seg == p.segments - 1)
+    carried(p.m[1].first ? p.m[1].first + bh * state : nullptr, p.segments * p.spans);
   float* to = OUT ? (seg_m == p.segments - 1 && m.last ? m.last + bh * state : nullptr)
                   : m.seg + (int64_t(seg_m) * BH + bh) * state;
   if (to) {

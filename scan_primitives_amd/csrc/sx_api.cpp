@@ -1280,6 +1280,8 @@ GradPieces carve_gradient(Carve& c, const DecayShapes& s, sx::DaParams& p) {
   carve_segments(c, p, p.m[1]);
   p.m[2].seg = p.m[1].seg;
   p.m[2].seg_decay = p.m[1].seg_decay;
+  for (int i = 0; i < 2; ++i)
+    p.m[i].marks = c.take<float>(s.B * s.H * p.segments * (p.spans - 1) * sx::mark_floats(p.dk, p.dv));
   const int chunk = sx::decay_attention_chunk(p.bf16 != 0);
   const int64_t BH = s.B * s.H;
   g.chunks = int((s.T + chunk - 1) / chunk);
@@ -1289,8 +1291,8 @@ GradPieces carve_gradient(Carve& c, const DecayShapes& s, sx::DaParams& p) {
   g.rows_chunk = c.take<float>(g.blocks * BH * g.chunks);
   g.sources_chunk = c.take<float>(g.blocks * BH * g.chunks);
   g.chunk_decay = c.take<float>(BH * g.chunks);
-  g.cross = c.take<double>(g.blocks * BH * (p.segments + 1));
-  g.partial = c.take<double>(BH * p.segments);
+  g.cross = c.take<double>(g.blocks * BH * (int64_t(p.segments) * p.spans + 1));
+  g.partial = c.take<double>(BH * p.segments * p.spans);
   // gradients of shared heads are summed over the heads that share them, from f32
   const int64_t n = s.B * s.T * s.H;
   g.share_q = c.take<float>(s.hq == s.H ? 0 : n * s.dk);
@@ -1501,6 +1503,10 @@ sx_status sx_decay_attention_backward(sx_dtype dtype, const int64_t* q_shape, co
   d.chunk_decay = w.chunk_decay;
   d.segments = p.segments;
   d.seg_tokens = p.seg_tokens;
+  d.spans = p.spans;
+  d.span_chunks = p.span_chunks;
+  d.states = p.m[0].marks;
+  d.adjoints = p.m[1].marks;
   d.cross = w.cross;
   d.initial = initial;
   d.grad_initial = grad_initial;

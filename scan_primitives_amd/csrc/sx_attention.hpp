@@ -46,8 +46,10 @@ struct DaMarch {
   float* seg_decay;     // [segments - 1][B * H]: product of a segment's decays
   float* mass;          // [column blocks][B * H][T]: the part of the decay's gradient that this march sees
   float* mass_chunk;    // [column blocks][B * H][chunks]: a chunk's mass against the state it entered with
-  double* cross;        // [column blocks][B * H][segments + 1]: the state against its adjoint at the segments' borders
-                        // (but the first)
+  double* cross;        // [column blocks][B * H][segments * spans + 1]: the state against its adjoint at the spans'
+                        // borders (but the first)
+  float* marks;         // [B * H][segments][spans - 1][dz][dx, to a multiple of 4]: the state at the spans' borders
+                        // within segments (grad_q, grad_k)
   float* chunk_decay;   // [B * H][chunks]: product of a chunk's decays (written by column block 0; nullptr: no)
 };
 
@@ -60,11 +62,15 @@ struct DaParams {
   int bf16;
   int segments;         // the tokens split into this many segments of seg_tokens
   int seg_tokens;       // a multiple of the chunk
+  int spans;            // and a segment into this many spans of span_chunks chunks (a gradient)
+  int span_chunks;
   int marches;          // 1 (forward) or 3 (gradient)
   DaMarch m[3];
 };
 
 int decay_attention_chunk(bool bf16);
+// Floats of a state in DaMarch::marks.
+__host__ __device__ inline int64_t mark_floats(int dk, int dv) { return int64_t(dk) * ((dv + 3) & ~3); }
 // Workgroups a head needs for `dz` columns.
 int decay_attention_column_blocks(int dz);
 // A march's shape: 16-row tiles of the state (2, 4, 8 or 16), and waves of 16 columns (4 or 8).
@@ -76,7 +82,7 @@ hipError_t launch_marches_bf16_any(const DaParams& p, int first, int count, bool
 hipError_t launch_marches_f32(const DaParams& p, int first, int count, bool local, hipStream_t stream);
 hipError_t launch_marches_f32_cut(const DaParams& p, int first, int count, bool local, hipStream_t stream);
 hipError_t launch_marches_f32_any(const DaParams& p, int first, int count, bool local, hipStream_t stream);
-// How the tokens are split: sets segments and seg_tokens.
+// How the tokens are split: sets segments and seg_tokens, spans and span_chunks.
 void decay_attention_split(DaParams& p);
 hipError_t launch_decay_attention(const DaParams& p, hipStream_t stream);
 
@@ -93,11 +99,13 @@ struct DaDecayGrad {
   const float* rows_chunk;     // [blocks][B * H][chunks]
   const float* sources_chunk;
   const float* chunk_decay;    // [B * H][chunks]
-  int segments, seg_tokens;
-  const double* cross;         // [blocks][B * H][segments + 1], but of the first border
+  int segments, seg_tokens, spans, span_chunks;
+  double* cross;               // [blocks][B * H][segments * spans + 1], but of the first border
+  const float* states;         // marks of the grad_q march and of the grad_k march
+  const float* adjoints;
   const float* initial;        // nullptr: zero
   const float* grad_initial;
-  double* partial;             // per_head: [segments][B * H]
+  double* partial;             // per_head: [segments * spans][B * H]
   float* grad_g;
   int per_head;
 };

@@ -187,6 +187,11 @@ def _whole_numbers(b=1, t=200, h=4, dk=16, dv=16, type=F32, cuts=False, lengths=
     ("cuts", dict(t=300, cuts=True)),
     ("segments, cuts", dict(t=1000, h=2, cuts=True)), ("two column blocks", dict(t=150, dk=130, dv=8)),
     ("shared", dict(t=150, h=6, hq=2)), ("ragged", dict(b=3, t=300, lengths=[300, 0, 77], cuts=True)),
+    # segments of several spans (256 tokens in f32, 512 in bf16 at most), rows that end in and between them
+    ("spans", dict(t=1500, h=260, dk=5, dv=3, cuts=True)),
+    ("spans, ragged", dict(b=4, t=1500, h=90, lengths=[1500, 0, 700, 1024], dk=5, dv=6)),
+    ("spans, two column blocks", dict(t=1100, h=260, dk=130, dv=9)),
+    ("spans and segments", dict(b=2, t=6000, h=50, lengths=[6000, 1111], dk=4, dv=7, cuts=True)),
 ])
 def test_the_decays_gradient_of_whole_numbers_is_exact(type, name, kwargs):
     s = _whole_numbers(type=type, **kwargs)
@@ -257,3 +262,22 @@ def test_a_first_token_that_cuts_starts_on_an_uncleared_slot(dv, g):
     s["state"][slot, 1] = float("inf")
     got, want = (sx.decay_attention_step(x["q"], x["k"], x["v"], x["g"], x["state"], slots=x["slots"]) for x in (s, e))
     assert torch.equal(got, want) and torch.equal(s["state"], e["state"])
+
+
+@pytest.mark.parametrize("type", [BF, F32])
+def test_what_large_tokens_leave_does_not_pass_between_them(type):
+    # The same with large tokens at both ends: what their roundings leave in a sum that is carried through the middle is
+    # known at neither end alone. The middle's spans start from sums of their own. (Of the middle, the tokens 512 and a
+    # span of 512 at most away from the large ones.)
+    t = 8300
+    s = make(b=1, t=t, h=260, dk=2, dv=2, type=type)
+    s["g"] = torch.full_like(s["g"], -0.05)
+    for part in (slice(0, t // 4), slice(3 * t // 4, t)):
+        s["v"][:, part] *= 1024
+        s["go"][:, part] *= 1024
+    middle = slice(t // 4 + 1024, 3 * t // 4 - 1024)
+    got = _backward(s, grad_state=False)[3]
+    ref, size = _oracle_vjp(s, grad_state=False), _oracle_vjp(s, grad_state=False, size=True)
+    mass = (np.abs(_np(s["q"])) * size[0]).sum(-1) + (np.abs(_np(s["k"])) * size[1]).sum(-1)
+    floor = 64.0 * mass[:, middle].max()
+    _close("grad_log_decay", got[:, middle], ref[3][:, middle], size[3][:, middle], _roundings(s), False, floor=floor)
