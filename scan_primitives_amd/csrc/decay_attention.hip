@@ -366,7 +366,7 @@ hipError_t launch_decay_attention(const DaParams& p, hipStream_t stream) {
   if (p.marches == 1) return launch(p, 0, 1, false, stream);
   // grad_v's march holds the state the other way round: the same launch where keys and values are of one
   // class, or where the device has room for all three marches at once (the larger class then costs less
-  // than a second launch: 333 tokens of 48 x 80 in f32, 28 us for the three, 44 in turn)
+  // than a second launch: 333 tokens of 48 x 80 in f32, 28 us for the three when this was chosen, 44 in turn; 25 now)
   const bool alike = march_tiles(p.dk) == march_tiles(p.dv) && march_waves(p.dk) == march_waves(p.dv);
   if (alike || 3 * int64_t(p.B) * p.H * p.segments <= device_cu_count()) return launch(p, 0, 3, false, stream);
   err = launch(p, 0, 2, false, stream);

@@ -19,15 +19,17 @@
 // the next chunk's arrive during the second half; x is read in the first alone.
 //
 // What bounds it (gfx950, 8192 tokens, 16 heads of 128 x 128 in bf16, one
-// workgroup of eight waves a compute unit): a chunk of 64 tokens takes 5.3 us;
-// of its about 10 800 cycles the matrix pipes are busy 3 100, the vector pipes
-// 4 200, LDS 3 000, and memory would take 6 000 at the rate of a copy. Two waves
-// a SIMD go through the same phases between the barriers and overlap these only
-// in part. Measured and not taken: two such workgroups a compute unit (128
-// registers a wave spill, and the loads ahead with them: 107 us for 97 at 512
-// heads of 512 tokens), four waves of 32 columns (spills as well), segments of
-// half the length (61 to 69 us, eight ragged rows of 2048 tokens, 16 heads of
-// 64 x 64: a workgroup's start costs as much as two chunks).
+// workgroup of eight waves a compute unit, 8 chunks each, 50.5 us): of a
+// chunk's share, 12 100 cycles of a busy compute unit, the matrix pipes take
+// 3 100, the vector pipes 4 600, LDS 5 400 (2 400 of them bank conflicts), and
+// memory would take 5 500 at the rate of a copy. Two waves a SIMD go through the
+// same phases between the barriers and overlap these only in part. Two such
+// workgroups do not fit a compute unit: 130 KB of LDS, 220 registers a wave.
+// Measured and not taken, in earlier forms: two smaller ones (128 registers a
+// wave spill, and the loads ahead with them: 107 us for 97 at 512 heads of 512
+// tokens), four waves of 32 columns (spills as well), segments of half the
+// length (61 to 69 us, eight ragged rows of 2048 tokens, 16 heads of 64 x 64: a
+// workgroup's start costs as much as two chunks).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -306,7 +308,7 @@ __device__ __forceinline__ const E* head_base(const HeadView& v, int b, int h) {
 // condition would have to be waited for where its lanes join the others again.) Rows of unit stride are
 // read in 16-byte pieces at any alignment, at 32-bit offsets from the tile's first token; where the last is
 // not whole (Cut), it is read up to the row's end and shifted into place, which other rows need not pay for
-// (the gradient of 4 x 4096 tokens of 8 heads of 128: 226.8 us, 232.5 as Cut). Else one element at a time.
+// (the gradient of 4 x 4096 tokens of 8 heads of 128 took 2.5% longer as Cut). Else one element at a time.
 enum class Rows { Elements, Cut, Whole };
 
 template <bool BF, int W, int THREADS, Rows R>
@@ -956,8 +958,8 @@ __device__ __forceinline__ void march(const DaParams& p, const DaMarch& m, int b
           for (int kt = 0; kt < NKT; ++kt)
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
-              // (not where a segment's own state is formed: it starts from zero, and this product cost 52 us for 44 in the
-              // gradient of 4 x 4096 tokens of 8 heads of 128)
+              // (not where a segment's own state is formed: it starts from zero, and this product cost 52 us for 44
+              // in the gradient of 4 x 4096 tokens of 8 heads of 128)
               if constexpr (OUT) st[kt][n] = decayed(st[kt][n], total);
               else st[kt][n] *= total;
             }

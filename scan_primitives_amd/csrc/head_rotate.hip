@@ -18,8 +18,8 @@
 // The angle is reduced in 64 bits: position times turns, its nearest whole
 // number taken off; 32 bits would lose the angle of far positions.
 //
-// Bound by memory: 4 x 4096 tokens of 16 + 16 heads of 128 in bf16 take 57.5 us,
-// 4.7 TB/s, what a copy of this size reaches; the gradient of 2 x 2048 tokens of
+// Bound by memory: 4 x 4096 tokens of 16 + 16 heads of 128 in bf16 take 59.0 us,
+// 4.6 TB/s, where a copy of this size reaches 4.8; the gradient of 2 x 2048 tokens of
 // 16 + 4 heads 19 us, 3.3 TB/s, of which the weights' sums over the workgroups
 // are 4.
 #include <hip/hip_runtime.h>
