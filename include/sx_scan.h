@@ -581,6 +581,243 @@ sx_status sx_head_norm_rotate_backward(sx_dtype dtype, const int64_t* q_shape, c
 /* Workspace bytes sx_head_norm_rotate_backward needs for the weights' gradients. */
 size_t sx_head_norm_rotate_backward_workspace_bytes(const int64_t* q_shape, const int64_t* k_shape);
 
+/* What an operator's result goes through: nothing, or u / (1 + exp(-u)). */
+typedef enum sx_activation { SX_ACT_NONE = 0, SX_ACT_SILU = 1 } sx_activation;
+
+/* Most taps of sx_causal_conv and most states a channel of sx_selective_scan. */
+#define SX_MAX_TAPS 8
+#define SX_MAX_STATES 32
+
+/*
+ * sx_causal_conv: a short causal convolution of each channel along the tokens,
+ *   u[t] = bias + sum over j of weight[j] x[t - (taps - 1) + j],  out[t] = act(u[t]),
+ * where the inputs before the first are `initial` (or zero). f32 sums, rounded to
+ * `dtype` once.
+ *
+ *  dtype         SX_F32 or SX_BF16: x, initial, out and final_state.
+ *  x             [B, T, D]: shape (3 entries), strides (NULL for contiguous; any
+ *                value) and data.
+ *  taps, weight  1..SX_MAX_TAPS (else SX_E_UNSUPPORTED), and f32, contiguous [D, taps].
+ *  bias          f32 [D], or NULL for zero.
+ *  initial       contiguous [B, taps - 1, D], oldest first, or NULL for zero.
+ *  lengths       int32 [B], or NULL. Tokens of row b from lengths[b] on do not
+ *                exist: they are not read, their rows of out are zero and the
+ *                state ends before them. Taken into [0, T].
+ *  activation    one of sx_activation.
+ *  out           contiguous [B, T, D], 16-byte aligned.
+ *  final_state   contiguous [B, taps - 1, D], 16-byte aligned: the last taps - 1
+ *                inputs, of `initial` too where there are fewer tokens; or NULL.
+ *
+ * No workspace. Outputs overlap no input and not each other (SX_E_ALIAS). Errors
+ * otherwise as sx_decay_attention.
+ */
+sx_status sx_causal_conv(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x, int64_t taps,
+                         const float* weight, const float* bias, const void* initial, const int32_t* lengths,
+                         sx_activation activation, void* out, void* final_state, void* stream);
+
+/*
+ * sx_causal_conv_backward: gradients of sx_causal_conv. With gu[t] = grad_out[t] act'(u[t]),
+ *   grad_x[s] = sum over j of weight[j] gu[s + (taps - 1) - j], and grad_state's row where x[s] is one of the last,
+ *   grad_weight[j] = sum over rows and tokens of gu[t] x[t - (taps - 1) + j],  grad_bias = sum of gu.
+ *
+ *  dtype .. activation   as for the forward call.
+ *  grad_out      [B, T, D], dtype `dtype`, with strides (NULL for contiguous).
+ *  grad_state    contiguous [B, taps - 1, D], dtype `dtype`: the gradient of
+ *                final_state, or NULL for none.
+ *  grad_x        contiguous [B, T, D], dtype `dtype`. Zero for tokens that do not exist.
+ *  grad_weight   f32, contiguous [D, taps].
+ *  grad_bias     f32 [D], or NULL where not wanted.
+ *  grad_initial  contiguous [B, taps - 1, D], dtype `dtype`, or NULL where not wanted.
+ *  workspace     at least sx_causal_conv_backward_workspace_bytes() bytes,
+ *                256-byte aligned; may hold anything.
+ *
+ * Summed in a fixed order (no atomics). Errors as sx_causal_conv.
+ */
+sx_status sx_causal_conv_backward(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x,
+                                  int64_t taps, const float* weight, const float* bias, const void* initial,
+                                  const int32_t* lengths, sx_activation activation, const int64_t* grad_out_strides,
+                                  const void* grad_out, const void* grad_state, void* grad_x, float* grad_weight,
+                                  float* grad_bias, void* grad_initial, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* Workspace bytes sx_causal_conv_backward needs, whatever the strides (0 for shapes it would reject). */
+size_t sx_causal_conv_backward_workspace_bytes(sx_dtype dtype, const int64_t* x_shape, int64_t taps);
+
+/*
+ * sx_causal_conv_step: one token of every request of a batch. The state of a
+ * request is its last taps - 1 inputs; they are read and moved up by one in place.
+ *
+ *  x             [B, D] with strides (NULL for contiguous).
+ *  pool, state_stride, state
+ *                dtype `dtype`, [pool, taps - 1, D]; each state contiguous,
+ *                `state_stride` elements from one to the next, none overlapping
+ *                (else SX_E_UNSUPPORTED).
+ *  slots         int32 [B]: the state of each row, or NULL (row b uses state b;
+ *                pool >= B then). A row whose slot lies outside [0, pool) is
+ *                idle: its row of out is zero and no state changes. Two rows with
+ *                the same slot race.
+ *  out           contiguous [B, D], 16-byte aligned.
+ *
+ * No workspace. Errors as sx_causal_conv.
+ */
+sx_status sx_causal_conv_step(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x,
+                              int64_t taps, const float* weight, const float* bias, sx_activation activation,
+                              int64_t pool, int64_t state_stride, void* state, const int32_t* slots, void* out,
+                              void* stream);
+
+/*
+ * sx_selective_scan: the scan of a selective state space. With N states h a
+ * channel from `initial` (or zero), for each token
+ *   dt = softplus(delta + delta_bias)   (delta + delta_bias where `softplus` is zero)
+ *   h[n] = exp(dt a[n]) h[n] + dt x b[n],   y = sum over n of c[n] h[n] + skip x,
+ *   out = y z / (1 + exp(-z))           (y where z is NULL).
+ * Steps, states and sums are f32 for f32 and bf16 operands alike; out is rounded
+ * to `dtype` once.
+ *
+ *  dtype         SX_F32 or SX_BF16: x, delta, b, c, z and out.
+ *  x, delta, z   [B, T, D] (x's shape), each with strides (NULL for contiguous; any
+ *                value). z and its strides may be NULL.
+ *  a             f32, contiguous [D, N], 1 <= N <= SX_MAX_STATES (else SX_E_UNSUPPORTED).
+ *  b, c          [B, T, G, N] (b's shape, 4 entries), each with strides; G divides
+ *                D, and channel d reads row d / (D / G).
+ *  skip, delta_bias  f32 [D], or NULL for zero.
+ *  initial       f32, contiguous [B, D, N], or NULL for zero.
+ *  lengths       int32 [B], or NULL. Tokens of row b from lengths[b] on do not
+ *                exist: they are not read, their rows of out are zero and the
+ *                state ends before them. Taken into [0, T].
+ *  out           contiguous [B, T, D], 16-byte aligned.
+ *  final_state   f32, contiguous [B, D, N], 16-byte aligned: the state after the
+ *                last token; or NULL.
+ *  workspace     at least sx_selective_scan_workspace_bytes() bytes, 256-byte
+ *                aligned; may hold anything; may be NULL when that is 0.
+ *
+ * An infinity or NaN of one token's x, delta or z stays in its channel, one of b
+ * or c in its group; of x, delta and b it reaches later tokens too, earlier ones
+ * never. Outputs overlap no input and not each other (SX_E_ALIAS). Errors
+ * otherwise as sx_decay_attention.
+ */
+sx_status sx_selective_scan(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x,
+                            const int64_t* delta_strides, const void* delta, const float* a, const int64_t* b_shape,
+                            const int64_t* b_strides, const void* b, const int64_t* c_strides, const void* c,
+                            const float* skip, const int64_t* z_strides, const void* z, const float* delta_bias,
+                            int softplus, const float* initial, const int32_t* lengths, void* out, float* final_state,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes sx_selective_scan needs (0 when none, or for shapes it would reject). */
+size_t sx_selective_scan_workspace_bytes(sx_dtype dtype, const int64_t* x_shape, const int64_t* b_shape);
+
+/*
+ * sx_selective_scan_backward: gradients of sx_selective_scan. With gy = grad_out
+ * z / (1 + exp(-z)) and lam the adjoint of h (grad_state after the last token),
+ *   lam = c gy + mu,  mu = exp(dt a) lam  (what is passed back),  q = mu h of the token before,
+ *   grad_c = sum over a group's channels of gy h,  grad_b = the same of dt x lam,
+ *   grad_a = sum over rows and tokens of dt q,  grad_x = dt sum over n of (lam b) + skip gy,
+ *   grad_delta = (sum over n of (a q) + x sum over n of (lam b)) softplus'(delta + delta_bias),
+ *   grad_z = grad_out y silu'(z),  grad_skip and grad_delta_bias sums of gy x and grad_delta.
+ *
+ *  dtype .. lengths  as for the forward call.
+ *  grad_out      [B, T, D], dtype `dtype`, with strides (NULL for contiguous).
+ *  grad_state    f32, contiguous [B, D, N]: the gradient of final_state, or NULL.
+ *  grad_x, grad_delta, grad_z  contiguous [B, T, D], dtype `dtype`; grad_z may be
+ *                NULL where z is.
+ *  grad_a        f32, contiguous [D, N].
+ *  grad_b, grad_c  contiguous [B, T, G, N], dtype `dtype`, summed in f32 and rounded once.
+ *  grad_skip, grad_delta_bias  f32 [D], or NULL where not wanted.
+ *  grad_initial  f32, contiguous [B, D, N], or NULL where not wanted.
+ *  workspace     at least sx_selective_scan_backward_workspace_bytes() bytes,
+ *                256-byte aligned; may hold anything. It holds the states of
+ *                every eighth token: 0.5 B T D N floats at N a power of two
+ *                from 4 on.
+ *
+ * Gradients of tokens that do not exist are zero. The outputs are 16-byte
+ * aligned and overlap nothing. Results do not change from call to call (no
+ * atomics). Errors as sx_selective_scan.
+ */
+sx_status sx_selective_scan_backward(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x,
+                                     const int64_t* delta_strides, const void* delta, const float* a,
+                                     const int64_t* b_shape, const int64_t* b_strides, const void* b,
+                                     const int64_t* c_strides, const void* c, const float* skip,
+                                     const int64_t* z_strides, const void* z, const float* delta_bias, int softplus,
+                                     const float* initial, const int32_t* lengths, const int64_t* grad_out_strides,
+                                     const void* grad_out, const float* grad_state, void* grad_x, void* grad_delta,
+                                     float* grad_a, void* grad_b, void* grad_c, float* grad_skip, void* grad_z,
+                                     float* grad_delta_bias, float* grad_initial, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* Workspace bytes sx_selective_scan_backward needs (0 for shapes it would reject). */
+size_t sx_selective_scan_backward_workspace_bytes(sx_dtype dtype, const int64_t* x_shape, const int64_t* b_shape);
+
+/*
+ * sx_selective_scan_step: one token of every request of a batch, the states
+ * updated in place.
+ *
+ *  x, delta, z   [B, D] (x's shape), b, c [B, G, N] (b's shape), each with strides.
+ *  a .. softplus  as for sx_selective_scan.
+ *  pool, state_stride, state
+ *                f32 [pool, D, N]; each state contiguous, `state_stride` elements
+ *                from one to the next, none overlapping (else SX_E_UNSUPPORTED).
+ *                On 16-byte borders throughout it is read and written in larger pieces.
+ *  slots         as for sx_causal_conv_step.
+ *  out           contiguous [B, D], 16-byte aligned.
+ *
+ * No workspace. Errors as sx_selective_scan.
+ */
+sx_status sx_selective_scan_step(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x,
+                                 const int64_t* delta_strides, const void* delta, const float* a,
+                                 const int64_t* b_shape, const int64_t* b_strides, const void* b,
+                                 const int64_t* c_strides, const void* c, const float* skip, const int64_t* z_strides,
+                                 const void* z, const float* delta_bias, int softplus, int64_t pool,
+                                 int64_t state_stride, float* state, const int32_t* slots, void* out, void* stream);
+
+/*
+ * sx_group_norm: the norm of groups of channels, channels last. Over the
+ * positions of a sample and the channels of a group,
+ *   u = (x - mean) / sqrt(variance + eps) weight + bias,  out = act(u).
+ * f32, the variance from differences to a mean; rounded to `dtype` once.
+ *
+ *  dtype         SX_F32 or SX_BF16: x and out.
+ *  x             [samples, positions, channels]: shape, strides (NULL for
+ *                contiguous; the channels next to each other, else SX_E_UNSUPPORTED)
+ *                and data.
+ *  groups        divides the channels.
+ *  weight, bias  f32 [channels], or NULL for ones and zeros.
+ *  out           contiguous, x's shape, 16-byte aligned.
+ *  workspace     at least sx_group_norm_workspace_bytes() bytes, 256-byte aligned;
+ *                may hold anything; may be NULL when that is 0.
+ *
+ * An infinity or NaN turns its sample's group to NaN and no other. Errors as
+ * sx_decay_attention.
+ */
+sx_status sx_group_norm(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x, int64_t groups,
+                        const float* weight, const float* bias, float eps, sx_activation activation, void* out,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes sx_group_norm needs (0 when none, or for shapes it would reject). */
+size_t sx_group_norm_workspace_bytes(sx_dtype dtype, const int64_t* x_shape, int64_t groups);
+
+/*
+ * sx_group_norm_backward: gradients of sx_group_norm. With n = (x - mean) r,
+ * r = 1 / sqrt(variance + eps) and gu = grad_out act'(u),
+ *   grad_weight = sum of gu n,  grad_bias = sum of gu,
+ *   grad_x = r (gu weight - mean(gu weight) - n mean(gu weight n)).
+ *
+ *  dtype .. activation   as for the forward call.
+ *  grad_out      x's shape, with strides as x has them.
+ *  grad_x        contiguous, x's shape, dtype `dtype`.
+ *  grad_weight, grad_bias  f32 [channels], or NULL where not wanted. Summed in a
+ *                fixed order (no atomics).
+ *  workspace     at least sx_group_norm_backward_workspace_bytes() bytes,
+ *                256-byte aligned; may hold anything.
+ */
+sx_status sx_group_norm_backward(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x,
+                                 int64_t groups, const float* weight, const float* bias, float eps,
+                                 sx_activation activation, const int64_t* grad_out_strides, const void* grad_out,
+                                 void* grad_x, float* grad_weight, float* grad_bias, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Workspace bytes sx_group_norm_backward needs (0 for shapes it would reject). */
+size_t sx_group_norm_backward_workspace_bytes(sx_dtype dtype, const int64_t* x_shape, int64_t groups);
+
 /* "E-DIM-001" etc. for a status; "OK" for SX_OK. Static storage. */
 const char* sx_status_name(sx_status status);
 

@@ -121,6 +121,36 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                                  _i64p, vp, vp, vp, c_f, c_int, vp, vp, vp, vp, vp, c_size, vp]
     lib.sx_head_norm_rotate_backward_workspace_bytes.restype = c_size
     lib.sx_head_norm_rotate_backward_workspace_bytes.argtypes = [_i64p, _i64p]
+    lib.sx_causal_conv.restype = c_int
+    lib.sx_causal_conv.argtypes = [c_int, *tensor, c_i64, vp, vp, vp, vp, c_int, vp, vp, vp]
+    lib.sx_causal_conv_backward.restype = c_int
+    lib.sx_causal_conv_backward.argtypes = [c_int, *tensor, c_i64, vp, vp, vp, vp, c_int, _i64p, vp, vp, vp, vp, vp, vp,
+                                            vp, c_size, vp]
+    lib.sx_causal_conv_backward_workspace_bytes.restype = c_size
+    lib.sx_causal_conv_backward_workspace_bytes.argtypes = [c_int, _i64p, c_i64]
+    lib.sx_causal_conv_step.restype = c_int
+    lib.sx_causal_conv_step.argtypes = [c_int, *tensor, c_i64, vp, vp, c_int, c_i64, c_i64, vp, vp, vp, vp]
+    view = [_i64p, vp]  # strides, data
+    scan = [c_int, *tensor, *view, vp, *tensor, *view, vp, *view, vp, c_int]
+    lib.sx_selective_scan.restype = c_int
+    lib.sx_selective_scan.argtypes = [*scan, vp, vp, vp, vp, vp, c_size, vp]
+    lib.sx_selective_scan_workspace_bytes.restype = c_size
+    lib.sx_selective_scan_workspace_bytes.argtypes = [c_int, _i64p, _i64p]
+    lib.sx_selective_scan_backward.restype = c_int
+    lib.sx_selective_scan_backward.argtypes = [*scan, vp, vp, *view, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, c_size,
+                                               vp]
+    lib.sx_selective_scan_backward_workspace_bytes.restype = c_size
+    lib.sx_selective_scan_backward_workspace_bytes.argtypes = [c_int, _i64p, _i64p]
+    lib.sx_selective_scan_step.restype = c_int
+    lib.sx_selective_scan_step.argtypes = [*scan, c_i64, c_i64, vp, vp, vp, vp]
+    lib.sx_group_norm.restype = c_int
+    lib.sx_group_norm.argtypes = [c_int, *tensor, c_i64, vp, vp, c_f, c_int, vp, vp, c_size, vp]
+    lib.sx_group_norm_workspace_bytes.restype = c_size
+    lib.sx_group_norm_workspace_bytes.argtypes = [c_int, _i64p, c_i64]
+    lib.sx_group_norm_backward.restype = c_int
+    lib.sx_group_norm_backward.argtypes = [c_int, *tensor, c_i64, vp, vp, c_f, c_int, *view, vp, vp, vp, vp, c_size, vp]
+    lib.sx_group_norm_backward_workspace_bytes.restype = c_size
+    lib.sx_group_norm_backward_workspace_bytes.argtypes = [c_int, _i64p, c_i64]
     lib.sx_matrix_scan_workspace_status.restype = c_int
     lib.sx_matrix_scan_workspace_status.argtypes = [vp, c_size, vp]
     lib.sx_set_lookback_spin_limit.restype = None
@@ -612,6 +642,9 @@ class _LongWay:
 
     decay_attention = decay_attention_backward = decay_attention_step = _none
     head_norm_rotate = head_norm_rotate_backward = _none
+    causal_conv = causal_conv_backward = causal_conv_step = _none
+    selective_scan = selective_scan_backward = selective_scan_step = _none
+    group_norm = group_norm_backward = _none
 
 
 _marshal = None
@@ -628,13 +661,17 @@ def _load_marshal():
         module = util.module_from_spec(util.spec_from_loader("_sx_marshal", loader))
         loader.exec_module(module)
     except ImportError as e:
-        warnings.warn(f"{MARSHAL_PATH} is not built or does not load ({e}): linear-attention calls cost more on the "
-                      "host; run `python -m scan_primitives_amd.build_lib`", RuntimeWarning, stacklevel=3)
+        warnings.warn(f"{MARSHAL_PATH} is not built or does not load ({e}): linear-attention and state-space calls cost "
+                      "more on the host; run `python -m scan_primitives_amd.build_lib`", RuntimeWarning, stacklevel=3)
         _marshal = _LongWay()
         return _marshal
     names = ("sx_decay_attention", "sx_decay_attention_workspace_bytes", "sx_decay_attention_backward",
              "sx_decay_attention_backward_workspace_bytes", "sx_decay_attention_step", "sx_head_norm_rotate",
-             "sx_head_norm_rotate_backward", "sx_head_norm_rotate_backward_workspace_bytes")
+             "sx_head_norm_rotate_backward", "sx_head_norm_rotate_backward_workspace_bytes", "sx_causal_conv",
+             "sx_causal_conv_backward", "sx_causal_conv_backward_workspace_bytes", "sx_causal_conv_step",
+             "sx_selective_scan", "sx_selective_scan_workspace_bytes", "sx_selective_scan_backward",
+             "sx_selective_scan_backward_workspace_bytes", "sx_selective_scan_step", "sx_group_norm",
+             "sx_group_norm_workspace_bytes", "sx_group_norm_backward", "sx_group_norm_backward_workspace_bytes")
     module.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
                 torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
     _marshal = module
@@ -1026,3 +1063,454 @@ class _HeadNormRotateFunction(torch.autograd.Function):
         gq, gk, gqw, gkw = head_norm_rotate_backward(q, k, positions, turns, grad_out_q, grad_out_k, q_weight=q_weight,
                                                      k_weight=k_weight, eps=ctx.eps, neighbours=ctx.neighbours)
         return gq, gk, None, None, gqw, gkw, None, None
+
+
+# ---------------------------------------------------------------- a layer on a selective state space
+
+_ACTIVATIONS = {None: 0, "silu": 1}
+
+
+def _activation(op: str, activation) -> int:
+    code = _ACTIVATIONS.get(activation) if activation is None or isinstance(activation, str) else None
+    if code is None:
+        raise SxError(SX_E_UNSUPPORTED, f"{op}: unknown activation {activation!r} (None or 'silu')")
+    return code
+
+
+def _require_state(op: str, state, dtype, shape) -> None:
+    """A pool of states that a step may write in place, each of them contiguous."""
+    if state.is_neg():
+        raise SxError(SX_E_UNSUPPORTED, f"{op}: state is a lazily negated view, which cannot be written in place")
+    if _records(state):
+        raise SxError(SX_E_UNSUPPORTED, f"{op}: state requires grad, and a step records none; detach it, or call the "
+                                        "step under torch.no_grad()")
+    if state.dim() != 3 or state.shape[1:] != shape:
+        raise SxError(SX_E_DIM_001, f"{op}: state is {tuple(state.shape)}, [states, {shape[0]}, {shape[1]}] is required")
+    _require(op, "state", state, dtype, None)
+    if state.numel() and not state[0].is_contiguous():
+        raise SxError(SX_E_UNSUPPORTED, f"{op}: each state must be contiguous (strides {tuple(state.stride())})")
+
+
+def _conv_operands(op, x, weight, bias, token_dims, more, optional):
+    """Checks what the C library cannot see; the dtype code, the device, and weight and bias as it takes them."""
+    index = _device_index(op, ("x", "weight", *(n for n, _ in more)), (x, weight, *(t for _, t in more)),
+                          (("bias", bias), *optional))
+    code = _require_dtype(op, ("x",), (x,))
+    if x.dim() != 2 + token_dims:
+        raise SxError(SX_E_DIM_001, f"{op}: x {tuple(x.shape)} must have {2 + token_dims} dims")
+    d = x.shape[-1]
+    if weight.dim() != 2 or weight.shape[0] != d:
+        raise SxError(SX_E_DIM_001, f"{op}: weight is {tuple(weight.shape)}, [{d}, taps] is required")
+    _require(op, "weight", weight, torch.float32, None)
+    _require(op, "bias", bias, torch.float32, (d,))
+    return code, index, weight.contiguous(), _contiguous(bias)
+
+
+def causal_conv(x: torch.Tensor, weight: torch.Tensor, bias=None, initial=None, lengths=None, activation=None,
+                return_state: bool = False):
+    """A short causal convolution of each channel along the tokens, on the GPU:
+    ``u[t] = bias + sum over j of weight[:, j] x[t - (taps - 1) + j]`` and ``out = u``, or ``u sigmoid(u)`` with
+    ``activation="silu"``.
+
+    ``x`` is ``[B, T, D]`` (f32 or bf16, any strides), ``weight`` f32 ``[D, taps]`` (1 to 8 taps, the last for the
+    token itself) and ``bias`` f32 ``[D]``. ``initial`` holds the ``taps - 1`` inputs before the first (x's dtype
+    ``[B, taps - 1, D]``, zeros when None); tokens of row b from ``lengths[b]`` (int32 ``[B]``) on do not exist.
+    Returns out ``[B, T, D]``, and the last ``taps - 1`` inputs too when ``return_state``. When autograd records, the
+    gradient runs through ``causal_conv_backward``.
+    """
+    got = (_marshal or _load_marshal()).causal_conv(x, weight, bias, initial, lengths, activation, return_state)
+    if got is not None:
+        return _done(got) if return_state else _done(got)[0]
+    _require_no_tangent(x, weight, bias, initial)
+    x, weight, bias, initial = _signed(x, weight, bias, initial)
+    if _records(x, weight, bias, initial):
+        out, state = _CausalConvFunction.apply(x, weight, bias, initial, lengths, activation, return_state)
+    else:
+        out, state = _causal_conv_forward(x, weight, bias, initial, lengths, activation, return_state)
+    return (out, state) if return_state else out
+
+
+def _causal_conv_forward(x, weight, bias, initial, lengths, activation, return_state):
+    op = "causal-conv"
+    act = _activation(op, activation)
+    code, index, weight, bias = _conv_operands(op, x, weight, bias, 1, (), (("initial", initial), ("lengths", lengths)))
+    b, _, d = x.shape
+    past = max(weight.shape[1] - 1, 0)
+    _require(op, "initial", initial, x.dtype, (b, past, d))
+    _require(op, "lengths", lengths, torch.int32, (b,))
+    initial, lengths = _contiguous(initial), _contiguous(lengths)
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    state = torch.empty((b, past, d), dtype=x.dtype, device=x.device) if return_state else None
+    _enqueue(index, load_library().sx_causal_conv, code, *_args(x), weight.shape[1], weight.data_ptr(), _ptr(bias),
+             _ptr(initial), _ptr(lengths), act, out.data_ptr(), _ptr(state))
+    return out, state
+
+
+@functools.lru_cache(maxsize=1024)
+def _conv_workspace_bytes(code, x_shape, taps):
+    return load_library().sx_causal_conv_backward_workspace_bytes(code, _i64(x_shape), taps)
+
+
+def causal_conv_backward(x, weight, grad_out, bias=None, initial=None, lengths=None, activation=None, grad_state=None):
+    """Gradients ``(grad_x, grad_weight, grad_bias, grad_initial)`` of a loss through
+    ``causal_conv(x, weight, bias, initial, lengths, activation)``.
+
+    ``grad_out`` is the loss's gradient with respect to out (its shape, x's dtype), ``grad_state`` the one with
+    respect to the last state (x's dtype, or None). Each gradient has its operand's shape and dtype; a bias that is
+    None has None; ``grad_initial`` is the gradient of the inputs before the first, also when those were zero.
+    """
+    got = (_marshal or _load_marshal()).causal_conv_backward(x, weight, grad_out, bias, initial, lengths, activation,
+                                                             grad_state)
+    if got is not None:
+        return _done(got)
+    _require_no_tangent(x, weight, grad_out, bias, initial, grad_state)
+    x, weight, grad_out, bias, initial, grad_state = _signed(x, weight, grad_out, bias, initial, grad_state)
+    op = "causal-conv gradient"
+    act = _activation(op, activation)
+    code, index, weight, bias = _conv_operands(
+        op, x, weight, bias, 1, (("grad_out", grad_out),),
+        (("initial", initial), ("lengths", lengths), ("grad_state", grad_state)))
+    b, _, d = x.shape
+    taps = weight.shape[1]
+    past = (b, max(taps - 1, 0), d)
+    _require(op, "initial", initial, x.dtype, past)
+    _require(op, "lengths", lengths, torch.int32, (b,))
+    _require(op, "grad_out", grad_out, x.dtype, x.shape)
+    _require(op, "grad_state", grad_state, x.dtype, past)
+    initial, lengths, grad_state = _contiguous(initial), _contiguous(lengths), _contiguous(grad_state)
+    dev = x.device
+    gx, gi = torch.empty(x.shape, dtype=x.dtype, device=dev), torch.empty(past, dtype=x.dtype, device=dev)
+    gw = torch.empty(weight.shape, dtype=torch.float32, device=dev)
+    gb = None if bias is None else torch.empty(bias.shape, dtype=torch.float32, device=dev)
+    nbytes = _conv_workspace_bytes(code, x.shape, taps)
+    ws = _workspace(nbytes, dev)
+    _enqueue(index, load_library().sx_causal_conv_backward, code, *_args(x), taps, weight.data_ptr(), _ptr(bias),
+             _ptr(initial), _ptr(lengths), act, _i64(grad_out.stride()), grad_out.data_ptr(), _ptr(grad_state),
+             gx.data_ptr(), gw.data_ptr(), _ptr(gb), gi.data_ptr(), _ptr(ws), nbytes)
+    return gx, gw, gb, gi
+
+
+class _CausalConvFunction(torch.autograd.Function):
+    """causal_conv with its gradient from the library: saves the inputs."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, initial, lengths, activation, return_state):
+        out, state = _causal_conv_forward(x, weight, bias, initial, lengths, activation, return_state)
+        ctx.save_for_backward(x, weight, bias, initial, lengths)
+        ctx.activation = activation
+        ctx.set_materialize_grads(False)
+        return out, state
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_out, grad_state):
+        x, weight, bias, initial, lengths = ctx.saved_tensors
+        if grad_out is None:
+            grad_out = torch.zeros((1, 1, 1), dtype=x.dtype, device=x.device).expand(x.shape)
+        gx, gw, gb, gi = causal_conv_backward(x, weight, grad_out, bias=bias, initial=initial, lengths=lengths,
+                                              activation=ctx.activation, grad_state=grad_state)
+        return gx, gw, gb, gi if initial is not None else None, None, None, None
+
+
+def causal_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, bias=None, slots=None,
+                     activation=None) -> torch.Tensor:
+    """One token of every request of a batch through ``causal_conv``.
+
+    ``x`` is ``[B, D]``; ``state`` (x's dtype ``[pool, taps - 1, D]``, each request's last inputs) is updated in
+    place; row b uses state ``slots[b]`` (int32 ``[B]``; state b when None). A row whose slot lies outside the pool is
+    idle: zero out, no state changed; two rows of one slot race. Returns out ``[B, D]``. No gradient is recorded, so
+    a ``state`` that autograd records is refused; one that it has saved is marked as modified in place.
+    """
+    got = (_marshal or _load_marshal()).causal_conv_step(x, weight, state, bias, slots, activation)
+    if got is not None:
+        return _done(got)[0]
+    _require_no_tangent(x, weight, state, bias)
+    x, weight, bias = _signed(x, weight, bias)
+    op = "causal-conv step"
+    act = _activation(op, activation)
+    code, index, weight, bias = _conv_operands(op, x, weight, bias, 0, (("state", state),), (("slots", slots),))
+    b, d = x.shape
+    _require_state(op, state, x.dtype, (max(weight.shape[1] - 1, 0), d))
+    _require(op, "slots", slots, torch.int32, (b,))
+    slots = _contiguous(slots)
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _enqueue(index, load_library().sx_causal_conv_step, code, *_args(x), weight.shape[1], weight.data_ptr(), _ptr(bias),
+             act, state.shape[0], state.stride(0), state.data_ptr(), _ptr(slots), out.data_ptr())
+    torch.autograd.graph.increment_version(state)
+    return out
+
+
+def _scan_operands(op, x, delta, a, b, c, skip, z, delta_bias, token_dims, more, optional):
+    """Checks what the C library cannot see; the dtype code, the device, and a, skip and delta_bias as it takes them."""
+    index = _device_index(op, ("x", "delta", "a", "b", "c", *(n for n, _ in more)),
+                          (x, delta, a, b, c, *(t for _, t in more)),
+                          (("skip", skip), ("z", z), ("delta_bias", delta_bias), *optional))
+    code = _require_dtype(op, ("x", "delta", "b", "c"), (x, delta, b, c))
+    for name, t, rank in (("x", x, 2 + token_dims), ("b", b, 3 + token_dims)):
+        if t.dim() != rank:
+            raise SxError(SX_E_DIM_001, f"{op}: {name} {tuple(t.shape)} must have {rank} dims")
+    d, n = x.shape[-1], b.shape[-1]
+    _require(op, "delta", delta, x.dtype, x.shape)
+    _require(op, "z", z, x.dtype, x.shape)
+    _require(op, "c", c, x.dtype, b.shape)
+    _require(op, "a", a, torch.float32, (d, n))
+    _require(op, "skip", skip, torch.float32, (d,))
+    _require(op, "delta_bias", delta_bias, torch.float32, (d,))
+    return code, index, a.contiguous(), _contiguous(skip), _contiguous(delta_bias)
+
+
+def _scan_args(x, delta, a, b, c, skip, z, delta_bias, softplus):
+    """The operands in the C entries' order."""
+    return (*_args(x), *_args(delta)[1:], a.data_ptr(), *_args(b), *_args(c)[1:], _ptr(skip),
+            *((None, None) if z is None else _args(z)[1:]), _ptr(delta_bias), 1 if softplus else 0)
+
+
+@functools.lru_cache(maxsize=1024)
+def _scan_workspace_bytes(code, x_shape, b_shape):
+    return load_library().sx_selective_scan_workspace_bytes(code, _i64(x_shape), _i64(b_shape))
+
+
+@functools.lru_cache(maxsize=1024)
+def _scan_backward_workspace_bytes(code, x_shape, b_shape):
+    return load_library().sx_selective_scan_backward_workspace_bytes(code, _i64(x_shape), _i64(b_shape))
+
+
+def selective_scan(x: torch.Tensor, delta: torch.Tensor, a: torch.Tensor, b: torch.Tensor, c: torch.Tensor, skip=None,
+                   z=None, delta_bias=None, softplus: bool = True, initial=None, lengths=None,
+                   return_state: bool = False):
+    """The scan of a selective state space, on the GPU. For each token, with N states a channel,
+    ``dt = softplus(delta + delta_bias)``, ``h = exp(dt a) h + dt x b``, ``y = c . h + skip x`` and
+    ``out = y z sigmoid(z)`` (y when z is None).
+
+    ``x``, ``delta`` and ``z`` are ``[B, T, D]``, ``b`` and ``c`` ``[B, T, G, N]`` (G divides D; D / G channels share a
+    row; N up to 32), all of one dtype (f32 or bf16) and any strides; ``a`` is f32 ``[D, N]``, ``skip`` and
+    ``delta_bias`` f32 ``[D]``. ``softplus=False`` takes ``delta + delta_bias`` as the step. ``initial`` is the state
+    before the first token (f32 ``[B, D, N]``, zero when None); tokens of row b from ``lengths[b]`` (int32 ``[B]``) on
+    do not exist. Returns out ``[B, T, D]``, and the last state too when ``return_state``. When autograd records, the
+    gradient runs through ``selective_scan_backward``.
+    """
+    got = (_marshal or _load_marshal()).selective_scan(x, delta, a, b, c, skip, z, delta_bias, softplus, initial,
+                                                       lengths, return_state)
+    if got is not None:
+        return _done(got) if return_state else _done(got)[0]
+    _require_no_tangent(x, delta, a, b, c, skip, z, delta_bias, initial)
+    x, delta, a, b, c, skip, z, delta_bias, initial = _signed(x, delta, a, b, c, skip, z, delta_bias, initial)
+    if _records(x, delta, a, b, c, skip, z, delta_bias, initial):
+        out, state = _SelectiveScanFunction.apply(x, delta, a, b, c, skip, z, delta_bias, softplus, initial, lengths,
+                                                  return_state)
+    else:
+        out, state = _selective_scan_forward(x, delta, a, b, c, skip, z, delta_bias, softplus, initial, lengths,
+                                             return_state)
+    return (out, state) if return_state else out
+
+
+def _selective_scan_forward(x, delta, a, b, c, skip, z, delta_bias, softplus, initial, lengths, return_state):
+    op = "selective-scan"
+    code, index, a, skip, delta_bias = _scan_operands(op, x, delta, a, b, c, skip, z, delta_bias, 1, (),
+                                                      (("initial", initial), ("lengths", lengths)))
+    state_shape = (x.shape[0], x.shape[2], b.shape[3])
+    _require(op, "initial", initial, torch.float32, state_shape)
+    _require(op, "lengths", lengths, torch.int32, (x.shape[0],))
+    initial, lengths = _contiguous(initial), _contiguous(lengths)
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    state = torch.empty(state_shape, dtype=torch.float32, device=x.device) if return_state else None
+    nbytes = _scan_workspace_bytes(code, x.shape, b.shape)
+    ws = _workspace(nbytes, x.device)
+    _enqueue(index, load_library().sx_selective_scan, code,
+             *_scan_args(x, delta, a, b, c, skip, z, delta_bias, softplus), _ptr(initial), _ptr(lengths),
+             out.data_ptr(), _ptr(state), _ptr(ws), nbytes)
+    return out, state
+
+
+def selective_scan_backward(x, delta, a, b, c, grad_out, skip=None, z=None, delta_bias=None, softplus: bool = True,
+                            initial=None, lengths=None, grad_state=None):
+    """Gradients ``(grad_x, grad_delta, grad_a, grad_b, grad_c, grad_skip, grad_z, grad_delta_bias, grad_initial)`` of
+    a loss through ``selective_scan(x, delta, a, b, c, skip, z, delta_bias, softplus, initial, lengths)``.
+
+    ``grad_out`` is the loss's gradient with respect to out (its shape, x's dtype), ``grad_state`` the one with
+    respect to the last state (f32, or None). Each gradient has its operand's shape and dtype; those of a skip, z or
+    delta_bias that is None are None; ``grad_initial`` is the gradient of the state before the first token, also when
+    that was zero.
+    """
+    got = (_marshal or _load_marshal()).selective_scan_backward(x, delta, a, b, c, grad_out, skip, z, delta_bias,
+                                                                softplus, initial, lengths, grad_state)
+    if got is not None:
+        return _done(got)
+    _require_no_tangent(x, delta, a, b, c, grad_out, skip, z, delta_bias, initial, grad_state)
+    x, delta, a, b, c, grad_out, skip, z, delta_bias, initial, grad_state = _signed(
+        x, delta, a, b, c, grad_out, skip, z, delta_bias, initial, grad_state)
+    op = "selective-scan gradient"
+    code, index, a, skip, delta_bias = _scan_operands(
+        op, x, delta, a, b, c, skip, z, delta_bias, 1, (("grad_out", grad_out),),
+        (("initial", initial), ("lengths", lengths), ("grad_state", grad_state)))
+    state_shape = (x.shape[0], x.shape[2], b.shape[3])
+    _require(op, "initial", initial, torch.float32, state_shape)
+    _require(op, "lengths", lengths, torch.int32, (x.shape[0],))
+    _require(op, "grad_out", grad_out, x.dtype, x.shape)
+    _require(op, "grad_state", grad_state, torch.float32, state_shape)
+    initial, lengths, grad_state = _contiguous(initial), _contiguous(lengths), _contiguous(grad_state)
+    empty = lambda like: None if like is None else torch.empty(like.shape, dtype=like.dtype, device=x.device)  # noqa: E731
+    gx, gdelta, ga, gb, gc, gskip, gz, gbias = (empty(t) for t in (x, delta, a, b, c, skip, z, delta_bias))
+    gi = torch.empty(state_shape, dtype=torch.float32, device=x.device)
+    nbytes = _scan_backward_workspace_bytes(code, x.shape, b.shape)
+    ws = _workspace(nbytes, x.device)
+    _enqueue(index, load_library().sx_selective_scan_backward, code,
+             *_scan_args(x, delta, a, b, c, skip, z, delta_bias, softplus), _ptr(initial), _ptr(lengths),
+             _i64(grad_out.stride()), grad_out.data_ptr(), _ptr(grad_state), gx.data_ptr(), gdelta.data_ptr(),
+             ga.data_ptr(), gb.data_ptr(), gc.data_ptr(), _ptr(gskip), _ptr(gz), _ptr(gbias), gi.data_ptr(), _ptr(ws),
+             nbytes)
+    return gx, gdelta, ga, gb, gc, gskip, gz, gbias, gi
+
+
+class _SelectiveScanFunction(torch.autograd.Function):
+    """selective_scan with its gradient from the library: saves the inputs."""
+
+    @staticmethod
+    def forward(ctx, x, delta, a, b, c, skip, z, delta_bias, softplus, initial, lengths, return_state):
+        out, state = _selective_scan_forward(x, delta, a, b, c, skip, z, delta_bias, softplus, initial, lengths,
+                                             return_state)
+        ctx.save_for_backward(x, delta, a, b, c, skip, z, delta_bias, initial, lengths)
+        ctx.softplus = softplus
+        ctx.set_materialize_grads(False)
+        return out, state
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_out, grad_state):
+        x, delta, a, b, c, skip, z, delta_bias, initial, lengths = ctx.saved_tensors
+        if grad_out is None:
+            grad_out = torch.zeros((1, 1, 1), dtype=x.dtype, device=x.device).expand(x.shape)
+        gx, gdelta, ga, gb, gc, gskip, gz, gbias, gi = selective_scan_backward(
+            x, delta, a, b, c, grad_out, skip=skip, z=z, delta_bias=delta_bias, softplus=ctx.softplus, initial=initial,
+            lengths=lengths, grad_state=grad_state)
+        return gx, gdelta, ga, gb, gc, gskip, gz, gbias, None, gi if initial is not None else None, None, None
+
+
+def selective_scan_step(x: torch.Tensor, delta: torch.Tensor, a: torch.Tensor, b: torch.Tensor, c: torch.Tensor,
+                        state: torch.Tensor, slots=None, skip=None, z=None, delta_bias=None,
+                        softplus: bool = True) -> torch.Tensor:
+    """One token of every request of a batch through ``selective_scan``.
+
+    ``x``, ``delta`` and ``z`` are ``[B, D]``, ``b`` and ``c`` ``[B, G, N]``. ``state`` (f32 ``[pool, D, N]``) is updated
+    in place; row b uses state ``slots[b]`` (int32 ``[B]``; state b when None). A row whose slot lies outside the pool
+    is idle: zero out, no state changed; two rows of one slot race. Returns out ``[B, D]``. No gradient is recorded,
+    so a ``state`` that autograd records is refused; one that it has saved is marked as modified in place.
+    """
+    got = (_marshal or _load_marshal()).selective_scan_step(x, delta, a, b, c, state, slots, skip, z, delta_bias,
+                                                            softplus)
+    if got is not None:
+        return _done(got)[0]
+    _require_no_tangent(x, delta, a, b, c, state, skip, z, delta_bias)
+    x, delta, a, b, c, skip, z, delta_bias = _signed(x, delta, a, b, c, skip, z, delta_bias)
+    op = "selective-scan step"
+    code, index, a, skip, delta_bias = _scan_operands(op, x, delta, a, b, c, skip, z, delta_bias, 0,
+                                                      (("state", state),), (("slots", slots),))
+    _require_state(op, state, torch.float32, (x.shape[1], b.shape[2]))
+    _require(op, "slots", slots, torch.int32, (x.shape[0],))
+    slots = _contiguous(slots)
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _enqueue(index, load_library().sx_selective_scan_step, code,
+             *_scan_args(x, delta, a, b, c, skip, z, delta_bias, softplus), state.shape[0], state.stride(0),
+             state.data_ptr(), _ptr(slots), out.data_ptr())
+    torch.autograd.graph.increment_version(state)
+    return out
+
+
+def _positions(t: torch.Tensor) -> torch.Tensor:
+    """[N, ..., C] as [N, positions, C] with channels next to each other: a view where the strides allow it."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        t = t.contiguous()
+    return t[:, None] if t.dim() == 2 else t.reshape(t.shape[0], -1 if t.numel() else math.prod(t.shape[1:-1]),
+                                                     t.shape[-1])
+
+
+def _norm_operands(op, x, weight, bias, more=()):
+    index = _device_index(op, ("x", *(n for n, _ in more)), (x, *(t for _, t in more)),
+                          (("weight", weight), ("bias", bias)))
+    code = _require_dtype(op, ("x",), (x,))
+    if x.dim() < 2:
+        raise SxError(SX_E_DIM_001, f"{op}: x {tuple(x.shape)} must be [samples, ..., channels]")
+    c = x.shape[-1]
+    _require(op, "weight", weight, torch.float32, (c,))
+    _require(op, "bias", bias, torch.float32, (c,))
+    return code, index, _contiguous(weight), _contiguous(bias)
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace_bytes(code, shape, groups, gradient):
+    lib = load_library()
+    entry = lib.sx_group_norm_backward_workspace_bytes if gradient else lib.sx_group_norm_workspace_bytes
+    return entry(code, _i64(shape), groups)
+
+
+def group_norm(x: torch.Tensor, groups: int, weight=None, bias=None, eps: float = 1e-5, activation=None) -> torch.Tensor:
+    """The norm of ``groups`` groups of channels, channels last, on the GPU: over a sample's positions and a group's
+    channels, ``u = (x - mean) / sqrt(variance + eps) weight + bias`` and ``out = u``, or ``u sigmoid(u)`` with
+    ``activation="silu"``.
+
+    ``x`` is ``[N, ..., C]`` (f32 or bf16); ``[N, C]`` norms every row on its own. ``weight`` and ``bias`` are f32
+    ``[C]`` (ones and zeros when None). Returns a contiguous result of x's shape and dtype. When autograd records, the
+    gradient runs through ``group_norm_backward``.
+    """
+    got = (_marshal or _load_marshal()).group_norm(x, groups, weight, bias, eps, activation)
+    if got is not None:
+        return _done(got)[0]
+    _require_no_tangent(x, weight, bias)
+    x, weight, bias = _signed(x, weight, bias)
+    if _records(x, weight, bias):
+        return _GroupNormFunction.apply(x, groups, weight, bias, eps, activation)
+    return _group_norm_forward(x, groups, weight, bias, eps, activation)
+
+
+def _group_norm_forward(x, groups, weight, bias, eps, activation):
+    op = "group-norm"
+    act = _activation(op, activation)
+    code, index, weight, bias = _norm_operands(op, x, weight, bias)
+    v = _positions(x)
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    nbytes = _norm_workspace_bytes(code, v.shape, groups, False)
+    ws = _workspace(nbytes, x.device)
+    _enqueue(index, load_library().sx_group_norm, code, *_args(v), groups, _ptr(weight), _ptr(bias), float(eps), act,
+             out.data_ptr(), _ptr(ws), nbytes)
+    return out
+
+
+def group_norm_backward(x, groups: int, grad_out, weight=None, bias=None, eps: float = 1e-5, activation=None):
+    """Gradients ``(grad_x, grad_weight, grad_bias)`` of a loss through
+    ``group_norm(x, groups, weight, bias, eps, activation)``, given its gradient with respect to the result (x's shape
+    and dtype). A weight or bias that is None has None for its gradient."""
+    got = (_marshal or _load_marshal()).group_norm_backward(x, groups, grad_out, weight, bias, eps, activation)
+    if got is not None:
+        return _done(got)
+    _require_no_tangent(x, grad_out, weight, bias)
+    x, grad_out, weight, bias = _signed(x, grad_out, weight, bias)
+    op = "group-norm gradient"
+    act = _activation(op, activation)
+    code, index, weight, bias = _norm_operands(op, x, weight, bias, (("grad_out", grad_out),))
+    _require(op, "grad_out", grad_out, x.dtype, x.shape)
+    v, g = _positions(x), _positions(grad_out)
+    gx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    gw, gb = (None if w is None else torch.empty(w.shape, dtype=w.dtype, device=x.device) for w in (weight, bias))
+    nbytes = _norm_workspace_bytes(code, v.shape, groups, True)
+    ws = _workspace(nbytes, x.device)
+    _enqueue(index, load_library().sx_group_norm_backward, code, *_args(v), groups, _ptr(weight), _ptr(bias),
+             float(eps), act, _i64(g.stride()), g.data_ptr(), gx.data_ptr(), _ptr(gw), _ptr(gb), _ptr(ws), nbytes)
+    return gx, gw, gb
+
+
+class _GroupNormFunction(torch.autograd.Function):
+    """group_norm with its gradient from the library: saves the inputs."""
+
+    @staticmethod
+    def forward(ctx, x, groups, weight, bias, eps, activation):
+        ctx.save_for_backward(x, weight, bias)
+        ctx.args = (groups, eps, activation)
+        return _group_norm_forward(x, groups, weight, bias, eps, activation)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_out):
+        x, weight, bias = ctx.saved_tensors
+        groups, eps, activation = ctx.args
+        gx, gw, gb = group_norm_backward(x, groups, grad_out, weight=weight, bias=bias, eps=eps, activation=activation)
+        return gx, None, gw, gb, None, None

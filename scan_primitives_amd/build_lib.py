@@ -24,7 +24,8 @@ MARSHAL_PATH = os.path.join(HERE, "_sx_marshal.so")
 SOURCES = ["sx_api.cpp", "element_scan.hip", "normcap_quad.hip", "matrix_scan.hip", "matrix_scan_grad.hip",
            "table_scan.hip", "decay_attention.hip", "decay_march_bf16.hip", "decay_march_bf16_cut.hip",
            "decay_march_bf16_any.hip", "decay_march_f32.hip", "decay_march_f32_cut.hip", "decay_march_f32_any.hip",
-           "head_rotate.hip"]
+           "head_rotate.hip", "causal_conv.hip", "selective_scan.hip", "selective_scan_grad.hip", "group_norm.hip",
+           "sum_rows.hip"]
 ARCH = "gfx950"
 
 # Packed FP32 (v_pk_*_f32) stays off for all device code: the kernels are

@@ -1,5 +1,5 @@
-// py_marshal.cpp: the short way from Python to the linear-attention entry points
-// of libsx_scan.so, for calls whose time is that of getting to the GPU.
+// py_marshal.cpp: the short way from Python to the linear-attention and state-space
+// entry points of libsx_scan.so, for calls whose time is that of getting to the GPU.
 //
 // Each function takes what the binding's function of the same name takes, in
 // order. Where every tensor is a plain one on the current device, of the expected
@@ -28,7 +28,21 @@ struct Entries {
   decltype(&sx_head_norm_rotate) head_norm_rotate;
   decltype(&sx_head_norm_rotate_backward) head_norm_rotate_backward;
   decltype(&sx_head_norm_rotate_backward_workspace_bytes) head_norm_rotate_backward_bytes;
+  decltype(&sx_causal_conv) causal_conv;
+  decltype(&sx_causal_conv_backward) causal_conv_backward;
+  decltype(&sx_causal_conv_backward_workspace_bytes) causal_conv_backward_bytes;
+  decltype(&sx_causal_conv_step) causal_conv_step;
+  decltype(&sx_selective_scan) selective_scan;
+  decltype(&sx_selective_scan_workspace_bytes) selective_scan_bytes;
+  decltype(&sx_selective_scan_backward) selective_scan_backward;
+  decltype(&sx_selective_scan_backward_workspace_bytes) selective_scan_backward_bytes;
+  decltype(&sx_selective_scan_step) selective_scan_step;
+  decltype(&sx_group_norm) group_norm;
+  decltype(&sx_group_norm_workspace_bytes) group_norm_bytes;
+  decltype(&sx_group_norm_backward) group_norm_backward;
+  decltype(&sx_group_norm_backward_workspace_bytes) group_norm_backward_bytes;
 } lib;
+constexpr int kEntries = 21;
 PyObject* current_device = nullptr;
 PyObject* raw_stream = nullptr;
 
@@ -287,14 +301,293 @@ PyObject* head_norm_rotate_backward(PyObject* const* a, Py_ssize_t n) {
       xq, xk, wq, wk);
 }
 
-// (addresses of the eight entries, torch's current device, its raw stream of a device)
+struct ConvCall {
+  const at::Tensor *x, *w;
+  const float* bias;
+  sx_dtype code;
+  int64_t d, taps;
+  sx_activation act;
+};
+
+// None or "silu"
+bool activation(PyObject* o, sx_activation* act) {
+  if (o == Py_None) return *act = SX_ACT_NONE, true;
+  if (!PyUnicode_CheckExact(o) || PyUnicode_CompareWithASCIIString(o, "silu") != 0) return false;
+  return *act = SX_ACT_SILU, true;
+}
+
+bool conv_args(Call& c, PyObject* x, PyObject* w, PyObject* bias, PyObject* act, int64_t rank, ConvCall* a) {
+  a->x = c.take(x);
+  if (!c.fit || a->x->dim() != rank || !float_type(*a->x, &a->code) || !activation(act, &a->act)) return false;
+  a->d = a->x->size(-1);
+  a->w = c.take(w, at::kFloat, 2);
+  if (!c.fit || a->w->size(0) != a->d || !a->w->is_contiguous()) return false;
+  a->taps = a->w->size(1);
+  a->bias = static_cast<const float*>(c.optional(bias, at::kFloat, {a->d}));
+  return c.fit && a->taps > 0;
+}
+const float* floats(const at::Tensor* t) { return static_cast<const float*>(t->data_ptr()); }
+
+// (x, weight, bias, initial, lengths, activation, return_state)
+PyObject* causal_conv(PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  ConvCall v;
+  if (n != 7 || (a[6] != Py_True && a[6] != Py_False) || !conv_args(c, a[0], a[1], a[2], a[5], 3, &v))
+    return the_long_way();
+  const int64_t b = v.x->size(0);
+  const void* initial = c.optional(a[3], v.x->scalar_type(), {b, v.taps - 1, v.d});
+  const void* lengths = c.optional(a[4], at::kInt, {b});
+  if (!c.here()) return the_long_way();
+  const at::Tensor out = at::empty(v.x->sizes(), v.x->options());
+  const at::Tensor state = a[6] == Py_True ? at::empty({b, v.taps - 1, v.d}, v.x->options()) : at::Tensor();
+  return answer(lib.causal_conv(v.code, v.x->sizes().data(), v.x->strides().data(), v.x->data_ptr(), v.taps,
+                                floats(v.w), v.bias, initial, static_cast<const int32_t*>(lengths), v.act,
+                                out.data_ptr(), data(state), c.stream()),
+                out, state);
+}
+
+// (x, weight, grad_out, bias, initial, lengths, activation, grad_state)
+PyObject* causal_conv_backward(PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  ConvCall v;
+  if (n != 8 || !conv_args(c, a[0], a[1], a[3], a[6], 3, &v)) return the_long_way();
+  const int64_t b = v.x->size(0);
+  const at::Tensor* go = c.take(a[2], v.x->scalar_type(), 3);
+  const void* initial = c.optional(a[4], v.x->scalar_type(), {b, v.taps - 1, v.d});
+  const void* lengths = c.optional(a[5], at::kInt, {b});
+  const void* gs = c.optional(a[7], v.x->scalar_type(), {b, v.taps - 1, v.d});
+  if (!c.here() || go->sizes() != v.x->sizes()) return the_long_way();
+  const at::Tensor gx = at::empty(v.x->sizes(), v.x->options()), gw = at::empty(v.w->sizes(), v.w->options()),
+                   gb = v.bias ? at::empty({v.d}, v.w->options()) : at::Tensor(),
+                   gi = at::empty({b, v.taps - 1, v.d}, v.x->options());
+  const size_t bytes = lib.causal_conv_backward_bytes(v.code, v.x->sizes().data(), v.taps);
+  const at::Tensor ws = workspace(bytes, *v.x);
+  return answer(lib.causal_conv_backward(v.code, v.x->sizes().data(), v.x->strides().data(), v.x->data_ptr(), v.taps,
+                                         floats(v.w), v.bias, initial, static_cast<const int32_t*>(lengths), v.act,
+                                         go->strides().data(), go->data_ptr(), gs, gx.data_ptr(),
+                                         static_cast<float*>(gw.data_ptr()), static_cast<float*>(data(gb)),
+                                         gi.data_ptr(), data(ws), bytes, c.stream()),
+                gx, gw, gb, gi);
+}
+
+// A pool of contiguous states [pool, rows, cols].
+const at::Tensor* pool_arg(Call& c, PyObject* o, at::ScalarType type, int64_t rows, int64_t cols) {
+  const at::Tensor* t = c.take(o, type, 3);
+  if (!t || t->size(1) != rows || t->size(2) != cols || (cols > 1 && t->stride(2) != 1) ||
+      (rows > 1 && t->stride(1) != cols))
+    return c.fit = false, nullptr;
+  return t;
+}
+// autograd tells by the version that a state it saved has been written to (a state of inference mode has none)
+void written(sx_status st, const at::Tensor* state) {
+  if (st == SX_OK && !state->is_inference()) state->unsafeGetTensorImpl()->bump_version();
+}
+
+// (x, weight, state, bias, slots, activation)
+PyObject* causal_conv_step(PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  ConvCall v;
+  if (n != 6 || !conv_args(c, a[0], a[1], a[3], a[5], 2, &v)) return the_long_way();
+  const at::Tensor* state = pool_arg(c, a[2], v.x->scalar_type(), v.taps - 1, v.d);
+  const void* slots = c.optional(a[4], at::kInt, {v.x->size(0)});
+  if (!c.here()) return the_long_way();
+  const at::Tensor out = at::empty(v.x->sizes(), v.x->options());
+  const sx_status st = lib.causal_conv_step(v.code, v.x->sizes().data(), v.x->strides().data(), v.x->data_ptr(), v.taps,
+                                            floats(v.w), v.bias, v.act, state->size(0), state->stride(0),
+                                            state->data_ptr(), static_cast<const int32_t*>(slots), out.data_ptr(),
+                                            c.stream());
+  written(st, state);
+  return answer(st, out);
+}
+
+struct ScanCall {
+  const at::Tensor *x, *delta, *a, *b, *c, *z;
+  const float *skip, *bias;
+  sx_dtype code;
+  int64_t d, n;
+  int softplus;
+};
+
+// x, delta, a, b, c at o[0 ..], skip, z, delta_bias, softplus at r[0 ..]
+bool scan_args(Call& c, PyObject* const* o, PyObject* const* r, int64_t rank, ScanCall* s) {
+  s->x = c.take(o[0]);
+  if (!c.fit || s->x->dim() != rank || !float_type(*s->x, &s->code) || (r[3] != Py_True && r[3] != Py_False))
+    return false;
+  const at::ScalarType type = s->x->scalar_type();
+  s->delta = c.take(o[1], type, rank);
+  s->a = c.take(o[2], at::kFloat, 2);
+  s->b = c.take(o[3], type, rank + 1);
+  s->c = c.take(o[4], type, rank + 1);
+  s->z = r[1] == Py_None ? nullptr : c.take(r[1], type, rank);
+  if (!c.fit) return false;
+  s->d = s->x->size(-1);
+  s->n = s->b->size(-1);
+  if (s->delta->sizes() != s->x->sizes() || (s->z && s->z->sizes() != s->x->sizes()) ||
+      s->c->sizes() != s->b->sizes() || s->a->size(0) != s->d || s->a->size(1) != s->n || !s->a->is_contiguous())
+    return false;
+  s->skip = static_cast<const float*>(c.optional(r[0], at::kFloat, {s->d}));
+  s->bias = static_cast<const float*>(c.optional(r[2], at::kFloat, {s->d}));
+  s->softplus = r[3] == Py_True;
+  return c.fit;
+}
+
+// Calls an entry with the operands in their order, then what is left.
+template <typename F, typename... T>
+sx_status scan_call(F entry, const ScanCall& s, T... rest) {
+  return entry(s.code, s.x->sizes().data(), s.x->strides().data(), s.x->data_ptr(), s.delta->strides().data(),
+               s.delta->data_ptr(), floats(s.a), s.b->sizes().data(), s.b->strides().data(), s.b->data_ptr(),
+               s.c->strides().data(), s.c->data_ptr(), s.skip, s.z ? s.z->strides().data() : nullptr,
+               s.z ? s.z->data_ptr() : nullptr, s.bias, s.softplus, rest...);
+}
+
+// (x, delta, a, b, c, skip, z, delta_bias, softplus, initial, lengths, return_state)
+PyObject* selective_scan(PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  ScanCall s;
+  if (n != 12 || (a[11] != Py_True && a[11] != Py_False) || !scan_args(c, a, a + 5, 3, &s)) return the_long_way();
+  const int64_t b = s.x->size(0);
+  const void* initial = c.optional(a[9], at::kFloat, {b, s.d, s.n});
+  const void* lengths = c.optional(a[10], at::kInt, {b});
+  if (!c.here()) return the_long_way();
+  const at::Tensor out = at::empty(s.x->sizes(), s.x->options());
+  const at::Tensor state = a[11] == Py_True ? at::empty({b, s.d, s.n}, s.a->options()) : at::Tensor();
+  const size_t bytes = lib.selective_scan_bytes(s.code, s.x->sizes().data(), s.b->sizes().data());
+  const at::Tensor ws = workspace(bytes, *s.x);
+  return answer(scan_call(lib.selective_scan, s, static_cast<const float*>(initial),
+                          static_cast<const int32_t*>(lengths), out.data_ptr(), static_cast<float*>(data(state)),
+                          data(ws), bytes, c.stream()),
+                out, state);
+}
+
+// (x, delta, a, b, c, grad_out, skip, z, delta_bias, softplus, initial, lengths, grad_state)
+PyObject* selective_scan_backward(PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  ScanCall s;
+  if (n != 13 || !scan_args(c, a, a + 6, 3, &s)) return the_long_way();
+  const int64_t b = s.x->size(0);
+  const at::Tensor* go = c.take(a[5], s.x->scalar_type(), 3);
+  const void* initial = c.optional(a[10], at::kFloat, {b, s.d, s.n});
+  const void* lengths = c.optional(a[11], at::kInt, {b});
+  const void* gs = c.optional(a[12], at::kFloat, {b, s.d, s.n});
+  if (!c.here() || go->sizes() != s.x->sizes()) return the_long_way();
+  const at::Tensor gx = at::empty(s.x->sizes(), s.x->options()), gd = at::empty(s.x->sizes(), s.x->options()),
+                   ga = at::empty(s.a->sizes(), s.a->options()), gb = at::empty(s.b->sizes(), s.x->options()),
+                   gc = at::empty(s.b->sizes(), s.x->options()),
+                   gskip = s.skip ? at::empty({s.d}, s.a->options()) : at::Tensor(),
+                   gz = s.z ? at::empty(s.x->sizes(), s.x->options()) : at::Tensor(),
+                   gbias = s.bias ? at::empty({s.d}, s.a->options()) : at::Tensor(),
+                   gi = at::empty({b, s.d, s.n}, s.a->options());
+  const size_t bytes = lib.selective_scan_backward_bytes(s.code, s.x->sizes().data(), s.b->sizes().data());
+  const at::Tensor ws = workspace(bytes, *s.x);
+  return answer(scan_call(lib.selective_scan_backward, s, static_cast<const float*>(initial),
+                          static_cast<const int32_t*>(lengths), go->strides().data(), go->data_ptr(),
+                          static_cast<const float*>(gs), gx.data_ptr(), gd.data_ptr(),
+                          static_cast<float*>(ga.data_ptr()), gb.data_ptr(), gc.data_ptr(),
+                          static_cast<float*>(data(gskip)), data(gz), static_cast<float*>(data(gbias)),
+                          static_cast<float*>(gi.data_ptr()), data(ws), bytes, c.stream()),
+                gx, gd, ga, gb, gc, gskip, gz, gbias, gi);
+}
+
+// (x, delta, a, b, c, state, slots, skip, z, delta_bias, softplus)
+PyObject* selective_scan_step(PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  ScanCall s;
+  if (n != 11 || !scan_args(c, a, a + 7, 2, &s)) return the_long_way();
+  const at::Tensor* state = pool_arg(c, a[5], at::kFloat, s.d, s.n);
+  const void* slots = c.optional(a[6], at::kInt, {s.x->size(0)});
+  if (!c.here()) return the_long_way();
+  const at::Tensor out = at::empty(s.x->sizes(), s.x->options());
+  const sx_status st = scan_call(lib.selective_scan_step, s, state->size(0), state->stride(0),
+                                 static_cast<float*>(state->data_ptr()), static_cast<const int32_t*>(slots),
+                                 out.data_ptr(), c.stream());
+  written(st, state);
+  return answer(st, out);
+}
+
+struct NormCall {
+  const at::Tensor* x;
+  int64_t shape[3], strides[3], groups;
+  const float *w, *bias;
+  sx_dtype code;
+  double eps;
+  sx_activation act;
+};
+
+// [N, ..., C] as [N, positions, C], where that is a view of channels next to each other
+bool positions(const at::Tensor& t, int64_t* shape, int64_t* strides) {
+  const int64_t rank = t.dim();
+  if (rank < 2 || t.size(-1) == 0 || (t.size(-1) > 1 && t.stride(-1) != 1)) return false;
+  shape[0] = t.size(0);
+  shape[1] = rank == 2 ? 1 : t.size(1);
+  shape[2] = t.size(-1);
+  strides[0] = t.stride(0);
+  strides[1] = rank == 2 ? shape[2] : t.stride(rank - 2);
+  strides[2] = 1;
+  for (int64_t i = 2; i < rank - 1; ++i) {
+    if (t.stride(i - 1) != t.stride(i) * t.size(i)) return false;
+    shape[1] *= t.size(i);
+  }
+  return true;
+}
+
+bool norm_args(Call& c, PyObject* x, PyObject* groups, PyObject* const* r, NormCall* a) {
+  a->x = c.take(x);
+  if (!c.fit || !float_type(*a->x, &a->code) || !positions(*a->x, a->shape, a->strides) || !PyLong_CheckExact(groups) ||
+      !activation(r[3], &a->act))
+    return false;
+  int over = 0;
+  a->groups = PyLong_AsLongLongAndOverflow(groups, &over);
+  a->w = static_cast<const float*>(c.optional(r[0], at::kFloat, {a->shape[2]}));
+  a->bias = static_cast<const float*>(c.optional(r[1], at::kFloat, {a->shape[2]}));
+  a->eps = c.number(r[2]);
+  return c.fit && !over;
+}
+
+// (x, groups, weight, bias, eps, activation)
+PyObject* group_norm(PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  NormCall v;
+  if (n != 6 || !norm_args(c, a[0], a[1], a + 2, &v) || !c.here()) return the_long_way();
+  const at::Tensor out = at::empty(v.x->sizes(), v.x->options());
+  const size_t bytes = lib.group_norm_bytes(v.code, v.shape, v.groups);
+  const at::Tensor ws = workspace(bytes, *v.x);
+  return answer(lib.group_norm(v.code, v.shape, v.strides, v.x->data_ptr(), v.groups, v.w, v.bias, float(v.eps), v.act,
+                               out.data_ptr(), data(ws), bytes, c.stream()),
+                out);
+}
+
+// (x, groups, grad_out, weight, bias, eps, activation)
+PyObject* group_norm_backward(PyObject* const* a, Py_ssize_t n) {
+  Call c;
+  NormCall v;
+  if (n != 7 || !norm_args(c, a[0], a[1], a + 3, &v)) return the_long_way();
+  const at::Tensor* go = c.take(a[2]);
+  int64_t gshape[3], gstrides[3];
+  if (!c.here() || go->scalar_type() != v.x->scalar_type() || go->sizes() != v.x->sizes() ||
+      !positions(*go, gshape, gstrides))
+    return the_long_way();
+  const auto f32 = v.x->options().dtype(at::kFloat);
+  const at::Tensor gx = at::empty(v.x->sizes(), v.x->options()),
+                   gw = v.w ? at::empty({v.shape[2]}, f32) : at::Tensor(),
+                   gb = v.bias ? at::empty({v.shape[2]}, f32) : at::Tensor();
+  const size_t bytes = lib.group_norm_backward_bytes(v.code, v.shape, v.groups);
+  const at::Tensor ws = workspace(bytes, *v.x);
+  return answer(lib.group_norm_backward(v.code, v.shape, v.strides, v.x->data_ptr(), v.groups, v.w, v.bias,
+                                        float(v.eps), v.act, gstrides, go->data_ptr(), gx.data_ptr(),
+                                        static_cast<float*>(data(gw)), static_cast<float*>(data(gb)), data(ws), bytes,
+                                        c.stream()),
+                gx, gw, gb);
+}
+
+// (addresses of the entries, torch's current device, its raw stream of a device)
 PyObject* bind(PyObject*, PyObject* args) {
   PyObject* at = nullptr;
   PyObject *device = nullptr, *stream = nullptr;
   if (!PyArg_ParseTuple(args, "O!OO", &PyTuple_Type, &at, &device, &stream)) return nullptr;
-  void* p[8];
-  if (PyTuple_GET_SIZE(at) != 8) return PyErr_SetString(PyExc_ValueError, "eight entries are expected"), nullptr;
-  for (int i = 0; i < 8; ++i) {
+  void* p[kEntries];
+  if (PyTuple_GET_SIZE(at) != kEntries)
+    return PyErr_Format(PyExc_ValueError, "%d entries are expected", kEntries), nullptr;
+  for (int i = 0; i < kEntries; ++i) {
     p[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(at, i));
     if (PyErr_Occurred()) return nullptr;
   }
@@ -305,7 +598,20 @@ PyObject* bind(PyObject*, PyObject* args) {
                 reinterpret_cast<decltype(lib.decay_attention_step)>(p[4]),
                 reinterpret_cast<decltype(lib.head_norm_rotate)>(p[5]),
                 reinterpret_cast<decltype(lib.head_norm_rotate_backward)>(p[6]),
-                reinterpret_cast<decltype(lib.head_norm_rotate_backward_bytes)>(p[7])};
+                reinterpret_cast<decltype(lib.head_norm_rotate_backward_bytes)>(p[7]),
+                reinterpret_cast<decltype(lib.causal_conv)>(p[8]),
+                reinterpret_cast<decltype(lib.causal_conv_backward)>(p[9]),
+                reinterpret_cast<decltype(lib.causal_conv_backward_bytes)>(p[10]),
+                reinterpret_cast<decltype(lib.causal_conv_step)>(p[11]),
+                reinterpret_cast<decltype(lib.selective_scan)>(p[12]),
+                reinterpret_cast<decltype(lib.selective_scan_bytes)>(p[13]),
+                reinterpret_cast<decltype(lib.selective_scan_backward)>(p[14]),
+                reinterpret_cast<decltype(lib.selective_scan_backward_bytes)>(p[15]),
+                reinterpret_cast<decltype(lib.selective_scan_step)>(p[16]),
+                reinterpret_cast<decltype(lib.group_norm)>(p[17]),
+                reinterpret_cast<decltype(lib.group_norm_bytes)>(p[18]),
+                reinterpret_cast<decltype(lib.group_norm_backward)>(p[19]),
+                reinterpret_cast<decltype(lib.group_norm_backward_bytes)>(p[20])};
   Py_INCREF(device);
   Py_INCREF(stream);
   current_device = device;
@@ -326,6 +632,14 @@ PyMethodDef methods[] = {
     {"decay_attention_step", method<decay_attention_step>(), METH_FASTCALL, nullptr},
     {"head_norm_rotate", method<head_norm_rotate>(), METH_FASTCALL, nullptr},
     {"head_norm_rotate_backward", method<head_norm_rotate_backward>(), METH_FASTCALL, nullptr},
+    {"causal_conv", method<causal_conv>(), METH_FASTCALL, nullptr},
+    {"causal_conv_backward", method<causal_conv_backward>(), METH_FASTCALL, nullptr},
+    {"causal_conv_step", method<causal_conv_step>(), METH_FASTCALL, nullptr},
+    {"selective_scan", method<selective_scan>(), METH_FASTCALL, nullptr},
+    {"selective_scan_backward", method<selective_scan_backward>(), METH_FASTCALL, nullptr},
+    {"selective_scan_step", method<selective_scan_step>(), METH_FASTCALL, nullptr},
+    {"group_norm", method<group_norm>(), METH_FASTCALL, nullptr},
+    {"group_norm_backward", method<group_norm_backward>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_sx_marshal", nullptr, -1, methods};

@@ -15,6 +15,7 @@
 
 #include "sx_attention.hpp"
 #include "sx_common.hpp"
+#include "sx_state_space.hpp"
 
 namespace sx {
 
@@ -1771,6 +1772,676 @@ sx_status sx_head_norm_rotate_backward(sx_dtype dtype, const int64_t* q_shape, c
   p.gkw = grad_k_weight;
   return device_status(sx::launch_head_rotate_backward(p, static_cast<hipStream_t>(stream)),
                        "head-norm-rotate gradient launch");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ causal convolution, selective scan, group norm
+
+namespace {
+
+constexpr int64_t kMostChannels = int64_t(1) << 24;
+constexpr int64_t kMostElements = int64_t(1) << 48;  // of one operand: no size of a workspace overflows below it
+
+bool activation_ok(const sx_activation& a) {
+  const int v = enum_code(a);
+  return v == SX_ACT_NONE || v == SX_ACT_SILU;
+}
+
+// An operand of `rank` dims, at most four.
+struct Operand {
+  const char* name;
+  int rank;
+  const int64_t* shape;
+  const int64_t* strides;  // nullptr: contiguous
+  const void* data;
+};
+
+int64_t numel_of(const Operand& a) {
+  int64_t n = 1;
+  for (int i = 0; i < a.rank; ++i) n *= a.shape[i];
+  return n;
+}
+
+void strides_of(const Operand& a, int64_t* st) {
+  if (a.strides) std::copy(a.strides, a.strides + a.rank, st); else contiguous_strides(a.rank, a.shape, st);
+}
+
+Span span_of(const Operand& a, size_t elem) {
+  Span s{a.name, 0, 0};
+  if (!a.data || numel_of(a) == 0) return s;
+  int64_t st[4];
+  strides_of(a, st);
+  span_bytes(a.data, a.rank, a.shape, st, elem, &s.lo, &s.hi);
+  return s;
+}
+
+sx_status shape_given(const char* op, const Operand& a) {
+  int64_t n;
+  if (!a.shape) return fail(SX_E_DIM_001, "%s: %s has no shape", op, a.name);
+  if (!checked_numel(a.rank, a.shape, &n))
+    return fail(SX_E_DIM_001, "%s: bad shape %s of %s", op, shape_str(a.rank, a.shape).c_str(), a.name);
+  return ok();
+}
+
+sx_status float_type(const char* op, const sx_dtype& dtype) {
+  if (!dtype_ok(dtype))
+    return fail(SX_E_DIM_002, "%s: the operands must be f32 or bf16 (dtype code %d)", op, enum_code(dtype));
+  return ok();
+}
+
+sx_status activation_given(const char* op, const sx_activation& a) {
+  if (!activation_ok(a)) return fail(SX_E_UNSUPPORTED, "%s: no activation of code %d", op, enum_code(a));
+  return ok();
+}
+
+// [B, T, D], or [B, D] with T = 1.
+sx_status token_shape(const char* op, const Operand& x) {
+  const sx_status st = shape_given(op, x);
+  if (st != SX_OK) return st;
+  if (x.shape[x.rank - 1] < 1)
+    return fail(SX_E_DIM_001, "%s: %s %s has no channels", op, x.name, shape_str(x.rank, x.shape).c_str());
+  if (x.shape[x.rank - 1] > kMostChannels || x.shape[0] > kMostTokens || numel_of(x) > kMostElements ||
+      (x.rank == 3 && x.shape[1] > kMostTokens))
+    return fail(SX_E_UNSUPPORTED, "%s: too many rows, tokens or channels (%s %s)", op, x.name,
+                shape_str(x.rank, x.shape).c_str());
+  return ok();
+}
+
+sx::TokenView token_view(const Operand& x) {
+  sx::TokenView v{};
+  if (!x.data) return v;
+  int64_t st[4];
+  strides_of(x, st);
+  v.p = x.data;
+  v.sb = st[0];
+  v.st = x.rank == 3 ? st[1] : 0;
+  v.sd = x.shape[x.rank - 1] == 1 ? 1 : st[x.rank - 1];
+  return v;
+}
+
+// A pool of states of `one` elements each, contiguous: its span, and whether they overlap.
+sx_status pool_span(const char* op, int64_t pool, int64_t stride, int64_t one, const void* state, int64_t rows,
+                    const int32_t* slots, size_t elem, Span* s) {
+  if (pool < 0) return fail(SX_E_DIM_001, "%s: a pool of %lld states", op, (long long)pool);
+  if (!slots && pool < rows)
+    return fail(SX_E_DIM_001, "%s: %lld states for %lld rows and no slots", op, (long long)pool, (long long)rows);
+  int64_t n;
+  const int64_t shape[2] = {pool, one}, st[2] = {stride, 1};
+  if (!checked_numel(2, shape, &n)) return fail(SX_E_DIM_001, "%s: bad pool of %lld states", op, (long long)pool);
+  if (pool > 1 && stride < one && -stride < one) return fail(SX_E_UNSUPPORTED, "%s: states overlap each other", op);
+  *s = Span{"state", 0, 0, unsigned(elem)};
+  if (state && n > 0) span_bytes(state, 2, shape, st, elem, &s->lo, &s->hi);
+  return ok();
+}
+
+struct ConvArgs {
+  Operand x;
+  int64_t taps;
+  const float *weight, *bias;
+};
+
+sx_status conv_shapes(const char* op, const sx_dtype& dtype, const ConvArgs& a, const sx_activation& act) {
+  sx_status st = float_type(op, dtype);
+  if (st == SX_OK) st = token_shape(op, a.x);
+  if (st == SX_OK) st = activation_given(op, act);
+  if (st != SX_OK) return st;
+  if (a.taps < 1) return fail(SX_E_DIM_001, "%s: a weight of %lld taps", op, (long long)a.taps);
+  if (a.taps > SX_MAX_TAPS)
+    return fail(SX_E_UNSUPPORTED, "%s: %lld taps, %d at most", op, (long long)a.taps, SX_MAX_TAPS);
+  return ok();
+}
+
+sx::CcParams conv_params(const sx_dtype& dtype, const ConvArgs& a, const int32_t* lengths, const sx_activation& act,
+                         bool gradient) {
+  sx::CcParams p{};
+  p.B = int(a.x.shape[0]);
+  p.T = int(a.x.shape[1]);
+  p.D = int(a.x.shape[2]);
+  p.K = int(a.taps);
+  p.x = token_view(a.x);
+  p.w = a.weight;
+  p.bias = a.bias;
+  p.lengths = lengths;
+  p.silu = act == SX_ACT_SILU;
+  p.bf16 = dtype == SX_BF16;
+  sx::causal_conv_split(p, gradient);
+  return p;
+}
+
+sx_status grid_fits(const char* op, double groups) {
+  if (groups > double(kMostGrid)) return fail(SX_E_UNSUPPORTED, "%s: too many elements for one launch", op);
+  return ok();
+}
+
+size_t conv_partial_floats(const sx::CcParams& p) { return size_t(p.B) * p.chunks * (p.K + 1) * size_t(p.D); }
+
+}  // namespace
+
+extern "C" {
+
+sx_status sx_causal_conv(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x, int64_t taps,
+                         const float* weight, const float* bias, const void* initial, const int32_t* lengths,
+                         sx_activation activation, void* out, void* final_state, void* stream) {
+  const char* op = "causal-conv";
+  const ConvArgs a{{"x", 3, x_shape, x_strides, x}, taps, weight, bias};
+  sx_status st = conv_shapes(op, dtype, a, activation);
+  if (st != SX_OK) return st;
+  const int64_t B = x_shape[0], D = x_shape[2], n = numel_of(a.x), state = B * (taps - 1) * D;
+  const size_t e = dtype == SX_BF16 ? 2 : 4;
+  if (B == 0 || (n == 0 && !final_state)) return ok();
+  if (n > 0) {
+    if (!x) return missing(op, "x");
+    if (!weight) return missing(op, "weight");
+    if (!out) return missing(op, "out");
+  }
+  const Span in[] = {span_of(a.x, e), flat_span("weight", weight, D * taps * 4), flat_span("bias", bias, D * 4),
+                     flat_span("initial", initial, state * int64_t(e)), flat_span("lengths", lengths, B * 4)};
+  const Span to[] = {flat_span("out", out, n * int64_t(e)),
+                     flat_span("the final state", final_state, state * int64_t(e))};
+  if ((st = no_overlap(op, in, 5, to, 2)) != SX_OK) return st;
+  sx::CcParams p = conv_params(dtype, a, lengths, activation, false);
+  if ((st = grid_fits(op, double(p.B) * p.chunks * double(D) / 256 + 1)) != SX_OK) return st;
+  p.initial = initial;
+  p.out = out;
+  p.last = final_state;
+  return device_status(sx::launch_causal_conv(p, static_cast<hipStream_t>(stream)), "causal-conv launch");
+}
+
+size_t sx_causal_conv_backward_workspace_bytes(sx_dtype dtype, const int64_t* x_shape, int64_t taps) {
+  const ConvArgs a{{"x", 3, x_shape, nullptr, nullptr}, taps, nullptr, nullptr};
+  if (conv_shapes("causal-conv gradient", dtype, a, SX_ACT_NONE) != SX_OK) return 0;
+  return conv_partial_floats(conv_params(dtype, a, nullptr, SX_ACT_NONE, true)) * sizeof(float);
+}
+
+sx_status sx_causal_conv_backward(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x,
+                                  int64_t taps, const float* weight, const float* bias, const void* initial,
+                                  const int32_t* lengths, sx_activation activation, const int64_t* grad_out_strides,
+                                  const void* grad_out, const void* grad_state, void* grad_x, float* grad_weight,
+                                  float* grad_bias, void* grad_initial, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  const char* op = "causal-conv gradient";
+  const ConvArgs a{{"x", 3, x_shape, x_strides, x}, taps, weight, bias};
+  sx_status st = conv_shapes(op, dtype, a, activation);
+  if (st != SX_OK) return st;
+  const Operand go{"grad_out", 3, x_shape, grad_out_strides, grad_out};
+  const int64_t B = x_shape[0], D = x_shape[2], n = numel_of(a.x), state = B * (taps - 1) * D;
+  const int64_t e = dtype == SX_BF16 ? 2 : 4;
+  if (!weight) return missing(op, "weight");
+  if (!grad_weight) return missing(op, "grad_weight");
+  if (n > 0) {
+    if (!x) return missing(op, "x");
+    if (!grad_out) return missing(op, "grad_out");
+    if (!grad_x) return missing(op, "grad_x");
+  }
+  const Span in[] = {span_of(a.x, e), span_of(go, e), flat_span("weight", weight, D * taps * 4),
+                     flat_span("bias", bias, D * 4), flat_span("initial", initial, state * e),
+                     flat_span("lengths", lengths, B * 4), flat_span("grad_state", grad_state, state * e)};
+  const Span to[] = {flat_span("grad_x", grad_x, n * e), flat_span("grad_weight", grad_weight, D * taps * 4),
+                     flat_span("grad_bias", grad_bias, D * 4), flat_span("grad_initial", grad_initial, state * e)};
+  if ((st = no_overlap(op, in, 7, to, 4)) != SX_OK) return st;
+  sx::CcParams p = conv_params(dtype, a, lengths, activation, true);
+  if ((st = grid_fits(op, double(p.B) * p.chunks * double(D) / 256 + 1)) != SX_OK) return st;
+  if ((st = check_workspace(op, workspace, workspace_bytes, conv_partial_floats(p) * sizeof(float))) != SX_OK) return st;
+  p.go = token_view(go);
+  p.initial = initial;
+  p.grad_state = grad_state;
+  p.out = grad_x;
+  p.last = grad_initial;
+  p.partial = static_cast<float*>(workspace);
+  p.gw = grad_weight;
+  p.gbias = grad_bias;
+  return device_status(sx::launch_causal_conv_backward(p, static_cast<hipStream_t>(stream)),
+                       "causal-conv gradient launch");
+}
+
+sx_status sx_causal_conv_step(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x,
+                              int64_t taps, const float* weight, const float* bias, sx_activation activation,
+                              int64_t pool, int64_t state_stride, void* state, const int32_t* slots, void* out,
+                              void* stream) {
+  const char* op = "causal-conv step";
+  const ConvArgs a{{"x", 2, x_shape, x_strides, x}, taps, weight, bias};
+  sx_status st = conv_shapes(op, dtype, a, activation);
+  if (st != SX_OK) return st;
+  const int64_t B = x_shape[0], D = x_shape[1], one = (taps - 1) * D;
+  const int64_t e = dtype == SX_BF16 ? 2 : 4;
+  Span to[] = {flat_span("out", out, B * D * e), {}};
+  if ((st = pool_span(op, pool, state_stride, one, state, B, slots, size_t(e), &to[1])) != SX_OK) return st;
+  if (B == 0) return ok();
+  if (!x) return missing(op, "x");
+  if (!weight) return missing(op, "weight");
+  if (!state && pool * one > 0) return missing(op, "state");
+  if (!out) return missing(op, "out");
+  const Span in[] = {span_of(a.x, e), flat_span("weight", weight, D * taps * 4), flat_span("bias", bias, D * 4),
+                     flat_span("slots", slots, B * 4)};
+  if ((st = no_overlap(op, in, 4, to, 2)) != SX_OK) return st;
+  if ((st = grid_fits(op, double(B) * double(D) / 256 + 1)) != SX_OK) return st;
+  const sx::TokenView v = token_view(a.x);
+  sx::CcStep p{};
+  p.B = int(B);
+  p.D = int(D);
+  p.K = int(taps);
+  p.x = x;
+  p.sb = v.sb;
+  p.sd = v.sd;
+  p.w = weight;
+  p.bias = bias;
+  p.state = state;
+  p.ss = state_stride;
+  p.pool = pool;
+  p.slots = slots;
+  p.silu = activation == SX_ACT_SILU;
+  p.bf16 = dtype == SX_BF16;
+  p.out = out;
+  return device_status(sx::launch_causal_conv_step(p, static_cast<hipStream_t>(stream)), "causal-conv step launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+struct ScanArgs {
+  Operand x, delta, z, b, c;
+  const float *a, *skip, *delta_bias;
+};
+
+sx_status scan_shapes(const char* op, const sx_dtype& dtype, const ScanArgs& a) {
+  sx_status st = float_type(op, dtype);
+  if (st == SX_OK) st = token_shape(op, a.x);
+  if (st == SX_OK) st = shape_given(op, a.b);
+  if (st != SX_OK) return st;
+  const int64_t* xs = a.x.shape;
+  const int64_t* bs = a.b.shape;
+  const int dims = a.x.rank - 1;  // rows and tokens
+  for (int i = 0; i < dims; ++i)
+    if (bs[i] != xs[i])
+      return fail(SX_E_DIM_001, "%s: b %s does not fit x %s", op, shape_str(a.b.rank, bs).c_str(),
+                  shape_str(a.x.rank, xs).c_str());
+  const int64_t D = xs[dims], G = bs[dims], N = bs[dims + 1];
+  if (G < 1 || D % G != 0)
+    return fail(SX_E_DIM_001, "%s: the %lld groups of b do not divide the %lld channels of x", op, (long long)G,
+                (long long)D);
+  if (N < 1) return fail(SX_E_DIM_001, "%s: no states (b %s)", op, shape_str(a.b.rank, bs).c_str());
+  if (N > SX_MAX_STATES)
+    return fail(SX_E_UNSUPPORTED, "%s: %lld states a channel, %d at most", op, (long long)N, SX_MAX_STATES);
+  return ok();
+}
+
+sx::RowView row_view(const Operand& a) {
+  int64_t st[4];
+  strides_of(a, st);
+  const int k = a.rank == 4 ? 1 : 0;
+  return {a.data, st[0], k ? st[1] : 0, st[k + 1], st[k + 2]};
+}
+
+sx::SsParams scan_params(const sx_dtype& dtype, const ScanArgs& a, bool gradient) {
+  sx::SsParams p{};
+  p.B = int(a.x.shape[0]);
+  p.T = int(a.x.shape[1]);
+  p.D = int(a.x.shape[2]);
+  p.G = int(a.b.shape[2]);
+  p.N = int(a.b.shape[3]);
+  p.x = token_view(a.x);
+  p.delta = token_view(a.delta);
+  p.z = token_view(a.z);
+  p.b = row_view(a.b);
+  p.c = row_view(a.c);
+  p.a = a.a;
+  p.skip = a.skip;
+  p.delta_bias = a.delta_bias;
+  p.bf16 = dtype == SX_BF16;
+  sx::selective_scan_split(p, gradient);
+  return p;
+}
+
+sx_status scan_pointers(const char* op, const ScanArgs& a) {
+  for (const Operand* o : {&a.x, &a.delta, &a.b, &a.c})
+    if (!o->data) return missing(op, o->name);
+  if (!a.a) return missing(op, "a");
+  return ok();
+}
+
+// The operands' spans; returns how many.
+int scan_spans(const ScanArgs& a, size_t e, Span* s) {
+  const int64_t D = a.x.shape[a.x.rank - 1], N = a.b.shape[a.b.rank - 1];
+  s[0] = span_of(a.x, e);
+  s[1] = span_of(a.delta, e);
+  s[2] = span_of(a.z, e);
+  s[3] = span_of(a.b, e);
+  s[4] = span_of(a.c, e);
+  s[5] = flat_span("a", a.a, D * N * 4);
+  s[6] = flat_span("skip", a.skip, D * 4);
+  s[7] = flat_span("delta_bias", a.delta_bias, D * 4);
+  return 8;
+}
+
+int64_t packed_floats(const sx::SsParams& p) { return int64_t(p.B) * p.waves * p.D * sx::kScanStates; }
+
+void carve_scan(Carve& c, sx::SsParams& p) {
+  const int64_t n = p.segments - 1;
+  p.seg_state = c.take<float>(n * packed_floats(p));
+  p.seg_steps = c.take<float>(n * p.B * p.D);
+}
+
+void carve_scan_gradient(Carve& c, sx::SsParams& p) {
+  const int64_t D = p.D, rows = int64_t(p.B) * p.segments, joined = p.segments > 1 ? p.segments : 0;
+  p.seg_state = c.take<float>(joined * packed_floats(p));
+  p.seg_adjoint = c.take<float>(joined * packed_floats(p));
+  p.seg_steps = c.take<float>(joined * p.B * D);
+  p.marks = c.take<float>(packed_floats(p) * p.row_marks);
+  p.mark_steps = c.take<float>(joined ? int64_t(p.B) * p.row_marks * D : 0);
+  p.rows_partial = c.take<float>(int64_t(p.B) * p.G * p.T * sx::selective_scan_grad_blocks(p) * 8 * p.waves);
+  p.a_partial = c.take<float>(rows * D * p.N);
+  p.skip_partial = c.take<float>(rows * D);
+  p.bias_partial = c.take<float>(rows * D);
+}
+
+sx_status scan_grid(const char* op, const sx::SsParams& p) {
+  const double blocks = double(p.G) * ((p.D / p.G + 63) / 64);
+  sx_status st = grid_fits(op, blocks * p.B * p.segments);
+  if (st == SX_OK) st = grid_fits(op, double(p.B) * p.G * p.T * 8 * p.waves / 256 + 1);
+  return st;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sx_selective_scan_workspace_bytes(sx_dtype dtype, const int64_t* x_shape, const int64_t* b_shape) {
+  const ScanArgs a{{"x", 3, x_shape}, {"delta", 3, x_shape}, {"z", 3, x_shape}, {"b", 4, b_shape}, {"c", 4, b_shape}};
+  if (scan_shapes("selective-scan", dtype, a) != SX_OK) return 0;
+  sx::SsParams p = scan_params(dtype, a, false);
+  Carve c{0};
+  carve_scan(c, p);
+  return c.used;
+}
+
+sx_status sx_selective_scan(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x,
+                            const int64_t* delta_strides, const void* delta, const float* a, const int64_t* b_shape,
+                            const int64_t* b_strides, const void* b, const int64_t* c_strides, const void* c,
+                            const float* skip, const int64_t* z_strides, const void* z, const float* delta_bias,
+                            int softplus, const float* initial, const int32_t* lengths, void* out, float* final_state,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  const char* op = "selective-scan";
+  const ScanArgs args{{"x", 3, x_shape, x_strides, x}, {"delta", 3, x_shape, delta_strides, delta},
+                      {"z", 3, x_shape, z_strides, z}, {"b", 4, b_shape, b_strides, b},
+                      {"c", 4, b_shape, c_strides, c}, a, skip, delta_bias};
+  sx_status st = scan_shapes(op, dtype, args);
+  if (st != SX_OK) return st;
+  const int64_t B = x_shape[0], T = x_shape[1], D = x_shape[2], N = b_shape[3], n = B * T * D, state = B * D * N;
+  if (B == 0 || (T == 0 && !final_state)) return ok();
+  if (n > 0) {
+    if ((st = scan_pointers(op, args)) != SX_OK) return st;
+    if (!out) return missing(op, "out");
+  }
+  const size_t e = dtype == SX_BF16 ? 2 : 4;
+  Span in[10];
+  int k = scan_spans(args, e, in);
+  in[k++] = flat_span("initial", initial, state * 4);
+  in[k++] = flat_span("lengths", lengths, B * 4);
+  const Span to[] = {flat_span("out", out, n * int64_t(e)), flat_span("the final state", final_state, state * 4)};
+  if ((st = no_overlap(op, in, k, to, 2)) != SX_OK) return st;
+  sx::SsParams p = scan_params(dtype, args, false);
+  if ((st = scan_grid(op, p)) != SX_OK) return st;
+  Carve w{reinterpret_cast<uintptr_t>(workspace)};
+  carve_scan(w, p);
+  if ((st = check_workspace(op, workspace, workspace_bytes, w.used)) != SX_OK) return st;
+  p.softplus = softplus != 0;
+  p.initial = initial;
+  p.lengths = lengths;
+  p.out = out;
+  p.last = final_state;
+  return device_status(sx::launch_selective_scan(p, static_cast<hipStream_t>(stream)), "selective-scan launch");
+}
+
+size_t sx_selective_scan_backward_workspace_bytes(sx_dtype dtype, const int64_t* x_shape, const int64_t* b_shape) {
+  const ScanArgs a{{"x", 3, x_shape}, {"delta", 3, x_shape}, {"z", 3, x_shape}, {"b", 4, b_shape}, {"c", 4, b_shape}};
+  if (scan_shapes("selective-scan gradient", dtype, a) != SX_OK) return 0;
+  sx::SsParams p = scan_params(dtype, a, true);
+  Carve c{0};
+  carve_scan_gradient(c, p);
+  return c.used;
+}
+
+sx_status sx_selective_scan_backward(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x,
+                                     const int64_t* delta_strides, const void* delta, const float* a,
+                                     const int64_t* b_shape, const int64_t* b_strides, const void* b,
+                                     const int64_t* c_strides, const void* c, const float* skip,
+                                     const int64_t* z_strides, const void* z, const float* delta_bias, int softplus,
+                                     const float* initial, const int32_t* lengths, const int64_t* grad_out_strides,
+                                     const void* grad_out, const float* grad_state, void* grad_x, void* grad_delta,
+                                     float* grad_a, void* grad_b, void* grad_c, float* grad_skip, void* grad_z,
+                                     float* grad_delta_bias, float* grad_initial, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  const char* op = "selective-scan gradient";
+  const ScanArgs args{{"x", 3, x_shape, x_strides, x}, {"delta", 3, x_shape, delta_strides, delta},
+                      {"z", 3, x_shape, z_strides, z}, {"b", 4, b_shape, b_strides, b},
+                      {"c", 4, b_shape, c_strides, c}, a, skip, delta_bias};
+  sx_status st = scan_shapes(op, dtype, args);
+  if (st != SX_OK) return st;
+  const Operand go{"grad_out", 3, x_shape, grad_out_strides, grad_out};
+  const int64_t B = x_shape[0], T = x_shape[1], D = x_shape[2], N = b_shape[3], n = B * T * D, state = B * D * N;
+  const int64_t rows = numel_of(args.b);
+  if (n > 0) {
+    if ((st = scan_pointers(op, args)) != SX_OK) return st;
+    if (!grad_out) return missing(op, "grad_out");
+    if (!grad_x) return missing(op, "grad_x");
+    if (!grad_delta) return missing(op, "grad_delta");
+    if (!grad_b) return missing(op, "grad_b");
+    if (!grad_c) return missing(op, "grad_c");
+    if (z && !grad_z) return missing(op, "grad_z");
+  }
+  if (B > 0 && !a) return missing(op, "a");
+  if (!grad_a) return missing(op, "grad_a");
+  const int64_t e = dtype == SX_BF16 ? 2 : 4;
+  Span in[12];
+  int k = scan_spans(args, size_t(e), in);
+  in[k++] = flat_span("initial", initial, state * 4);
+  in[k++] = flat_span("lengths", lengths, B * 4);
+  in[k++] = span_of(go, size_t(e));
+  in[k++] = flat_span("grad_state", grad_state, state * 4);
+  const Span to[] = {flat_span("grad_x", grad_x, n * e),
+                     flat_span("grad_delta", grad_delta, n * e),
+                     flat_span("grad_a", grad_a, D * N * 4),
+                     flat_span("grad_b", grad_b, rows * e),
+                     flat_span("grad_c", grad_c, rows * e),
+                     flat_span("grad_skip", grad_skip, D * 4),
+                     flat_span("grad_z", z ? grad_z : nullptr, n * e),
+                     flat_span("grad_delta_bias", grad_delta_bias, D * 4),
+                     flat_span("grad_initial", grad_initial, state * 4)};
+  if ((st = no_overlap(op, in, k, to, 9)) != SX_OK) return st;
+  sx::SsParams p = scan_params(dtype, args, true);
+  if ((st = scan_grid(op, p)) != SX_OK) return st;
+  Carve w{reinterpret_cast<uintptr_t>(workspace)};
+  carve_scan_gradient(w, p);
+  if ((st = check_workspace(op, workspace, workspace_bytes, w.used)) != SX_OK) return st;
+  p.softplus = softplus != 0;
+  p.initial = initial;
+  p.lengths = lengths;
+  p.go = token_view(go);
+  p.grad_state = grad_state;
+  p.gx = grad_x;
+  p.gdelta = grad_delta;
+  p.gz = grad_z;
+  p.gb = grad_b;
+  p.gc = grad_c;
+  p.ga = grad_a;
+  p.gskip = grad_skip;
+  p.gbias = grad_delta_bias;
+  p.ginitial = grad_initial;
+  return device_status(sx::launch_selective_scan_backward(p, static_cast<hipStream_t>(stream)),
+                       "selective-scan gradient launch");
+}
+
+sx_status sx_selective_scan_step(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x,
+                                 const int64_t* delta_strides, const void* delta, const float* a,
+                                 const int64_t* b_shape, const int64_t* b_strides, const void* b,
+                                 const int64_t* c_strides, const void* c, const float* skip, const int64_t* z_strides,
+                                 const void* z, const float* delta_bias, int softplus, int64_t pool,
+                                 int64_t state_stride, float* state, const int32_t* slots, void* out, void* stream) {
+  const char* op = "selective-scan step";
+  const ScanArgs args{{"x", 2, x_shape, x_strides, x}, {"delta", 2, x_shape, delta_strides, delta},
+                      {"z", 2, x_shape, z_strides, z}, {"b", 3, b_shape, b_strides, b},
+                      {"c", 3, b_shape, c_strides, c}, a, skip, delta_bias};
+  sx_status st = scan_shapes(op, dtype, args);
+  if (st != SX_OK) return st;
+  const int64_t B = x_shape[0], D = x_shape[1], N = b_shape[2], e = dtype == SX_BF16 ? 2 : 4;
+  Span to[] = {flat_span("out", out, B * D * e), {}};
+  if ((st = pool_span(op, pool, state_stride, D * N, state, B, slots, sizeof(float), &to[1])) != SX_OK) return st;
+  if (B == 0) return ok();
+  if ((st = scan_pointers(op, args)) != SX_OK) return st;
+  if (!state && pool > 0) return missing(op, "state");
+  if (!out) return missing(op, "out");
+  Span in[9];
+  int k = scan_spans(args, size_t(e), in);
+  in[k++] = flat_span("slots", slots, B * 4);
+  if ((st = no_overlap(op, in, k, to, 2)) != SX_OK) return st;
+  if ((st = grid_fits(op, double(B) * double(D) * 8 / 256 + 1)) != SX_OK) return st;
+  sx::SsStep p{};
+  p.B = int(B);
+  p.D = int(D);
+  p.G = int(b_shape[1]);
+  p.N = int(N);
+  p.x = token_view(args.x);
+  p.delta = token_view(args.delta);
+  p.z = token_view(args.z);
+  p.b = row_view(args.b);
+  p.c = row_view(args.c);
+  p.a = a;
+  p.skip = skip;
+  p.delta_bias = delta_bias;
+  p.softplus = softplus != 0;
+  p.bf16 = dtype == SX_BF16;
+  p.state = state;
+  p.ss = state_stride;
+  p.pool = pool;
+  p.slots = slots;
+  p.out = out;
+  return device_status(sx::launch_selective_scan_step(p, static_cast<hipStream_t>(stream)),
+                       "selective-scan step launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+sx_status plan_norm(const char* op, const sx_dtype& dtype, const Operand& x, int64_t groups, float eps,
+                    const sx_activation& act, bool gradient, sx::GnParams* p) {
+  sx_status st = float_type(op, dtype);
+  if (st == SX_OK) st = shape_given(op, x);
+  if (st == SX_OK) st = activation_given(op, act);
+  if (st != SX_OK) return st;
+  const int64_t c = x.shape[2];
+  if (c < 1) return fail(SX_E_DIM_001, "%s: x %s has no channels", op, shape_str(3, x.shape).c_str());
+  if (groups < 1 || c % groups != 0)
+    return fail(SX_E_DIM_001, "%s: %lld groups do not divide %lld channels", op, (long long)groups, (long long)c);
+  if (!(eps >= 0.0f)) return fail(SX_E_DIM_001, "%s: eps %g is negative", op, double(eps));
+  if (c > kMostChannels || x.shape[0] > kMostElements || x.shape[1] > kMostElements || numel_of(x) > kMostElements)
+    return fail(SX_E_UNSUPPORTED, "%s: too many samples, positions or channels (x %s)", op,
+                shape_str(3, x.shape).c_str());
+  int64_t xs[4];
+  strides_of(x, xs);
+  if (c > 1 && xs[2] != 1) return fail(SX_E_UNSUPPORTED, "%s: channels of %s must lie next to each other", op, x.name);
+  *p = sx::GnParams{};
+  p->n = x.shape[0];
+  p->s = x.shape[1];
+  p->c = int(c);
+  p->g = int(groups);
+  p->x = x.data;
+  p->xn = xs[0];
+  p->xs = xs[1];
+  p->eps = eps;
+  p->silu = act == SX_ACT_SILU;
+  p->bf16 = dtype == SX_BF16;
+  sx::group_norm_split(*p, gradient);
+  return grid_fits(op, sx::group_norm_workgroups(*p));
+}
+
+size_t carve_norm(Carve& c, sx::GnParams& p, bool gradient) {
+  p.stats = c.take<float>(sx::group_norm_stats_floats(p));
+  if (gradient) p.sums = c.take<float>(sx::group_norm_sums_floats(p));
+  return c.used;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sx_group_norm_workspace_bytes(sx_dtype dtype, const int64_t* x_shape, int64_t groups) {
+  sx::GnParams p;
+  if (plan_norm("group-norm", dtype, {"x", 3, x_shape}, groups, 0.0f, SX_ACT_NONE, false, &p) != SX_OK) return 0;
+  Carve c{0};
+  return p.n * p.s == 0 ? 0 : carve_norm(c, p, false);
+}
+
+sx_status sx_group_norm(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x, int64_t groups,
+                        const float* weight, const float* bias, float eps, sx_activation activation, void* out,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  const char* op = "group-norm";
+  const Operand xa{"x", 3, x_shape, x_strides, x};
+  sx::GnParams p;
+  sx_status st = plan_norm(op, dtype, xa, groups, eps, activation, false, &p);
+  if (st != SX_OK) return st;
+  const int64_t n = numel_of(xa), e = p.bf16 ? 2 : 4;
+  if (n == 0) return ok();
+  if (!x) return missing(op, "x");
+  if (!out) return missing(op, "out");
+  const Span in[] = {span_of(xa, size_t(e)), flat_span("weight", weight, int64_t(p.c) * 4),
+                     flat_span("bias", bias, int64_t(p.c) * 4)};
+  const Span to[] = {flat_span("out", out, n * e)};
+  if ((st = no_overlap(op, in, 3, to, 1)) != SX_OK) return st;
+  Carve c{reinterpret_cast<uintptr_t>(workspace)};
+  if ((st = check_workspace(op, workspace, workspace_bytes, carve_norm(c, p, false))) != SX_OK) return st;
+  p.w = weight;
+  p.bias = bias;
+  p.out = out;
+  return device_status(sx::launch_group_norm(p, static_cast<hipStream_t>(stream)), "group-norm launch");
+}
+
+size_t sx_group_norm_backward_workspace_bytes(sx_dtype dtype, const int64_t* x_shape, int64_t groups) {
+  sx::GnParams p;
+  if (plan_norm("group-norm gradient", dtype, {"x", 3, x_shape}, groups, 0.0f, SX_ACT_NONE, true, &p) != SX_OK) return 0;
+  Carve c{0};
+  return p.n * p.s == 0 ? 0 : carve_norm(c, p, true);
+}
+
+sx_status sx_group_norm_backward(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x,
+                                 int64_t groups, const float* weight, const float* bias, float eps,
+                                 sx_activation activation, const int64_t* grad_out_strides, const void* grad_out,
+                                 void* grad_x, float* grad_weight, float* grad_bias, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  const char* op = "group-norm gradient";
+  const Operand xa{"x", 3, x_shape, x_strides, x}, go{"grad_out", 3, x_shape, grad_out_strides, grad_out};
+  sx::GnParams p;
+  sx_status st = plan_norm(op, dtype, xa, groups, eps, activation, true, &p);
+  if (st != SX_OK) return st;
+  int64_t gs[4];
+  strides_of(go, gs);
+  if (p.c > 1 && gs[2] != 1)
+    return fail(SX_E_UNSUPPORTED, "%s: channels of grad_out must lie next to each other", op);
+  const int64_t n = numel_of(xa), e = p.bf16 ? 2 : 4, c = p.c;
+  if (n > 0) {
+    if (!x) return missing(op, "x");
+    if (!grad_out) return missing(op, "grad_out");
+    if (!grad_x) return missing(op, "grad_x");
+  }
+  const Span in[] = {span_of(xa, size_t(e)), span_of(go, size_t(e)), flat_span("weight", weight, c * 4),
+                     flat_span("bias", bias, c * 4)};
+  const Span to[] = {flat_span("grad_x", grad_x, n * e), flat_span("grad_weight", grad_weight, c * 4),
+                     flat_span("grad_bias", grad_bias, c * 4)};
+  if ((st = no_overlap(op, in, 4, to, 3)) != SX_OK) return st;
+  Carve w{reinterpret_cast<uintptr_t>(workspace)};
+  if (n > 0 && (st = check_workspace(op, workspace, workspace_bytes, carve_norm(w, p, true))) != SX_OK) return st;
+  p.w = weight;
+  p.bias = bias;
+  p.go = grad_out;
+  p.gon = gs[0];
+  p.gos = gs[1];
+  p.out = grad_x;
+  p.gw = grad_weight;
+  p.gbias = grad_bias;
+  return device_status(sx::launch_group_norm_backward(p, static_cast<hipStream_t>(stream)),
+                       "group-norm gradient launch");
 }
 
 }  // extern "C"
