@@ -7,7 +7,7 @@
 //   gx = dt sum over n of (lam b) + skip gy,  gdelta = gdt sigmoid(delta + delta_bias)
 //   gz = gout y silu'(z),  gskip = sum of gy x,  gbias = sum of gdelta,  ginitial = mu of the first token
 //
-// Three passes. mark_states marches forward and leaves the state before every
+// Three passes. scan_march goes forward and leaves the state before every
 // eighth token; where the tokens are split into segments each marches from zero,
 // with its adjoint: lam at its start is a sum over its tokens of the decays up to them, c and gy.
 // carry joins the segments, states forward and adjoints back. grad_march then takes
@@ -16,155 +16,14 @@
 // What is left is sums over workgroups (sum_rows, token_rows).
 //
 // grad_march: a lane has two channels and four states of each, so that what is
-// summed over channels is summed over two for nothing; over the lanes, 64 values
-// at a time (eight tokens of four states of b and of c) fold into one a lane: each
-// step adds halves of a pair of registers to one, 141 instructions for 64 sums.
+// summed over channels is summed over two for nothing; over the lanes, 64 sums at
+// a time (eight tokens of four states of b and of c) fold into one a lane, in 140 additions.
 #include <algorithm>
 
 #include "scan_march.hpp"
 
 namespace sx {
 namespace {
-
-constexpr int kTile = 2 * kMarkTokens, kChannels = 64;
-
-// The marks of row b, and the segments' own states, sums of dt and adjoints (JOIN: more than one segment).
-template <bool BF, int W, bool WIDE, bool JOIN>
-__global__ __launch_bounds__(kWave* W) void mark_states(SsParams p) {
-  using P = Piece<BF, 4>;
-  using Raw = typename P::Raw;
-  constexpr int kPieces = kTile * kChannels / 4, kPasses = (kPieces + kWave * W - 1) / (kWave * W);
-  __shared__ float ldt[2][kTile][kChannels], ldx[2][kTile][kChannels], lgy[JOIN ? 2 : 1][JOIN ? kTile : 1][kChannels];
-  const int tid = int(threadIdx.x), lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int n0 = wave * kScanStates;
-  const int per_group = p.D / p.G, blocks = (per_group + kChannels - 1) / kChannels;
-  uint32_t at = blockIdx.x;
-  const int cb = int(at % uint32_t(blocks));
-  at /= uint32_t(blocks);
-  const int g = int(at % uint32_t(p.G));
-  at /= uint32_t(p.G);
-  const int b = int(at % uint32_t(p.B)), seg = int(at / uint32_t(p.B));
-  const int d0 = g * per_group + cb * kChannels, channels = min(kChannels, per_group - cb * kChannels);
-  const int s0 = seg * p.seg_tokens, s1 = min(s0 + p.seg_tokens, p.T);
-  const int end = min(s1, row_length(p.lengths, b, p.T));
-  const int tiles = end > s0 ? (end - s0 + kTile - 1) / kTile : 0;
-  const int q0 = tid / (kChannels / 4), c4 = tid % (kChannels / 4) * 4, left = channels - c4;
-  constexpr int kStep = W * kWave / (kChannels / 4);
-  const bool mine = left > 0 && q0 < kTile;
-  float bias[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) bias[i] = mine && i < left && p.delta_bias ? p.delta_bias[d0 + c4 + i] : 0.0f;
-  const int64_t xo = int64_t(b) * p.x.sb + int64_t(d0 + c4) * p.x.sd;
-  const int64_t deltao = int64_t(b) * p.delta.sb + int64_t(d0 + c4) * p.delta.sd;
-  const int64_t zo = int64_t(b) * p.z.sb + int64_t(d0 + c4) * p.z.sd;
-  const int64_t goo = int64_t(b) * p.go.sb + int64_t(d0 + c4) * p.go.sd;
-  Raw xin[kPasses], din[kPasses], zin[kPasses], gin[kPasses];
-  const auto read = [&](int tile) {
-#pragma unroll
-    for (int k = 0; k < kPasses; ++k) {
-      const int t = s0 + tile * kTile + q0 + k * kStep;
-      const bool live = mine && q0 + k * kStep < kTile && t < end;
-      xin[k] = live ? four_channels<BF, WIDE>(p.x, xo + int64_t(t) * p.x.st, left) : P::zero();
-      din[k] = live ? four_channels<BF, WIDE>(p.delta, deltao + int64_t(t) * p.delta.st, left) : P::zero();
-      if (JOIN) gin[k] = live ? four_channels<BF, WIDE>(p.go, goo + int64_t(t) * p.go.st, left) : P::zero();
-      if (JOIN && p.z.p) zin[k] = live ? four_channels<BF, WIDE>(p.z, zo + int64_t(t) * p.z.st, left) : P::zero();
-    }
-  };
-  const auto convert = [&](int tile) {
-#pragma unroll
-    for (int k = 0; k < kPasses; ++k) {
-      const int q = q0 + k * kStep, t = s0 + tile * kTile + q;
-      if (!mine || q >= kTile) continue;
-      float x[4], v[4];
-      P::open(xin[k], x);
-      P::open(din[k], v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] += bias[i];
-        if (p.softplus) v[i] = softplus_of(v[i]);
-        v[i] = t < end ? v[i] : 0.0f;
-        x[i] *= v[i];
-      }
-      *reinterpret_cast<f32x4*>(&ldt[tile & 1][q][c4]) = f32x4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4*>(&ldx[tile & 1][q][c4]) = f32x4{x[0], x[1], x[2], x[3]};
-      if constexpr (JOIN) {
-        float gy[4], z[4];
-        P::open(gin[k], gy);
-        if (p.z.p) {
-          P::open(zin[k], z);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) gy[i] *= silu_of(z[i]);
-        }
-        *reinterpret_cast<f32x4*>(&lgy[tile & 1][q][c4]) = f32x4{gy[0], gy[1], gy[2], gy[3]};
-      }
-    }
-  };
-  RowRaw<BF> brow, crow;
-  const int64_t bo = int64_t(b) * p.b.sb + int64_t(g) * p.b.sg, co = int64_t(b) * p.c.sb + int64_t(g) * p.c.sg;
-  const auto read_rows = [&](int tile) {
-    const int t = s0 + tile * kTile + lane % kTile;
-    const bool live = t < end;
-    brow.load(p.b, bo + int64_t(live ? t : 0) * p.b.st, n0, p.N, live);
-    if (JOIN) crow.load(p.c, co + int64_t(live ? t : 0) * p.c.st, n0, p.N, live);
-  };
-  const bool is = lane < channels;
-  const int64_t d = d0 + lane;
-  float rate[kScanStates], h[kScanStates], through[kScanStates], adj[kScanStates], steps = 0.0f;
-  rates(p.a, d, n0, p.N, is, rate);
-  read_states(JOIN ? nullptr : p.initial, int64_t(b) * p.D + d, n0, p.N, is, h);
-#pragma unroll
-  for (int i = 0; i < kScanStates; ++i) {
-    through[i] = 1.0f;
-    adj[i] = 0.0f;
-  }
-  const auto mark = [&](int t) {
-    if (!is) return;
-    const int64_t row = int64_t(b) * p.row_marks + t / kMarkTokens;
-    *reinterpret_cast<f32x4*>(p.marks + packed_at(p, row, wave, d)) = f32x4{h[0], h[1], h[2], h[3]};
-    if (JOIN && wave == 0) p.mark_steps[row * p.D + d] = steps;
-  };
-  if (tiles > 0) {
-    read(0);
-    read_rows(0);
-    convert(0);
-    if (tiles > 1) read(1);
-  }
-  __syncthreads();
-  for (int tile = 0; tile < tiles; ++tile) {
-    const int buf = tile & 1, t0 = s0 + tile * kTile;
-    float bv[kScanStates], cv[kScanStates];
-    brow.open(bv);
-    if (JOIN) crow.open(cv);
-    if (tile + 1 < tiles) read_rows(tile + 1);
-    each<kTile>([&](auto J) {
-      constexpr int j = decltype(J)::value;
-      if (j == 0) mark(t0);
-      if (j == kMarkTokens && t0 + kMarkTokens < end) mark(t0 + kMarkTokens);
-      const float dt = ldt[buf][j][lane], dx = ldx[buf][j][lane];
-#pragma unroll
-      for (int i = 0; i < kScanStates; ++i) {
-        const float e = exp2_of(dt * rate[i]);
-        h[i] = fmaf(e, h[i], of_token<j>(bv[i]) * dx);
-        if constexpr (JOIN) {
-          through[i] *= e;
-          adj[i] = fmaf(through[i], of_token<j>(cv[i]) * lgy[buf][j][lane], adj[i]);
-        }
-      }
-      steps += dt;
-    });
-    if (tile + 1 < tiles) {
-      convert(tile + 1);
-      if (tile + 2 < tiles) read(tile + 2);
-    }
-    __syncthreads();
-  }
-  if (JOIN && is) {
-    const int64_t row = int64_t(seg) * p.B + b;
-    *reinterpret_cast<f32x4*>(p.seg_state + packed_at(p, row, wave, d)) = f32x4{h[0], h[1], h[2], h[3]};
-    *reinterpret_cast<f32x4*>(p.seg_adjoint + packed_at(p, row, wave, d)) = f32x4{adj[0], adj[1], adj[2], adj[3]};
-    if (wave == 0) p.seg_steps[row * p.D + d] = steps;
-  }
-}
 
 // A segment's own state becomes the one at its start (blockIdx.y 0), its own adjoint the one that enters at its
 // end (1).
@@ -206,53 +65,95 @@ __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
 }
 
-// v[k] summed over the wave's lanes, in lane k. Registers k and k + H become one whose lanes with bit H of their
-// number clear hold k's sum so far, the others that of k + H.
-__device__ __forceinline__ float fold64(float (&v)[64], int lane) {
-#pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[k]), __float_as_uint(v[k + 32]), false, false);
-    v[k] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-  }
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[k]), __float_as_uint(v[k + 16]), false, false);
-    v[k] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-  }
-  // within a row of 16 the partner is the mirrored lane of the row, of its half, then two and one lanes away
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const bool up = lane & 8;
-    v[k] = (up ? v[k + 8] : v[k]) + dpp<0x140>(up ? v[k] : v[k + 8]);
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const bool up = lane & 4;
-    v[k] = (up ? v[k + 4] : v[k]) + dpp<0x141>(up ? v[k] : v[k + 4]);
-  }
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const bool up = lane & 2;
-    v[k] = (up ? v[k + 2] : v[k]) + dpp<0x4e>(up ? v[k] : v[k + 2]);
-  }
-  const bool up = lane & 1;
-  return (up ? v[1] : v[0]) + dpp<0xb1>(up ? v[0] : v[1]);
+// Sums over lanes: a step adds two registers into one whose lanes with a bit of their number clear hold the first's
+// sum so far and the others the second's. Bit 3's partner is the mirrored lane of the row of 16, bit 2's that of its
+// half, and which register a lane takes is the instruction's bank mask. Of the eight sums of a token: four in each
+// of two registers. The wait is for a sum that was written just before.
+__device__ __forceinline__ void fold_token(const float (&v)[8], float (&s)[2]) {
+  float r[4];
+#define SX_PAIR(O, A, B, HOW, LOW, HIGH)                                            \
+  "v_add_f32_dpp %" O ", %" A ", %" A " " HOW " row_mask:0xf bank_mask:" LOW "\n\t" \
+  "v_add_f32_dpp %" O ", %" B ", %" B " " HOW " row_mask:0xf bank_mask:" HIGH "\n\t"
+#define SX_ROW(O, A, B) SX_PAIR(O, A, B, "row_mirror", "0x3", "0xc")
+#define SX_HALF(O, A, B) SX_PAIR(O, A, B, "row_half_mirror", "0x5", "0xa")
+  asm("s_nop 1\n\t" SX_ROW("2", "6", "10") SX_ROW("3", "7", "11") SX_ROW("4", "8", "12") SX_ROW("5", "9", "13")
+          SX_HALF("0", "2", "4") SX_HALF("1", "3", "5")
+      : "=&v"(s[0]), "=&v"(s[1]), "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3])
+      : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]));
+#undef SX_HALF
+#undef SX_ROW
+#undef SX_PAIR
 }
 
-constexpr int kWide = 128;  // channels of a workgroup of grad_march
+// ... and of eight tokens: rows of 16 lanes (bits 5 and 4) take the tokens apart, quads are summed whole, and lane k
+// of a quad keeps the fourth register k. The lane's sum is of token 4 bit5 + 2 bit4 + bit1, of b (bit 3 clear) or c,
+// state 2 bit2 + bit0.
+__device__ __forceinline__ float fold_tokens(float (&s)[8][2], int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(s[j][m]), __float_as_uint(s[j + 4][m]), false, false);
+      s[j][m] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(s[j][m]), __float_as_uint(s[j + 2][m]), false, false);
+      s[j][m] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+      s[j][m] += dpp<0xb1>(s[j][m]);
+      s[j][m] += dpp<0x4e>(s[j][m]);
+    }
+  const float even = lane & 1 ? s[0][1] : s[0][0], odd = lane & 1 ? s[1][1] : s[1][0];
+  return lane & 2 ? odd : even;
+}
+
+// lam = mu + c gy in place of mu, and source = sum over states of b lam, of token J's rows in two channels: lane J of
+// each row of 16 has b, lane 8 + J c (see read_out).
+template <int J>
+__device__ __forceinline__ void adjoints(const float (&rows)[kScanStates], const float (&gy)[2],
+                                         float (&mu)[2][kScanStates], float (&source)[2]) {
+#define SX_AT(N) " row_newbcast:%" N " row_mask:0xf bank_mask:0xf\n\t"
+#define SX_LAM(G, M0, M1, M2, M3)                                                    \
+  "v_fmac_f32_dpp %" M0 ", %10, %" G SX_AT("17") "v_fmac_f32_dpp %" M1 ", %11, %" G SX_AT("17") \
+      "v_fmac_f32_dpp %" M2 ", %12, %" G SX_AT("17") "v_fmac_f32_dpp %" M3 ", %13, %" G SX_AT("17")
+#define SX_SOURCE(O, M0, M1, M2, M3)                                                 \
+  "v_mul_f32_dpp %" O ", %10, %" M0 SX_AT("16") "v_fmac_f32_dpp %" O ", %11, %" M1 SX_AT("16") \
+      "v_fmac_f32_dpp %" O ", %12, %" M2 SX_AT("16") "v_fmac_f32_dpp %" O ", %13, %" M3 SX_AT("16")
+  asm("s_nop 1\n\t" SX_LAM("14", "0", "1", "2", "3") SX_LAM("15", "4", "5", "6", "7")
+          SX_SOURCE("8", "0", "1", "2", "3") SX_SOURCE("9", "4", "5", "6", "7")
+      : "+v"(mu[0][0]), "+v"(mu[0][1]), "+v"(mu[0][2]), "+v"(mu[0][3]), "+v"(mu[1][0]), "+v"(mu[1][1]),
+        "+v"(mu[1][2]), "+v"(mu[1][3]), "=&v"(source[0]), "=&v"(source[1])
+      : "v"(rows[0]), "v"(rows[1]), "v"(rows[2]), "v"(rows[3]), "v"(gy[0]), "v"(gy[1]), "n"(J), "n"(J + 8));
+#undef SX_SOURCE
+#undef SX_LAM
+#undef SX_AT
+}
+
+constexpr int kWide = kGradChannels;
 
 template <int W>
-struct GradLds {
+struct alignas(16) GradLds {
   float dt[kMarkTokens][kWide], x[kMarkTokens][kWide], gy[kMarkTokens][kWide];
+  float bias[kWide], skip[kWide];
+  // the waves' parts of y, of sum b lam and of sum a q
   float y[W][kMarkTokens][kWide], source[W][kMarkTokens][kWide], decay[W][kMarkTokens][kWide];
 };
 
-template <bool BF, int W, bool WIDE, bool JOIN>
-__global__ __launch_bounds__(kWave* W) void grad_march(SsParams p) {
+// Two waves a SIMD, but where a thread has so many pieces of a span that the registers do not suffice for it (4 x 1024
+// tokens of 2048 channels of 4 states in f32: 156 us, 306 with two).
+constexpr int grad_waves_per_simd(bool bf16, int W) { return W == 1 || (W == 2 && !bf16) ? 1 : 2; }
+
+template <bool BF, int W, Rows R, bool JOIN>
+__global__ __launch_bounds__(kWave* W, grad_waves_per_simd(BF, W)) void grad_march(SsParams p) {
   using P = Piece<BF, 4>;
   using Raw = typename P::Raw;
-  constexpr int M = kMarkTokens;
-  constexpr int kPieces = M * kWide / 4, kPasses = (kPieces + kWave * W - 1) / (kWave * W);
+  constexpr int M = kMarkTokens, kThreads = kWave * W;
+  static_assert(M == 8, "the sums over lanes take eight tokens");
+  constexpr int kPieces = M * kWide / 4, kPasses = (kPieces + kThreads - 1) / kThreads;
+  constexpr int kStep = kThreads / (kWide / 4), kAtOnce = kStep < M ? kStep : M;
+  constexpr bool WHOLE = R != Rows::Any;
   __shared__ GradLds<W> l;
   const int tid = int(threadIdx.x), lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int n0 = wave * kScanStates;
@@ -266,46 +167,37 @@ __global__ __launch_bounds__(kWave* W) void grad_march(SsParams p) {
   const int d0 = g * per_group + cb * kWide, channels = min(kWide, per_group - cb * kWide);
   const int s0 = seg * p.seg_tokens, s1 = min(s0 + p.seg_tokens, p.T);
   const int end = min(s1, row_length(p.lengths, b, p.T));
-  const int spans = end > s0 ? (end - s0 + M - 1) / M : 0;
-  const int q0 = tid / (kWide / 4), c4 = tid % (kWide / 4) * 4, left = channels - c4;
-  constexpr int kStep = W * kWave / (kWide / 4), kAtOnce = kStep < M ? kStep : M;
-  const bool mine = left > 0 && q0 < M;
-  float bias[4], skip[4], gskip[4] = {}, gbias[4] = {};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool is = mine && i < left;
-    bias[i] = is && p.delta_bias ? p.delta_bias[d0 + c4 + i] : 0.0f;
-    skip[i] = is && p.skip ? p.skip[d0 + c4 + i] : 0.0f;
+  const int last = end - s0 - 1, spans = last >= 0 ? last / M + 1 : 0;
+  const int q0 = tid / (kWide / 4), c0 = tid % (kWide / 4) * 4;
+  const int c4 = R == Rows::Early ? min(c0, channels - 4) : c0, left = channels - c4;
+  const bool mine = left > 0 && q0 < M, working = kThreads <= kPieces || q0 < M;
+  float gskip[4] = {}, gbias[4] = {};
+  for (int c = tid; c < kWide; c += kThreads) {
+    l.bias[c] = c < channels && p.delta_bias ? p.delta_bias[d0 + c] : 0.0f;
+    l.skip[c] = c < channels && p.skip ? p.skip[d0 + c] : 0.0f;
   }
-  const int64_t xo = int64_t(b) * p.x.sb + int64_t(d0 + c4) * p.x.sd;
-  const int64_t deltao = int64_t(b) * p.delta.sb + int64_t(d0 + c4) * p.delta.sd;
-  const int64_t zo = int64_t(b) * p.z.sb + int64_t(d0 + c4) * p.z.sd;
-  const int64_t goo = int64_t(b) * p.go.sb + int64_t(d0 + c4) * p.go.sd;
-  Raw xin[kPasses], din[kPasses], zin[kPasses], gin[kPasses];
-  Raw xnow[kPasses], dnow[kPasses], znow[kPasses], gnow[kPasses];
-  const auto read = [&](int span) {
+  const TileReader<BF, R> xr(p.x, b, s0, d0, c4, channels), dr(p.delta, b, s0, d0, c4, channels);
+  const TileReader<BF, R> zr(p.z, b, s0, d0, c4, channels), gr(p.go, b, s0, d0, c4, channels);
+  const bool gated = p.z.p;
+  struct Pieces {
+    Raw x[kPasses], delta[kPasses], z[kPasses], go[kPasses];
+  };
+  const auto read = [&](int span, Pieces& to) {
+    if (!working) return;
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
-      const int t = s0 + span * M + q0 + k * kStep;
-      const bool live = mine && q0 + k * kStep < M && t < end;
-      xin[k] = live ? four_channels<BF, WIDE>(p.x, xo + int64_t(t) * p.x.st, left) : P::zero();
-      din[k] = live ? four_channels<BF, WIDE>(p.delta, deltao + int64_t(t) * p.delta.st, left) : P::zero();
-      gin[k] = live ? four_channels<BF, WIDE>(p.go, goo + int64_t(t) * p.go.st, left) : P::zero();
-      if (p.z.p) zin[k] = live ? four_channels<BF, WIDE>(p.z, zo + int64_t(t) * p.z.st, left) : P::zero();
+      const int q = q0 + k * kStep;
+      to.x[k] = xr.read(p.x, span * M, q, last, left);
+      to.delta[k] = dr.read(p.delta, span * M, q, last, left);
+      to.go[k] = gr.read(p.go, span * M, q, last, left);
+      if (gated) to.z[k] = zr.read(p.z, span * M, q, last, left);
     }
   };
-  const auto step_of = [&](float v) { return p.softplus ? softplus_of(v) : v; };
+  Pieces in;
 
   // lanes 0 .. 7 of each row of 16 have the tokens' rows of b, 8 .. 15 those of c
-  RowRaw<BF> rows;
-  const bool second = lane & M;
-  const RowView& rv = second ? p.c : p.b;
-  const int64_t ro = int64_t(b) * rv.sb + int64_t(g) * rv.sg;
-  const auto read_rows = [&](int span) {
-    const int t = s0 + span * M + lane % M;
-    const bool live = t < end;
-    rows.load(rv, ro + int64_t(live ? t : 0) * rv.st, n0, p.N, live);
-  };
+  RowReader<BF, false> rows(lane & M ? p.c : p.b, b, g, s0, n0, p.N);
+  const int j8 = lane % M;
 
   // two channels a lane
   const int64_t d = d0 + 2 * lane;
@@ -338,54 +230,56 @@ __global__ __launch_bounds__(kWave* W) void grad_march(SsParams p) {
   };
 
   // channels that do not exist add nothing to the sums over channels
-  for (int i = tid; i < M * kWide; i += kWave * W) {
+  for (int i = tid; i < M * kWide; i += kThreads) {
     (&l.dt[0][0])[i] = 0.0f;
     (&l.x[0][0])[i] = 0.0f;
     (&l.gy[0][0])[i] = 0.0f;
   }
   if (spans > 0) {
-    read(spans - 1);
-    read_rows(spans - 1);
+    read(spans - 1, in);
+    rows.read((spans - 1) * M, j8, last);
     read_marks(spans - 1);
   }
   __syncthreads();
   for (int span = spans - 1; span >= 0; --span) {
-    const int t0 = s0 + span * M;
+    const int t0 = span * M, room = last - t0;  // room: the last token of the span there is
     // dt, x and gy of the tokens
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
       const int q = q0 + k * kStep;
-      xnow[k] = xin[k];
-      dnow[k] = din[k];
-      gnow[k] = gin[k];
-      znow[k] = zin[k];
-      if (!mine || q >= M) continue;
+      if (!mine || (kPasses * kStep > M && q >= M)) continue;
       float x[4], v[4], gy[4], z[4];
-      P::open(xin[k], x);
-      P::open(din[k], v);
-      P::open(gin[k], gy);
-      if (p.z.p) {
-        P::open(zin[k], z);
+      P::open(in.x[k], x);
+      P::open(in.delta[k], v);
+      P::open(in.go[k], gy);
+      if (gated) {
+        P::open(in.z[k], z);
 #pragma unroll
         for (int i = 0; i < 4; ++i) gy[i] *= silu_of(z[i]);
       }
+      lds_add<R>(l.bias, c4, v);
+      if (p.softplus) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = t0 + q < end && i < left ? step_of(v[i] + bias[i]) : 0.0f;
-      if (!WIDE) {
+        for (int i = 0; i < 4; ++i) v[i] = softplus_of(v[i]);
+      }
+      if (!WHOLE || room < M - 1) {  // a token or channel that does not exist
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[i] = i < left ? x[i] : 0.0f;
-          gy[i] = i < left ? gy[i] : 0.0f;
+          const bool there = q <= room && i < left;
+          v[i] = there ? v[i] : 0.0f;
+          x[i] = there ? x[i] : 0.0f;
+          gy[i] = there ? gy[i] : 0.0f;
         }
       }
-      *reinterpret_cast<f32x4*>(&l.dt[q][c4]) = f32x4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4*>(&l.x[q][c4]) = f32x4{x[0], x[1], x[2], x[3]};
-      *reinterpret_cast<f32x4*>(&l.gy[q][c4]) = f32x4{gy[0], gy[1], gy[2], gy[3]};
+      lds_put<R>(l.dt[q], c4, v);
+      lds_put<R>(l.x[q], c4, x);
+      lds_put<R>(l.gy[q], c4, gy);
     }
     float rowv[kScanStates];  // of b and of c
-    rows.open(rowv);
-    // the states before each token, from the mark on; and the decays
-    float hs[M + 1][2][kScanStates], es[M][2][kScanStates];
+    rows.open(t0, j8, last, M, rowv);
+    // the states before each token, from the mark on; the decays are formed again on the way back, which their
+    // registers are worth
+    float hs[M + 1][2][kScanStates];
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -393,92 +287,130 @@ __global__ __launch_bounds__(kWave* W) void grad_march(SsParams p) {
         hs[0][c][i] = marks[c][i];
         if constexpr (JOIN) hs[0][c][i] = fmaf(exp2_of(mark_steps[c] * rate[c][i]), start[c][i], hs[0][c][i]);
       }
-    if (span > 0) {
-      read(span - 1);
-      read_rows(span - 1);
-      read_marks(span - 1);
-    }
     __syncthreads();
-    each<M>([&](auto J) {
-      constexpr int j = decltype(J)::value;
-      float y[2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float dt = l.dt[j][2 * lane + c], dx = dt * l.x[j][2 * lane + c];
-        y[c] = 0.0f;
+    each<2>([&](auto Q) {
+      constexpr int j4 = 4 * decltype(Q)::value;
+      float dx[4][2], es[4][2][kScanStates];
+      each<4>([&](auto J) {
+        constexpr int k = decltype(J)::value, j = j4 + k;
+        const float2 dt = *reinterpret_cast<const float2*>(&l.dt[j][2 * lane]);
+        const float2 x = *reinterpret_cast<const float2*>(&l.x[j][2 * lane]);
+        dx[k][0] = dt.x * x.x;
+        dx[k][1] = dt.y * x.y;
 #pragma unroll
         for (int i = 0; i < kScanStates; ++i) {
-          es[j][c][i] = exp2_of(dt * rate[c][i]);
-          hs[j + 1][c][i] = fmaf(es[j][c][i], hs[j][c][i], of_token<j>(rowv[i]) * dx);
-          y[c] = fmaf(of_token<M + j>(rowv[i]), hs[j + 1][c][i], y[c]);
+          es[k][0][i] = exp2_of(dt.x * rate[0][i]);
+          es[k][1][i] = exp2_of(dt.y * rate[1][i]);
         }
+      });
+      __builtin_amdgcn_sched_barrier(0);
+      each<4>([&](auto J) {
+        constexpr int k = decltype(J)::value, j = j4 + k;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < kScanStates; ++i) hs[j + 1][c][i] = fmaf(es[k][c][i], hs[j][c][i], of_token<j>(rowv[i]) * dx[k][c]);
+      });
+      if (gated) {
+        float y[2][4];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float after[4][kScanStates] = {
+              {hs[j4 + 1][c][0], hs[j4 + 1][c][1], hs[j4 + 1][c][2], hs[j4 + 1][c][3]},
+              {hs[j4 + 2][c][0], hs[j4 + 2][c][1], hs[j4 + 2][c][2], hs[j4 + 2][c][3]},
+              {hs[j4 + 3][c][0], hs[j4 + 3][c][1], hs[j4 + 3][c][2], hs[j4 + 3][c][3]},
+              {hs[j4 + 4][c][0], hs[j4 + 4][c][1], hs[j4 + 4][c][2], hs[j4 + 4][c][3]}};
+          read_out<M + j4>(rowv, after, y[c]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<float2*>(&l.y[wave][j4 + k][2 * lane]) = make_float2(y[0][k], y[1][k]);
       }
-      if (p.z.p) *reinterpret_cast<float2*>(&l.y[wave][j][2 * lane]) = make_float2(y[0], y[1]);
     });
-    float sums[64];  // token, b or c, state
+    float sums[M][2];
+    Pieces now;
     each<M>([&](auto J) {
       constexpr int j = M - 1 - decltype(J)::value;
-      float source[2], decay[2];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sums[8 * j + i] = 0.0f;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float dt = l.dt[j][2 * lane + c], dx = dt * l.x[j][2 * lane + c], gy = l.gy[j][2 * lane + c];
-        source[c] = decay[c] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kScanStates; ++i) {
-          const float lam = fmaf(of_token<M + j>(rowv[i]), gy, mu[c][i]);
-          sums[8 * j + i] = fmaf(lam, dx, sums[8 * j + i]);
-          sums[8 * j + 4 + i] = fmaf(gy, hs[j + 1][c][i], sums[8 * j + 4 + i]);
-          source[c] = fmaf(of_token<j>(rowv[i]), lam, source[c]);
-          mu[c][i] = es[j][c][i] * lam;
-          const float q = mu[c][i] * hs[j][c][i];
-          ga[c][i] = fmaf(dt, q, ga[c][i]);
-          decay[c] = fmaf(rate[c][i], q, decay[c]);
+      // half of the states are done with: their registers take this span's operands once more, for the results, and
+      // the next one's
+      if constexpr (j == M / 2 - 1) {
+        read(span, now);
+        if (span > 0) {
+          read(span - 1, in);
+          rows.read(t0 - M, j8, last);
+          read_marks(span - 1);
         }
       }
+      const float2 dt2 = *reinterpret_cast<const float2*>(&l.dt[j][2 * lane]);
+      const float2 x2 = *reinterpret_cast<const float2*>(&l.x[j][2 * lane]);
+      const float2 gy2 = *reinterpret_cast<const float2*>(&l.gy[j][2 * lane]);
+      const float dt[2] = {dt2.x, dt2.y}, x[2] = {x2.x, x2.y}, gy[2] = {gy2.x, gy2.y};
+      float source[2], decay[2] = {0.0f, 0.0f}, shares[8];
+      adjoints<j>(rowv, gy, mu, source);  // mu is lam here
+#pragma unroll
+      for (int i = 0; i < kScanStates; ++i) {
+        shares[i] = fmaf(mu[1][i], dt[1] * x[1], mu[0][i] * (dt[0] * x[0]));
+        shares[4 + i] = fmaf(gy[1], hs[j + 1][1][i], gy[0] * hs[j + 1][0][i]);
+      }
+      fold_token(shares, sums[j]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < kScanStates; ++i) {
+          mu[c][i] *= exp2_of(dt[c] * rate[c][i]);
+          const float q = mu[c][i] * hs[j][c][i];
+          ga[c][i] = fmaf(dt[c], q, ga[c][i]);
+          decay[c] = fmaf(rate[c][i], q, decay[c]);
+        }
       *reinterpret_cast<float2*>(&l.source[wave][j][2 * lane]) = make_float2(source[0], source[1]);
       *reinterpret_cast<float2*>(&l.decay[wave][j][2 * lane]) = make_float2(decay[0], decay[1]);
+      // no more than two tokens' operands at a time: with all eight's the wave's registers do not suffice
+      if constexpr (j % 2 == 0) __builtin_amdgcn_sched_barrier(0);
     });
-    const float sum = fold64(sums, lane);
     {
-      const int t = t0 + lane / 8, which = lane / 4 % 2, n = n0 + lane % 4;
-      if (t < end)
-        p.rows_partial[(((int64_t(b) * p.G + g) * p.T + t) * blocks + cb) * (8 * W) + which * 4 * W + n] = sum;
+      const float sum = fold_tokens(sums, lane);
+      const int q = (lane >> 5 & 1) * 4 + (lane >> 4 & 1) * 2 + (lane >> 1 & 1), which = lane >> 3 & 1;
+      const int n = n0 + (lane >> 2 & 1) * 2 + (lane & 1);
+      if (q <= room)
+        p.rows_partial[(((int64_t(b) * p.G + g) * p.T + s0 + t0 + q) * blocks + cb) * (8 * W) + which * 4 * W + n] = sum;
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
-      const int q = q0 + k * kStep, t = t0 + q;
-      if (!mine || q >= M || t >= end) continue;
+      const int q = q0 + k * kStep;
+      if (!mine || q > room || (kPasses * kStep > M && q >= M)) continue;
       float x[4], v[4], go[4], z[4], gx[4], gd[4], gz[4];
-      P::open(xnow[k], x);
-      P::open(dnow[k], v);
-      P::open(gnow[k], go);
-      if (p.z.p) P::open(znow[k], z);
-      f32x4 y = zero4(), source = zero4(), decay = zero4();
+      P::open(now.x[k], x);
+      P::open(now.delta[k], v);
+      P::open(now.go[k], go);
+      if (gated) P::open(now.z[k], z);
+      float y[4], source[4] = {}, decay[4] = {}, dt[4] = {}, gy[4] = {}, skip[4] = {};
+      lds_add<R>(l.bias, c4, v);
+      lds_add<R>(l.skip, c4, skip);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = skip[i] * x[i];
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        if (p.z.p) y += *reinterpret_cast<const f32x4*>(&l.y[w][q][c4]);
-        source += *reinterpret_cast<const f32x4*>(&l.source[w][q][c4]);
-        decay += *reinterpret_cast<const f32x4*>(&l.decay[w][q][c4]);
+        if (gated) lds_add<R>(l.y[w][q], c4, y);
+        lds_add<R>(l.source[w][q], c4, source);
+        lds_add<R>(l.decay[w][q], c4, decay);
       }
-      const f32x4 dt = *reinterpret_cast<const f32x4*>(&l.dt[q][c4]);
-      const f32x4 gy = *reinterpret_cast<const f32x4*>(&l.gy[q][c4]);
+      lds_add<R>(l.dt[q], c4, dt);
+      lds_add<R>(l.gy[q], c4, gy);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         gx[i] = fmaf(dt[i], source[i], skip[i] * gy[i]);
         gskip[i] = fmaf(gy[i], x[i], gskip[i]);
         // the rates stand times log2(e)
         gd[i] = fmaf(decay[i], 1.0f / kLog2e, x[i] * source[i]);
-        if (p.softplus) gd[i] *= sigmoid_of(v[i] + bias[i]);
+        if (p.softplus) gd[i] *= sigmoid_of(v[i]);
         gbias[i] += gd[i];
-        if (p.z.p) gz[i] = go[i] * fmaf(skip[i], x[i], y[i]) * silu_slope(z[i]);
+        if (gated) gz[i] = go[i] * y[i] * silu_slope(z[i]);
       }
-      const int64_t o = (int64_t(b) * p.T + t) * p.D + d0 + c4;
-      put_channels<BF, WIDE>(p.gx, o, left, gx);
-      put_channels<BF, WIDE>(p.gdelta, o, left, gd);
-      if (p.z.p) put_channels<BF, WIDE>(p.gz, o, left, gz);
+      const int64_t o = (int64_t(b) * p.T + s0 + t0) * p.D + d0 + (int64_t(q) * p.D + c4);
+      put_channels<BF, WHOLE>(p.gx, o, left, gx);
+      put_channels<BF, WHOLE>(p.gdelta, o, left, gd);
+      if (gated) put_channels<BF, WHOLE>(p.gz, o, left, gz);
     }
     // the next span's dt, x and gy go where these were read
     __syncthreads();
@@ -488,9 +420,9 @@ __global__ __launch_bounds__(kWave* W) void grad_march(SsParams p) {
     const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int t = max(end, s0) + q0; t < s1; t += kAtOnce) {
       const int64_t o = (int64_t(b) * p.T + t) * p.D + d0 + c4;
-      put_channels<BF, WIDE>(p.gx, o, left, none);
-      put_channels<BF, WIDE>(p.gdelta, o, left, none);
-      if (p.z.p) put_channels<BF, WIDE>(p.gz, o, left, none);
+      put_channels<BF, WHOLE>(p.gx, o, left, none);
+      put_channels<BF, WHOLE>(p.gdelta, o, left, none);
+      if (gated) put_channels<BF, WHOLE>(p.gz, o, left, none);
     }
   }
   const int64_t row = int64_t(seg) * p.B + b;
@@ -509,7 +441,7 @@ __global__ __launch_bounds__(kWave* W) void grad_march(SsParams p) {
     }
   }
   __syncthreads();
-  for (int c = tid; c < channels; c += kWave * W) {
+  for (int c = tid; c < channels; c += kThreads) {
     float a = 0.0f, v = 0.0f;
 #pragma unroll
     for (int q = 0; q < kAtOnce; ++q) {
@@ -542,32 +474,33 @@ __global__ __launch_bounds__(256) void token_rows(SsParams p, int blocks) {
   Piece<BF, 1>::store(out + ((int64_t(b) * p.T + t) * p.G + g) * p.N + n, {v});
 }
 
-template <bool BF, int W, bool WIDE, bool JOIN>
+template <bool BF, int W, Rows R, bool JOIN>
 hipError_t launch_join(const SsParams& p, hipStream_t stream) {
   const int64_t per_group = p.D / p.G;
   const int64_t units = int64_t(p.G) * p.B * p.segments;
-  mark_states<BF, W, WIDE, JOIN>
+  scan_march<BF, W, R, JOIN ? March::JoinedMarks : March::Marks>
       <<<unsigned((per_group + kChannels - 1) / kChannels * units), kWave * W, 0, stream>>>(p);
   if (JOIN) {
     const int64_t n = int64_t(p.B) * p.waves * p.D;
     carry<<<dim3(unsigned((n + 255) / 256), 2), 256, 0, stream>>>(p);
   }
-  grad_march<BF, W, WIDE, JOIN><<<unsigned((per_group + kWide - 1) / kWide * units), kWave * W, 0, stream>>>(p);
+  grad_march<BF, W, R, JOIN><<<unsigned((per_group + kWide - 1) / kWide * units), kWave * W, 0, stream>>>(p);
   return hipGetLastError();
 }
 
-template <bool BF, int W, bool WIDE>
+template <bool BF, int W, Rows R>
 hipError_t launch_waves(const SsParams& p, hipStream_t stream) {
-  return p.segments > 1 ? launch_join<BF, W, WIDE, true>(p, stream) : launch_join<BF, W, WIDE, false>(p, stream);
+  return p.segments > 1 ? launch_join<BF, W, R, true>(p, stream) : launch_join<BF, W, R, false>(p, stream);
 }
 
-template <bool BF, bool WIDE>
+template <bool BF, Rows R>
 hipError_t launch_states(const SsParams& p, hipStream_t stream) {
   switch (p.waves) {
-    case 1: return launch_waves<BF, 1, WIDE>(p, stream);
-    case 2: return launch_waves<BF, 2, WIDE>(p, stream);
-    case 4: return launch_waves<BF, 4, WIDE>(p, stream);
-    default: return launch_waves<BF, 8, WIDE>(p, stream);
+    case 1: return launch_waves<BF, 1, R>(p, stream);
+    case 2: return launch_waves<BF, 2, R>(p, stream);
+    case 3: return launch_waves<BF, 3, R>(p, stream);
+    case 4: return launch_waves<BF, 4, R>(p, stream);
+    default: return launch_waves<BF, 8, R>(p, stream);
   }
 }
 
@@ -576,12 +509,14 @@ hipError_t launch_states(const SsParams& p, hipStream_t stream) {
 int selective_scan_grad_blocks(const SsParams& p) { return (p.D / p.G + kWide - 1) / kWide; }
 
 hipError_t launch_selective_scan_backward(const SsParams& p, hipStream_t stream) {
-  const bool wide = p.x.sd == 1 && p.delta.sd == 1 && p.go.sd == 1 && (!p.z.p || p.z.sd == 1) &&
-                    (p.D / p.G) % 4 == 0;
   hipError_t err = hipSuccess;
   if (p.B > 0) {
-    if (p.bf16) err = wide ? launch_states<true, true>(p, stream) : launch_states<true, false>(p, stream);
-    else err = wide ? launch_states<false, true>(p, stream) : launch_states<false, false>(p, stream);
+    // both passes': workgroups of 64 and of 128 channels have four at least
+    const Rows rows = scan_rows(p, true, kWide);
+    const Rows r = rows == Rows::Any ? rows : scan_rows(p, true, kChannels);
+    if (r == Rows::Whole) err = p.bf16 ? launch_states<true, Rows::Whole>(p, stream) : launch_states<false, Rows::Whole>(p, stream);
+    else if (r == Rows::Early) err = p.bf16 ? launch_states<true, Rows::Early>(p, stream) : launch_states<false, Rows::Early>(p, stream);
+    else err = p.bf16 ? launch_states<true, Rows::Any>(p, stream) : launch_states<false, Rows::Any>(p, stream);
     if (err != hipSuccess) return err;
     const int64_t n = int64_t(p.B) * p.G * p.T * 8 * p.waves;
     const int blocks = selective_scan_grad_blocks(p);

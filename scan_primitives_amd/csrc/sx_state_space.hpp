@@ -81,7 +81,7 @@ constexpr int kScanStates = 4;  // states a wave holds of each of its channels
 
 struct SsParams {
   int B, T, D, G, N;
-  int waves;               // of a workgroup: ceil(N / 4), to a power of two
+  int waves;               // of a workgroup: ceil(N / 4), eight above four
   TokenView x, delta, z;   // z.p nullptr: no gate
   RowView b, c;
   const float* a;          // [D, N]
@@ -111,6 +111,7 @@ struct SsParams {
   float *ga, *gskip, *gbias, *ginitial;
 };
 constexpr int kMarkTokens = 8;
+constexpr int kGradChannels = 128;  // of a workgroup of the gradient's march
 int selective_scan_grad_blocks(const SsParams& p);  // workgroups a group's channels make
 void selective_scan_split(SsParams& p, bool gradient);
 hipError_t launch_selective_scan(const SsParams& p, hipStream_t stream);
