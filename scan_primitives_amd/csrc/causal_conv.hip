@@ -134,7 +134,7 @@ __global__ __launch_bounds__(kThreads) void conv_forward(CcParams p) {
 #pragma unroll
         for (int k = 0; k < V; ++k) u[k] = silu_of(u[k]);
       }
-      if (t + i < end) P::store(out + int64_t(t + i) * p.D, u);
+      if (t + i < end) store_stream<BF, V>(out + int64_t(t + i) * p.D, u);
       C::shift(past, v[i]);
     }
   }
@@ -342,9 +342,11 @@ int piece_channels(const CcParams& p, bool gradient) {
 void causal_conv_split(CcParams& p, bool gradient) {
   // whatever the strides, for the workspace goes by it
   const int64_t v = p.bf16 && !gradient ? 8 : 4, pieces = (p.D + v - 1) / v;
-  // eight waves a SIMD
-  const int64_t want = int64_t(device_cu_count()) * 4 * 8 * kWave / std::max<int64_t>(1, pieces * p.B);
-  const int64_t chunk = std::max<int64_t>(8, (p.T + std::max<int64_t>(want, 1) - 1) / std::max<int64_t>(want, 1));
+  // Two waves a SIMD (8 ragged rows of 2048 tokens of 4096 channels in bf16: 77, 68, 57, 48, 49 us with 16, 8, 4, 2, 1;
+  // the gradient of 4 x 2048 x 2048 54, 43, 35, 49 with 8, 4, 2, 1), of 8 tokens at least, 16 of a gradient, whose first
+  // and last are read twice.
+  const int64_t want = std::max<int64_t>(1, int64_t(device_cu_count()) * 4 * 2 * kWave / std::max<int64_t>(1, pieces * p.B));
+  const int64_t chunk = std::max<int64_t>(gradient ? 16 : 8, (p.T + want - 1) / want);
   p.chunk = int(std::min<int64_t>((chunk + kAhead - 1) / kAhead * kAhead, 1 << 20));
   p.chunks = int(std::max<int64_t>(1, (int64_t(p.T) + p.chunk - 1) / p.chunk));
 }

@@ -124,7 +124,7 @@ __global__ __launch_bounds__(kThreads) void rows_forward(GnParams p) {
         v[m][k] = fmaf(v[m][k] * r, ch[m].w[k], ch[m].bias[k]);
         if (p.silu) v[m][k] = silu_of(v[m][k]);
       }
-      if (is[m] && row < p.n) P::store(static_cast<E*>(p.out) + row * p.c + c[m], v[m]);
+      if (is[m] && row < p.n) store_stream<BF, V>(static_cast<E*>(p.out) + row * p.c + c[m], v[m]);
     }
   }
 }
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(kThreads) void rows_backward(GnParams p) {
     for (int m = 0; m < M; ++m) {
 #pragma unroll
       for (int k = 0; k < V; ++k) v[m][k] = r * (g[m][k] - s1 - v[m][k] * s2);
-      if (is[m] && row < p.n) P::store(static_cast<E*>(p.out) + row * p.c + c[m], v[m]);
+      if (is[m] && row < p.n) store_stream<BF, V>(static_cast<E*>(p.out) + row * p.c + c[m], v[m]);
     }
   }
   if (s.any) {
@@ -272,249 +272,371 @@ struct Place {
   __device__ __forceinline__ int groups_here(const GnParams& p) const { return min(k.groups, p.g - group); }
 };
 
-struct Moments {  // of `n` values: their mean and squared distances from it
-  float n, mean, m2;
-  __device__ __forceinline__ void join(const Moments& o) {
-    const float all = n + o.n, part = all > 0.0f ? o.n / all : 0.0f, off = o.mean - mean;
-    mean = fmaf(off, part, mean);
-    m2 += o.m2 + off * off * n * part;
-    n = all;
-  }
-  __device__ __forceinline__ void over_wave() {
+// f(position, count there are) of a thread's positions, kAtOnce at a time: what they read is on its way before the
+// first is used, which stores between them would keep apart.
+constexpr int kAtOnce = 4;
+template <int V, typename F>
+__device__ __forceinline__ void each_positions(const Place<V>& a, F&& f) {
+  for (int64_t t = a.p0 + a.off; t < a.p1; t += int64_t(a.k.rows) * kAtOnce)
+    f(t, int(min(int64_t(kAtOnce), (a.p1 - t + a.k.rows - 1) / a.k.rows)));
+}
+
+// Sums of K values a thread over the threads of its group, in every thread: a wave takes a group at a time. `v` are
+// zero in threads without a piece. Ends with l free again.
+template <int K, int V>
+__device__ __forceinline__ void group_sums_of(const GnParams& p, const Place<V>& a, float (*l)[kThreads], float (&v)[K]) {
+  const int tid = int(threadIdx.x), lane = tid % kWave, per = a.k.parts == 1 ? a.k.pieces : a.k.width;
 #pragma unroll
-    for (int m = 1; m < kWave; m *= 2) join({__shfl_xor(n, m), __shfl_xor(mean, m), __shfl_xor(m2, m)});
+  for (int k = 0; k < K; ++k) l[k][tid] = v[k];
+  __syncthreads();
+  for (int g = tid / kWave; g < a.groups_here(p); g += kThreads / kWave) {
+    float sum[K] = {};
+    for (int i = lane; i < per * a.k.rows; i += kWave) {
+      const int at = i / per * a.k.width + g * per + i % per;
+#pragma unroll
+      for (int k = 0; k < K; ++k) sum[k] += l[k][at];
+    }
+#pragma unroll
+    for (int m = 1; m < kWave; m *= 2)
+#pragma unroll
+      for (int k = 0; k < K; ++k) sum[k] += __shfl_xor(sum[k], m);
+    // the group's own first slot: no other wave reads it
+    if (lane == 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) l[k][g * per] = sum[k];
+    }
   }
+  __syncthreads();
+  const int g = a.any && a.k.parts == 1 ? a.piece / a.k.pieces : 0;
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = l[k][g * per];
+  __syncthreads();
+}
+
+struct Moments {  // of n values: their mean and squared distances from it
+  float n, mean, m2;
+};
+struct Norm {
+  float mean, r;
 };
 
+// The moments of a block's part of a thread's group. A thread sums differences from its first value, and the threads
+// differences from the mean of the group's first, so that no large mean cancels.
 template <bool BF, int V>
-__global__ __launch_bounds__(kThreads) void map_stats(GnParams p) {
+__device__ __forceinline__ Moments block_stats(const GnParams& p, const Place<V>& a, float (*l)[kThreads]) {
   using P = Piece<BF, V>;
   using E = typename P::E;
-  __shared__ Moments l[kThreads];
-  const Place<V> a(p);
   const E* x = static_cast<const E*>(p.x) + a.sample * p.xn + a.c;
-  // differences from the thread's first value
   float shift = 0.0f, sum = 0.0f, sq = 0.0f, n = 0.0f;
   if (a.any && a.p0 + a.off < a.p1) {
     float first[V];
     P::open(P::load(x + (a.p0 + a.off) * p.xs), first);
     shift = first[0];
-#pragma unroll 4
-    for (int64_t t = a.p0 + a.off; t < a.p1; t += a.k.rows) {
-      float v[V];
-      P::open(P::load(x + t * p.xs), v);
+    each_positions(a, [&](int64_t t, int count) {
+      typename P::Raw raw[kAtOnce];
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float d = v[k] - shift;
-        sum += d;
-        sq = fmaf(d, d, sq);
+      for (int i = 0; i < kAtOnce; ++i) raw[i] = P::load(x + (t + int64_t(min(i, count - 1)) * a.k.rows) * p.xs);
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (i >= count) break;
+        float v[V];
+        P::open(raw[i], v);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const float d = v[k] - shift;
+          sum += d;
+          sq = fmaf(d, d, sq);
+        }
+        n += float(V);
       }
-      n += float(V);
-    }
+    });
   }
-  const float off = n > 0.0f ? sum / n : 0.0f;
-  l[threadIdx.x] = {n, shift + off, fmaxf(sq - sum * off, 0.0f)};
+  const float mean = n > 0.0f ? shift + sum / n : 0.0f, m2 = n > 0.0f ? fmaxf(sq - sum * (sum / n), 0.0f) : 0.0f;
+  l[0][threadIdx.x] = mean;
   __syncthreads();
-  // a wave a group: its threads' values, of `pieces` pieces next to each other in each of the rows
-  const int lane = int(threadIdx.x) % kWave, per = a.k.parts == 1 ? a.k.pieces : a.k.width;
-  for (int g = int(threadIdx.x) / kWave; g < a.groups_here(p); g += kThreads / kWave) {
-    Moments m{0.0f, 0.0f, 0.0f};
-    for (int i = lane; i < per * a.k.rows; i += kWave) m.join(l[i / per * a.k.width + g * per + i % per]);
-    m.over_wave();
-    if (lane == 0) {
-      float* to = p.stats + ((((a.sample * p.chunks + a.chunk) * p.g) + a.group + g) * a.k.parts + a.part) * 3;
-      to[0] = m.n;
-      to[1] = m.mean;
-      to[2] = m.m2;
-    }
-  }
+  const int g = a.any && a.k.parts == 1 ? a.piece / a.k.pieces : 0;
+  const float about = l[0][g * (a.k.parts == 1 ? a.k.pieces : a.k.width)];  // the group's first piece has positions
+  __syncthreads();
+  const float off = mean - about;
+  float v[3] = {n, n * off, n > 0.0f ? fmaf(n * off, off, m2) : 0.0f};
+  group_sums_of<3>(p, a, l, v);
+  const float rest = v[1] / v[0];
+  return {v[0], about + rest, fmaxf(v[2] - v[1] * rest, 0.0f)};
 }
 
-// Mean and 1 / sqrt(variance + eps) of the block's groups, from all chunks, into lm and lr.
+// The first thread of each of the block's groups.
 template <int V>
-__device__ __forceinline__ void joined_stats(const GnParams& p, const Place<V>& a, float* lm, float* lr) {
-  const int lane = int(threadIdx.x) % kWave, entries = p.chunks * a.k.parts;
-  for (int g = int(threadIdx.x) / kWave; g < a.groups_here(p); g += kThreads / kWave) {
-    Moments m{0.0f, 0.0f, 0.0f};
-    for (int i = lane; i < entries; i += kWave) {
-      const float* from = p.stats + (((a.sample * p.chunks + i / a.k.parts) * p.g + a.group + g) * a.k.parts +
-                                     i % a.k.parts) * 3;
-      m.join({from[0], from[1], from[2]});
-    }
-    m.over_wave();
-    if (lane == 0) {
-      lm[g] = m.mean;
-      lr[g] = rsqrtf(m.m2 / m.n + p.eps);
-    }
-  }
-  __syncthreads();
+__device__ __forceinline__ bool first_of_group(const Place<V>& a) {
+  return a.any && a.off == 0 && (a.k.parts == 1 ? a.piece % a.k.pieces == 0 : a.piece == 0);
+}
+
+// Where the values of a thread's group and a chunk are, of an array [samples][chunks][groups][parts].
+template <int V>
+__device__ __forceinline__ int64_t own_entry(const GnParams& p, const Place<V>& a) {
+  const int g = a.k.parts == 1 ? a.piece / a.k.pieces : 0;
+  return ((a.sample * p.chunks + a.chunk) * p.g + a.group + g) * a.k.parts + a.part;
 }
 
 template <bool BF, int V>
-__global__ __launch_bounds__(kThreads) void map_forward(GnParams p) {
+__global__ __launch_bounds__(kThreads) void map_stats(GnParams p) {
+  __shared__ float l[3][kThreads];
+  const Place<V> a(p);
+  const Moments m = block_stats<BF, V>(p, a, l);
+  if (first_of_group(a)) {
+    float* to = p.stats + own_entry(p, a) * 3;
+    to[0] = m.n;
+    to[1] = m.mean;
+    to[2] = m.m2;
+  }
+}
+
+// Sums of K values over a block's groups' entries (chunks, and parts of wide groups), into l[..][group]: thread t has
+// group t % groups and every (threads / groups)-th entry, value(group, entry, v).
+template <int K, int V, typename F>
+__device__ __forceinline__ void entry_sums(const GnParams& p, const Place<V>& a, float (*l)[kThreads], F&& value) {
+  const int groups = a.groups_here(p), slots = kThreads / groups, entries = p.chunks * a.k.parts;
+  const int tid = int(threadIdx.x), g = tid % groups, slot = tid / groups;
+  float sum[K] = {};
+  if (slot < slots) {
+#pragma unroll 4
+    for (int i = slot; i < entries; i += slots) {
+      float v[K];
+      value(g, i, v);
+#pragma unroll
+      for (int k = 0; k < K; ++k) sum[k] += v[k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) l[k][tid] = sum[k];
+  __syncthreads();
+  for (int have = slots; have > 1;) {
+    const int half = (have + 1) / 2;
+    if (slot < have - half) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) l[k][tid] += l[k][tid + half * groups];
+    }
+    have = half;
+    __syncthreads();
+  }
+}
+
+// Where the values of a block's group and entry are, of an array [samples][chunks][groups][parts].
+template <int V>
+__device__ __forceinline__ int64_t entry_at(const GnParams& p, const Place<V>& a, int g, int i) {
+  return ((a.sample * p.chunks + i / a.k.parts) * p.g + a.group + g) * a.k.parts + i % a.k.parts;
+}
+
+// Mean and 1 / sqrt(variance + eps) of a thread's group, from all chunks: sums about the first entry's mean.
+template <int V>
+__device__ __forceinline__ Norm joined_stats(const GnParams& p, const Place<V>& a, float (*l)[kThreads]) {
+  const auto first = [&](int g) { return p.stats[entry_at(p, a, g, 0) * 3 + 1]; };
+  entry_sums<3>(p, a, l, [&](int g, int i, float (&v)[3]) {
+    const float* from = p.stats + entry_at(p, a, g, i) * 3;
+    const float off = from[1] - first(g);
+    v[0] = from[0];
+    v[1] = from[0] * off;
+    v[2] = fmaf(v[1], off, from[2]);
+  });
+  const int g = a.any && a.k.parts == 1 ? a.piece / a.k.pieces : 0;
+  const float off = l[1][g] / l[0][g];
+  const Norm n{first(g) + off, rsqrtf(fmaxf(l[2][g] - l[1][g] * off, 0.0f) / l[0][g] + p.eps)};
+  __syncthreads();
+  return n;
+}
+
+template <bool BF, int V>
+__device__ __forceinline__ void normalise(const GnParams& p, const Place<V>& a, const Norm& n) {
   using P = Piece<BF, V>;
   using E = typename P::E;
-  __shared__ float lm[kThreads], lr[kThreads];
-  const Place<V> a(p);
-  joined_stats<V>(p, a, lm, lr);
   if (!a.any) return;
   Chan<BF, V> ch;
   ch.load(p, a.c, true);
-  const int g = a.k.parts == 1 ? a.piece / a.k.pieces : 0;
-  const float mean = lm[g], r = lr[g];
   const E* x = static_cast<const E*>(p.x) + a.sample * p.xn + a.c;
   E* out = static_cast<E*>(p.out) + a.sample * p.s * p.c + a.c;
-#pragma unroll 4
-  for (int64_t t = a.p0 + a.off; t < a.p1; t += a.k.rows) {
-    float v[V];
-    P::open(P::load(x + t * p.xs), v);
+  each_positions(a, [&](int64_t t, int count) {
+    typename P::Raw raw[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      v[k] = fmaf((v[k] - mean) * r, ch.w[k], ch.bias[k]);
-      if (p.silu) v[k] = silu_of(v[k]);
+    for (int i = 0; i < kAtOnce; ++i) raw[i] = P::load(x + (t + int64_t(min(i, count - 1)) * a.k.rows) * p.xs);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (i >= count) break;
+      float v[V];
+      P::open(raw[i], v);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        v[k] = fmaf((v[k] - n.mean) * n.r, ch.w[k], ch.bias[k]);
+        if (p.silu) v[k] = silu_of(v[k]);
+      }
+      store_stream<BF, V>(out + (t + int64_t(i) * a.k.rows) * p.c, v);
     }
-    P::store(out + t * p.c, v);
-  }
+  });
 }
 
-// Each channel's sums of gu n and gu over a chunk, and each group's of gu w n and gu w (behind them, [parts][2]).
+// Each channel's sums of gu n and gu over a chunk, into p.sums; and those of gu w n (s2) and gu w (s1) of a thread's
+// group over it.
 template <bool BF, int V>
-__global__ __launch_bounds__(kThreads) void map_sums(GnParams p, float* group_sums) {
+__device__ __forceinline__ void block_sums(const GnParams& p, const Place<V>& a, const Norm& n, float (*l)[kThreads],
+                                           float (*share)[kThreads][V], float* s1, float* s2) {
   using P = Piece<BF, V>;
   using E = typename P::E;
-  __shared__ float lm[kThreads], lr[kThreads], l[2][kThreads][V];
-  const Place<V> a(p);
-  joined_stats<V>(p, a, lm, lr);
   Chan<BF, V> ch;
   ch.load(p, a.c, a.any);
   float gw[V] = {}, gb[V] = {};
   if (a.any) {
-    const int g = a.k.parts == 1 ? a.piece / a.k.pieces : 0;
-    const float mean = lm[g], r = lr[g];
     const E* x = static_cast<const E*>(p.x) + a.sample * p.xn + a.c;
     const E* go = static_cast<const E*>(p.go) + a.sample * p.gon + a.c;
-#pragma unroll 4
-    for (int64_t t = a.p0 + a.off; t < a.p1; t += a.k.rows) {
-      float v[V], gu[V];
-      P::open(P::load(x + t * p.xs), v);
-      P::open(P::load(go + t * p.gos), gu);
+    each_positions(a, [&](int64_t t, int count) {
+      typename P::Raw raw[kAtOnce], graw[kAtOnce];
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float n = (v[k] - mean) * r;
-        if (p.silu) gu[k] *= silu_slope(fmaf(n, ch.w[k], ch.bias[k]));
-        gw[k] = fmaf(gu[k], n, gw[k]);
-        gb[k] += gu[k];
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int64_t at = t + int64_t(min(i, count - 1)) * a.k.rows;
+        raw[i] = P::load(x + at * p.xs);
+        graw[i] = P::load(go + at * p.gos);
       }
-    }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (i >= count) break;
+        float v[V], gu[V];
+        P::open(raw[i], v);
+        P::open(graw[i], gu);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const float y = (v[k] - n.mean) * n.r;
+          if (p.silu) gu[k] *= silu_slope(fmaf(y, ch.w[k], ch.bias[k]));
+          gw[k] = fmaf(gu[k], y, gw[k]);
+          gb[k] += gu[k];
+        }
+      }
+    });
   }
+  float v[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    l[0][threadIdx.x][k] = gw[k];
-    l[1][threadIdx.x][k] = gb[k];
+    share[0][threadIdx.x][k] = gw[k];
+    share[1][threadIdx.x][k] = gb[k];
+    v[0] = fmaf(ch.w[k], gb[k], v[0]);
+    v[1] = fmaf(ch.w[k], gw[k], v[1]);
   }
-  __syncthreads();
-  const int64_t row = a.sample * p.chunks + a.chunk;
+  group_sums_of<2>(p, a, l, v);
+  *s1 = v[0];
+  *s2 = v[1];
   if (a.any && a.off == 0) {
     for (int i = 1; i < a.k.rows; ++i)
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        gw[k] += l[0][i * a.k.width + a.piece][k];
-        gb[k] += l[1][i * a.k.width + a.piece][k];
+        gw[k] += share[0][i * a.k.width + a.piece][k];
+        gb[k] += share[1][i * a.k.width + a.piece][k];
       }
-    float s1 = 0.0f, s2 = 0.0f;
+    float* to = p.sums + (a.sample * p.chunks + a.chunk) * 2 * p.c + a.c;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      p.sums[row * 2 * p.c + a.c + k] = gw[k];
-      p.sums[(row * 2 + 1) * p.c + a.c + k] = gb[k];
-      s1 = fmaf(ch.w[k], gb[k], s1);
-      s2 = fmaf(ch.w[k], gw[k], s2);
+      to[k] = gw[k];
+      to[p.c + k] = gb[k];
     }
-    lm[a.piece] = s1;
-    lr[a.piece] = s2;
-  } else if (a.off == 0) {
-    lm[a.piece] = 0.0f;
-    lr[a.piece] = 0.0f;
   }
-  __syncthreads();
-  const int lane = int(threadIdx.x) % kWave, per = a.k.parts == 1 ? a.k.pieces : a.k.width;
-  for (int g = int(threadIdx.x) / kWave; g < a.groups_here(p); g += kThreads / kWave) {
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int i = lane; i < per; i += kWave) {
-      s1 += lm[g * per + i];
-      s2 += lr[g * per + i];
+}
+
+template <bool BF, int V>
+__device__ __forceinline__ void pass_back(const GnParams& p, const Place<V>& a, const Norm& n, float s1, float s2) {
+  using P = Piece<BF, V>;
+  using E = typename P::E;
+  if (!a.any) return;
+  const float inv = 1.0f / (float(p.s) * float(p.c / p.g));
+  s1 *= inv;
+  s2 *= inv;
+  Chan<BF, V> ch;
+  ch.load(p, a.c, true);
+  const E* x = static_cast<const E*>(p.x) + a.sample * p.xn + a.c;
+  const E* go = static_cast<const E*>(p.go) + a.sample * p.gon + a.c;
+  E* out = static_cast<E*>(p.out) + a.sample * p.s * p.c + a.c;
+  each_positions(a, [&](int64_t t, int count) {
+    typename P::Raw raw[kAtOnce], graw[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int64_t at = t + int64_t(min(i, count - 1)) * a.k.rows;
+      raw[i] = P::load(x + at * p.xs);
+      graw[i] = P::load(go + at * p.gos);
     }
 #pragma unroll
-    for (int m = 1; m < kWave; m *= 2) {
-      s1 += __shfl_xor(s1, m);
-      s2 += __shfl_xor(s2, m);
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (i >= count) break;
+      float v[V], gu[V];
+      P::open(raw[i], v);
+      P::open(graw[i], gu);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const float y = (v[k] - n.mean) * n.r;
+        if (p.silu) gu[k] *= silu_slope(fmaf(y, ch.w[k], ch.bias[k]));
+        v[k] = n.r * (gu[k] * ch.w[k] - s1 - y * s2);
+      }
+      store_stream<BF, V>(out + (t + int64_t(i) * a.k.rows) * p.c, v);
     }
-    if (lane == 0) {
-      float* to = group_sums + ((row * p.g + a.group + g) * a.k.parts + a.part) * 2;
-      to[0] = s1;
-      to[1] = s2;
-    }
+  });
+}
+
+template <bool BF, int V>
+__global__ __launch_bounds__(kThreads) void map_forward(GnParams p) {
+  __shared__ float l[3][kThreads];
+  const Place<V> a(p);
+  normalise<BF, V>(p, a, joined_stats<V>(p, a, l));
+}
+
+template <bool BF, int V>
+__global__ __launch_bounds__(kThreads) void map_sums(GnParams p, float* group_sums) {
+  __shared__ float l[3][kThreads], share[2][kThreads][V];
+  const Place<V> a(p);
+  const Norm n = joined_stats<V>(p, a, l);
+  float s1, s2;
+  block_sums<BF, V>(p, a, n, l, share, &s1, &s2);
+  if (first_of_group(a)) {
+    float* to = group_sums + own_entry(p, a) * 2;
+    to[0] = s1;
+    to[1] = s2;
   }
 }
 
 template <bool BF, int V>
 __global__ __launch_bounds__(kThreads) void map_backward(GnParams p, const float* group_sums) {
-  using P = Piece<BF, V>;
-  using E = typename P::E;
-  __shared__ float lm[kThreads], lr[kThreads], l1[kThreads], l2[kThreads];
+  __shared__ float l[3][kThreads];
   const Place<V> a(p);
-  const int lane = int(threadIdx.x) % kWave, entries = p.chunks * a.k.parts;
-  const float inv = 1.0f / (float(p.s) * float(p.c / p.g));
-  for (int g = int(threadIdx.x) / kWave; g < a.groups_here(p); g += kThreads / kWave) {
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int i = lane; i < entries; i += kWave) {
-      const float* from = group_sums + (((a.sample * p.chunks + i / a.k.parts) * p.g + a.group + g) * a.k.parts +
-                                        i % a.k.parts) * 2;
-      s1 += from[0];
-      s2 += from[1];
-    }
-#pragma unroll
-    for (int m = 1; m < kWave; m *= 2) {
-      s1 += __shfl_xor(s1, m);
-      s2 += __shfl_xor(s2, m);
-    }
-    if (lane == 0) {
-      l1[g] = s1 * inv;
-      l2[g] = s2 * inv;
-    }
+  entry_sums<2>(p, a, l, [&](int g, int i, float (&v)[2]) {
+    const float* from = group_sums + entry_at(p, a, g, i) * 2;
+    v[0] = from[0];
+    v[1] = from[1];
+  });
+  const int g = a.any && a.k.parts == 1 ? a.piece / a.k.pieces : 0;
+  const float s1 = l[0][g], s2 = l[1][g];
+  __syncthreads();
+  pass_back<BF, V>(p, a, joined_stats<V>(p, a, l), s1, s2);
+}
+
+// A block that has its groups whole (one chunk, no wide groups) does all of it in one launch: 4 positions of 256
+// channels take 8.5 us, 13.2 in two.
+template <bool BF, int V>
+__global__ __launch_bounds__(kThreads) void map_alone(GnParams p, int gradient) {
+  __shared__ float l[3][kThreads], share[2][kThreads][V];
+  const Place<V> a(p);
+  const Moments m = block_stats<BF, V>(p, a, l);
+  const Norm n{m.mean, rsqrtf(m.m2 / m.n + p.eps)};
+  if (!gradient) {
+    normalise<BF, V>(p, a, n);
+    return;
   }
-  joined_stats<V>(p, a, lm, lr);
-  if (!a.any) return;
-  Chan<BF, V> ch;
-  ch.load(p, a.c, true);
-  const int g = a.k.parts == 1 ? a.piece / a.k.pieces : 0;
-  const float mean = lm[g], r = lr[g], s1 = l1[g], s2 = l2[g];
-  const E* x = static_cast<const E*>(p.x) + a.sample * p.xn + a.c;
-  const E* go = static_cast<const E*>(p.go) + a.sample * p.gon + a.c;
-  E* out = static_cast<E*>(p.out) + a.sample * p.s * p.c + a.c;
-#pragma unroll 4
-  for (int64_t t = a.p0 + a.off; t < a.p1; t += a.k.rows) {
-    float v[V], gu[V];
-    P::open(P::load(x + t * p.xs), v);
-    P::open(P::load(go + t * p.gos), gu);
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const float n = (v[k] - mean) * r;
-      if (p.silu) gu[k] *= silu_slope(fmaf(n, ch.w[k], ch.bias[k]));
-      v[k] = r * (gu[k] * ch.w[k] - s1 - n * s2);
-    }
-    P::store(out + t * p.c, v);
-  }
+  float s1, s2;
+  block_sums<BF, V>(p, a, n, l, share, &s1, &s2);
+  pass_back<BF, V>(p, a, n, s1, s2);
 }
 
 // ---------------------------------------------------------------- which
 
-// Channels of a piece: 16 bytes where groups are whole pieces, else one.
+// Channels of a piece: up to 16 bytes, as many as groups are whole pieces of.
 int piece_channels(const GnParams& p) {
-  const int v = p.bf16 ? 8 : 4;
-  return p.c / p.g % v == 0 ? v : 1;
+  const int per = p.c / p.g;
+  return p.bf16 && per % 8 == 0 ? 8 : per % 4 == 0 ? 4 : per % 2 == 0 ? 2 : 1;
 }
 
 constexpr int kMostPieces = 4;  // of a lane that holds a row's group
+constexpr int kMapPerCu = 2, kMostEntries = 4096;
 
 // Lanes that hold a group of a row; 0: too wide, or samples of several positions.
 int row_lanes(const GnParams& p) {
@@ -534,7 +656,9 @@ RowGrid row_grid(const GnParams& p, int lanes, bool gradient) {
   RowGrid r;
   r.rows = p.g >= slots ? 1 : slots / p.g;
   r.y = p.g >= slots ? (p.g + slots - 1) / slots : 1;
-  const int64_t want = std::max<int64_t>(1, int64_t(device_cu_count()) * (gradient ? 4 : 8) / r.y);
+  // 16384 rows of 2048 channels in bf16: 47.6, 37.9, 35.7, 45.3 us with 16, 8, 4, 2 workgroups a compute unit; the
+  // gradient of 16000 rows of 1024: 70.9, 48.7, 44.3, 58.7 with 8, 4, 2, 1
+  const int64_t want = std::max<int64_t>(1, int64_t(device_cu_count()) * (gradient ? 2 : 4) / r.y);
   r.x = int(std::max<int64_t>(1, std::min(want, (p.n + r.rows - 1) / r.rows)));
   return r;
 }
@@ -568,6 +692,10 @@ hipError_t launch(const GnParams& p, bool gradient, hipStream_t stream) {
     return hipGetLastError();
   }
   const unsigned grid = unsigned(p.n * p.chunks * blocks_of<V>(p).count);
+  if (p.chunks == 1 && blocks_of<V>(p).parts == 1) {
+    map_alone<BF, V><<<grid, kThreads, 0, stream>>>(p, gradient ? 1 : 0);
+    return hipGetLastError();
+  }
   map_stats<BF, V><<<grid, kThreads, 0, stream>>>(p);
   if (!gradient) {
     map_forward<BF, V><<<grid, kThreads, 0, stream>>>(p);
@@ -579,16 +707,27 @@ hipError_t launch(const GnParams& p, bool gradient, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <bool BF>
 hipError_t launch_any(const GnParams& p, bool gradient, hipStream_t stream) {
-  const bool wide = piece_channels(p) > 1;
-  if (p.bf16) return wide ? launch<true, 8>(p, gradient, stream) : launch<true, 1>(p, gradient, stream);
-  return wide ? launch<false, 4>(p, gradient, stream) : launch<false, 1>(p, gradient, stream);
+  switch (piece_channels(p)) {
+    case 8:
+      if constexpr (BF) return launch<BF, 8>(p, gradient, stream);
+      return hipErrorInvalidValue;  // f32 pieces have four channels
+    case 4: return launch<BF, 4>(p, gradient, stream);
+    case 2: return launch<BF, 2>(p, gradient, stream);
+    default: return launch<BF, 1>(p, gradient, stream);
+  }
+}
+
+hipError_t launch_any(const GnParams& p, bool gradient, hipStream_t stream) {
+  return p.bf16 ? launch_any<true>(p, gradient, stream) : launch_any<false>(p, gradient, stream);
 }
 
 Blocks blocks_for(const GnParams& p) {
   switch (piece_channels(p)) {
     case 8: return blocks_of<8>(p);
     case 4: return blocks_of<4>(p);
+    case 2: return blocks_of<2>(p);
     default: return blocks_of<1>(p);
   }
 }
@@ -604,9 +743,14 @@ void group_norm_split(GnParams& p, bool gradient) {
     return;
   }
   const Blocks k = blocks_for(p);
-  // Four workgroups a compute unit, of eight positions a thread at least.
-  const int64_t want = std::max<int64_t>(1, int64_t(device_cu_count()) * 4 / std::max<int64_t>(1, p.n * k.count));
-  const int64_t chunk = std::max<int64_t>(int64_t(k.rows) * 8, (p.s + want - 1) / want);
+  const int bytes = piece_channels(p) * (p.bf16 ? 2 : 4), per_cu = std::min(8, kMapPerCu * 16 / bytes);
+  // Two workgroups a compute unit (more where a piece is narrow: 3000 positions of 333 channels in bf16 take 48 us with
+  // four, 73 with two), of eight positions a thread at least, and as few chunks as a workgroup joins by the
+  // way (every workgroup joins those of its sample).
+  const int64_t want = std::max<int64_t>(1, int64_t(device_cu_count()) * per_cu / std::max<int64_t>(1, p.n * k.count));
+  const int64_t most = std::max<int64_t>(1, kMostEntries / (int64_t(k.groups) * k.parts));
+  const int64_t split = std::min(want, most);
+  const int64_t chunk = std::max<int64_t>(int64_t(k.rows) * 8, (p.s + split - 1) / split);
   p.chunk = chunk;
   p.chunks = int(std::max<int64_t>(1, (p.s + chunk - 1) / chunk));
 }
