@@ -370,12 +370,22 @@ __global__ __launch_bounds__(kWave* W, march_waves_per_simd(W)) void scan_march(
   rates(p.a, d, n0, p.N, is, rate);
   read_states(OUT || KIND == March::Marks ? p.initial : nullptr, int64_t(b) * p.D + d, n0, p.N, is, h);
   if constexpr (OUT) {
-    for (int m = 0; m < seg; ++m) {
-      const int64_t row = int64_t(m) * p.B + b;
-      const f32x4 own = is ? *reinterpret_cast<const f32x4*>(p.seg_state + packed_at(p, row, wave, d)) : zero4();
-      const float sum = is ? p.seg_steps[row * p.D + d] : 0.0f;
+    constexpr int A = 8;  // segments read ahead of the chain
+    for (int m = 0; m < seg; m += A) {
+      f32x4 own[A];
+      float sum[A];
 #pragma unroll
-      for (int i = 0; i < kScanStates; ++i) h[i] = fmaf(exp2_of(sum * rate[i]), h[i], own[i]);
+      for (int k = 0; k < A; ++k) {
+        const int64_t row = int64_t(min(m + k, seg - 1)) * p.B + b;
+        own[k] = is ? *reinterpret_cast<const f32x4*>(p.seg_state + packed_at(p, row, wave, d)) : zero4();
+        sum[k] = is ? p.seg_steps[row * p.D + d] : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < A; ++k) {
+        if (m + k >= seg) break;
+#pragma unroll
+        for (int i = 0; i < kScanStates; ++i) h[i] = fmaf(exp2_of(sum[k] * rate[i]), h[i], own[k][i]);
+      }
     }
   }
 #pragma unroll
@@ -421,7 +431,7 @@ __global__ __launch_bounds__(kWave* W, march_waves_per_simd(W)) void scan_march(
     }
     each<kTile / 4>([&](auto Q) {
       constexpr int j4 = 4 * decltype(Q)::value;
-      float e[4][kScanStates], u[4][kScanStates], gy[4], before = 0.0f;
+      float e[4][kScanStates], u[4][kScanStates], gy[4], read[4][kScanStates], before = 0.0f;  // read: c gy
       each<4>([&](auto J) {
         constexpr int k = decltype(J)::value;
 #pragma unroll
@@ -443,6 +453,7 @@ __global__ __launch_bounds__(kWave* W, march_waves_per_simd(W)) void scan_march(
       if constexpr (ADJOINT) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) gy[k] = l.y[buf][0][j4 + k][lane];
+        sources<j4>(cv, gy, read);
       }
       __builtin_amdgcn_sched_barrier(0);
       if (MARK && j4 == 0) mark(s0 + t0, before);
@@ -456,7 +467,7 @@ __global__ __launch_bounds__(kWave* W, march_waves_per_simd(W)) void scan_march(
           if constexpr (OUT) hs[k][i] = h[i];
           if constexpr (ADJOINT) {
             through[i] *= e[k][i];
-            adj[i] = fmaf(through[i], of_token<j4 + k>(cv[i]) * gy[k], adj[i]);
+            adj[i] = fmaf(through[i], read[k][i], adj[i]);
           }
         }
       });

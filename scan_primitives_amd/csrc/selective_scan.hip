@@ -157,9 +157,13 @@ void selective_scan_split(SsParams& p, bool gradient) {
   const int64_t width = gradient ? kGradChannels : kChannels;
   const int64_t waves = (per_group + width - 1) / width * p.G * p.B * p.waves;
   const int64_t tiles = (int64_t(p.T) + kTile - 1) / kTile;
-  // Four waves a SIMD (of the gradient two, which its registers leave); segments of a tile at least (333 tokens of
-  // 3 x 210 channels: the gradient takes 48 us, 116 with four tiles).
-  int64_t segments = std::max<int64_t>(1, std::min(int64_t(device_cu_count()) * (gradient ? 8 : 16) / std::max<int64_t>(waves, 1), tiles));
+  // Four waves a SIMD (of the gradient two, which its registers leave). Segments of a tile at least (333 tokens of
+  // 3 x 210 channels: the gradient takes 48 us, 116 with four tiles; the result of 100 tokens of 2048 12.5, 17), of two
+  // in a result of more than eight, whose segments each join all before (400 tokens of 1536 channels: 18.4 us, 21 with
+  // one); up to four tiles cost less than a second launch (37 tokens of 2048 channels: 10.1 us, 11.8 in segments).
+  const int64_t most = gradient ? tiles : tiles > 8 ? tiles / 2 : tiles > 4 ? tiles : 1;
+  const int64_t want = int64_t(device_cu_count()) * (gradient ? 8 : 16) / std::max<int64_t>(waves, 1);
+  const int64_t segments = std::max<int64_t>(1, std::min(want, most));
   const int64_t per = std::max<int64_t>(1, (tiles + segments - 1) / segments);
   p.seg_tokens = int(std::min<int64_t>(per * kTile, int64_t(1) << 30));
   p.segments = int(std::max<int64_t>(1, (tiles + per - 1) / per));
