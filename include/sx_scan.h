@@ -692,8 +692,8 @@ sx_status sx_causal_conv_step(sx_dtype dtype, const int64_t* x_shape, const int6
  *                aligned; may hold anything; may be NULL when that is 0.
  *
  * An infinity or NaN of one token's x, delta or z stays in its channel, one of b
- * or c in its group; of x, delta and b it reaches later tokens too, earlier ones
- * never. Outputs overlap no input and not each other (SX_E_ALIAS). Errors
+ * or c in its group (an infinity may come out as NaN); of x, delta and b it
+ * reaches later tokens too, earlier ones never. Outputs overlap no input and not each other (SX_E_ALIAS). Errors
  * otherwise as sx_decay_attention.
  */
 sx_status sx_selective_scan(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x,

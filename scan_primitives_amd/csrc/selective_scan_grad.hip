@@ -68,7 +68,7 @@ __device__ __forceinline__ float dpp(float v) {
 // Sums over lanes: a step adds two registers into one whose lanes with a bit of their number clear hold the first's
 // sum so far and the others the second's. Bit 3's partner is the mirrored lane of the row of 16, bit 2's that of its
 // half, and which register a lane takes is the instruction's bank mask. Of the eight sums of a token: four in each
-// of two registers. The wait is for a sum that was written just before.
+// of two registers. The waits are for a sum that was written just before, and for a swap that takes one just behind.
 __device__ __forceinline__ void fold_token(const float (&v)[8], float (&s)[2]) {
   float r[4];
 #define SX_PAIR(O, A, B, HOW, LOW, HIGH)                                            \
@@ -77,7 +77,7 @@ __device__ __forceinline__ void fold_token(const float (&v)[8], float (&s)[2]) {
 #define SX_ROW(O, A, B) SX_PAIR(O, A, B, "row_mirror", "0x3", "0xc")
 #define SX_HALF(O, A, B) SX_PAIR(O, A, B, "row_half_mirror", "0x5", "0xa")
   asm("s_nop 1\n\t" SX_ROW("2", "6", "10") SX_ROW("3", "7", "11") SX_ROW("4", "8", "12") SX_ROW("5", "9", "13")
-          SX_HALF("0", "2", "4") SX_HALF("1", "3", "5")
+          SX_HALF("0", "2", "4") SX_HALF("1", "3", "5") "s_nop 1"
       : "=&v"(s[0]), "=&v"(s[1]), "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3])
       : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]));
 #undef SX_HALF

@@ -83,6 +83,14 @@ CASES = {
     "a channel more than a block": dict(d=65, type=F32),
     "a channel more than two blocks": dict(d=129),
     "whole blocks": dict(d=256, type=F32),
+    "four channels more than a block": dict(d=68, t=40),
+    "five channels more than a block": dict(d=69, t=40, type=F32, initial=True),
+    "three channels more than two blocks": dict(d=131, t=40, initial=True),
+    "five channels more than two blocks": dict(d=133, t=300, type=F32),
+    "seventy channels a group": dict(d=210, g=3, t=50, initial=True),
+    "five channels": dict(d=5, t=33),
+    "eleven states": dict(n=11, t=60, d=70, initial=True),
+    "ten states, many segments": dict(b=1, n=10, t=700, d=66, initial=True),
     "groups": dict(d=96, g=3, initial=True),
     "groups of odd sizes": dict(d=99, g=3, type=F32, initial=True),
     "a group a channel": dict(d=12, g=12, type=F32, n=6),
@@ -307,6 +315,20 @@ def test_gradient_matches_differences_of_the_forward_call(t, gate, softplus):
         want = (grad.double() * step.double()).sum().item()
         # the third derivative's share e^2 times a few, and f32 roundings of 2 t 12 values over 2 e
         assert abs(d - want) <= 5e-3 * abs(want) + 1e-2 * grad.double().norm().item(), n
+
+
+def test_far_apart_tokens():
+    # tokens 2^24 elements apart: offsets within a tile pass what its 32-bit ones are used for
+    t, d, far = 18, 16, 1 << 24
+    s, g = make(b=1, t=t, d=d, initial=True)
+    want = (*sx.selective_scan(return_state=True, **s), *sx.selective_scan_backward(**s, **g))
+    room = torch.zeros(t * far + 64, dtype=BF, device=DEV)
+    for i, (where, n) in enumerate(((s, "x"), (s, "delta"), (s, "z"), (g, "grad_out"), (s, "b"), (s, "c"))):
+        view = room.as_strided(where[n].shape, (0, far, *where[n].stride()[2:]), i * 32)
+        view.copy_(where[n])
+        where[n] = view
+    for a, b in zip((*sx.selective_scan(return_state=True, **s), *sx.selective_scan_backward(**s, **g)), want):
+        assert torch.equal(a, b)
 
 
 def test_far_apart_rows_and_a_pool_past_32_bits():
