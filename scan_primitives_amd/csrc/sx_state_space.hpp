@@ -301,18 +301,17 @@ __device__ __forceinline__ float sigmoid_of(float v) {
 }
 
 // log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|), to f32's accuracy also where it is small: with
-// s = e / (2 + e) <= 1/3, log1p(e) = 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 + ...); what is left out is below 2e-9 of it.
+// s = e / (2 + e) <= 1/3, log1p(e) = 2 atanh(s) = s p(s^2), p(q) = 2 (1 + q/3 + q^2/5 + ...). The coefficients are those
+// of the polynomial of degree four that is nearest to p on [0, 1/9]: off by at most 8e-9 of it (the series' own need
+// degree seven; 8192 tokens of 4096 channels take 270 us, 278 with those).
 __device__ __forceinline__ float softplus_of(float v) {
   const float e = exp2_of(-kLog2e * fabsf(v));
   const float s = e * __builtin_amdgcn_rcpf(2.0f + e), q = s * s;
-  float p = fmaf(q, 1.0f / 15.0f, 1.0f / 13.0f);
-  p = fmaf(q, p, 1.0f / 11.0f);
-  p = fmaf(q, p, 1.0f / 9.0f);
-  p = fmaf(q, p, 1.0f / 7.0f);
-  p = fmaf(q, p, 1.0f / 5.0f);
-  p = fmaf(q, p, 1.0f / 3.0f);
-  p = fmaf(q, p, 1.0f);
-  return fmaf(2.0f * s, p, fmaxf(v, 0.0f));
+  float p = fmaf(q, 0.2817833423614502f, 0.27960601449012756f);
+  p = fmaf(q, p, 0.40024909377098083f);
+  p = fmaf(q, p, 0.6666631698608398f);
+  p = fmaf(q, p, 2.0f);
+  return fmaf(s, p, fmaxf(v, 0.0f));
 }
 
 // silu(u) = u sigmoid(u), and its slope.
