@@ -531,7 +531,8 @@ __global__ __launch_bounds__(kWave* W, march_waves_per_simd(W)) void scan_march(
   }
 }
 
-// How a call's arrays can be read. Twelve tokens by elements take 1.6 times what they take by fours.
+// How a call's arrays can be read: 8192 tokens of 4096 channels of 16 states in bf16 take 247 us by fours, of 4095
+// channels 258 (Early), of 4096 that lie two apart 324 by elements (one operand over and over).
 inline Rows scan_rows(const SsParams& p, bool gradient, int channels) {
   const int64_t most = int64_t(1) << 24, per_group = p.D / p.G;
   bool unit = per_group % channels == 0 || per_group % channels >= 4;  // a workgroup has four channels at least
