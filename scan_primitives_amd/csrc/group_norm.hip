@@ -30,11 +30,31 @@ struct Chan {  // V channels' weights
   __device__ __forceinline__ void load(const GnParams& p, int c, bool is) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      w[v] = is ? (p.w ? p.w[c + v] : 1.0f) : 0.0f;
-      bias[v] = is && p.bias ? p.bias[c + v] : 0.0f;
+      w[v] = is ? 1.0f : 0.0f;
+      bias[v] = 0.0f;
+    }
+    if (is && p.w) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) w[v] = p.w[c + v];
+    }
+    if (is && p.bias) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) bias[v] = p.bias[c + v];
     }
   }
+  // gu = gy silu'(u), of n. One branch for all channels, here and in silu_all: one each would form them one after
+  // the other.
+  __device__ __forceinline__ void pass_silu(const float (&n)[V], float (&gu)[V]) const {
+#pragma unroll
+    for (int v = 0; v < V; ++v) gu[v] *= silu_slope(fmaf(n[v], w[v], bias[v]));
+  }
 };
+
+template <int V>
+__device__ __forceinline__ void silu_all(float (&u)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) u[v] = silu_of(u[v]);
+}
 
 // ---------------------------------------------------------------- rows
 
@@ -121,10 +141,8 @@ __global__ __launch_bounds__(kThreads) void rows_forward(GnParams p) {
 #pragma unroll
     for (int m = 0; m < M; ++m) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        v[m][k] = fmaf(v[m][k] * r, ch[m].w[k], ch[m].bias[k]);
-        if (p.silu) v[m][k] = silu_of(v[m][k]);
-      }
+      for (int k = 0; k < V; ++k) v[m][k] = fmaf(v[m][k] * r, ch[m].w[k], ch[m].bias[k]);
+      if (p.silu) silu_all<V>(v[m]);
       if (is[m] && row < p.n) store_stream<BF, V>(static_cast<E*>(p.out) + row * p.c + c[m], v[m]);
     }
   }
@@ -182,18 +200,19 @@ __global__ __launch_bounds__(kThreads) void rows_backward(GnParams p) {
     const float r = rsqrtf(fmaf(lanes_sum<L>(sq, l[1]), inv, p.eps));
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-    for (int m = 0; m < M; ++m)
+    for (int m = 0; m < M; ++m) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[m][k] *= r;
+      if (p.silu) ch[m].pass_silu(v[m], g[m]);
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        const float n = v[m][k] * r;
-        if (p.silu) g[m][k] *= silu_slope(fmaf(n, ch[m].w[k], ch[m].bias[k]));
-        gw[m][k] = fmaf(g[m][k], n, gw[m][k]);
+        gw[m][k] = fmaf(g[m][k], v[m][k], gw[m][k]);
         gb[m][k] += g[m][k];
         g[m][k] *= ch[m].w[k];
         s1 += g[m][k];
-        s2 = fmaf(g[m][k], n, s2);
-        v[m][k] = n;
+        s2 = fmaf(g[m][k], v[m][k], s2);
       }
+    }
     s1 = lanes_sum<L>(s1, l[2]) * inv;
     s2 = lanes_sum<L>(s2, l[3]) * inv;
 #pragma unroll
@@ -273,14 +292,53 @@ struct Place {
   __device__ __forceinline__ int groups_here(const GnParams& p) const { return min(k.groups, p.g - group); }
 };
 
-// f(position, count there are) of a thread's positions, kAtOnce at a time: what they read is on its way before the
-// first is used, which stores between them would keep apart.
+// A thread's positions of x (and of the result's gradient, GO), kAtOnce ahead of what is done with them: the first are
+// on their way from the constructor on, which stands before the chunks' values are joined. 8 x 4096 positions of 512
+// channels in bf16: the gradient takes @@ us, 66 without.
 constexpr int kAtOnce = 4;
-template <int V, typename F>
-__device__ __forceinline__ void each_positions(const Place<V>& a, F&& f) {
-  for (int64_t t = a.p0 + a.off; t < a.p1; t += int64_t(a.k.rows) * kAtOnce)
-    f(t, int(min(int64_t(kAtOnce), (a.p1 - t + a.k.rows - 1) / a.k.rows)));
-}
+template <bool BF, int V, bool GO>
+struct Ahead {
+  using P = Piece<BF, V>;
+  using E = typename P::E;
+  const E *x, *go;        // the thread's first position, then the one after each kAtOnce
+  int64_t x_step, g_step; // to its next
+  int left, rows;         // positions of the chunk from there on (a chunk of 2^31 would not fit the memory)
+  typename P::Raw xin[kAtOnce], gin[GO ? kAtOnce : 1];
+  __device__ __forceinline__ Ahead(const GnParams& p, const Place<V>& a)
+      : x(static_cast<const E*>(p.x) + a.sample * p.xn + (a.p0 + a.off) * p.xs + a.c),
+        go(GO ? static_cast<const E*>(p.go) + a.sample * p.gon + (a.p0 + a.off) * p.gos + a.c : nullptr),
+        x_step(a.k.rows * p.xs), g_step(a.k.rows * p.gos), left(a.any ? int(a.p1 - a.p0) - a.off : 0), rows(a.k.rows) {
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      xin[i] = P::zero();
+      if constexpr (GO) gin[i] = P::zero();
+      read(i, 0);
+    }
+  }
+  __device__ __forceinline__ void read(int i, int ahead) {
+    if (left <= (i + ahead) * rows) return;
+    xin[i] = P::load(x + (i + ahead) * x_step);
+    if constexpr (GO) gin[i] = P::load(go + (i + ahead) * g_step);
+  }
+  // f(how many positions of the thread's before, x, gradient)
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) {
+    for (int64_t n = 0; left > 0; n += kAtOnce) {
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (left <= i * rows) break;
+        float v[V], gu[V] = {};
+        P::open(xin[i], v);
+        if constexpr (GO) P::open(gin[i], gu);
+        read(i, kAtOnce);
+        f(n + i, v, gu);
+      }
+      x += kAtOnce * x_step;
+      if constexpr (GO) go += kAtOnce * g_step;
+      left -= kAtOnce * rows;
+    }
+  }
+};
 
 // Sums of K values a thread over the threads of its group, in every thread: a wave takes a group at a time. `v` are
 // zero in threads without a piece. Ends with l free again.
@@ -326,32 +384,19 @@ struct Norm {
 template <bool BF, int V>
 __device__ __forceinline__ Moments block_stats(const GnParams& p, const Place<V>& a, float (*l)[kThreads]) {
   using P = Piece<BF, V>;
-  using E = typename P::E;
-  const E* x = static_cast<const E*>(p.x) + a.sample * p.xn + a.c;
-  float shift = 0.0f, sum = 0.0f, sq = 0.0f, n = 0.0f;
-  if (a.any && a.p0 + a.off < a.p1) {
-    float first[V];
-    P::open(P::load(x + (a.p0 + a.off) * p.xs), first);
-    shift = first[0];
-    each_positions(a, [&](int64_t t, int count) {
-      typename P::Raw raw[kAtOnce];
+  Ahead<BF, V, false> in(p, a);
+  float first[V], sum = 0.0f, sq = 0.0f, n = 0.0f;
+  P::open(in.xin[0], first);
+  const float shift = first[0];
+  in.each([&](int64_t, const float(&v)[V], const float(&)[V]) {
 #pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) raw[i] = P::load(x + (t + int64_t(min(i, count - 1)) * a.k.rows) * p.xs);
-#pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        if (i >= count) break;
-        float v[V];
-        P::open(raw[i], v);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const float d = v[k] - shift;
-          sum += d;
-          sq = fmaf(d, d, sq);
-        }
-        n += float(V);
-      }
-    });
-  }
+    for (int k = 0; k < V; ++k) {
+      const float d = v[k] - shift;
+      sum += d;
+      sq = fmaf(d, d, sq);
+    }
+    n += float(V);
+  });
   const float mean = n > 0.0f ? shift + sum / n : 0.0f, m2 = n > 0.0f ? fmaxf(sq - sum * (sum / n), 0.0f) : 0.0f;
   l[0][threadIdx.x] = mean;
   __syncthreads();
@@ -446,70 +491,38 @@ __device__ __forceinline__ Norm joined_stats(const GnParams& p, const Place<V>& 
 }
 
 template <bool BF, int V>
-__device__ __forceinline__ void normalise(const GnParams& p, const Place<V>& a, const Norm& n) {
-  using P = Piece<BF, V>;
-  using E = typename P::E;
-  if (!a.any) return;
+__device__ __forceinline__ void normalise(const GnParams& p, const Place<V>& a, Ahead<BF, V, false>& in, const Norm& n) {
+  using E = typename Piece<BF, V>::E;
   Chan<BF, V> ch;
-  ch.load(p, a.c, true);
-  const E* x = static_cast<const E*>(p.x) + a.sample * p.xn + a.c;
-  E* out = static_cast<E*>(p.out) + a.sample * p.s * p.c + a.c;
-  each_positions(a, [&](int64_t t, int count) {
-    typename P::Raw raw[kAtOnce];
+  ch.load(p, a.c, a.any);
+  E* out = static_cast<E*>(p.out) + (a.sample * p.s + a.p0 + a.off) * p.c + a.c;
+  const int64_t step = int64_t(a.k.rows) * p.c;
+  in.each([&](int64_t t, float(&v)[V], const float(&)[V]) {
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) raw[i] = P::load(x + (t + int64_t(min(i, count - 1)) * a.k.rows) * p.xs);
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      if (i >= count) break;
-      float v[V];
-      P::open(raw[i], v);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        v[k] = fmaf((v[k] - n.mean) * n.r, ch.w[k], ch.bias[k]);
-        if (p.silu) v[k] = silu_of(v[k]);
-      }
-      store_stream<BF, V>(out + (t + int64_t(i) * a.k.rows) * p.c, v);
-    }
+    for (int k = 0; k < V; ++k) v[k] = fmaf((v[k] - n.mean) * n.r, ch.w[k], ch.bias[k]);
+    if (p.silu) silu_all<V>(v);
+    store_stream<BF, V>(out + t * step, v);
   });
 }
 
 // Each channel's sums of gu n and gu over a chunk, into p.sums; and those of gu w n (s2) and gu w (s1) of a thread's
 // group over it.
 template <bool BF, int V>
-__device__ __forceinline__ void block_sums(const GnParams& p, const Place<V>& a, const Norm& n, float (*l)[kThreads],
-                                           float (*share)[kThreads][V], float* s1, float* s2) {
-  using P = Piece<BF, V>;
-  using E = typename P::E;
+__device__ __forceinline__ void block_sums(const GnParams& p, const Place<V>& a, Ahead<BF, V, true>& in, const Norm& n,
+                                           float (*l)[kThreads], float (*share)[kThreads][V], float* s1, float* s2) {
   Chan<BF, V> ch;
   ch.load(p, a.c, a.any);
   float gw[V] = {}, gb[V] = {};
-  if (a.any) {
-    const E* x = static_cast<const E*>(p.x) + a.sample * p.xn + a.c;
-    const E* go = static_cast<const E*>(p.go) + a.sample * p.gon + a.c;
-    each_positions(a, [&](int64_t t, int count) {
-      typename P::Raw raw[kAtOnce], graw[kAtOnce];
+  in.each([&](int64_t, float(&v)[V], float(&gu)[V]) {
 #pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        const int64_t at = t + int64_t(min(i, count - 1)) * a.k.rows;
-        raw[i] = P::load(x + at * p.xs);
-        graw[i] = P::load(go + at * p.gos);
-      }
+    for (int k = 0; k < V; ++k) v[k] = (v[k] - n.mean) * n.r;
+    if (p.silu) ch.pass_silu(v, gu);
 #pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        if (i >= count) break;
-        float v[V], gu[V];
-        P::open(raw[i], v);
-        P::open(graw[i], gu);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const float y = (v[k] - n.mean) * n.r;
-          if (p.silu) gu[k] *= silu_slope(fmaf(y, ch.w[k], ch.bias[k]));
-          gw[k] = fmaf(gu[k], y, gw[k]);
-          gb[k] += gu[k];
-        }
-      }
-    });
-  }
+    for (int k = 0; k < V; ++k) {
+      gw[k] = fmaf(gu[k], v[k], gw[k]);
+      gb[k] += gu[k];
+    }
+  });
   float v[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int k = 0; k < V; ++k) {
@@ -538,40 +551,23 @@ __device__ __forceinline__ void block_sums(const GnParams& p, const Place<V>& a,
 }
 
 template <bool BF, int V>
-__device__ __forceinline__ void pass_back(const GnParams& p, const Place<V>& a, const Norm& n, float s1, float s2) {
-  using P = Piece<BF, V>;
-  using E = typename P::E;
-  if (!a.any) return;
+__device__ __forceinline__ void pass_back(const GnParams& p, const Place<V>& a, Ahead<BF, V, true>& in, const Norm& n,
+                                          float s1, float s2) {
+  using E = typename Piece<BF, V>::E;
   const float inv = 1.0f / (float(p.s) * float(p.c / p.g));
   s1 *= inv;
   s2 *= inv;
   Chan<BF, V> ch;
-  ch.load(p, a.c, true);
-  const E* x = static_cast<const E*>(p.x) + a.sample * p.xn + a.c;
-  const E* go = static_cast<const E*>(p.go) + a.sample * p.gon + a.c;
-  E* out = static_cast<E*>(p.out) + a.sample * p.s * p.c + a.c;
-  each_positions(a, [&](int64_t t, int count) {
-    typename P::Raw raw[kAtOnce], graw[kAtOnce];
+  ch.load(p, a.c, a.any);
+  E* out = static_cast<E*>(p.out) + (a.sample * p.s + a.p0 + a.off) * p.c + a.c;
+  const int64_t step = int64_t(a.k.rows) * p.c;
+  in.each([&](int64_t t, float(&v)[V], float(&gu)[V]) {
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int64_t at = t + int64_t(min(i, count - 1)) * a.k.rows;
-      raw[i] = P::load(x + at * p.xs);
-      graw[i] = P::load(go + at * p.gos);
-    }
+    for (int k = 0; k < V; ++k) v[k] = (v[k] - n.mean) * n.r;
+    if (p.silu) ch.pass_silu(v, gu);
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      if (i >= count) break;
-      float v[V], gu[V];
-      P::open(raw[i], v);
-      P::open(graw[i], gu);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float y = (v[k] - n.mean) * n.r;
-        if (p.silu) gu[k] *= silu_slope(fmaf(y, ch.w[k], ch.bias[k]));
-        v[k] = n.r * (gu[k] * ch.w[k] - s1 - y * s2);
-      }
-      store_stream<BF, V>(out + (t + int64_t(i) * a.k.rows) * p.c, v);
-    }
+    for (int k = 0; k < V; ++k) v[k] = n.r * (gu[k] * ch.w[k] - s1 - v[k] * s2);
+    store_stream<BF, V>(out + t * step, v);
   });
 }
 
@@ -579,16 +575,18 @@ template <bool BF, int V>
 __global__ __launch_bounds__(kThreads) void map_forward(GnParams p) {
   __shared__ float l[3][kThreads];
   const Place<V> a(p);
-  normalise<BF, V>(p, a, joined_stats<V>(p, a, l));
+  Ahead<BF, V, false> in(p, a);
+  normalise<BF, V>(p, a, in, joined_stats<V>(p, a, l));
 }
 
 template <bool BF, int V>
 __global__ __launch_bounds__(kThreads) void map_sums(GnParams p, float* group_sums) {
   __shared__ float l[3][kThreads], share[2][kThreads][V];
   const Place<V> a(p);
+  Ahead<BF, V, true> in(p, a);
   const Norm n = joined_stats<V>(p, a, l);
   float s1, s2;
-  block_sums<BF, V>(p, a, n, l, share, &s1, &s2);
+  block_sums<BF, V>(p, a, in, n, l, share, &s1, &s2);
   if (first_of_group(a)) {
     float* to = group_sums + own_entry(p, a) * 2;
     to[0] = s1;
@@ -600,6 +598,7 @@ template <bool BF, int V>
 __global__ __launch_bounds__(kThreads) void map_backward(GnParams p, const float* group_sums) {
   __shared__ float l[3][kThreads];
   const Place<V> a(p);
+  Ahead<BF, V, true> in(p, a);
   entry_sums<2>(p, a, l, [&](int g, int i, float (&v)[2]) {
     const float* from = group_sums + entry_at(p, a, g, i) * 2;
     v[0] = from[0];
@@ -608,7 +607,7 @@ __global__ __launch_bounds__(kThreads) void map_backward(GnParams p, const float
   const int g = a.any && a.k.parts == 1 ? a.piece / a.k.pieces : 0;
   const float s1 = l[0][g], s2 = l[1][g];
   __syncthreads();
-  pass_back<BF, V>(p, a, joined_stats<V>(p, a, l), s1, s2);
+  pass_back<BF, V>(p, a, in, joined_stats<V>(p, a, l), s1, s2);
 }
 
 // A block that has its groups whole (one chunk, no wide groups) does all of it in one launch: 4 positions of 256
@@ -620,12 +619,17 @@ __global__ __launch_bounds__(kThreads) void map_alone(GnParams p, int gradient) 
   const Moments m = block_stats<BF, V>(p, a, l);
   const Norm n{m.mean, rsqrtf(m.m2 / m.n + p.eps)};
   if (!gradient) {
-    normalise<BF, V>(p, a, n);
+    Ahead<BF, V, false> in(p, a);
+    normalise<BF, V>(p, a, in, n);
     return;
   }
   float s1, s2;
-  block_sums<BF, V>(p, a, n, l, share, &s1, &s2);
-  pass_back<BF, V>(p, a, n, s1, s2);
+  {
+    Ahead<BF, V, true> in(p, a);
+    block_sums<BF, V>(p, a, in, n, l, share, &s1, &s2);
+  }
+  Ahead<BF, V, true> in(p, a);
+  pass_back<BF, V>(p, a, in, n, s1, s2);
 }
 
 // ---------------------------------------------------------------- which
