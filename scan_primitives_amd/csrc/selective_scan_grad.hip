@@ -395,9 +395,12 @@ __global__ __launch_bounds__(kWave* W, grad_waves_per_simd(BF, W)) void grad_mar
       for (int i = 0; i < 4; ++i) y[i] = skip[i] * x[i];
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        if (gated) lds_add<R>(l.y[w][q], c4, y);
         lds_add<R>(l.source[w][q], c4, source);
         lds_add<R>(l.decay[w][q], c4, decay);
+      }
+      if (gated) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) lds_add<R>(l.y[w][q], c4, y);
       }
       lds_add<R>(l.dt[q], c4, dt);
       lds_add<R>(l.gy[q], c4, gy);
@@ -407,14 +410,21 @@ __global__ __launch_bounds__(kWave* W, grad_waves_per_simd(BF, W)) void grad_mar
         gskip[i] = fmaf(gy[i], x[i], gskip[i]);
         // the rates stand times log2(e)
         gd[i] = fmaf(decay[i], 1.0f / kLog2e, x[i] * source[i]);
-        if (p.softplus) gd[i] *= sigmoid_of(v[i]);
-        gbias[i] += gd[i];
-        if (gated) gz[i] = go[i] * y[i] * silu_slope(z[i]);
       }
+      if (p.softplus) {  // once for the four, which are formed side by side so
+#pragma unroll
+        for (int i = 0; i < 4; ++i) gd[i] *= sigmoid_of(v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) gbias[i] += gd[i];
       const int64_t o = (int64_t(b) * p.T + s0 + t0) * p.D + d0 + (int64_t(q) * p.D + c4);
       put_channels<BF, WHOLE>(p.gx, o, left, gx);
       put_channels<BF, WHOLE>(p.gdelta, o, left, gd);
-      if (gated) put_channels<BF, WHOLE>(p.gz, o, left, gz);
+      if (gated) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) gz[i] = go[i] * y[i] * silu_slope(z[i]);
+        put_channels<BF, WHOLE>(p.gz, o, left, gz);
+      }
     }
     // the next span's dt, x and gy go where these were read
     __syncthreads();
