@@ -10,7 +10,7 @@
 // last K - 1 inputs in registers; the run's first K - 1 are read again from the run before
 // (from `initial` at the start). The last piece of a row starts early enough to
 // be whole: the channels it shares with the piece before get the same values from both.
-// Bound by memory: 8 ragged rows of 2048 tokens of 4096 channels in bf16 take 49 us; their bytes at a copy's rate
+// Bound by memory: 8 ragged rows of 2048 tokens of 4096 channels in bf16 take 46 us; their bytes at a copy's rate
 // would take 41.
 #include <algorithm>
 
@@ -35,7 +35,11 @@ struct Conv {
     for (int v = 0; v < V; ++v) {
 #pragma unroll
       for (int j = 0; j < K; ++j) w[j][v] = wp[int64_t(d0 + v) * K + j];
-      bias[v] = bp ? bp[d0 + v] : 0.0f;
+      bias[v] = 0.0f;
+    }
+    if (bp) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) bias[v] = bp[d0 + v];
     }
   }
   // u from the inputs before and the present one
@@ -109,15 +113,15 @@ __global__ __launch_bounds__(kThreads) void conv_forward(CcParams p) {
   using E = typename C::E;
   const Run r = run_of<V>(p);
   if (!r.any) return;
-  const C c(p.w, p.bias, r.d0);
-  float past[C::kPast][V];
-  read_past<BF, V, K>(p, r, past);
   const int end = min(r.t1, r.n);  // tokens there are
   const E* x = static_cast<const E*>(p.x.p) + int64_t(r.b) * p.x.sb + int64_t(r.d0) * p.x.sd;
   E* out = static_cast<E*>(p.out) + int64_t(r.b) * p.T * p.D + r.d0;
   typename P::Raw raw[kAhead];
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) raw[i] = r.t0 + i < end ? P::load(x + int64_t(r.t0 + i) * p.x.st) : P::zero();
+  const C c(p.w, p.bias, r.d0);
+  float past[C::kPast][V];
+  read_past<BF, V, K>(p, r, past);
   for (int t = r.t0; t < end; t += kAhead) {
     float v[kAhead][V];
 #pragma unroll
@@ -343,8 +347,8 @@ int piece_channels(const CcParams& p, bool gradient) {
 void causal_conv_split(CcParams& p, bool gradient) {
   // whatever the strides, for the workspace goes by it
   const int64_t v = p.bf16 && !gradient ? 8 : 4, pieces = (p.D + v - 1) / v;
-  // Two waves a SIMD (8 ragged rows of 2048 tokens of 4096 channels in bf16: 77, 68, 57, 48, 49 us with 16, 8, 4, 2, 1;
-  // the gradient of 4 x 2048 x 2048 54, 43, 35, 49 with 8, 4, 2, 1), of 8 tokens at least, 16 of a gradient, whose first
+  // Two waves a SIMD (8 ragged rows of 2048 tokens of 4096 channels in bf16: 48, 47, 46, 49 us with 4, 3, 2, 1; the
+  // gradient of 4 x 2048 x 2048 42, 36, 35, 47), of 8 tokens at least, 16 of a gradient, whose first
   // and last are read twice.
   const int64_t want = std::max<int64_t>(1, int64_t(device_cu_count()) * 4 * 2 * kWave / std::max<int64_t>(1, pieces * p.B));
   const int64_t chunk = std::max<int64_t>(gradient ? 16 : 8, (p.T + want - 1) / want);
