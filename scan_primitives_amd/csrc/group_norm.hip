@@ -201,8 +201,10 @@ __global__ __launch_bounds__(kThreads) void rows_backward(GnParams p) {
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int m = 0; m < M; ++m) {
+      // a lane without channels or behind the last row adds zeros, also where r is infinite (no eps, no variance)
+      const float scale = is[m] && row < p.n ? r : 0.0f;
 #pragma unroll
-      for (int k = 0; k < V; ++k) v[m][k] *= r;
+      for (int k = 0; k < V; ++k) v[m][k] *= scale;
       if (p.silu) ch[m].pass_silu(v[m], g[m]);
 #pragma unroll
       for (int k = 0; k < V; ++k) {
