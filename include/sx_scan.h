@@ -785,7 +785,8 @@ sx_status sx_selective_scan_step(sx_dtype dtype, const int64_t* x_shape, const i
  *  workspace     at least sx_group_norm_workspace_bytes() bytes, 256-byte aligned;
  *                may hold anything; may be NULL when that is 0.
  *
- * An infinity or NaN turns its sample's group to NaN and no other. Errors as
+ * An infinity or NaN turns its sample's group to NaN and no other. A variance
+ * past f32's range counts as infinite: u is the bias then. Errors as
  * sx_decay_attention.
  */
 sx_status sx_group_norm(sx_dtype dtype, const int64_t* x_shape, const int64_t* x_strides, const void* x, int64_t groups,

@@ -381,6 +381,13 @@ struct Norm {
   float mean, r;
 };
 
+// Squared distance from the mean of n values with these sums. Below zero by rounding it is zero; what is not finite
+// stays so: the mean of a group with an infinity is infinite, and only an infinite or lost variance turns all to NaN.
+__device__ __forceinline__ float spread_of(float squares, float sum, float n) {
+  const float d = fmaf(-sum, sum / n, squares);
+  return d < 0.0f ? 0.0f : d;
+}
+
 // The moments of a block's part of a thread's group. A thread sums differences from its first value, and the threads
 // differences from the mean of the group's first, so that no large mean cancels.
 template <bool BF, int V>
@@ -399,7 +406,7 @@ __device__ __forceinline__ Moments block_stats(const GnParams& p, const Place<V>
     }
     n += float(V);
   });
-  const float mean = n > 0.0f ? shift + sum / n : 0.0f, m2 = n > 0.0f ? fmaxf(sq - sum * (sum / n), 0.0f) : 0.0f;
+  const float mean = n > 0.0f ? shift + sum / n : 0.0f, m2 = n > 0.0f ? spread_of(sq, sum, n) : 0.0f;
   l[0][threadIdx.x] = mean;
   __syncthreads();
   const int g = a.any && a.k.parts == 1 ? a.piece / a.k.pieces : 0;
@@ -408,8 +415,7 @@ __device__ __forceinline__ Moments block_stats(const GnParams& p, const Place<V>
   const float off = mean - about;
   float v[3] = {n, n * off, n > 0.0f ? fmaf(n * off, off, m2) : 0.0f};
   group_sums_of<3>(p, a, l, v);
-  const float rest = v[1] / v[0];
-  return {v[0], about + rest, fmaxf(v[2] - v[1] * rest, 0.0f)};
+  return {v[0], about + v[1] / v[0], spread_of(v[2], v[1], v[0])};
 }
 
 // The first thread of each of the block's groups.
@@ -486,8 +492,8 @@ __device__ __forceinline__ Norm joined_stats(const GnParams& p, const Place<V>& 
     v[2] = fmaf(v[1], off, from[2]);
   });
   const int g = a.any && a.k.parts == 1 ? a.piece / a.k.pieces : 0;
-  const float off = l[1][g] / l[0][g];
-  const Norm n{first(g) + off, rsqrtf(fmaxf(l[2][g] - l[1][g] * off, 0.0f) / l[0][g] + p.eps)};
+  const float count = l[0][g], sum = l[1][g];
+  const Norm n{first(g) + sum / count, rsqrtf(spread_of(l[2][g], sum, count) / count + p.eps)};
   __syncthreads();
   return n;
 }

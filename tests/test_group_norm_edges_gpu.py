@@ -20,3 +20,46 @@ def test_no_eps(shape, groups, act, type, monkeypatch):
     monkeypatch.setitem(norm.CASES, "no eps", dict(shape=shape, groups=groups, act=act, type=type, eps=0.0))
     norm.test_forward("no eps")
     norm.test_backward("no eps")
+
+
+# x, groups, and positions of an infinity: [.., channel of the group's sixteen or more]
+PLACES = [((3, 20, 64), 4, [(1, 0, 20), (1, 0, 21), (1, 7, 18), (1, 19, 31)]),               # a workgroup a sample
+          ((2, 20000, 32), 2, [(1, 0, 17), (1, 9, 21), (1, 12345, 16), (1, 19999, 31)]),     # many chunks a sample
+          ((2, 10, 6000), 2, [(1, 0, 3001), (1, 9, 3777), (1, 4, 5999)]),                    # groups wider than a workgroup
+          ((3, 9000), 1, [(1, 0), (1, 1), (1, 5003), (1, 8999)]),                            # rows wider than one
+          ((40, 64), 4, [(1, 16), (1, 21), (1, 31)])]
+
+
+@pytest.mark.parametrize("type", [BF, F32])
+@pytest.mark.parametrize("act", [None, "silu"])
+@pytest.mark.parametrize("shape,groups,places", PLACES)
+def test_an_infinity_anywhere_turns_its_group_to_nan(shape, groups, places, act, type):
+    s, go = norm.make(shape=shape, groups=groups, act=act, type=type)
+    clean, grads, x = sx.group_norm(**s), sx.group_norm_backward(grad_out=go, **s), s["x"].clone()
+    per = shape[-1] // groups
+    for place in places:
+        for value in (float("inf"), float("-inf"), float("nan")):
+            s["x"].copy_(x)
+            s["x"][place] = value
+            first = place[-1] // per * per
+            bad = torch.zeros_like(clean, dtype=torch.bool)
+            bad[place[0], ..., first:first + per] = True
+            out, got = sx.group_norm(**s), sx.group_norm_backward(grad_out=go, **s)
+            for a, b in ((out, clean), (got[0], grads[0])):
+                assert torch.isnan(a[bad]).all() and torch.equal(a[~bad], b[~bad]), (place, value)
+            keep = torch.ones(shape[-1], dtype=torch.bool, device=DEV)
+            keep[first:first + per] = False
+            assert torch.equal(got[1][keep], grads[1][keep]) and torch.equal(got[2][keep], grads[2][keep])
+
+
+@pytest.mark.parametrize("type", [BF, F32])
+@pytest.mark.parametrize("shape,groups", [((40, 64), 4), ((3, 20, 64), 4), ((1, 20000, 32), 2), ((2, 10, 6000), 2),
+                                          ((3, 9000), 1)])
+def test_squares_past_the_range_are_an_infinite_variance(shape, groups, type):
+    s, go = norm.make(shape=shape, groups=groups, type=type)
+    for size in (1e20, 1e30):
+        big = dict(s, x=s["x"] * size)
+        out, got = sx.group_norm(**big), sx.group_norm_backward(grad_out=go, **big)
+        assert torch.equal(out, s["bias"].expand(shape).to(type))
+        assert not got[0].any() and not got[1].any()
+        assert torch.isfinite(got[2]).all() and got[2].any()
