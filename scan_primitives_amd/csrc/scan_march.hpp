@@ -77,6 +77,37 @@ __device__ __forceinline__ void rates(const float* a, int64_t d, int n0, int N, 
   for (int i = 0; i < kScanStates; ++i) r[i] = is && n0 + i < N ? a[d * N + n0 + i] * kLog2e : 0.0f;
 }
 
+// Whether a wave's states may grow: a positive rate, or steps of any sign.
+__device__ __forceinline__ bool may_grow(const SsParams& p, const float (&rate)[kScanStates]) {
+  bool any = !p.softplus;
+#pragma unroll
+  for (int i = 0; i < kScanStates; ++i) any |= !(rate[i] <= 0.0f);
+  return __any(any);
+}
+
+// exp2(e) v, where exp2(e) alone may lie outside f32's range: 2^300 turns the least value there is to infinity.
+__device__ __forceinline__ float times_exp2(float v, float e) {
+  const float in = e > 300.0f ? 300.0f : e < -300.0f ? -300.0f : e, whole = floorf(in);
+  return ldexpf(v * exp2_of(in - whole), int(whole));
+}
+
+// States (or adjoints) over tokens whose dt add up to `steps`: exp2(steps rate) h + own in place of h. Where states
+// grow, the decay alone may be infinite while its product is not: a zero stays zero, a small state comes out as token
+// by token.
+__device__ __forceinline__ void carry_over(bool grows, float steps, const float (&rate)[kScanStates], const f32x4& own,
+                                           float (&h)[kScanStates]) {
+  if (!grows) {
+#pragma unroll
+    for (int i = 0; i < kScanStates; ++i) h[i] = fmaf(exp2_of(steps * rate[i]), h[i], own[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kScanStates; ++i) {
+      const float e = steps * rate[i];
+      h[i] = e <= 127.0f ? fmaf(exp2_of(e), h[i], own[i]) : times_exp2(h[i], e) + own[i];
+    }
+  }
+}
+
 // h[n0 .. n0 + 3] of one channel in [.., D, N].
 __device__ __forceinline__ void read_states(const float* p, int64_t row, int n0, int N, bool is,
                                             float (&h)[kScanStates]) {
@@ -249,6 +280,49 @@ __device__ __forceinline__ void sources(const float (&b)[kScanStates], const flo
 #undef SX_ROW
 }
 
+// A wave's adjoints of its segment once more, by the exponents' sums and an element at a time: the sum over the tokens
+// of c gy times the decays up to each. What it needs is formed again from the block's number, and all of it behind the
+// march: in the march the same costs every call registers (4 x 2048 tokens of 2048 channels in bf16: 395 us, 354).
+template <bool BF>
+__device__ __forceinline__ void adjoint_again(const SsParams& p) {
+  using E = typename Piece<BF, 1>::E;
+  uint32_t at = blockIdx.x;
+  asm volatile("" : "+s"(at));  // nothing of it is kept over the march
+  const int per_group = p.D / p.G, blocks = (per_group + kChannels - 1) / kChannels;
+  const int cb = int(at % uint32_t(blocks));
+  at /= uint32_t(blocks);
+  const int g = int(at % uint32_t(p.G));
+  at /= uint32_t(p.G);
+  const int64_t b = at % uint32_t(p.B), seg = at / uint32_t(p.B);
+  const int lane = int(threadIdx.x) % kWave, wave = int(threadIdx.x) / kWave, n0 = wave * kScanStates;
+  if (lane >= min(kChannels, per_group - cb * kChannels)) return;
+  const int64_t d = int64_t(g) * per_group + cb * kChannels + lane;
+  const int s0 = int(seg) * p.seg_tokens, end = min(min(s0 + p.seg_tokens, p.T), row_length(p.lengths, int(b), p.T));
+  const auto element = [](const void* from, int64_t i) {
+    float v[1];
+    Piece<BF, 1>::open(static_cast<const E*>(from)[i], v);
+    return v[0];
+  };
+  const auto token = [&](const TokenView& v, int64_t t) { return element(v.p, b * v.sb + t * v.st + d * v.sd); };
+  float rate[kScanStates], adj[kScanStates] = {}, steps = 0.0f;
+  rates(p.a, d, n0, p.N, true, rate);
+  const float bias = p.delta_bias ? p.delta_bias[d] : 0.0f;
+#pragma unroll 1
+  for (int t = s0; t < end; ++t) {
+    const float v = token(p.delta, t) + bias;
+    float gy = token(p.go, t);
+    if (p.z.p) gy *= silu_of(token(p.z, t));
+    steps += p.softplus ? softplus_of(v) : v;
+#pragma unroll
+    for (int i = 0; i < kScanStates; ++i) {
+      if (n0 + i >= p.N) break;
+      const float c = element(p.c.p, b * p.c.sb + int64_t(t) * p.c.st + g * p.c.sg + (n0 + i) * p.c.sn);
+      adj[i] += times_exp2(c * gy, steps * rate[i]);
+    }
+  }
+  *reinterpret_cast<f32x4*>(p.seg_adjoint + packed_at(p, seg * p.B + b, wave, d)) = f32x4{adj[0], adj[1], adj[2], adj[3]};
+}
+
 template <int W, March KIND>
 struct alignas(16) MarchLds {
   float dt[2][kTile][kChannels];
@@ -272,6 +346,7 @@ __global__ __launch_bounds__(kWave* W, march_waves_per_simd(W)) void scan_march(
   constexpr int kPasses = (kPieces + kThreads - 1) / kThreads, kStep = kThreads / (kChannels / 4);
   constexpr int kAtOnce = kStep < kTile ? kStep : kTile;
   __shared__ MarchLds<W, KIND> l;
+  __shared__ int back;  // JoinedMarks without softplus: a step is negative
   const int tid = int(threadIdx.x), lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int n0 = wave * kScanStates;
   // where the workgroup is
@@ -337,6 +412,9 @@ __global__ __launch_bounds__(kWave* W, march_waves_per_simd(W)) void scan_march(
           x[i] = q <= room ? x[i] : 0.0f;
         }
       }
+      if (ADJOINT && !p.softplus) {
+        if (fminf(fminf(v[0], v[1]), fminf(v[2], v[3])) < 0.0f) back = 1;
+      }
       lds_put<R>(l.dt[tile & 1][q], c4, v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] *= v[i];
@@ -371,22 +449,25 @@ __global__ __launch_bounds__(kWave* W, march_waves_per_simd(W)) void scan_march(
   read_states(OUT || KIND == March::Marks ? p.initial : nullptr, int64_t(b) * p.D + d, n0, p.N, is, h);
   if constexpr (OUT) {
     constexpr int A = 8;  // segments read ahead of the chain
-    for (int m = 0; m < seg; m += A) {
-      f32x4 own[A];
-      float sum[A];
+    const auto chain = [&](auto grows) {
+      for (int m = 0; m < seg; m += A) {
+        f32x4 own[A];
+        float sum[A];
 #pragma unroll
-      for (int k = 0; k < A; ++k) {
-        const int64_t row = int64_t(min(m + k, seg - 1)) * p.B + b;
-        own[k] = is ? *reinterpret_cast<const f32x4*>(p.seg_state + packed_at(p, row, wave, d)) : zero4();
-        sum[k] = is ? p.seg_steps[row * p.D + d] : 0.0f;
+        for (int k = 0; k < A; ++k) {
+          const int64_t row = int64_t(min(m + k, seg - 1)) * p.B + b;
+          own[k] = is ? *reinterpret_cast<const f32x4*>(p.seg_state + packed_at(p, row, wave, d)) : zero4();
+          sum[k] = is ? p.seg_steps[row * p.D + d] : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < A; ++k) {
+          if (m + k >= seg) break;
+          carry_over(grows, sum[k], rate, own[k], h);
+        }
       }
-#pragma unroll
-      for (int k = 0; k < A; ++k) {
-        if (m + k >= seg) break;
-#pragma unroll
-        for (int i = 0; i < kScanStates; ++i) h[i] = fmaf(exp2_of(sum[k] * rate[i]), h[i], own[k][i]);
-      }
-    }
+    };
+    if (may_grow(p, rate)) chain(std::true_type());
+    else chain(std::false_type());
   }
 #pragma unroll
   for (int i = 0; i < kScanStates; ++i) {
@@ -400,6 +481,10 @@ __global__ __launch_bounds__(kWave* W, march_waves_per_simd(W)) void scan_march(
     if (ADJOINT && wave == 0) p.mark_steps[row * p.D + d] = before;
   };
 
+  if (ADJOINT && !p.softplus) {
+    if (tid == 0) back = 0;
+    __syncthreads();
+  }
   if (tiles > 0) {
     read(0);
     read_rows(0);
@@ -528,6 +613,14 @@ __global__ __launch_bounds__(kWave* W, march_waves_per_simd(W)) void scan_march(
     if (ADJOINT)
       *reinterpret_cast<f32x4*>(p.seg_adjoint + packed_at(p, row, wave, d)) = f32x4{adj[0], adj[1], adj[2], adj[3]};
     if (wave == 0) p.seg_steps[row * p.D + d] = steps;
+  }
+  if constexpr (ADJOINT) {
+    // Where states grow, the decays' product may have left f32's range, and with steps of both signs come back: what
+    // it multiplied may be zero or small. (Lanes without a channel hold what LDS held.)
+    bool lost = !p.softplus && back;
+#pragma unroll
+    for (int i = 0; i < kScanStates; ++i) lost |= !(through[i] < INFINITY);
+    if (__any(lost && is)) adjoint_again<BF>(p);
   }
 }
 

@@ -44,6 +44,7 @@ __global__ __launch_bounds__(256) void carry(SsParams p) {
   f32x4* at = reinterpret_cast<f32x4*>(back ? p.seg_adjoint : p.seg_state) + idx;
   const float* steps = p.seg_steps + b * p.D + d;
   constexpr int A = 4;  // segments read ahead of the chain
+  const bool grows = may_grow(p, rate);
   for (int m = 0; m < p.segments; m += A) {
     f32x4 own[A];
     float sum[A];
@@ -58,8 +59,7 @@ __global__ __launch_bounds__(256) void carry(SsParams p) {
       if (m + k >= p.segments) break;
       const int j = back ? p.segments - 1 - (m + k) : m + k;
       at[j * p.B * row] = f32x4{h[0], h[1], h[2], h[3]};
-#pragma unroll
-      for (int i = 0; i < kScanStates; ++i) h[i] = fmaf(exp2_of(sum[k] * rate[i]), h[i], own[k][i]);
+      carry_over(grows, sum[k], rate, own[k], h);
     }
   }
 }
@@ -222,6 +222,7 @@ __global__ __launch_bounds__(kWave* W, grad_waves_per_simd(BF, W)) void grad_mar
       read_states(p.grad_state, int64_t(b) * p.D + d + c, n0, p.N, is[c], mu[c]);
     }
   }
+  const bool grows = JOIN && (may_grow(p, rate[0]) || may_grow(p, rate[1]));
   f32x4 marks[2];
   float mark_steps[2];
   const auto read_marks = [&](int span) {
@@ -285,12 +286,11 @@ __global__ __launch_bounds__(kWave* W, grad_waves_per_simd(BF, W)) void grad_mar
     // registers are worth
     float hs[M + 1][2][kScanStates];
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int i = 0; i < kScanStates; ++i) {
-        hs[0][c][i] = marks[c][i];
-        if constexpr (JOIN) hs[0][c][i] = fmaf(exp2_of(mark_steps[c] * rate[c][i]), start[c][i], hs[0][c][i]);
-      }
+      for (int i = 0; i < kScanStates; ++i) hs[0][c][i] = JOIN ? start[c][i] : marks[c][i];
+      if constexpr (JOIN) carry_over(grows, mark_steps[c], rate[c], marks[c], hs[0][c]);
+    }
     __syncthreads();
     each<2>([&](auto Q) {
       constexpr int j4 = 4 * decltype(Q)::value;
