@@ -71,10 +71,18 @@ struct RowRaw {
   }
 };
 
-// a[d, n0 .. n0 + 3] for exp2: times log2(e), zero where there are none.
+// A rate for exp2: a log2(e), never infinite, for a step of zero (a token that does not exist has one) leaves the state
+// as it is.
+__device__ __forceinline__ float rate_of(float a) {
+  constexpr float kMost = 3.4028234663852886e38f;
+  const float r = a * kLog2e;
+  return r < -kMost ? -kMost : r > kMost ? kMost : r;
+}
+
+// a[d, n0 .. n0 + 3] for exp2, zero where there are none.
 __device__ __forceinline__ void rates(const float* a, int64_t d, int n0, int N, bool is, float (&r)[kScanStates]) {
 #pragma unroll
-  for (int i = 0; i < kScanStates; ++i) r[i] = is && n0 + i < N ? a[d * N + n0 + i] * kLog2e : 0.0f;
+  for (int i = 0; i < kScanStates; ++i) r[i] = is && n0 + i < N ? rate_of(a[d * N + n0 + i]) : 0.0f;
 }
 
 // Whether a wave's states may grow: a positive rate, or steps of any sign.

@@ -85,6 +85,7 @@ __global__ __launch_bounds__(256) void scan_step(SsStep p) {
   const float x = value(p.x), z = p.z.p ? value(p.z) : 0.0f, skip = p.skip ? p.skip[d] : 0.0f;
   float dt = value(p.delta) + (p.delta_bias ? p.delta_bias[d] : 0.0f), y = 0.0f;
   if (p.softplus) dt = softplus_of(dt);
+  const bool still = dt == 0.0f;  // whatever the rate (one times log2(e) may be infinite)
 #pragma unroll
   for (int i = 0; i < S; ++i) {
     float bv[4], cv[4];
@@ -92,7 +93,7 @@ __global__ __launch_bounds__(256) void scan_step(SsStep p) {
     P4::open(craw[i], cv);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      h[i][k] = fmaf(exp2_of(dt * (rate[i][k] * kLog2e)), h[i][k], dt * x * bv[k]);
+      h[i][k] = fmaf(still ? 1.0f : exp2_of(dt * (rate[i][k] * kLog2e)), h[i][k], dt * x * bv[k]);
       y = fmaf(cv[k], h[i][k], y);
     }
     if constexpr (VEC) {
