@@ -1930,9 +1930,9 @@ sx_status sx_causal_conv(sx_dtype dtype, const int64_t* x_shape, const int64_t* 
   const int64_t B = x_shape[0], D = x_shape[2], n = numel_of(a.x), state = B * (taps - 1) * D;
   const size_t e = dtype == SX_BF16 ? 2 : 4;
   if (B == 0 || (n == 0 && !final_state)) return ok();
+  if (!weight) return missing(op, "weight");  // a launch reads it, also of no tokens
   if (n > 0) {
     if (!x) return missing(op, "x");
-    if (!weight) return missing(op, "weight");
     if (!out) return missing(op, "out");
   }
   const Span in[] = {span_of(a.x, e), flat_span("weight", weight, D * taps * 4), flat_span("bias", bias, D * 4),
@@ -2174,6 +2174,7 @@ sx_status sx_selective_scan(sx_dtype dtype, const int64_t* x_shape, const int64_
     if ((st = scan_pointers(op, args)) != SX_OK) return st;
     if (!out) return missing(op, "out");
   }
+  if (!a) return missing(op, "a");  // a launch reads it, also of no tokens
   const size_t e = dtype == SX_BF16 ? 2 : 4;
   Span in[10];
   int k = scan_spans(args, e, in);
