@@ -13,6 +13,7 @@
 // Bound by memory: 8 ragged rows of 2048 tokens of 4096 channels in bf16 take 45.5 us; their bytes at a copy's rate
 // would take 41.
 #include <algorithm>
+#include <cmath>
 
 #include "sx_state_space.hpp"
 
@@ -290,9 +291,11 @@ __global__ __launch_bounds__(kThreads) void conv_step(CcStep p) {
 
 constexpr int kForward = 0, kBackward = 1;
 
+int64_t run_threads(const CcParams& p, int v) { return int64_t((p.D + v - 1) / v) * p.chunks * p.B; }
+
 template <bool BF, int V, int K>
 hipError_t launch_run(const CcParams& p, int which, hipStream_t stream) {
-  const int64_t threads = int64_t((p.D + V - 1) / V) * p.chunks * p.B;
+  const int64_t threads = run_threads(p, V);
   const unsigned grid = unsigned((threads + kThreads - 1) / kThreads);
   if (which == kForward) conv_forward<BF, V, K><<<grid, kThreads, 0, stream>>>(p);
   else conv_backward<BF, V, K><<<grid, kThreads, 0, stream>>>(p);
@@ -341,8 +344,18 @@ int piece_channels(const CcParams& p, bool gradient) {
   const bool unit = p.x.sd == 1 && (!gradient || p.go.sd == 1);
   return unit && p.D >= v ? v : 1;
 }
+int step_channels(const CcStep& p) {
+  const int v = p.bf16 ? 8 : 4;
+  return p.sd == 1 && p.D % v == 0 ? v : 1;
+}
+double workgroups(double threads) { return std::ceil(threads / kThreads); }
 
 }  // namespace
+
+double causal_conv_workgroups(const CcParams& p, bool gradient) {
+  return workgroups(double(run_threads(p, piece_channels(p, gradient))));
+}
+double causal_conv_step_workgroups(const CcStep& p) { return workgroups(double(p.D / step_channels(p)) * p.B); }
 
 void causal_conv_split(CcParams& p, bool gradient) {
   // whatever the strides, for the workspace goes by it
@@ -377,12 +390,9 @@ hipError_t launch_causal_conv_backward(const CcParams& p, hipStream_t stream) {
 }
 
 hipError_t launch_causal_conv_step(const CcStep& p, hipStream_t stream) {
-  if (p.bf16) {
-    if (p.sd == 1 && p.D % 8 == 0) return step_taps<true, 8>(p, stream);
-    return step_taps<true, 1>(p, stream);
-  }
-  if (p.sd == 1 && p.D % 4 == 0) return step_taps<false, 4>(p, stream);
-  return step_taps<false, 1>(p, stream);
+  const int v = step_channels(p);
+  if (p.bf16) return v == 1 ? step_taps<true, 1>(p, stream) : step_taps<true, 8>(p, stream);
+  return v == 1 ? step_taps<false, 1>(p, stream) : step_taps<false, 4>(p, stream);
 }
 
 }  // namespace sx

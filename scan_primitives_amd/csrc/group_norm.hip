@@ -16,6 +16,7 @@
 // Bound by memory: 16384 rows of 2048 channels in bf16 take 23 to 25 us (5.5 TB/s), the gradient of
 // 8 x 4096 positions of 512 channels 57 to 59 us: three launches, of which the first two read what the third reads again.
 #include <algorithm>
+#include <cmath>
 
 #include "sx_state_space.hpp"
 
@@ -769,8 +770,10 @@ void group_norm_split(GnParams& p, bool gradient) {
   p.chunks = int(std::max<int64_t>(1, (p.s + chunk - 1) / chunk));
 }
 
-double group_norm_workgroups(const GnParams& p) {
-  return row_lanes(p) ? double(p.chunks) : double(p.n) * double(p.chunks) * blocks_for(p).count;
+double group_norm_workgroups(const GnParams& p, bool gradient) {
+  if (!row_lanes(p)) return double(p.n) * double(p.chunks) * blocks_for(p).count;
+  const RowGrid r = row_grid(p, row_lanes(p), gradient);
+  return r.y > 65535 ? HUGE_VAL : double(r.x) * r.y;  // a grid has no more rows of workgroups
 }
 
 int64_t group_norm_stats_floats(const GnParams& p) {

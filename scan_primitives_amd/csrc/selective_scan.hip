@@ -141,10 +141,11 @@ void launch_step(const SsStep& p, bool vec, hipStream_t stream) {
 
 template <bool BF>
 void launch_step_states(const SsStep& p, bool vec, hipStream_t stream) {
-  if (p.N <= 4) launch_step<BF, 1, 1>(p, vec, stream);
-  else if (p.N <= 8) launch_step<BF, 1, 2>(p, vec, stream);
-  else if (p.N <= 16) launch_step<BF, 2, 2>(p, vec, stream);
-  else launch_step<BF, 4, 2>(p, vec, stream);
+  switch (selective_scan_step_lanes(p.N)) {
+    case 1: p.N <= 4 ? launch_step<BF, 1, 1>(p, vec, stream) : launch_step<BF, 1, 2>(p, vec, stream); break;
+    case 2: launch_step<BF, 2, 2>(p, vec, stream); break;
+    default: launch_step<BF, 4, 2>(p, vec, stream);
+  }
 }
 
 }  // namespace
@@ -175,6 +176,8 @@ void selective_scan_split(SsParams& p, bool gradient) {
   p.segments = int(std::max<int64_t>(1, (tiles + per - 1) / per));
   p.row_marks = int((int64_t(p.T) + kMarkTokens - 1) / kMarkTokens);
 }
+
+int selective_scan_step_lanes(int N) { return N <= 8 ? 1 : N <= 16 ? 2 : 4; }
 
 hipError_t launch_selective_scan_step(const SsStep& p, hipStream_t stream) {
   const bool vec = p.N % 4 == 0 && p.ss % 4 == 0 && (reinterpret_cast<uintptr_t>(p.state) & 15u) == 0 &&

@@ -8,6 +8,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <cstdarg>
 #include <cstdio>
@@ -1909,8 +1910,9 @@ sx::CcParams conv_params(const sx_dtype& dtype, const ConvArgs& a, const int32_t
   return p;
 }
 
-sx_status grid_fits(const char* op, double groups) {
-  if (groups > double(kMostGrid)) return fail(SX_E_UNSUPPORTED, "%s: too many elements for one launch", op);
+// A launch takes fewer than 2^32 threads along its grid.
+sx_status grid_fits(const char* op, double groups, int threads) {
+  if (groups * threads >= 4294967296.0) return fail(SX_E_UNSUPPORTED, "%s: too many elements for one launch", op);
   return ok();
 }
 
@@ -1941,7 +1943,7 @@ sx_status sx_causal_conv(sx_dtype dtype, const int64_t* x_shape, const int64_t* 
                      flat_span("the final state", final_state, state * int64_t(e))};
   if ((st = no_overlap(op, in, 5, to, 2)) != SX_OK) return st;
   sx::CcParams p = conv_params(dtype, a, lengths, activation, false);
-  if ((st = grid_fits(op, double(p.B) * p.chunks * double(D) / 256 + 1)) != SX_OK) return st;
+  if ((st = grid_fits(op, sx::causal_conv_workgroups(p, false), 256)) != SX_OK) return st;
   p.initial = initial;
   p.out = out;
   p.last = final_state;
@@ -1981,9 +1983,9 @@ sx_status sx_causal_conv_backward(sx_dtype dtype, const int64_t* x_shape, const 
                      flat_span("grad_bias", grad_bias, D * 4), flat_span("grad_initial", grad_initial, state * e)};
   if ((st = no_overlap(op, in, 7, to, 4)) != SX_OK) return st;
   sx::CcParams p = conv_params(dtype, a, lengths, activation, true);
-  if ((st = grid_fits(op, double(p.B) * p.chunks * double(D) / 256 + 1)) != SX_OK) return st;
-  if ((st = check_workspace(op, workspace, workspace_bytes, conv_partial_floats(p) * sizeof(float))) != SX_OK) return st;
   p.go = token_view(go);
+  if ((st = grid_fits(op, sx::causal_conv_workgroups(p, true), 256)) != SX_OK) return st;
+  if ((st = check_workspace(op, workspace, workspace_bytes, conv_partial_floats(p) * sizeof(float))) != SX_OK) return st;
   p.initial = initial;
   p.grad_state = grad_state;
   p.out = grad_x;
@@ -2015,7 +2017,6 @@ sx_status sx_causal_conv_step(sx_dtype dtype, const int64_t* x_shape, const int6
   const Span in[] = {span_of(a.x, e), flat_span("weight", weight, D * taps * 4), flat_span("bias", bias, D * 4),
                      flat_span("slots", slots, B * 4)};
   if ((st = no_overlap(op, in, 4, to, 2)) != SX_OK) return st;
-  if ((st = grid_fits(op, double(B) * double(D) / 256 + 1)) != SX_OK) return st;
   const sx::TokenView v = token_view(a.x);
   sx::CcStep p{};
   p.B = int(B);
@@ -2033,6 +2034,7 @@ sx_status sx_causal_conv_step(sx_dtype dtype, const int64_t* x_shape, const int6
   p.silu = activation == SX_ACT_SILU;
   p.bf16 = dtype == SX_BF16;
   p.out = out;
+  if ((st = grid_fits(op, sx::causal_conv_step_workgroups(p), 256)) != SX_OK) return st;
   return device_status(sx::launch_causal_conv_step(p, static_cast<hipStream_t>(stream)), "causal-conv step launch");
 }
 
@@ -2136,10 +2138,12 @@ void carve_scan_gradient(Carve& c, sx::SsParams& p) {
   p.bias_partial = c.take<float>(rows * D);
 }
 
-sx_status scan_grid(const char* op, const sx::SsParams& p) {
+// The largest launches: the march, and of the gradient the sums of a token's rows and of the rates.
+sx_status scan_grid(const char* op, const sx::SsParams& p, bool gradient) {
   const double blocks = double(p.G) * ((p.D / p.G + 63) / 64);
-  sx_status st = grid_fits(op, blocks * p.B * p.segments);
-  if (st == SX_OK) st = grid_fits(op, double(p.B) * p.G * p.T * 8 * p.waves / 256 + 1);
+  sx_status st = grid_fits(op, blocks * p.B * p.segments, 64 * p.waves);
+  if (st == SX_OK && gradient) st = grid_fits(op, std::ceil(double(p.B) * p.G * p.T * 8 * p.waves / 256), 256);
+  if (st == SX_OK && gradient) st = grid_fits(op, std::ceil(double(p.D) * p.N / 64), 1024);
   return st;
 }
 
@@ -2183,7 +2187,7 @@ sx_status sx_selective_scan(sx_dtype dtype, const int64_t* x_shape, const int64_
   const Span to[] = {flat_span("out", out, n * int64_t(e)), flat_span("the final state", final_state, state * 4)};
   if ((st = no_overlap(op, in, k, to, 2)) != SX_OK) return st;
   sx::SsParams p = scan_params(dtype, args, false);
-  if ((st = scan_grid(op, p)) != SX_OK) return st;
+  if ((st = scan_grid(op, p, false)) != SX_OK) return st;
   Carve w{reinterpret_cast<uintptr_t>(workspace)};
   carve_scan(w, p);
   if ((st = check_workspace(op, workspace, workspace_bytes, w.used)) != SX_OK) return st;
@@ -2252,7 +2256,7 @@ sx_status sx_selective_scan_backward(sx_dtype dtype, const int64_t* x_shape, con
                      flat_span("grad_initial", grad_initial, state * 4)};
   if ((st = no_overlap(op, in, k, to, 9)) != SX_OK) return st;
   sx::SsParams p = scan_params(dtype, args, true);
-  if ((st = scan_grid(op, p)) != SX_OK) return st;
+  if ((st = scan_grid(op, p, true)) != SX_OK) return st;
   Carve w{reinterpret_cast<uintptr_t>(workspace)};
   carve_scan_gradient(w, p);
   if ((st = check_workspace(op, workspace, workspace_bytes, w.used)) != SX_OK) return st;
@@ -2297,7 +2301,8 @@ sx_status sx_selective_scan_step(sx_dtype dtype, const int64_t* x_shape, const i
   int k = scan_spans(args, size_t(e), in);
   in[k++] = flat_span("slots", slots, B * 4);
   if ((st = no_overlap(op, in, k, to, 2)) != SX_OK) return st;
-  if ((st = grid_fits(op, double(B) * double(D) * 8 / 256 + 1)) != SX_OK) return st;
+  if ((st = grid_fits(op, std::ceil(double(B) * double(D) * sx::selective_scan_step_lanes(int(N)) / 256), 256)) != SX_OK)
+    return st;
   sx::SsStep p{};
   p.B = int(B);
   p.D = int(D);
@@ -2355,7 +2360,7 @@ sx_status plan_norm(const char* op, const sx_dtype& dtype, const Operand& x, int
   p->silu = act == SX_ACT_SILU;
   p->bf16 = dtype == SX_BF16;
   sx::group_norm_split(*p, gradient);
-  return grid_fits(op, sx::group_norm_workgroups(*p));
+  return grid_fits(op, sx::group_norm_workgroups(*p, gradient), 256);
 }
 
 size_t carve_norm(Carve& c, sx::GnParams& p, bool gradient) {

@@ -57,6 +57,7 @@ struct CcParams {
   float* gbias;            // [D] or nullptr
 };
 void causal_conv_split(CcParams& p, bool gradient);
+double causal_conv_workgroups(const CcParams& p, bool gradient);  // of 256
 hipError_t launch_causal_conv(const CcParams& p, hipStream_t stream);
 hipError_t launch_causal_conv_backward(const CcParams& p, hipStream_t stream);
 
@@ -72,6 +73,7 @@ struct CcStep {
   int silu, bf16;
   void* out;
 };
+double causal_conv_step_workgroups(const CcStep& p);  // of 256
 hipError_t launch_causal_conv_step(const CcStep& p, hipStream_t stream);
 
 // ---------------------------------------------------------------- selective scan
@@ -128,6 +130,7 @@ struct SsStep {
   const int32_t* slots;
   void* out;
 };
+int selective_scan_step_lanes(int N);  // that a channel takes
 hipError_t launch_selective_scan_step(const SsStep& p, hipStream_t stream);
 
 // ---------------------------------------------------------------- group norm
@@ -152,7 +155,7 @@ struct GnParams {
   float* gbias;
 };
 void group_norm_split(GnParams& p, bool gradient);
-double group_norm_workgroups(const GnParams& p);  // of its largest launch
+double group_norm_workgroups(const GnParams& p, bool gradient);  // of its largest launch; infinite where none takes it
 // Floats of workspace: stats, then sums (rows of the channels' gradients).
 int64_t group_norm_stats_floats(const GnParams& p);
 int64_t group_norm_sums_floats(const GnParams& p);
