@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import operator
 import os
 import warnings
 
@@ -1424,6 +1425,17 @@ def _positions(t: torch.Tensor) -> torch.Tensor:
                                                      t.shape[-1])
 
 
+def _group_count(op: str, groups) -> int:
+    """groups as the library takes it: ctypes would cut a larger number to 64 bits, which may be another's count."""
+    try:
+        count = operator.index(groups)
+    except TypeError:
+        raise SxError(SX_E_DIM_001, f"{op}: {groups!r} groups: a whole number is required") from None
+    if not 1 <= count < 1 << 63:
+        raise SxError(SX_E_DIM_001, f"{op}: {count} groups")
+    return count
+
+
 def _norm_operands(op, x, weight, bias, more=()):
     index = _device_index(op, ("x", *(n for n, _ in more)), (x, *(t for _, t in more)),
                           (("weight", weight), ("bias", bias)))
@@ -1466,6 +1478,7 @@ def _group_norm_forward(x, groups, weight, bias, eps, activation):
     op = "group-norm"
     act = _activation(op, activation)
     code, index, weight, bias = _norm_operands(op, x, weight, bias)
+    groups = _group_count(op, groups)
     v = _positions(x)
     out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     nbytes = _norm_workspace_bytes(code, v.shape, groups, False)
@@ -1488,6 +1501,7 @@ def group_norm_backward(x, groups: int, grad_out, weight=None, bias=None, eps: f
     act = _activation(op, activation)
     code, index, weight, bias = _norm_operands(op, x, weight, bias, (("grad_out", grad_out),))
     _require(op, "grad_out", grad_out, x.dtype, x.shape)
+    groups = _group_count(op, groups)
     v, g = _positions(x), _positions(grad_out)
     gx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     gw, gb = (None if w is None else torch.empty(w.shape, dtype=w.dtype, device=x.device) for w in (weight, bias))

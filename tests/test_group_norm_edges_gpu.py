@@ -63,3 +63,15 @@ def test_squares_past_the_range_are_an_infinite_variance(shape, groups, type):
         assert torch.equal(out, s["bias"].expand(shape).to(type))
         assert not got[0].any() and not got[1].any()
         assert torch.isfinite(got[2]).all() and got[2].any()
+
+
+def test_group_counts_past_64_bits():
+    s, go = norm.make(shape=(6, 32), type=F32)
+    for groups in (2 ** 64 + 4, 4 - 2 ** 64, 2 ** 63, 4.0, "4", None):
+        for call in (lambda g: sx.group_norm(s["x"], g), lambda g: sx.group_norm_backward(s["x"], g, go)):
+            with pytest.raises(sx.SxError) as e:
+                call(groups)
+            assert e.value.code == B.SX_E_DIM_001, groups
+    want = sx.group_norm(s["x"], 4)
+    for groups in (torch.tensor([4, 8]).numpy()[0], torch.tensor(4)):
+        assert torch.equal(sx.group_norm(s["x"], groups), want)
