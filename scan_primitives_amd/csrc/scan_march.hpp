@@ -15,28 +15,21 @@ __device__ __forceinline__ float of_token(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x150 + J, 0xf, 0xf, true));
 }
 
-// f(integral_constant<int, 0>) ... f(integral_constant<int, N - 1>), or last to first.
+// f(integral_constant<int, 0>) ... f(integral_constant<int, N - 1>).
 template <int N, typename F>
 __device__ __forceinline__ void each(F&& f) {
   [&]<int... I>(std::integer_sequence<int, I...>) { (f(std::integral_constant<int, I>{}), ...); }
   (std::make_integer_sequence<int, N>{});
 }
 
-// Four channels of one token. WIDE: they lie next to each other and exist all; else an element at a time, those
-// behind the last (`left` of them exist) read as the last.
-template <bool BF, bool WIDE>
+// Four channels of one token, an element at a time: those behind the last (`left` of them exist) read as the last.
+template <bool BF>
 __device__ __forceinline__ typename Piece<BF, 4>::Raw four_channels(const TokenView& v, int64_t at, int left) {
-  using P = Piece<BF, 4>;
-  using E = typename P::E;
-  const E* p = static_cast<const E*>(v.p) + at;
-  if constexpr (WIDE) {
-    return P::load(p);
-  } else {
-    return P::of(p[0], p[min(1, left - 1) * v.sd], p[min(2, left - 1) * v.sd], p[min(3, left - 1) * v.sd]);
-  }
+  const auto* p = static_cast<const typename Piece<BF, 4>::E*>(v.p) + at;
+  return Piece<BF, 4>::of(p[0], p[min(1, left - 1) * v.sd], p[min(2, left - 1) * v.sd], p[min(3, left - 1) * v.sd]);
 }
 
-// Four channels of a contiguous result.
+// Four channels of a contiguous result. WIDE: all exist; else `left` of them.
 template <bool BF, bool WIDE>
 __device__ __forceinline__ void put_channels(void* out, int64_t at, int left, const float (&v)[4]) {
   using P = Piece<BF, 4>;
@@ -50,26 +43,6 @@ __device__ __forceinline__ void put_channels(void* out, int64_t at, int left, co
       if (i < left) Piece<BF, 1>::store(p + i, {v[i]});
   }
 }
-
-// States n0 .. n0 + 3 of a token's row of b or c, zero where there are none.
-template <bool BF>
-struct RowRaw {
-  typename Piece<BF, 1>::E e[kScanStates];
-  __device__ __forceinline__ void load(const RowView& v, int64_t at, int n0, int N, bool live) {
-    using E = typename Piece<BF, 1>::E;
-    const E* p = static_cast<const E*>(v.p) + at;
-#pragma unroll
-    for (int i = 0; i < kScanStates; ++i) e[i] = live && n0 + i < N ? p[(n0 + i) * v.sn] : E(0);
-  }
-  __device__ __forceinline__ void open(float (&f)[kScanStates]) const {
-#pragma unroll
-    for (int i = 0; i < kScanStates; ++i) {
-      float one[1];
-      Piece<BF, 1>::open(e[i], one);
-      f[i] = one[0];
-    }
-  }
-};
 
 // A rate for exp2: a log2(e), never infinite, for a step of zero (a token that does not exist has one) leaves the state
 // as it is.
@@ -193,7 +166,7 @@ struct TileReader {
       const E* from = base + int64_t(t) * row;
       return P::load(from + (off + uint32_t(min(q, last - t)) * row));
     } else {
-      return left > 0 && t + q <= last ? four_channels<BF, false>(v, at + int64_t(t + q) * st, left) : P::zero();
+      return left > 0 && t + q <= last ? four_channels<BF>(v, at + int64_t(t + q) * st, left) : P::zero();
     }
   }
 };

@@ -78,7 +78,6 @@ hipError_t launch_causal_conv_step(const CcStep& p, hipStream_t stream);
 
 // ---------------------------------------------------------------- selective scan
 
-constexpr int kScanMaxN = 32;   // states a channel
 constexpr int kScanStates = 4;  // states a wave holds of each of its channels
 
 struct SsParams {
