@@ -58,7 +58,8 @@ __device__ __forceinline__ void rates(const float* a, int64_t d, int n0, int N, 
   for (int i = 0; i < kScanStates; ++i) r[i] = is && n0 + i < N ? rate_of(a[d * N + n0 + i]) : 0.0f;
 }
 
-// Whether a wave's states may grow: a positive rate, or steps of any sign.
+// Whether a wave's states may grow: a positive rate, or steps of any sign. It waits for the rates: asked for behind the
+// first loads that do not.
 __device__ __forceinline__ bool may_grow(const SsParams& p, const float (&rate)[kScanStates]) {
   bool any = !p.softplus;
 #pragma unroll
@@ -75,6 +76,7 @@ __device__ __forceinline__ float times_exp2(float v, float e) {
 // States (or adjoints) over tokens whose dt add up to `steps`: exp2(steps rate) h + own in place of h. Where states
 // grow, the decay alone may be infinite while its product is not: a zero stays zero, a small state comes out as token
 // by token.
+constexpr float kMostExponent = 127.0f;
 __device__ __forceinline__ void carry_over(bool grows, float steps, const float (&rate)[kScanStates], const f32x4& own,
                                            float (&h)[kScanStates]) {
   if (!grows) {
@@ -84,7 +86,7 @@ __device__ __forceinline__ void carry_over(bool grows, float steps, const float 
 #pragma unroll
     for (int i = 0; i < kScanStates; ++i) {
       const float e = steps * rate[i];
-      h[i] = e <= 127.0f ? fmaf(exp2_of(e), h[i], own[i]) : times_exp2(h[i], e) + own[i];
+      h[i] = e <= kMostExponent ? fmaf(exp2_of(e), h[i], own[i]) : times_exp2(h[i], e) + own[i];
     }
   }
 }
@@ -430,25 +432,35 @@ __global__ __launch_bounds__(kWave* W, march_waves_per_simd(W)) void scan_march(
   read_states(OUT || KIND == March::Marks ? p.initial : nullptr, int64_t(b) * p.D + d, n0, p.N, is, h);
   if constexpr (OUT) {
     constexpr int A = 8;  // segments read ahead of the chain
-    const auto chain = [&](auto grows) {
-      for (int m = 0; m < seg; m += A) {
-        f32x4 own[A];
-        float sum[A];
+    for (int m = 0; m < seg; m += A) {
+      f32x4 own[A];
+      float sum[A];
 #pragma unroll
-        for (int k = 0; k < A; ++k) {
-          const int64_t row = int64_t(min(m + k, seg - 1)) * p.B + b;
-          own[k] = is ? *reinterpret_cast<const f32x4*>(p.seg_state + packed_at(p, row, wave, d)) : zero4();
-          sum[k] = is ? p.seg_steps[row * p.D + d] : 0.0f;
-        }
+      for (int k = 0; k < A; ++k) {
+        const int64_t row = int64_t(min(m + k, seg - 1)) * p.B + b;
+        own[k] = is ? *reinterpret_cast<const f32x4*>(p.seg_state + packed_at(p, row, wave, d)) : zero4();
+        sum[k] = is ? p.seg_steps[row * p.D + d] : 0.0f;
+      }
+      // one look at all of them: few have grown so far
+      bool apart = false;
+      if (may_grow(p, rate)) {
+        float most = 0.0f;
+#pragma unroll
+        for (int k = 0; k < A; ++k)
+#pragma unroll
+          for (int i = 0; i < kScanStates; ++i) most = fmaxf(most, sum[k] * rate[i]);
+        apart = __any(most > kMostExponent);
+      }
+      const auto chain = [&](auto grown) {
 #pragma unroll
         for (int k = 0; k < A; ++k) {
           if (m + k >= seg) break;
-          carry_over(grows, sum[k], rate, own[k], h);
+          carry_over(grown, sum[k], rate, own[k], h);
         }
-      }
-    };
-    if (may_grow(p, rate)) chain(std::true_type());
-    else chain(std::false_type());
+      };
+      if (apart) chain(std::true_type());
+      else chain(std::false_type());
+    }
   }
 #pragma unroll
   for (int i = 0; i < kScanStates; ++i) {

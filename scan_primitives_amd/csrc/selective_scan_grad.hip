@@ -44,24 +44,34 @@ __global__ __launch_bounds__(256) void carry(SsParams p) {
   f32x4* at = reinterpret_cast<f32x4*>(back ? p.seg_adjoint : p.seg_state) + idx;
   const float* steps = p.seg_steps + b * p.D + d;
   constexpr int A = 4;  // segments read ahead of the chain
-  const bool grows = may_grow(p, rate);
-  for (int m = 0; m < p.segments; m += A) {
+  struct Runs {
     f32x4 own[A];
     float sum[A];
+  } next;
+  const auto read = [&](int m) {
 #pragma unroll
     for (int k = 0; k < A; ++k) {
       const int s = min(m + k, p.segments - 1), j = back ? p.segments - 1 - s : s;
-      own[k] = at[j * p.B * row];
-      sum[k] = steps[int64_t(j) * p.B * p.D];
+      next.own[k] = at[j * p.B * row];
+      next.sum[k] = steps[int64_t(j) * p.B * p.D];
     }
+  };
+  read(0);
+  const auto chain = [&](auto grows) {
+    for (int m = 0; m < p.segments; m += A) {
+      const Runs now = next;
+      if (m + A < p.segments) read(m + A);
 #pragma unroll
-    for (int k = 0; k < A; ++k) {
-      if (m + k >= p.segments) break;
-      const int j = back ? p.segments - 1 - (m + k) : m + k;
-      at[j * p.B * row] = f32x4{h[0], h[1], h[2], h[3]};
-      carry_over(grows, sum[k], rate, own[k], h);
+      for (int k = 0; k < A; ++k) {
+        if (m + k >= p.segments) break;
+        const int j = back ? p.segments - 1 - (m + k) : m + k;
+        at[j * p.B * row] = f32x4{h[0], h[1], h[2], h[3]};
+        carry_over(grows, now.sum[k], rate, now.own[k], h);
+      }
     }
-  }
+  };
+  if (may_grow(p, rate)) chain(std::true_type());
+  else chain(std::false_type());
 }
 
 template <int CTRL>
@@ -222,7 +232,6 @@ __global__ __launch_bounds__(kWave* W, grad_waves_per_simd(BF, W)) void grad_mar
       read_states(p.grad_state, int64_t(b) * p.D + d + c, n0, p.N, is[c], mu[c]);
     }
   }
-  const bool grows = JOIN && (may_grow(p, rate[0]) || may_grow(p, rate[1]));
   f32x4 marks[2];
   float mark_steps[2];
   const auto read_marks = [&](int span) {
@@ -245,6 +254,7 @@ __global__ __launch_bounds__(kWave* W, grad_waves_per_simd(BF, W)) void grad_mar
     rows.read((spans - 1) * M, j8, last);
     read_marks(spans - 1);
   }
+  const bool grows = JOIN && (may_grow(p, rate[0]) || may_grow(p, rate[1]));
   __syncthreads();
   for (int span = spans - 1; span >= 0; --span) {
     const int t0 = span * M, room = last - t0;  // room: the last token of the span there is
