@@ -11,10 +11,10 @@
 // differences from the mean; a lane keeps its channels from row to row, so the weights
 // are read once and their gradients stay in registers (rows_*).
 // Else the positions are cut into chunks: one launch leaves each chunk's count, mean and
-// squared distance from it (joined pair by pair, so no large mean cancels), the next
+// squared distance from it (joined so that no large mean cancels), the next
 // joins the chunks' and normalises; the gradient has one more for its two sums (map_*).
 // Bound by memory: 16384 rows of 2048 channels in bf16 take 23 to 25 us (5.5 TB/s), the gradient of
-// 8 x 4096 positions of 512 channels 57 to 59 us: three launches, of which the first two read what the third reads again.
+// 8 x 4096 positions of 512 channels 58 to 60 us: three launches, of which the first two read what the third reads again.
 #include <algorithm>
 #include <cmath>
 
@@ -382,22 +382,43 @@ struct Norm {
   float mean, r;
 };
 
+// 1 / n of a count, to 2^-44 of it: an instruction's 2^-22, refined.
+__device__ __forceinline__ double inverse_of(float n) {
+  const double r = __builtin_amdgcn_rcpf(n);
+  return r * fma(-double(n), r, 2.0);
+}
+
 // Squared distance from the mean of n values with these sums. Below zero by rounding it is zero; what is not finite
 // stays so: the mean of a group with an infinity is infinite, and only an infinite or lost variance turns all to NaN.
 __device__ __forceinline__ float spread_of(float squares, float sum, float n) {
   const float d = fmaf(-sum, sum / n, squares);
   return d < 0.0f ? 0.0f : d;
 }
+__device__ __forceinline__ double spread_of(double squares, double sum, float n) {
+  const double d = fma(-sum, sum * inverse_of(n), squares);
+  return d < 0.0 ? 0.0 : d;
+}
 
-// The moments of a block's part of a thread's group. A thread sums differences from its first value, and the threads
-// differences from the mean of the group's first, so that no large mean cancels.
+// The moments of a block's part of a thread's group. A thread sums differences from the mean of its first four
+// positions, and the threads differences from the mean of a few of theirs, so that no large mean cancels, and no outlier
+// among the first (4096 positions of 16 channels a group, the first position off by 300: 2e-7 of a result's size, 3e-6
+// with differences from the very first).
 template <bool BF, int V>
 __device__ __forceinline__ Moments block_stats(const GnParams& p, const Place<V>& a, float (*l)[kThreads]) {
   using P = Piece<BF, V>;
   Ahead<BF, V, false> in(p, a);
-  float first[V], sum = 0.0f, sq = 0.0f, n = 0.0f;
-  P::open(in.xin[0], first);
-  const float shift = first[0];
+  float shift = 0.0f, sum = 0.0f, sq = 0.0f, n = 0.0f;
+  {
+    const int count = in.left > 3 * in.rows ? 4 : in.left > in.rows ? 2 : 1;
+    const float share = 1.0f / float(count * V);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      float v[V];
+      P::open(in.xin[i], v);
+#pragma unroll
+      for (int k = 0; k < V; ++k) shift = i < count ? fmaf(v[k], share, shift) : shift;
+    }
+  }
   in.each([&](int64_t, const float(&v)[V], const float(&)[V]) {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -411,7 +432,17 @@ __device__ __forceinline__ Moments block_stats(const GnParams& p, const Place<V>
   l[0][threadIdx.x] = mean;
   __syncthreads();
   const int g = a.any && a.k.parts == 1 ? a.piece / a.k.pieces : 0;
-  const float about = l[0][g * (a.k.parts == 1 ? a.k.pieces : a.k.width)];  // the group's first piece has positions
+  float about = 0.0f;
+  {
+    const int per = a.k.parts == 1 ? a.k.pieces : a.k.width;
+    const int here = a.k.parts == 1 ? a.k.pieces : min(kThreads, a.k.pieces - a.part * kThreads);
+    // rows of threads that have positions; else pieces of the first, far from each other
+    const bool rows = a.k.rows >= 4 && a.p1 - a.p0 >= 4;
+    const int bits = rows ? 2 : here >= 8 ? 3 : here >= 4 ? 2 : here >= 2 ? 1 : 0;
+    const int step = rows ? a.k.width : here >> bits;
+    for (int i = 0; i < 1 << bits; ++i) about += l[0][g * per + i * step];
+    about = ldexpf(about, -bits);
+  }
   __syncthreads();
   const float off = mean - about;
   float v[3] = {n, n * off, n > 0.0f ? fmaf(n * off, off, m2) : 0.0f};
@@ -447,15 +478,15 @@ __global__ __launch_bounds__(kThreads) void map_stats(GnParams p) {
 
 // Sums of K values over a block's groups' entries (chunks, and parts of wide groups), into l[..][group]: thread t has
 // group t % groups and every (threads / groups)-th entry, value(group, entry, v).
-template <int K, int V, typename F>
-__device__ __forceinline__ void entry_sums(const GnParams& p, const Place<V>& a, float (*l)[kThreads], F&& value) {
+template <int K, typename T, int V, typename F>
+__device__ __forceinline__ void entry_sums(const GnParams& p, const Place<V>& a, T (*l)[kThreads], F&& value) {
   const int groups = a.groups_here(p), slots = kThreads / groups, entries = p.chunks * a.k.parts;
   const int tid = int(threadIdx.x), g = tid % groups, slot = tid / groups;
-  float sum[K] = {};
+  T sum[K] = {};
   if (slot < slots) {
 #pragma unroll 4
     for (int i = slot; i < entries; i += slots) {
-      float v[K];
+      T v[K];
       value(g, i, v);
 #pragma unroll
       for (int k = 0; k < K; ++k) sum[k] += v[k];
@@ -481,20 +512,22 @@ __device__ __forceinline__ int64_t entry_at(const GnParams& p, const Place<V>& a
   return ((a.sample * p.chunks + i / a.k.parts) * p.g + a.group + g) * a.k.parts + i % a.k.parts;
 }
 
-// Mean and 1 / sqrt(variance + eps) of a thread's group, from all chunks: sums about the first entry's mean.
+// Mean and 1 / sqrt(variance + eps) of a thread's group, from all chunks: sums about the first entry's mean, in 64 bits,
+// which a first chunk far from the others needs (of 200000 positions, off by 300: 1e-7 of a result's size, 1.5e-5 in 32).
 template <int V>
-__device__ __forceinline__ Norm joined_stats(const GnParams& p, const Place<V>& a, float (*l)[kThreads]) {
+__device__ __forceinline__ Norm joined_stats(const GnParams& p, const Place<V>& a, double (*l)[kThreads]) {
   const auto first = [&](int g) { return p.stats[entry_at(p, a, g, 0) * 3 + 1]; };
-  entry_sums<3>(p, a, l, [&](int g, int i, float (&v)[3]) {
+  entry_sums<3>(p, a, l, [&](int g, int i, double (&v)[3]) {
     const float* from = p.stats + entry_at(p, a, g, i) * 3;
-    const float off = from[1] - first(g);
+    const double off = double(from[1]) - double(first(g));
     v[0] = from[0];
-    v[1] = from[0] * off;
-    v[2] = fmaf(v[1], off, from[2]);
+    v[1] = v[0] * off;
+    v[2] = fma(v[1], off, double(from[2]));
   });
   const int g = a.any && a.k.parts == 1 ? a.piece / a.k.pieces : 0;
-  const float count = l[0][g], sum = l[1][g];
-  const Norm n{first(g) + sum / count, rsqrtf(spread_of(l[2][g], sum, count) / count + p.eps)};
+  const float count = float(l[0][g]);
+  const Norm n{float(double(first(g)) + l[1][g] * inverse_of(count)),
+               rsqrtf(float(spread_of(l[2][g], l[1][g], count)) / count + p.eps)};
   __syncthreads();
   return n;
 }
@@ -582,7 +615,7 @@ __device__ __forceinline__ void pass_back(const GnParams& p, const Place<V>& a, 
 
 template <bool BF, int V>
 __global__ __launch_bounds__(kThreads) void map_forward(GnParams p) {
-  __shared__ float l[3][kThreads];
+  __shared__ double l[3][kThreads];
   const Place<V> a(p);
   Ahead<BF, V, false> in(p, a);
   normalise<BF, V>(p, a, in, joined_stats<V>(p, a, l));
@@ -590,10 +623,11 @@ __global__ __launch_bounds__(kThreads) void map_forward(GnParams p) {
 
 template <bool BF, int V>
 __global__ __launch_bounds__(kThreads) void map_sums(GnParams p, float* group_sums) {
-  __shared__ float l[3][kThreads], share[2][kThreads][V];
+  __shared__ double joined[3][kThreads];
+  __shared__ float l[2][kThreads], share[2][kThreads][V];
   const Place<V> a(p);
   Ahead<BF, V, true> in(p, a);
-  const Norm n = joined_stats<V>(p, a, l);
+  const Norm n = joined_stats<V>(p, a, joined);
   float s1, s2;
   block_sums<BF, V>(p, a, in, n, l, share, &s1, &s2);
   if (first_of_group(a)) {
@@ -605,7 +639,8 @@ __global__ __launch_bounds__(kThreads) void map_sums(GnParams p, float* group_su
 
 template <bool BF, int V>
 __global__ __launch_bounds__(kThreads) void map_backward(GnParams p, const float* group_sums) {
-  __shared__ float l[3][kThreads];
+  __shared__ double joined[3][kThreads];
+  __shared__ float l[2][kThreads];
   const Place<V> a(p);
   Ahead<BF, V, true> in(p, a);
   entry_sums<2>(p, a, l, [&](int g, int i, float (&v)[2]) {
@@ -616,7 +651,7 @@ __global__ __launch_bounds__(kThreads) void map_backward(GnParams p, const float
   const int g = a.any && a.k.parts == 1 ? a.piece / a.k.pieces : 0;
   const float s1 = l[0][g], s2 = l[1][g];
   __syncthreads();
-  pass_back<BF, V>(p, a, in, joined_stats<V>(p, a, l), s1, s2);
+  pass_back<BF, V>(p, a, in, joined_stats<V>(p, a, joined), s1, s2);
 }
 
 // A block that has its groups whole (one chunk, no wide groups) does all of it in one launch: 4 positions of 256

@@ -4,9 +4,10 @@ import pytest
 import torch
 
 import scan_primitives_amd as sx
+from oracle import state_space as os_
 from scan_primitives_amd import _binding as B
 from tests import test_group_norm_gpu as norm
-from tests.test_causal_conv_gpu import BF, DEV, F32
+from tests.test_causal_conv_gpu import BF, DEV, F32, close
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +76,16 @@ def test_group_counts_past_64_bits():
     want = sx.group_norm(s["x"], 4)
     for groups in (torch.tensor([4, 8]).numpy()[0], torch.tensor(4)):
         assert torch.equal(sx.group_norm(s["x"], groups), want)
+
+
+@pytest.mark.parametrize("far", [300.0, 1e5])
+@pytest.mark.parametrize("shape,groups,first", [((1, 200000, 16), 4, 800), ((1, 1000000, 4), 1, 4000),
+                                                ((2, 4096, 512), 32, 16), ((2, 4096, 512), 32, 1), ((4, 9000), 1, 8)])
+def test_what_stands_first_may_lie_far_from_the_rest(shape, groups, first, far):
+    # A thread sums at most 64 values (of a wide row 36) and a workgroup its 256 threads' about references that one
+    # outlier does not move far, chunks are joined in 64 bits: 8 (sqrt(64) + sqrt(256)) steps of the variance, half as many
+    # of its root, and 16 for the rest.
+    s, _ = norm.make(shape=shape, groups=groups, type=F32)
+    s["x"][:, :first] += far
+    size, *_ = norm._size(s)
+    close("out", sx.group_norm(**s), os_.group_norm(**norm._host(s)), size, 4 * (64 ** 0.5 + 256 ** 0.5) + 16)
