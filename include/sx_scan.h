@@ -672,7 +672,9 @@ sx_status sx_causal_conv_step(sx_dtype dtype, const int64_t* x_shape, const int6
  *   h[n] = exp(dt a[n]) h[n] + dt x b[n],   y = sum over n of c[n] h[n] + skip x,
  *   out = y z / (1 + exp(-z))           (y where z is NULL).
  * Steps, states and sums are f32 for f32 and bf16 operands alike; out is rounded
- * to `dtype` once.
+ * to `dtype` once. Rates and steps have any sign: a state may grow, and one of
+ * zero stays zero while no token's own decay exp(dt a) passes f32's range. A step of
+ * zero keeps a state whatever its rate.
  *
  *  dtype         SX_F32 or SX_BF16: x, delta, b, c, z and out.
  *  x, delta, z   [B, T, D] (x's shape), each with strides (NULL for contiguous; any
@@ -726,8 +728,9 @@ size_t sx_selective_scan_workspace_bytes(sx_dtype dtype, const int64_t* x_shape,
  *  grad_initial  f32, contiguous [B, D, N], or NULL where not wanted.
  *  workspace     at least sx_selective_scan_backward_workspace_bytes() bytes,
  *                256-byte aligned; may hold anything. It holds the states of
- *                every eighth token: 0.5 B T D N floats at N a power of two
- *                from 4 on.
+ *                every eighth token, 0.125 B T D N floats for N of 4, 8, 12, 16
+ *                or 32 (others take those of the next), and sums: 0.15 to 0.16
+ *                B T D N in all for many tokens of 16 or 32 states.
  *
  * Gradients of tokens that do not exist are zero. The outputs are 16-byte
  * aligned and overlap nothing. Results do not change from call to call (no

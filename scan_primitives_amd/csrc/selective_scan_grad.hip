@@ -20,8 +20,9 @@
 // a time (eight tokens of four states of b and of c) fold into one a lane, in 140 additions.
 //
 // Bound by the issue of vector instructions (75% of the cycles of grad_march, which leaves two waves a SIMD: its
-// registers hold the states before eight tokens). 4 x 2048 tokens of 2048 channels of 16 states in bf16: 348 us, of
-// them 111 scan_march, 6 carry, 270 grad_march under a profiler, 11 the sums; the bytes alone would take 46.
+// registers hold the states before eight tokens). 4 x 2048 tokens of 2048 channels of 16 states in bf16: 354 us; the
+// bytes alone would take 46. Under a profiler, where a launch costs some more, 114 scan_march, 7 carry, 272 grad_march
+// and 11 the sums.
 #include <algorithm>
 
 #include "scan_march.hpp"
