@@ -440,8 +440,8 @@ __device__ __forceinline__ Moments block_stats(const GnParams& p, const Place<V>
     const bool rows = a.k.rows >= 4 && a.p1 - a.p0 >= 4;
     const int bits = rows ? 2 : here >= 8 ? 3 : here >= 4 ? 2 : here >= 2 ? 1 : 0;
     const int step = rows ? a.k.width : here >> bits;
-    for (int i = 0; i < 1 << bits; ++i) about += l[0][g * per + i * step];
-    about = ldexpf(about, -bits);
+    const float share = ldexpf(1.0f, -bits);  // of each first: their sum may pass the range
+    for (int i = 0; i < 1 << bits; ++i) about = fmaf(l[0][g * per + i * step], share, about);
   }
   __syncthreads();
   const float off = mean - about;

@@ -89,3 +89,12 @@ def test_what_stands_first_may_lie_far_from_the_rest(shape, groups, first, far):
     s["x"][:, :first] += far
     size, *_ = norm._size(s)
     close("out", sx.group_norm(**s), os_.group_norm(**norm._host(s)), size, 4 * (64 ** 0.5 + 256 ** 0.5) + 16)
+
+
+@pytest.mark.parametrize("value", [0.1, 2e38, -3.3e38])
+@pytest.mark.parametrize("shape,groups", [((3, 20, 64), 4), ((1, 20000, 32), 2), ((2, 10, 6000), 2), ((2, 300, 33), 3)])
+def test_equal_values_of_any_size_have_no_variance(shape, groups, value):
+    s, go = norm.make(shape=shape, groups=groups, type=F32)
+    s["x"].fill_(value)
+    assert torch.equal(sx.group_norm(**s), s["bias"].expand(shape))
+    assert all(torch.isfinite(t).all() for t in sx.group_norm_backward(grad_out=go, **s))
