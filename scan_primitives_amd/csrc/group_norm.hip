@@ -441,7 +441,11 @@ __device__ __forceinline__ Moments block_stats(const GnParams& p, const Place<V>
     const int bits = rows ? 2 : here >= 8 ? 3 : here >= 4 ? 2 : here >= 2 ? 1 : 0;
     const int step = rows ? a.k.width : here >> bits;
     const float share = ldexpf(1.0f, -bits);  // of each first: their sum may pass the range
-    for (int i = 0; i < 1 << bits; ++i) about = fmaf(l[0][g * per + i * step], share, about);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // (all on their way at once)
+      const bool is = i < 1 << bits;
+      about = fmaf(l[0][g * per + (is ? i * step : 0)], is ? share : 0.0f, about);
+    }
   }
   __syncthreads();
   const float off = mean - about;
